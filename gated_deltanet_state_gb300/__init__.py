@@ -20,7 +20,7 @@ from typing import Optional
 import torch
 
 from . import inputs
-from .inputs import BF16, F32, LayerShape
+from .inputs import BF16, F32, AttnShape, LayerShape
 
 __all__ = [
     "GdnError", "LayerShape", "StatePool", "load_library", "library_path", "make_desc",
@@ -33,7 +33,9 @@ __all__ = [
     "gdn_mixed_workspace_size", "gdn_mixed_step",
     "gdn_core_prefill_workspace_size", "gdn_core_prefill", "gdn_core_decode",
     "gdn_decode_step", "gdn_checkpoint_resume", "gdn_checkpoint_save", "gdn_replay_append",
-    "gdn_replay_rollback", "gdn_replay_flush", "REPLAY_LOG_SLOTS", "PREFILL_AUTO", "PREFILL_FUSED", "PREFILL_TWO_KERNELS", "STATUS",
+    "gdn_replay_rollback", "gdn_replay_flush", "AttnShape", "KVPool", "make_attn_desc", "gdn_kv_page_bytes", "gdn_kv_tables", "gdn_kv_append", "gdn_kv_gather",
+    "gdn_attn_decode_workspace_size", "gdn_attn_decode", "gdn_attn_prefill", "ATTN_DECODE_ROWS", "KV_BLOCK",
+    "REPLAY_LOG_SLOTS", "PREFILL_AUTO", "PREFILL_FUSED", "PREFILL_TWO_KERNELS", "STATUS",
 ]
 
 REPLAY_LOG_SLOTS = 32
@@ -174,6 +176,7 @@ def load_library(build_if_missing: bool = True):
         "gdn_replay_rollback": ([_P, _P, i32, i32, _P, _P], i32),
         "gdn_replay_flush": ([D, PL, ctypes.POINTER(_ReplayArgs), _P], i32),
     }
+    sig.update(attention._signatures())
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -589,3 +592,11 @@ def gdn_replay_flush(shape: LayerShape, pool: StatePool, *, ckpt_slot, log_x, lo
     st = lib.gdn_replay_flush(ctypes.byref(make_desc(shape)), ctypes.byref(pool.abi()), ctypes.byref(a),
                               _stream(stream))
     return _check(st, "gdn_replay_flush") if raise_on_error else st
+
+
+# --------------------------------------------------------------------------- the attention layers
+
+from . import attention  # noqa: E402  (needs the names above)
+from .attention import (  # noqa: E402
+    ATTN_DECODE_ROWS, KV_BLOCK, KVPool, gdn_attn_decode, gdn_attn_decode_workspace_size, gdn_attn_prefill,
+    gdn_kv_append, gdn_kv_gather, gdn_kv_page_bytes, gdn_kv_tables, make_attn_desc)

@@ -1,0 +1,173 @@
+// attn.h — parameters and launchers of the attention layers' kernels (the
+// 8-bit K / V cache and the attention that reads it; not exported).
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn {
+
+constexpr int kKvBlock = GDN_KV_BLOCK;
+
+// The cache of one layer: page layout of include/gdn.h.
+struct KvCache {
+  char* base;
+  int64_t page_bytes;
+  int32_t num_pages;
+  int32_t page_tokens;
+  int32_t Hkv, d;
+};
+
+// Offsets within a page: block b of head h.
+__host__ __device__ inline int64_t kv_block_index(const KvCache& c, int h, int b) {
+  return (int64_t)h * (c.page_tokens / kKvBlock) + b;
+}
+__host__ __device__ inline int64_t kv_codes_bytes(const KvCache& c) { return (int64_t)c.Hkv * c.page_tokens * c.d; }
+
+struct KvTablesParams {
+  int32_t N, max_pages, num_free, num_pages, page_tokens;
+  int32_t seqs_per_cta, slices;
+  int64_t T;
+  const int32_t* kv_len;
+  const int32_t* new_len;
+  const int32_t* free_pages;
+  int32_t* block_table;
+  int32_t* cu_seqlens;
+  int32_t* cu_kv;
+  int32_t* kv_len_out;
+  int64_t* positions;
+  int64_t* slot_map;
+  int32_t* pages_taken;
+  int32_t* err;
+};
+
+struct KvAppendParams {
+  KvCache c;
+  int64_t T, k_stride, v_stride;
+  const void* k;
+  const void* v;
+  const int64_t* slot_map;
+  int32_t* err;
+};
+
+struct KvGatherParams {
+  KvCache c;
+  int32_t N, max_pages;
+  int64_t T;
+  const int32_t* cu_kv;
+  const int32_t* block_table;
+  void* k;
+  void* v;
+  int32_t* err;
+};
+
+struct AttnDecodeParams {
+  KvCache c;
+  int32_t N, max_pages, Hq, G, max_q, max_kv, max_pieces;
+  int64_t T, q_stride;
+  float scale_log2;   // scale * log2(e)
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* block_table;
+  const void* q;
+  void* o;
+  float* lse;
+  float* part_o;      // [max_pieces][T * Hq][d] sums of p v (nullptr: one piece, written to o)
+  float2* part_ml;    // [max_pieces][T * Hq] (m, l) of the pieces
+  int32_t* err;
+};
+
+struct AttnPrefillParams {
+  int32_t N, Hq, Hkv, G, d, max_q, max_kv;
+  int64_t Tq, Tk, q_stride, k_stride, v_stride;
+  float scale_log2;
+  const int32_t* cu_q;
+  const int32_t* cu_kv;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  int32_t* err;
+  int64_t wait_cycles;
+};
+
+// Keys of a decode sequence are cut into pieces by its own length alone, so a
+// row's sums are formed in the same order whatever batch it is in.  256-token
+// pieces spread a short context over more SMs; 512 keep the pieces' outputs
+// (4 G d bytes each, written and read once) under 3 % of the keys' bytes at
+// G = 6; beyond 38,912 tokens 76 pieces a head are one CTA on each of the 152
+// SMs for two kv heads.
+constexpr int kMaxPieces = 76;
+__host__ __device__ inline int decode_piece_tokens(int L) {
+  if (L <= 2048) return 256;
+  if (L <= 512 * kMaxPieces) return 512;
+  return ((L + kMaxPieces - 1) / kMaxPieces + 127) / 128 * 128;
+}
+__host__ __device__ inline int decode_pieces(int L) {
+  const int c = decode_piece_tokens(L);
+  return (L + c - 1) / c;
+}
+// The most pieces of any length up to L (2,048 tokens make 8 pieces, 2,049 make 5).
+__host__ __device__ inline int decode_max_pieces(int L) {
+  int m = decode_pieces(L < 2048 ? L : 2048);
+  if (L > 2048 && decode_pieces(L < 512 * kMaxPieces ? L : 512 * kMaxPieces) > m)
+    m = decode_pieces(L < 512 * kMaxPieces ? L : 512 * kMaxPieces);
+  return m < 1 ? 1 : m;
+}
+
+cudaError_t launch_kv_tables(const KvTablesParams& p, cudaStream_t st);
+cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_kv_gather(const KvGatherParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_attn_decode(const AttnDecodeParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStream_t st);
+
+}  // namespace gdn
+
+#ifdef __CUDACC__
+#include <cuda_fp16.h>
+
+namespace gdn {
+
+// ---- e4m3 ----------------------------------------------------------------------
+// Two fp32 values to e4m3, nearest even, saturating (lo in the low byte); NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return e4m3x2(a, b) | (e4m3x2(c, d) << 16);
+}
+// Two e4m3 codes (the low 16 bits of w) to fp32.
+__device__ __forceinline__ float2 e4m3_f32x2(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+__device__ __forceinline__ void e4m3_f32x16(const uint4& v, float (&f)[16]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = e4m3_f32x2(w[i]), b = e4m3_f32x2(w[i] >> 16);
+    f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = b.x, f[4 * i + 3] = b.y;
+  }
+}
+
+// ---- cache addressing ------------------------------------------------------------
+__device__ __forceinline__ const uint8_t* kv_k_block(const KvCache& c, int page, int h, int b) {
+  return reinterpret_cast<const uint8_t*>(c.base) + (int64_t)page * c.page_bytes +
+         kv_block_index(c, h, b) * (c.d * kKvBlock);
+}
+__device__ __forceinline__ const uint8_t* kv_v_block(const KvCache& c, int page, int h, int b) {
+  return kv_k_block(c, page, h, b) + kv_codes_bytes(c);
+}
+__device__ __forceinline__ const float* kv_k_scale(const KvCache& c, int page, int h, int b) {
+  return reinterpret_cast<const float*>(c.base + (int64_t)page * c.page_bytes + 2 * kv_codes_bytes(c)) +
+         kv_block_index(c, h, b);
+}
+__device__ __forceinline__ const float* kv_v_scale(const KvCache& c, int page, int h, int b) {
+  return kv_k_scale(c, page, h, b) + (int64_t)c.Hkv * (c.page_tokens / kKvBlock);
+}
+
+}  // namespace gdn
+#endif

@@ -1,0 +1,385 @@
+// attn_simt.cu — attention over the 8-bit cache and over packed prompts with
+// fp32 arithmetic on the CUDA cores: every dtype, head size and group size;
+// and the kernel that joins the pieces of a decode row.
+#include "attn.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kDecRows = 8;        // (row, head of the group) pairs a CTA
+constexpr int kDecWarps = 4;
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T> __device__ __forceinline__ void put1(void* o, int64_t i, float v) {
+  static_cast<T*>(o)[i] = from_f32<T>(v);
+}
+
+}  // namespace
+
+// One piece of one sequence's keys, for one kv head and up to 8 of its query
+// rows.  A warp takes every fourth block of 16 tokens: the lanes hold one
+// token each (two lanes share one, half of d each) for the scores, one element
+// of the head each (d / 32 of them) for the values; each warp keeps its own
+// softmax statistics, joined at the end.
+template <typename T>
+__global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const AttnDecodeParams p) {
+  extern __shared__ float smem[];
+  const int d = p.c.d, piece = blockIdx.x, s = blockIdx.z;
+  const int groups = (p.max_q * p.G + kDecRows - 1) / kDecRows;
+  const int h = blockIdx.y / groups, r0 = blockIdx.y % groups * kDecRows;
+  const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
+  if (n <= 0) return;
+  if (n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) {
+    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
+    return;
+  }
+  const int pt = decode_piece_tokens(L);
+  const int k0 = piece * pt, k1 = min(L, k0 + pt);
+  if (r0 >= n * p.G || (piece > 0 && k0 >= L)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = min(kDecRows, n * p.G - r0);
+  float* sq = smem;                                  // [8][d]
+  float* sp = smem + kDecRows * d + warp * kDecRows * 16;   // [8][16] of this warp
+  for (int i = threadIdx.x; i < kDecRows * d; i += blockDim.x) {
+    const int r = i / d, e = i - r * d;
+    float x = 0.f;
+    if (r < rows) {
+      const int row = (r0 + r) / p.G, g = (r0 + r) % p.G;
+      x = to_f32(static_cast<const T*>(p.q)[(int64_t)(q0 + row) * p.q_stride + (int64_t)(h * p.G + g) * d + e]);
+    }
+    sq[i] = x * p.scale_log2;
+  }
+  __syncthreads();
+  float O[kDecRows][8], m[kDecRows], l[kDecRows];
+#pragma unroll
+  for (int r = 0; r < kDecRows; ++r) {
+    m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) O[r][i] = 0.f;
+  }
+  const int t = lane & 15, hf = lane >> 4;
+  for (int kb = k0 + warp * kKvBlock; kb < k1; kb += kDecWarps * kKvBlock) {
+    const int j = kb / p.c.page_tokens, b = (kb - j * p.c.page_tokens) / kKvBlock;
+    const int page = j < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + j] : -1;
+    if (page < 0 || page >= p.c.num_pages) {
+      if (lane == 0) set_error(p.err, GDN_ERR_PAGE_RANGE);
+      continue;
+    }
+    const uint8_t* kp = kv_k_block(p.c, page, h, b) + (t >> 3) * (d / 16) * 128 + (t & 7) * 16;
+    float acc[kDecRows] = {};
+    for (int c = hf; c < d / 16; c += 2) {
+      float f[16];
+      e4m3_f32x16(*reinterpret_cast<const uint4*>(kp + c * 128), f);
+#pragma unroll
+      for (int r = 0; r < kDecRows; ++r) {
+        const float4* q4 = reinterpret_cast<const float4*>(sq + r * d + c * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 q = q4[i];
+          acc[r] = fmaf(q.x, f[4 * i], acc[r]);
+          acc[r] = fmaf(q.y, f[4 * i + 1], acc[r]);
+          acc[r] = fmaf(q.z, f[4 * i + 2], acc[r]);
+          acc[r] = fmaf(q.w, f[4 * i + 3], acc[r]);
+        }
+      }
+    }
+    const float ks = *kv_k_scale(p.c, page, h, b), vs = *kv_v_scale(p.c, page, h, b);
+    const int pos = kb + t;
+#pragma unroll
+    for (int r = 0; r < kDecRows; ++r) {
+      float x = acc[r] + __shfl_xor_sync(0xffffffffu, acc[r], 16);
+      // keys that this row sees: L - n + row + 1
+      x = pos < L - n + (r0 + r) / p.G + 1 ? x * ks : -INFINITY;
+      // the largest over the block's finite and infinite scores; NaN reaches l
+      float mx = x;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[r], mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float a = fast_exp2(m[r] - ref), e = fast_exp2(x - ref);
+      float sum = e;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      m[r] = mn;
+      l[r] = l[r] * a + sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) O[r][i] *= a;
+      if (hf == 0) sp[r * 16 + t] = e * vs;
+    }
+    __syncwarp();
+    const uint8_t* vp = kv_v_block(p.c, page, h, b);
+    const bool edge = kb + kKvBlock > L - n + 1;   // some row does not see some token
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = lane + 32 * i;
+      if (e < d) {
+        float f[16];
+        e4m3_f32x16(*reinterpret_cast<const uint4*>(vp + e * kKvBlock), f);
+#pragma unroll
+        for (int r = 0; r < kDecRows; ++r) {
+          const int seen = L - n + (r0 + r) / p.G + 1 - kb;
+          const float4* p4 = reinterpret_cast<const float4*>(sp + r * 16);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float4 w = p4[u];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // a masked token's value may be NaN: it is left out, not times 0
+              const float v = edge && 4 * u + k >= seen ? 0.f : f[4 * u + k];
+              O[r][i] = fmaf((&w.x)[k], v, O[r][i]);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  // join the warps: through shared memory, in the order of the warps
+  __syncthreads();
+  float* so = smem;                         // [4][8][d]
+  float* sm = smem + kDecWarps * kDecRows * d;   // [4][8]
+  float* sl = sm + kDecWarps * kDecRows;
+#pragma unroll
+  for (int r = 0; r < kDecRows; ++r) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < d) so[(warp * kDecRows + r) * d + lane + 32 * i] = O[r][i];
+    if (lane == 0) sm[warp * kDecRows + r] = m[r], sl[warp * kDecRows + r] = l[r];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * d; i += blockDim.x) {
+    const int r = i / d, e = i - r * d;
+    float mx = -INFINITY;
+    for (int w = 0; w < kDecWarps; ++w) mx = fmaxf(mx, sm[w * kDecRows + r]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float acc = 0.f, sum = 0.f;
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float a = fast_exp2(sm[w * kDecRows + r] - ref);
+      acc += a * so[(w * kDecRows + r) * d + e];
+      sum += a * sl[w * kDecRows + r];
+    }
+    const int64_t rh = (int64_t)(q0 + (r0 + r) / p.G) * p.Hq + h * p.G + (r0 + r) % p.G;
+    if (p.part_o) {
+      p.part_o[((int64_t)piece * p.T * p.Hq + rh) * d + e] = acc;
+      if (e == 0) p.part_ml[(int64_t)piece * p.T * p.Hq + rh] = make_float2(mx, sum);
+    } else {
+      put1<T>(p.o, rh * d + e, sum == 0.f ? 0.f : acc / sum);
+      if (p.lse && e == 0) p.lse[rh] = sum == 0.f ? -INFINITY : mx * 0.693147180559945309f + logf(sum);
+    }
+  }
+}
+
+// Joins the pieces of every row in their order: o = sum_i w_i O_i / sum_i w_i l_i,
+// w_i = 2^(m_i - max m).  A warp a (row, head).
+template <typename T>
+__global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeParams p) {
+  const int s = blockIdx.y;
+  const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
+  if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
+  const int pieces = max(1, decode_pieces(L)), lane = threadIdx.x & 31, d = p.c.d;
+  const int64_t R = p.T * p.Hq;
+  for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n * p.Hq; i += gridDim.x * 4) {
+    const int64_t rh = (int64_t)q0 * p.Hq + i;
+    float mx = -INFINITY;
+    for (int j = 0; j < pieces; ++j) mx = fmaxf(mx, p.part_ml[j * R + rh].x);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, acc[8] = {};
+    for (int j = 0; j < pieces; ++j) {
+      const float2 ml = p.part_ml[j * R + rh];
+      const float w = fast_exp2(ml.x - ref);
+      sum += w * ml.y;
+      const float* o = p.part_o + (j * R + rh) * d;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lane + 32 * e < d) acc[e] += w * o[lane + 32 * e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (lane + 32 * e < d) put1<T>(p.o, rh * d + lane + 32 * e, sum == 0.f ? 0.f : acc[e] / sum);
+    if (p.lse && lane == 0) p.lse[rh] = sum == 0.f ? -INFINITY : mx * 0.693147180559945309f + logf(sum);
+  }
+}
+
+namespace {
+
+template <typename T>
+cudaError_t decode_simt(const AttnDecodeParams& p, cudaStream_t st) {
+  const int groups = (p.max_q * p.G + kDecRows - 1) / kDecRows;
+  const size_t sm_run = (size_t)(kDecRows * p.c.d + kDecWarps * kDecRows * 16) * 4;
+  const size_t sm_join = (size_t)(kDecWarps * kDecRows * (p.c.d + 2)) * 4;
+  const size_t sm = sm_run > sm_join ? sm_run : sm_join;   // at most 33 KB
+  attn_decode_simt_kernel<T><<<dim3(p.max_pieces, p.c.Hkv * groups, p.N), 32 * kDecWarps, sm, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.part_o) return e;
+  attn_decode_join_kernel<T><<<dim3((unsigned)((p.max_q * p.Hq + 3) / 4), p.N), 128, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
+  return dtype == GDN_BF16 ? decode_simt<__nv_bfloat16>(p, st) : decode_simt<float>(p, st);
+}
+
+// ---- prefill ----------------------------------------------------------------------------
+namespace {
+
+constexpr int kPreRows = 64, kPreKeys = 32;
+
+}  // namespace
+
+// 64 query rows of one kv head's group (row i of the tile: token i / G, head
+// i % G, so that the group shares the keys) against its keys, 32 at a time.
+// 256 threads: 16 x 16, each 4 rows by 2 keys of the scores and 4 rows by
+// d / 16 elements of the outputs.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_prefill_simt_kernel(const AttnPrefillParams p) {
+  extern __shared__ float smem[];
+  const int d = p.d, ld = d + 4;
+  const int s = blockIdx.z, h = blockIdx.y;
+  const int q0 = p.cu_q[s], n = p.cu_q[s + 1] - q0, k0 = p.cu_kv[s], L = p.cu_kv[s + 1] - k0;
+  if (n <= 0) return;
+  if (n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || k0 < 0 || (int64_t)q0 + n > p.Tq || (int64_t)k0 + L > p.Tk) {
+    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
+    return;
+  }
+  // the last tiles first: they see the most keys
+  const int tiles = (int)(((int64_t)n * p.G + kPreRows - 1) / kPreRows);
+  const int tile = tiles - 1 - (int)blockIdx.x;
+  if (tile < 0) return;
+  const int64_t r0 = (int64_t)tile * kPreRows;
+  float* sq = smem;                       // [64][ld]
+  float* sk = sq + kPreRows * ld;         // [32][ld]
+  float* sv = sk + kPreKeys * ld;         // [32][ld]
+  float* sp = sv + kPreKeys * ld;         // [64][36]
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  for (int i = threadIdx.x; i < kPreRows * d; i += 256) {
+    const int r = i / d, e = i - r * d;
+    const int64_t row = (r0 + r) / p.G;
+    const int g = (int)((r0 + r) % p.G);
+    sq[r * ld + e] = row < n ? p.scale_log2 * to_f32(static_cast<const T*>(p.q)[(q0 + row) * p.q_stride + (int64_t)(h * p.G + g) * d + e])
+                             : 0.f;
+  }
+  float O[4][16], m[4], l[4];
+  int lim[4];   // keys that each of this thread's rows sees
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = -INFINITY, l[i] = 0.f;
+    const int64_t row = (r0 + 4 * ty + i) / p.G;
+    lim[i] = row < n ? max(0, (int)(L - n + row + 1)) : 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) O[i][j] = 0.f;
+  }
+  const int last = (int)min((int64_t)n - 1, (r0 + kPreRows - 1) / p.G), most = max(0, L - n + last + 1);
+  const int least = max(0, (int)(L - n + r0 / p.G + 1));
+  for (int kb = 0; kb < most; kb += kPreKeys) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kPreKeys * d; i += 256) {
+      const int r = i / d, e = i - r * d;
+      const bool in = kb + r < L;
+      sk[r * ld + e] = in ? to_f32(static_cast<const T*>(p.k)[(int64_t)(k0 + kb + r) * p.k_stride + (int64_t)h * d + e]) : 0.f;
+      sv[r * ld + e] = in ? to_f32(static_cast<const T*>(p.v)[(int64_t)(k0 + kb + r) * p.v_stride + (int64_t)h * d + e]) : 0.f;
+    }
+    __syncthreads();
+    float x[4][2] = {};
+    for (int e = 0; e < d; e += 4) {
+      float4 a[4], b[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * ld + e);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * ld + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[i][j] = fmaf(a[i].x, b[j].x, x[i][j]);
+          x[i][j] = fmaf(a[i].y, b[j].y, x[i][j]);
+          x[i][j] = fmaf(a[i].z, b[j].z, x[i][j]);
+          x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (kb + tx + 16 * j >= lim[i]) x[i][j] = -INFINITY;
+      float mx = fmaxf(x[i][0], x[i][1]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
+      const float a = fast_exp2(m[i] - ref);
+      const float e0 = fast_exp2(x[i][0] - ref), e1 = fast_exp2(x[i][1] - ref);
+      float sum = e0 + e1;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      m[i] = mn, l[i] = l[i] * a + sum;
+      sp[(4 * ty + i) * 36 + tx] = e0;
+      sp[(4 * ty + i) * 36 + tx + 16] = e1;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) O[i][j] *= a;
+    }
+    __syncwarp();   // a row's 16 threads are in one warp
+    const int keys = min(kPreKeys, L - kb);
+    const bool edge = kb + keys > least;
+    for (int k = 0; k < keys; ++k) {
+      float w[4];
+      bool see[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = sp[(4 * ty + i) * 36 + k], see[i] = !edge || kb + k < lim[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = 4 * tx + 64 * j;
+        if (e < d) {
+          const float4 v = *reinterpret_cast<const float4*>(sv + k * ld + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (see[i]) {   // a masked key's value may be NaN
+              O[i][4 * j] = fmaf(w[i], v.x, O[i][4 * j]);
+              O[i][4 * j + 1] = fmaf(w[i], v.y, O[i][4 * j + 1]);
+              O[i][4 * j + 2] = fmaf(w[i], v.z, O[i][4 * j + 2]);
+              O[i][4 * j + 3] = fmaf(w[i], v.w, O[i][4 * j + 3]);
+            }
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 4 * ty + i, row = r / p.G;
+    if (row >= n) continue;
+    const int64_t rh = (q0 + row) * p.Hq + h * p.G + r % p.G;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int e = 4 * tx + 64 * (j >> 2) + (j & 3);
+      if (e < d) put1<T>(p.o, rh * d + e, l[i] == 0.f ? 0.f : O[i][j] / l[i]);
+    }
+    if (p.lse && tx == 0) p.lse[rh] = l[i] == 0.f ? -INFINITY : m[i] * 0.693147180559945309f + logf(l[i]);
+  }
+}
+
+namespace {
+
+template <typename T>
+cudaError_t prefill_simt(const AttnPrefillParams& p, cudaStream_t st) {
+  const int64_t tiles = ((int64_t)p.max_q * p.G + kPreRows - 1) / kPreRows;
+  const size_t sm = (size_t)((kPreRows + 2 * kPreKeys) * (p.d + 4) + kPreRows * 36) * 4;   // 142,336 B at d = 256
+  cudaError_t e = cudaFuncSetAttribute(attn_prefill_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  attn_prefill_simt_kernel<T><<<dim3((unsigned)tiles, p.Hkv, p.N), 256, sm, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStream_t st) {
+  return dtype == GDN_BF16 ? prefill_simt<__nv_bfloat16>(p, st) : prefill_simt<float>(p, st);
+}
+
+}  // namespace gdn

@@ -1,0 +1,434 @@
+// kv_cache.cu — the paged 8-bit K / V cache of the attention layers: a step's
+// tables, the append of new rows and the read-back of a cached prefix
+// (layout and rules: include/gdn.h).
+#include "attn.h"
+
+namespace gdn {
+
+namespace {
+
+// Exclusive prefix sums of two ints over a CTA of 256 threads; the totals come
+// back in ta, tb.
+__device__ __forceinline__ void scan2_256(int& a, int& b, int& ta, int& tb, int* sh /* [16] */) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int ia = a, ib = b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int xa = __shfl_up_sync(0xffffffffu, ia, o), xb = __shfl_up_sync(0xffffffffu, ib, o);
+    if (lane >= o) ia += xa, ib += xb;
+  }
+  if (lane == 31) sh[w] = ia, sh[8 + w] = ib;
+  __syncthreads();
+  int ba = 0, bb = 0;
+  ta = tb = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i == w) ba = ta, bb = tb;
+    ta += sh[i], tb += sh[8 + i];
+  }
+  __syncthreads();
+  a = ba + ia - a;
+  b = bb + ib - b;
+}
+
+}  // namespace
+
+// Tables of a step.  CTA (x, y): requests [x * seqs_per_cta, ...), slice y of
+// their tokens.  Every CTA forms the running sums up to its own requests from
+// the lengths themselves (N loads of 8 bytes from L2), so one launch does all
+// and no CTA waits on another.
+__global__ void __launch_bounds__(256) kv_tables_kernel(const KvTablesParams p) {
+  __shared__ int sh[16];
+  __shared__ int s_first[64], s_row[64], s_ok[64];   // of this CTA's requests
+  const int s0 = blockIdx.x * p.seqs_per_cta, s1 = min(p.N, s0 + p.seqs_per_cta);
+  int need0 = 0, row0 = 0, kv0 = 0, taken = 0;   // running sums before the scanned chunk
+  for (int c0 = 0; c0 < s1; ) {
+    // chunks of 256 requests up to s0, then the CTA's own (at most 64)
+    const int c1 = c0 < s0 ? min(s0, c0 + 256) : s1;
+    const int s = c0 + threadIdx.x;
+    int kv = 0, add = 0, need = 0, have = 0;
+    bool ok = true;
+    if (s < c1) {
+      kv = p.kv_len[s], add = p.new_len[s];
+      const int64_t total = (int64_t)kv + add;
+      ok = kv >= 0 && add >= 0 && total <= 0x7fffffff && (total + p.page_tokens - 1) / p.page_tokens <= p.max_pages;
+      if (kv < 0) kv = 0;
+      if (add < 0) add = 0;
+      have = (int)(((int64_t)kv + p.page_tokens - 1) / p.page_tokens);
+      need = ok ? (int)((total + p.page_tokens - 1) / p.page_tokens) - have : 0;
+    }
+    int first = need, row = add, tn, ta;
+    scan2_256(first, row, tn, ta, sh);
+    first += need0, row += row0;
+    ok = ok && (need == 0 || first + need <= p.num_free);
+    int out = s < c1 ? kv + (ok ? add : 0) : 0, got = s < c1 && ok ? need : 0, to, tg;
+    const int kv_out = out;
+    scan2_256(out, got, to, tg, sh);
+    if (c0 >= s0 && s < c1) {
+      s_first[s - s0] = first, s_row[s - s0] = row, s_ok[s - s0] = ok;
+      if (blockIdx.y == 0) {
+        if (!ok) set_error(p.err, GDN_ERR_PAGE_RANGE);
+        p.cu_seqlens[s] = row;
+        p.cu_kv[s] = kv0 + out;
+        p.kv_len_out[s] = kv_out;
+        if (s == p.N - 1) {
+          p.cu_seqlens[p.N] = row0 + ta;
+          p.cu_kv[p.N] = kv0 + to;
+          p.pages_taken[0] = taken + tg;
+        }
+      }
+    }
+    need0 += tn, row0 += ta, kv0 += to, taken += tg;
+    c0 = c1;
+  }
+  __syncthreads();
+  const int me = blockIdx.y * blockDim.x + threadIdx.x, step = gridDim.y * blockDim.x;
+  for (int s = s0; s < s1; ++s) {
+    const int first = s_first[s - s0], kv = max(0, p.kv_len[s]), add = max(0, p.new_len[s]);
+    const bool ok = s_ok[s - s0];
+    const int have = (int)(((int64_t)kv + p.page_tokens - 1) / p.page_tokens);
+    int32_t* bt = p.block_table + (int64_t)s * p.max_pages;
+    if (ok) {
+      const int want = (int)(((int64_t)kv + add + p.page_tokens - 1) / p.page_tokens);
+      for (int j = have + me; j < want; j += step) bt[j] = p.free_pages[first + j - have];
+    }
+    const int64_t r0 = s_row[s - s0];
+    for (int i = me; i < add; i += step) {
+      if (r0 + i >= p.T) break;
+      const int64_t pos = (int64_t)kv + i;
+      int64_t slot = -1;
+      if (ok) {
+        const int j = (int)(pos / p.page_tokens);
+        // a fresh page's id comes from the list: the table's entry may not be written yet
+        const int page = j < have ? bt[j] : p.free_pages[first + j - have];
+        if (page >= 0 && page < p.num_pages)
+          slot = (int64_t)page * p.page_tokens + (int)(pos - (int64_t)j * p.page_tokens);
+        else
+          set_error(p.err, GDN_ERR_PAGE_RANGE);
+      }
+      p.positions[r0 + i] = pos;
+      p.slot_map[r0 + i] = slot;
+    }
+  }
+  // rows past the last request's
+  if (s1 == p.N)
+    for (int64_t t = (int64_t)row0 + me; t < p.T; t += step) p.positions[t] = 0, p.slot_map[t] = -1;
+}
+
+cudaError_t launch_kv_tables(const KvTablesParams& q, cudaStream_t st) {
+  KvTablesParams p = q;
+  // at most 1,024 groups of requests re-form the sums before them; tokens
+  // beyond about 1,024 a CTA spread over y
+  p.seqs_per_cta = (p.N + 1023) / 1024;
+  const int gx = (p.N + p.seqs_per_cta - 1) / p.seqs_per_cta;
+  int64_t gy = p.T / ((int64_t)gx * 1024);
+  gy = gy < 1 ? 1 : gy > 64 ? 64 : gy;
+  kv_tables_kernel<<<dim3(gx, (unsigned)gy), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// ---- append -------------------------------------------------------------------------
+namespace {
+
+// Eight consecutive elements of a row, as loaded.
+template <typename T> struct Row8;
+template <> struct Row8<__nv_bfloat16> {
+  uint4 w;
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void load(const void* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ float get(int i) const {
+    const uint32_t x = (&w.x)[i >> 1];
+    return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+  }
+};
+template <> struct Row8<float> {
+  float4 a, b;
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ void load(const void* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ float get(int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
+};
+
+// The smallest power of two, at least 2^-64, with amax / scale <= 448 (finite amax >= 0).
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  // 448 = 1.75 * 2^8: amax = 1.m * 2^e needs 2^(e - 8), one more when 1.m > 1.75
+  int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  if (b < 0x00800000u || e < -64) e = -64;   // subnormal amax: far below 448 * 2^-64
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+}  // namespace
+
+// New rows into the cache.  A CTA takes W rows; a run of rows of one block of
+// 16 tokens is handled, for one kv head and K or V, by LPT lanes with 8
+// elements of the head each: the run's rows are read into registers once, give
+// the block's scale, and are written as codes in the operand layout.
+template <typename T, int LPT, int W>
+__global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) {
+  constexpr int kSlots = 256 / LPT;   // runs in work at once
+  __shared__ int64_t s_slot[W + kKvBlock];
+  __shared__ int s_lead[W], s_len[W], s_n;
+  const int64_t t0 = (int64_t)blockIdx.x * W;
+  for (int i = threadIdx.x; i < W + kKvBlock; i += 256) s_slot[i] = t0 + i < p.T ? p.slot_map[t0 + i] : -1;
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  if (threadIdx.x < W) {
+    const int i = threadIdx.x;
+    const int64_t slot = s_slot[i];
+    const int64_t before = i > 0 ? s_slot[i - 1] : t0 > 0 ? p.slot_map[t0 - 1] : -1;
+    if (slot >= 0 && !(before >= 0 && slot == before + 1 && slot % kKvBlock != 0)) {
+      int n = 1;
+      while (n < kKvBlock && (slot + n) % kKvBlock != 0 && s_slot[i + n] == slot + n) ++n;
+      // the order of the list does not matter: runs are independent
+      const int at = atomicAdd(&s_n, 1);
+      s_lead[at] = i, s_len[at] = n;
+    }
+  }
+  __syncthreads();
+  const int sub = threadIdx.x / LPT, lane = threadIdx.x % LPT;
+  const unsigned mask = (LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (threadIdx.x % 32 / LPT * LPT));
+  const int e0 = lane * 8, d = p.c.d;
+  const bool on = e0 < d;
+  const int h = blockIdx.y;
+  for (int task = sub; task < 2 * s_n; task += kSlots) {
+    const int i = s_lead[task >> 1], run = s_len[task >> 1];
+    const bool is_v = task & 1;
+    const int64_t slot = s_slot[i];
+    const int64_t page = slot / p.c.page_tokens;
+    if (page >= p.c.num_pages) {
+      if (lane == 0) set_error(p.err, GDN_ERR_PAGE_RANGE);
+      continue;
+    }
+    const int in_page = (int)(slot - page * p.c.page_tokens), b = in_page / kKvBlock, off = in_page % kKvBlock;
+    const T* src = static_cast<const T*>(is_v ? p.v : p.k) + (t0 + i - off) * (is_v ? p.v_stride : p.k_stride) + (int64_t)h * d + e0;
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    Row8<T> r[kKvBlock];   // by token of the block
+    const float before = off ? *(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)) : 0.f;
+#pragma unroll
+    for (int t = 0; t < kKvBlock; ++t) {
+      if (on && t >= off && t < off + run) r[t].load(src + t * stride);
+      else r[t].zero();
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int t = 0; t < kKvBlock; ++t)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(r[t].get(e)));   // NaN falls out
+    if (__any_sync(mask, !(amax < __int_as_float(0x7f800000)))) {   // an infinity: finite values only
+      amax = 0.f;
+#pragma unroll
+      for (int t = 0; t < kKvBlock; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = fabsf(r[t].get(e));
+          if (x < __int_as_float(0x7f800000)) amax = fmaxf(amax, x);
+        }
+    }
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
+    const float now = fmaxf(pow2_scale(amax), before);
+    const float inv = 1.0f / now;   // a power of two: exact
+    if (lane == 0) *const_cast<float*>(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)) = now;
+    if (!on) continue;
+    const bool raise = off && now > before;
+    const float ratio = before * inv;
+    if (!is_v) {
+      uint8_t* dst = const_cast<uint8_t*>(kv_k_block(p.c, (int)page, h, b)) + (e0 / 16) * 128 + (e0 & 8);
+      const int half = d / 16 * 128;
+#pragma unroll
+      for (int t = 0; t < kKvBlock; ++t) {
+        uint2* q = reinterpret_cast<uint2*>(dst + (t >> 3) * half + (t & 7) * 16);
+        if (t >= off && t < off + run) {
+          *q = make_uint2(e4m3x4(r[t].get(0) * inv, r[t].get(1) * inv, r[t].get(2) * inv, r[t].get(3) * inv),
+                          e4m3x4(r[t].get(4) * inv, r[t].get(5) * inv, r[t].get(6) * inv, r[t].get(7) * inv));
+        } else if (raise && t < off) {
+          const uint2 o = *q;
+          const float2 a = e4m3_f32x2(o.x), b2 = e4m3_f32x2(o.x >> 16), c = e4m3_f32x2(o.y), f = e4m3_f32x2(o.y >> 16);
+          *q = make_uint2(e4m3x4(a.x * ratio, a.y * ratio, b2.x * ratio, b2.y * ratio),
+                          e4m3x4(c.x * ratio, c.y * ratio, f.x * ratio, f.y * ratio));
+        }
+      }
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(const_cast<uint8_t*>(kv_v_block(p.c, (int)page, h, b)) + e0 * kKvBlock);
+      const bool part = run < kKvBlock;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint4 old = make_uint4(0, 0, 0, 0), res;
+        if (part) old = dst[e];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t x = e4m3x4(r[4 * w].get(e) * inv, r[4 * w + 1].get(e) * inv, r[4 * w + 2].get(e) * inv,
+                              r[4 * w + 3].get(e) * inv);
+          if (part) {
+            uint32_t o = (&old.x)[w];
+            // bytes of tokens [lo, hi) of this word are new, those before are older tokens
+            const int lo = min(max(off - 4 * w, 0), 4), hi = min(max(off + run - 4 * w, 0), 4);
+            const uint32_t m_lo = lo == 4 ? 0xffffffffu : (1u << (8 * lo)) - 1u;
+            const uint32_t m_hi = hi == 4 ? 0xffffffffu : (1u << (8 * hi)) - 1u;
+            if (raise) {
+              const float2 a = e4m3_f32x2(o), c = e4m3_f32x2(o >> 16);
+              const uint32_t moved = e4m3x4(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio);
+              o = (moved & m_lo) | (o & ~m_lo);
+            }
+            const uint32_t fresh = m_hi & ~m_lo;
+            x = (x & fresh) | (o & ~fresh);
+          }
+          (&res.x)[w] = x;
+        }
+        dst[e] = res;
+      }
+    }
+  }
+}
+
+namespace {
+
+template <typename T, int LPT>
+cudaError_t append_rows(const KvAppendParams& p, cudaStream_t st) {
+  // few rows (a decode step: every row a run of its own): 4 a CTA, so that the
+  // runs of a step spread over the SMs; many (prompts): 64, about four runs
+  if (p.T <= 4096) {
+    kv_append_kernel<T, LPT, 4><<<dim3((unsigned)((p.T + 3) / 4), p.c.Hkv), 256, 0, st>>>(p);
+  } else {
+    kv_append_kernel<T, LPT, 64><<<dim3((unsigned)((p.T + 63) / 64), p.c.Hkv), 256, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t append_dtype(const KvAppendParams& p, cudaStream_t st) {
+  if (p.c.d > 128) return append_rows<T, 32>(p, st);
+  if (p.c.d > 64) return append_rows<T, 16>(p, st);
+  return append_rows<T, 8>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t st) {
+  return dtype == GDN_BF16 ? append_dtype<__nv_bfloat16>(p, st) : append_dtype<float>(p, st);
+}
+
+// ---- gather ---------------------------------------------------------------------------
+namespace {
+
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&f)[8]) {
+  uint4 w;
+  __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = w;
+}
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+}  // namespace
+
+// The cached rows of a prefix back as plain rows.  A CTA takes 64 output rows;
+// each block of 16 tokens that starts among them is read, for one head and K or
+// V, by LPT lanes with 8 elements each (V's operand tiles are transposed in
+// registers) and written as row pieces of 8 elements.
+template <typename T, int LPT>
+__global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherParams p) {
+  constexpr int kSlots = 256 / LPT, W = 64;
+  __shared__ int s_row[W], s_len[W], s_page[W], s_blk[W], s_n;
+  const int64_t t0 = (int64_t)blockIdx.x * W;
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  if (threadIdx.x < W && t0 + threadIdx.x < p.T) {
+    const int64_t t = t0 + threadIdx.x;
+    int lo = 0, hi = p.N;   // the sequence s with cu[s] <= t < cu[s + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu_kv[mid + 1] > t) hi = mid;
+      else lo = mid + 1;
+    }
+    if (lo < p.N && t >= p.cu_kv[lo]) {
+      const int64_t pos = t - p.cu_kv[lo];
+      if (pos % kKvBlock == 0) {
+        const int64_t j = pos / p.c.page_tokens;
+        int page = j < p.max_pages ? p.block_table[(int64_t)lo * p.max_pages + j] : -1;
+        if (page < 0 || page >= p.c.num_pages) {
+          set_error(p.err, GDN_ERR_PAGE_RANGE);
+          page = -1;
+        }
+        const int64_t left = min((int64_t)p.cu_kv[lo + 1], p.T) - t;
+        const int at = atomicAdd(&s_n, 1);
+        s_row[at] = threadIdx.x;
+        s_len[at] = left < kKvBlock ? (int)left : kKvBlock;
+        s_page[at] = page;
+        s_blk[at] = (int)(pos - j * p.c.page_tokens) / kKvBlock;
+      }
+    }
+  }
+  __syncthreads();
+  const int sub = threadIdx.x / LPT, lane = threadIdx.x % LPT;
+  const int e0 = lane * 8, d = p.c.d, Hkv = p.c.Hkv;
+  if (e0 >= d) return;
+  for (int task = sub; task < 2 * s_n * Hkv; task += kSlots) {
+    const bool is_v = task & 1;
+    const int i = (task >> 1) / Hkv, h = (task >> 1) % Hkv;
+    const int page = s_page[i], b = s_blk[i], len = s_len[i];
+    T* dst = static_cast<T*>(is_v ? p.v : p.k) + ((t0 + s_row[i]) * Hkv + h) * d + e0;
+    const int64_t stride = (int64_t)Hkv * d;
+    if (page < 0) {
+      const float z[8] = {};
+      for (int t = 0; t < len; ++t) put8(dst + t * stride, z);
+      continue;
+    }
+    const float scale = *(is_v ? kv_v_scale(p.c, page, h, b) : kv_k_scale(p.c, page, h, b));
+    if (!is_v) {
+      const uint8_t* src = kv_k_block(p.c, page, h, b) + (e0 / 16) * 128 + (e0 & 8);
+      const int half = d / 16 * 128;
+      uint2 w[kKvBlock];
+#pragma unroll
+      for (int t = 0; t < kKvBlock; ++t) w[t] = *reinterpret_cast<const uint2*>(src + (t >> 3) * half + (t & 7) * 16);
+#pragma unroll
+      for (int t = 0; t < kKvBlock; ++t) {
+        if (t >= len) break;
+        const float2 a = e4m3_f32x2(w[t].x), b2 = e4m3_f32x2(w[t].x >> 16), c = e4m3_f32x2(w[t].y), f = e4m3_f32x2(w[t].y >> 16);
+        const float x[8] = {a.x * scale, a.y * scale, b2.x * scale, b2.y * scale,
+                            c.x * scale, c.y * scale, f.x * scale, f.y * scale};
+        put8(dst + t * stride, x);
+      }
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(kv_v_block(p.c, page, h, b) + e0 * kKvBlock);
+      uint4 w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = src[e];
+#pragma unroll
+      for (int t = 0; t < kKvBlock; t += 2) {
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = e4m3_f32x2((&w[e].x)[t >> 2] >> (8 * (t & 2)));
+          x[e] = f.x * scale, y[e] = f.y * scale;
+        }
+        if (t < len) put8(dst + t * stride, x);
+        if (t + 1 < len) put8(dst + (t + 1) * stride, y);
+      }
+    }
+  }
+}
+
+namespace {
+
+template <typename T>
+cudaError_t gather_dtype(const KvGatherParams& p, cudaStream_t st) {
+  const unsigned g = (unsigned)((p.T + 63) / 64);
+  if (p.c.d > 128) kv_gather_kernel<T, 32><<<g, 256, 0, st>>>(p);
+  else if (p.c.d > 64) kv_gather_kernel<T, 16><<<g, 256, 0, st>>>(p);
+  else kv_gather_kernel<T, 8><<<g, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_gather(const KvGatherParams& p, int dtype, cudaStream_t st) {
+  return dtype == GDN_BF16 ? gather_dtype<__nv_bfloat16>(p, st) : gather_dtype<float>(p, st);
+}
+
+}  // namespace gdn

@@ -79,7 +79,42 @@ QWEN27B = LayerShape(16, 48, 128, 128, block_size=896, chunk_size=64, page_bytes
 QWEN4B = LayerShape(16, 32, 128, 128, block_size=640, chunk_size=64, page_bytes=5 * 512 * 1024)
 
 
-def with_(shape: LayerShape, **kw) -> LayerShape:
+@dataclass(frozen=True)
+class AttnShape:
+    """Shape of one attention layer plus the geometry of its 8-bit cache."""
+    num_q_heads: int
+    num_kv_heads: int
+    head_dim: int
+    page_tokens: int             # tokens of a KV page, a multiple of 16
+    dtype: int = BF16
+    scale: float = 0.0           # of the scores; 0: 1 / sqrt(head_dim)
+
+    @property
+    def softmax_scale(self) -> float:
+        return self.scale or self.head_dim ** -0.5
+
+    @property
+    def codes_bytes(self) -> int:
+        """Bytes of a page's K codes (and of its V codes)."""
+        return self.num_kv_heads * self.page_tokens * self.head_dim
+
+    @property
+    def page_bytes(self) -> int:
+        scales = self.num_kv_heads * (self.page_tokens // 16) * 4
+        return (2 * self.codes_bytes + 2 * scales + 255) // 256 * 256
+
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DTYPE[self.dtype]
+
+
+# Attention layers beside the GDN layers above: 4,096 B of bf16 K and V a token
+# (1,024 channels each), pages of the GDN block size; a tiny fp32 one.
+ATTN27B = AttnShape(24, 4, 256, page_tokens=896)
+ATTN4B = AttnShape(16, 4, 256, page_tokens=640)
+ATTN_TINY = AttnShape(4, 2, 32, page_tokens=64, dtype=F32)
+
+
+def with_(shape, **kw):
     return replace(shape, **kw)
 
 

@@ -557,6 +557,213 @@ gdn_status gdn_replay_rollback(int32_t* log_len, const int32_t* accepted,
 gdn_status gdn_replay_flush(const gdn_layer_desc* desc, const gdn_pool* pool,
                             const gdn_replay_args* args, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The attention layers of a hybrid model: a paged 8-bit K / V cache and the
+ * attention that reads it.
+ *
+ * A hybrid model interleaves its GDN layers with full-attention layers whose
+ * cache is paged too ("Hybrid linear attention (gated DeltaNet)", "Why this
+ * family is different", item 2: one pool of uniform pages).  For one such
+ * layer, with q of Hq heads, k and v of Hkv heads and query head h reading kv
+ * head floor(h / (Hq / Hkv)):
+ *
+ *   o[t][h]   = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q_t . k_j)
+ *   lse[t][h] = log sum_j p_j
+ *
+ * over the keys j that row t may see: of a sequence with n new rows and L keys
+ * (its new rows' own among them, last), row i sees keys 0 .. L - n + i.  A row
+ * that sees none gives o = 0 and lse = -inf.  Keys and values that a row may
+ * not see never reach it, whatever they hold (infinities, NaN, pages that were
+ * never written).
+ *
+ * The cache
+ * ---------
+ * A KV page holds page_tokens tokens of all kv heads in 8 bits: e4m3 codes
+ * with one fp32 scale, a power of two, for each block of GDN_KV_BLOCK = 16
+ * tokens and head, apart for K and V; a value is code * scale.  Page layout
+ * (e4m3 has 3 fraction bits at any scale, so a power of two loses nothing over
+ * another scale, and raising one moves the codes already there without a new
+ * rounding except among subnormals):
+ *
+ *   K codes  [Hkv][page_tokens/16][2][d/16][8][16]  token 16 b + 8 h + r of the
+ *            page, element 16 c + e: a block is the tensor cores' 8 x 16 byte
+ *            operand tiles, rows of tokens
+ *   V codes  [Hkv][page_tokens/16][d][16]           token 16 b + t: the same
+ *            tiles transposed, rows of elements
+ *   K scales [Hkv][page_tokens/16] fp32, V scales the same
+ *   padding up to page_bytes
+ *
+ * so that a block of either is d * 16 contiguous bytes that a bulk copy brings
+ * into shared memory as an operand.  Pages live in a gdn_pool (base and
+ * page_bytes multiples of 256; page_bytes may be larger than
+ * gdn_kv_page_bytes, so KV pages and GDN state pages can share one pool).  A
+ * block table row maps a sequence's token t to the page
+ * block_table[s][t / page_tokens].
+ * ------------------------------------------------------------------------- */
+
+/* Tokens that share a scale. */
+#define GDN_KV_BLOCK 16
+/* Most new rows a sequence in one gdn_attn_decode call: the replay log's. */
+#define GDN_ATTN_DECODE_ROWS GDN_REPLAY_LOG_SLOTS
+
+/* Shape of one attention layer. */
+typedef struct gdn_attn_desc {
+  int32_t num_q_heads;   /* Hq, a multiple of Hkv                            */
+  int32_t num_kv_heads;  /* Hkv                                              */
+  int32_t head_dim;      /* d: a multiple of 16, 16 .. 256                   */
+  int32_t page_tokens;   /* tokens of a KV page: a multiple of 16            */
+  int32_t dtype;         /* GDN_F32 or GDN_BF16: q, k, v, o                  */
+  float scale;           /* of the scores, finite and > 0 (1 / sqrt(d))      */
+  int32_t reserved;      /* must be 0                                        */
+} gdn_attn_desc;
+
+/* Bytes of one KV page of this layer, a multiple of 256; -1 for a malformed
+ * desc. */
+int64_t gdn_kv_page_bytes(const gdn_attn_desc* desc);
+
+/* Block tables, slot maps and positions of one step, from request lengths.
+ * Request s holds kv_len[s] tokens and adds new_len[s]; the pages that this
+ * takes beyond those it has (ceil(kv_len / page_tokens)) come from
+ * free_pages, in order of the requests and of the pages in each, and their
+ * ids go into its block_table row.  A request with a negative length, with
+ * more pages than max_pages, or for which too few free pages are left sets
+ * GDN_ERR_PAGE_RANGE and is left out: its row stays, its tokens' slots are -1
+ * and kv_len_out[s] = kv_len[s] (a negative one: 0).  So is, with slot -1, a
+ * token whose page id is not in [0, num_pages).  No list is changed: the
+ * caller drops the first *pages_taken entries of free_pages, and the same
+ * call gives the same answer again. */
+typedef struct gdn_kv_tables_args {
+  int32_t num_seqs;              /* N >= 0                                    */
+  int32_t max_pages;             /* row stride of block_table                 */
+  int32_t num_free;              /* entries of free_pages                     */
+  int32_t num_pages;             /* pages of the pool                         */
+  int64_t total_tokens;          /* rows of positions and slot_map; rows past
+                                    the new tokens get slot -1, position 0    */
+  const int32_t* kv_len;         /* [N] tokens in the cache                   */
+  const int32_t* new_len;        /* [N] tokens to add                         */
+  const int32_t* free_pages;     /* [num_free] page ids                       */
+  int32_t* block_table;          /* [N][max_pages] in and out                 */
+  int32_t* cu_seqlens;           /* [N+1] out: running sum of new_len         */
+  int32_t* cu_kv;                /* [N+1] out: running sum of kv_len_out      */
+  int32_t* kv_len_out;           /* [N] out: kv_len + new_len; not kv_len     */
+  int64_t* positions;            /* [T] out: position in its sequence         */
+  int64_t* slot_map;             /* [T] out: page * page_tokens + offset      */
+  int32_t* pages_taken;          /* [1] out                                   */
+  int32_t* dev_error;
+} gdn_kv_tables_args;
+
+gdn_status gdn_kv_tables(const gdn_attn_desc* desc, const gdn_kv_tables_args* args, void* stream);
+
+/* New K and V rows into the cache.  Row t goes to slot slot_map[t] = page *
+ * page_tokens + offset (-1: skipped; a page outside the pool sets
+ * GDN_ERR_PAGE_RANGE and is skipped).  Rows of one block of 16 tokens must
+ * stand one after another in ascending order, and no two runs of rows may
+ * share a block; a run that starts inside a block keeps the tokens before it.
+ *
+ * The scale of a block is the smallest power of two, at least 2^-64, with
+ * max |x| / scale <= 448 over the run's finite values; where tokens stand
+ * before the run it is at least their scale, and when it rises their codes
+ * are converted to it.  Values beyond (infinities) saturate at 448 * scale,
+ * NaN stays NaN.  k and v rows are [Hkv][d] dense, k_stride / v_stride
+ * elements apart (multiples of 16 bytes), so slices of a fused projection's
+ * rows can be given as they are. */
+typedef struct gdn_kv_append_args {
+  int64_t total_tokens;          /* T >= 0                                    */
+  int64_t k_stride, v_stride;    /* elements between rows, >= Hkv*d           */
+  const void* k;                 /* [T] rows, dtype, 16-byte aligned          */
+  const void* v;
+  const int64_t* slot_map;       /* [T]                                       */
+  int32_t* dev_error;
+} gdn_kv_append_args;
+
+gdn_status gdn_kv_append(const gdn_attn_desc* desc, const gdn_pool* pool,
+                         const gdn_kv_append_args* args, void* stream);
+
+/* Cached K and V back as plain rows: token t of sequence s, 0 <= t < L_s =
+ * cu_kv[s+1] - cu_kv[s], goes to row cu_kv[s] + t of k and v (dense, dtype;
+ * exact in bf16 while the scale is).  A prompt's next chunk attends over its
+ * cached prefix with gdn_attn_prefill through this.  Tokens whose page id is
+ * outside the pool set GDN_ERR_PAGE_RANGE and give zeros. */
+typedef struct gdn_kv_gather_args {
+  int32_t num_seqs;              /* N >= 0                                    */
+  int32_t max_pages;             /* row stride of block_table                 */
+  int64_t total_tokens;          /* rows of k and v: cu_kv[N]                 */
+  const int32_t* cu_kv;          /* [N+1], non-decreasing, cu_kv[0] = 0       */
+  const int32_t* block_table;    /* [N][max_pages]                            */
+  void* k;                       /* [T][Hkv][d] dtype, 16-byte aligned        */
+  void* v;
+  int32_t* dev_error;
+} gdn_kv_gather_args;
+
+gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
+                         const gdn_kv_gather_args* args, void* stream);
+
+/* Attention of 1 to 32 new rows a sequence over the 8-bit cache: a decode
+ * step, or the rows of a draft being verified.  The new rows' own K and V are
+ * in the cache already (kv_len[s] counts them).  A sequence with more rows
+ * than max_q_len or more keys than max_kv_len, or whose table holds a page
+ * outside the pool, sets GDN_ERR_INVALID_ARG / GDN_ERR_PAGE_RANGE; its
+ * outputs are not written (the page fault: that piece's keys are left out).
+ *
+ * The keys of a sequence are cut into pieces by its own kv_len alone, the
+ * pieces run in parallel and are joined in order: a row's bits do not depend
+ * on the batch around it. */
+typedef struct gdn_attn_decode_args {
+  int32_t num_seqs;              /* N >= 0                                    */
+  int32_t max_pages;             /* row stride of block_table                 */
+  int32_t max_q_len;             /* host bound on new rows a sequence, 1..32  */
+  int32_t max_kv_len;            /* host bound on kv_len                      */
+  int64_t total_tokens;          /* T = cu_seqlens[N]                         */
+  int64_t q_stride;              /* elements between rows of q, >= Hq*d       */
+  const int32_t* cu_seqlens;     /* [N+1] rows of q                           */
+  const int32_t* kv_len;         /* [N]                                       */
+  const int32_t* block_table;    /* [N][max_pages]                            */
+  const void* q;                 /* [T] rows of [Hq][d] dtype, 16-byte aligned */
+  void* o;                       /* [T][Hq][d] dtype                          */
+  float* lse;                    /* [T][Hq] or NULL                           */
+  int32_t* dev_error;
+} gdn_attn_decode_args;
+
+/* Device workspace bytes (256-byte aligned scratch, as the prefill's): the
+ * pieces' outputs and softmax statistics.  0 for a malformed desc. */
+size_t gdn_attn_decode_workspace_size(const gdn_attn_desc* desc, int32_t num_seqs, int64_t total_tokens,
+                                      int32_t max_kv_len);
+gdn_status gdn_attn_decode(const gdn_attn_desc* desc, const gdn_pool* pool, const gdn_attn_decode_args* args,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Causal attention over packed sequences: sequence s has rows
+ * [cu_seqlens[s], cu_seqlens[s+1]) of q and [cu_kv[s], cu_kv[s+1]) of k and v
+ * (a whole prompt: both alike; a chunk after a prefix: more keys than rows).
+ * The desc's page_tokens is not used.  Rows of q, k, v are q_stride,
+ * k_stride, v_stride elements apart.  max_q_len and max_kv_len bound a
+ * sequence's rows and keys (0: total_q / total_kv); a longer one sets
+ * GDN_ERR_INVALID_ARG and is skipped.  A row's bits depend on its own keys
+ * only: not on the batch, nor on how a prompt was cut into chunks. */
+typedef struct gdn_attn_prefill_args {
+  int32_t num_seqs;              /* N >= 0                                    */
+  int32_t max_q_len;
+  int32_t max_kv_len;
+  int32_t reserved;              /* 0                                         */
+  int64_t total_q;               /* rows of q, o, lse                         */
+  int64_t total_kv;              /* rows of k, v                              */
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* cu_seqlens;     /* [N+1]                                     */
+  const int32_t* cu_kv;          /* [N+1]                                     */
+  const void* q;                 /* [total_q] rows of [Hq][d], 16-byte aligned */
+  const void* k;                 /* [total_kv] rows of [Hkv][d]               */
+  const void* v;
+  void* o;                       /* [total_q][Hq][d] dtype                    */
+  float* lse;                    /* [total_q][Hq] or NULL                     */
+  int32_t* dev_error;
+  int64_t wait_cycles;           /* bound of each device-side wait in SM
+                                    clocks; 0: the default (~2 s); < 0 makes
+                                    every such wait of the tensor-core path
+                                    report GDN_ERR_TIMEOUT at once (outputs
+                                    are then not written)                     */
+} gdn_attn_prefill_args;
+
+gdn_status gdn_attn_prefill(const gdn_attn_desc* desc, const gdn_attn_prefill_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
