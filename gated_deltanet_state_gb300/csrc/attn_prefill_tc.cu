@@ -1,0 +1,579 @@
+// attn_prefill_tc.cu — causal attention over packed prompts on the tensor
+// cores (bf16, d = 64, 128, 256).
+//
+// S = Q K^T and O += P V are tcgen05 products of 128 query rows (row i of a
+// tile: token i / G, head i % G of the group, so that the group shares the
+// keys) with 128 keys, accumulated in tensor memory.  The softmax runs between
+// them with the running maximum and sum of a row held in one thread.
+#include <cuda.h>
+
+#include "attn.h"
+#include "launch.h"
+#include "tc.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kTile = 128;          // rows and keys of a tile
+constexpr long long kPreWait = 4000000000LL;
+
+template <int D>
+struct PreCfg {
+  static constexpr int NQ = D == 256 ? 1 : 2;            // row tiles a CTA
+  static constexpr int SLOTS = D == 256 ? 2 : 1;         // score buffers a row tile
+  static constexpr int UD = D < 128 ? D : 128;           // head elements of a staged unit
+  static constexpr int U = D / UD;                       // units of a key tile
+  static constexpr uint32_t UNIT = kTile * UD * 2;
+  static constexpr int STAGES = D == 64 ? 8 : 5;
+  static constexpr uint32_t Q_BYTES = kTile * D * 2;
+  static constexpr uint32_t DATA = NQ * Q_BYTES + STAGES * UNIT;
+  static constexpr int THREADS = NQ * 128 + 128;
+  // tensor memory columns: scores (the weights overwrite them), then outputs
+  static constexpr uint32_t S0 = 0, O0 = 256;
+  // registers: a softmax thread holds a row's 128 scores
+};
+
+struct PreShared {
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], drain;
+  uint32_t tmem;
+  int fail, bad_any;
+  // first key, counted from the first guarded tile's, with NaN, +inf, -inf in
+  // each element of V; 0xffff: none
+  uint16_t bad[3][256];
+};
+template <int D>
+constexpr uint32_t kPreSmem = PreCfg<D>::DATA + sizeof(PreShared) + 1024;   // 1,024 to align the tiles
+static_assert(kPreSmem<256> <= 232448 && kPreSmem<128> <= 232448, "227 KB a CTA");
+
+// Minimum of a 16-bit word in shared memory.
+__device__ __forceinline__ void min16(uint16_t* at, uint32_t v) {
+  unsigned* w = reinterpret_cast<unsigned*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)3);
+  const int sft = (reinterpret_cast<uintptr_t>(at) & 2) * 8;
+  unsigned old = *w;
+  while (((old >> sft) & 0xffffu) > v) {
+    const unsigned seen = atomicCAS(w, old, (old & ~(0xffffu << sft)) | (v << sft));
+    if (seen == old) break;
+    old = seen;
+  }
+}
+
+// Waits for a phase: bounded, and given up at once when another role has.
+__device__ __forceinline__ bool pre_wait(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
+  if (limit < 0) {
+    *fail = 1;
+    return false;
+  }
+  if (tc::mbar_test_wait(m, parity)) return true;
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait(m, parity)) {
+    if (*fail) return false;
+    if (clock64() - t0 > limit) {
+      *fail = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* m) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(m)) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Shared-memory descriptor of V as the N x K operand with N contiguous: rows of
+// 64 elements (128 B, swizzled) for one key, 8-key groups 1,024 B apart, the
+// next 64 elements a whole block of keys (128 x 128 B) further.
+__device__ __forceinline__ uint64_t desc_v(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((kTile * 128) >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+constexpr uint32_t kTransposedB = 1u << 16;   // instruction descriptor: B is N-contiguous
+
+// Geometry of one CTA's row tiles.
+struct PreTile {
+  int s, h, q0, n, k0, L;
+  int64_t r0;            // first row (token * G + head) of the CTA's first tile
+  int nk[2], nkmax;      // key tiles of each row tile
+  int least;             // keys that every row sees
+};
+
+template <int D>
+__device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t, bool report) {
+  constexpr int NQ = PreCfg<D>::NQ;
+  const int pairs = p.N * p.Hkv;
+  const int back = blockIdx.x / pairs, pr = blockIdx.x - back * pairs;
+  t.s = pr / p.Hkv;
+  t.h = pr - t.s * p.Hkv;
+  t.q0 = p.cu_q[t.s];
+  t.n = p.cu_q[t.s + 1] - t.q0;
+  t.k0 = p.cu_kv[t.s];
+  t.L = p.cu_kv[t.s + 1] - t.k0;
+  if (t.n <= 0) return false;
+  if (t.n > p.max_q || t.L > p.max_kv || t.L < 0 || t.q0 < 0 || t.k0 < 0 || (int64_t)t.q0 + t.n > p.Tq ||
+      (int64_t)t.k0 + t.L > p.Tk) {
+    if (report) set_error(p.err, GDN_ERR_INVALID_ARG);
+    return false;
+  }
+  const int64_t rows = (int64_t)t.n * p.G;
+  const int tiles = (int)((rows + NQ * kTile - 1) / (NQ * kTile));
+  if (back >= tiles) return false;
+  t.r0 = (int64_t)(tiles - 1 - back) * NQ * kTile;   // the last rows, which see the most keys, first
+  t.nkmax = 0;
+  for (int q = 0; q < 2; ++q) {
+    const int64_t r = t.r0 + q * kTile;
+    t.nk[q] = 0;
+    if (q < NQ && r < rows) {
+      const int last = (int)min((int64_t)t.n - 1, (r + kTile - 1) / p.G);
+      t.nk[q] = (max(0, t.L - t.n + last + 1) + kTile - 1) / kTile;
+    }
+    t.nkmax = max(t.nkmax, t.nk[q]);
+  }
+  t.least = max(0, t.L - t.n + (int)(t.r0 / p.G) + 1);
+  return true;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
+    attn_prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap) {
+  using C = PreCfg<D>;
+  extern __shared__ uint8_t dyn[];
+  PreTile t;
+  if (!pre_tile<D>(p, t, threadIdx.x == 0)) return;
+  uint8_t* base = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  uint8_t* sq = base;
+  uint8_t* ring = base + C::NQ * C::Q_BYTES;
+  PreShared& sh = *reinterpret_cast<PreShared*>(base + C::DATA);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long limit = p.wait_cycles > 0 ? p.wait_cycles : p.wait_cycles < 0 ? -1 : kPreWait;
+  volatile int* fail = &sh.fail;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sh.s_full[i], 1);
+      tc::mbar_init(&sh.p_full[i], 128);
+      tc::mbar_init(&sh.o_done[i], 1);
+      tc::mbar_init(&sh.q_full[i], 128);
+    }
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], 64);
+    tc::mbar_init(&sh.drain, 1);
+    sh.fail = 0, sh.bad_any = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  for (int i = threadIdx.x; i < 3 * 256; i += C::THREADS) (&sh.bad[0][0])[i] = 0xffff;
+  if (warp == 0) {
+    tc::tmem_alloc(&sh.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = sh.tmem;
+  const int wg = warp >> 2;
+  int issued = 0, raw = 0;   // units loaded, those of them for the guards first (the loading thread's)
+  uint32_t raw_bits = 0;     // which of the last 32 went to the guards
+
+  if (wg < C::NQ) {
+    // ---- softmax of row tile wg: one thread a row ----
+    const int q = wg, i = threadIdx.x & 127;
+    const int nk = t.nk[q];
+    const int64_t rbase = t.r0 + q * kTile, r = rbase + i;
+    const int tok = (int)(r / p.G), g = (int)(r - (int64_t)tok * p.G);
+    const bool valid = tok < t.n;
+    const int lim = valid ? max(0, t.L - t.n + tok + 1) : 0;
+    const int64_t row_off = ((int64_t)(t.q0 + tok) * p.Hq + t.h * p.G + g);
+    const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21);   // this warp's 32 lanes
+    const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q);
+    if (nk > 0) {
+      constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a row, rows a warp loads at once
+      for (int rr = (warp & 3) * 32 + lane / CH; rr < (warp & 3) * 32 + 32; rr += RP) {
+        const int64_t r2 = rbase + rr, tk = r2 / p.G;
+        const int c = lane % CH;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (tk < t.n)
+          w = *reinterpret_cast<const uint4*>(qg + (t.q0 + tk) * p.q_stride + (int64_t)(t.h * p.G + (int)(r2 - tk * p.G)) * D + c * 8);
+        *reinterpret_cast<uint4*>(sq + q * C::Q_BYTES + tc::sw128_offset(rr, c * 8, kTile)) = w;
+      }
+      tc::fence_async_smem();
+      mbar_arrive(&sh.q_full[q]);
+    }
+    float m = -INFINITY, l = 0.f;
+    const float c = p.scale_log2;
+    // keys that all of this warp's rows see: below it no mask
+    int wlim = valid ? lim : 0x7fffffff;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wlim = min(wlim, __shfl_xor_sync(0xffffffffu, wlim, o));
+    bool ok = true;
+    for (int j = 0; j < nk; ++j) {
+      const int b = C::SLOTS == 2 ? (j & 1) : q;
+      const uint32_t par = C::SLOTS == 2 ? (uint32_t)(j >> 1) & 1 : (uint32_t)j & 1;
+      ok = pre_wait(&sh.s_full[b], par, limit, fail);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc::fence_after_sync();
+      const uint32_t scol = lanes + C::S0 + (uint32_t)b * 128;
+      uint32_t s[4][32];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) tc::tmem_ld32_nowait(scol + u * 32, s[u]);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int u = 0; u < 4; ++u) tc::tmem_ld_fence(s[u]);
+      const int seen = lim - j * kTile;   // keys of this tile that the row sees
+      if ((j + 1) * kTile > wlim) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (u * 32 + k >= seen) s[u][k] = 0xff800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[u][k]));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // the reference of the weights moves only when the maximum has grown by
+      // 2^8: weights stay below 2^8, and a row's choice depends on that row alone
+      float alpha = 1.f;
+      bool grow = false;
+      if (j == 0) {
+        m = mt;
+      } else if ((mt - m) * c > 8.f) {
+        alpha = ex2((m - mt) * c);
+        m = mt;
+        l *= alpha;
+        grow = true;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        // O of the tiles before: wait for their products, scale this warp's rows
+        ok = pre_wait(&sh.o_done[q], (uint32_t)(j - 1) & 1, limit, fail);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int e = 0; e < D; e += 16) {
+          float o[16];
+          const uint32_t col = lanes + C::O0 + (uint32_t)q * D + e;
+          tc::tmem_ld16(col, o);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] *= alpha;
+          tc::tmem_st16(col, o);
+        }
+        tc::tmem_st_wait();
+      }
+      const float ref = m == -INFINITY ? 0.f : -m * c;
+      const f32x2 cc = pack2(c, c), rr = pack2(ref, ref);
+      f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float2 x = unpack2(fma2(pack2(__uint_as_float(s[u][2 * k]), __uint_as_float(s[u][2 * k + 1])), cc, rr));
+          const float a = ex2(x.x), b2 = ex2(x.y);
+          sum[k & 1] = add2(sum[k & 1], pack2(a, b2));
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b2);
+          w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        tc::tmem_st16u(scol + u * 16, w);
+      }
+      l += sum2(add2(sum[0], sum[1]));
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      mbar_arrive(&sh.p_full[b]);
+    }
+    // ---- outputs ----
+    // (with two score buffers the last scores only say that O of three tiles
+    // before is done: one phase at a time, so that none is taken for another)
+    if (ok && C::SLOTS == 2 && nk > 1) ok = pre_wait(&sh.o_done[q], (uint32_t)(nk - 2) & 1, limit, fail);
+    if (ok && nk > 0) ok = pre_wait(&sh.o_done[q], (uint32_t)(nk - 1) & 1, limit, fail);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc::fence_after_sync();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool bad = nk > 0 && *(volatile int*)&sh.bad_any;
+      __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.o) + row_off * D;
+#pragma unroll 1
+      for (int e = 0; e < D; e += 32) {
+        float o[32];
+        if (nk > 0) {
+          tc::tmem_ld32(lanes + C::O0 + (uint32_t)q * D + e, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (bad) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int mine = lim - t.least / kTile * kTile;
+            const bool hi = sh.bad[1][e + k] < mine, lo = sh.bad[2][e + k] < mine;
+            if (hi) o[k] = INFINITY;
+            if (lo) o[k] = -INFINITY;
+            if (sh.bad[0][e + k] < mine || (hi && lo)) o[k] = __int_as_float(0x7fffffff);
+          }
+        }
+        if (valid) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              // a row that sees no key is 0, whatever its lanes of O hold
+              const __nv_bfloat162 h2 = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
+                                                 : __floats2bfloat162_rn(o[k + 2 * u] * inv, o[k + 2 * u + 1] * inv);
+              w[u] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            *reinterpret_cast<uint4*>(og + e + k) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (valid && p.lse) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
+    }
+  } else if (warp == C::NQ * 4 && lane == 0) {
+    // ---- loads ----
+    // a V tile that some row sees in part arrives on the guards' barriers, who
+    // hand it on; they follow within the ring, so 8 barriers never alias
+    auto tile = [&](const CUtensorMap* map, int j, bool guarded) {
+      for (int u = 0; u < C::U; ++u) {
+        const int st = issued % C::STAGES;
+        if (issued >= C::STAGES && !pre_wait(&sh.empty[st], (uint32_t)(issued / C::STAGES - 1) & 1, limit, fail)) return false;
+        uint64_t* bar = guarded ? &sh.v_raw[raw++ & 7] : &sh.full[st];
+        tc::mbar_expect_tx(bar, C::UNIT);
+        for (int b = 0; b < C::UD / 64; ++b)
+          tc::tma_load_3d(ring + st * C::UNIT + b * (kTile * 128), map, u * C::UD + b * 64, t.h, t.k0 + j * kTile, bar);
+        ++issued;
+        raw_bits = raw_bits << 1 | (guarded ? 1u : 0u);
+      }
+      return true;
+    };
+    // in the order the products take them
+    bool ok = limit >= 0 && (t.nkmax == 0 || tile(&kmap, 0, false));
+    if (ok && C::NQ == 1 && t.nkmax > 1) ok = tile(&kmap, 1, false);
+    constexpr int ahead = C::NQ == 1 ? 2 : 1;
+    for (int j = 0; ok && j < t.nkmax; ++j) 
+      ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + ahead >= t.nkmax || tile(&kmap, j + ahead, false));
+  } else if (warp == C::NQ * 4 + 1 && lane == 0) {
+    // ---- products ----
+    const uint32_t ring0 = smem_u32(ring), sq0 = smem_u32(sq);
+    constexpr uint32_t id_qk = tc::idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t id_pv = tc::idesc_bf16_f32(kTile, C::UD) | kTransposedB;
+    int it = 0, guarded = 0;
+    bool ok = true;
+    auto full = [&](int n) { return pre_wait(&sh.full[n % C::STAGES], (uint32_t)(n / C::STAGES) & 1, limit, fail); };
+    auto qk_unit = [&](int q, uint32_t scol, int n, int u) {
+      const uint64_t a = tc::desc_sw128(sq0 + q * C::Q_BYTES + u * (C::UD / 64) * (kTile * 128));
+      const uint64_t b = tc::desc_sw128(ring0 + (n % C::STAGES) * C::UNIT);
+#pragma unroll
+      for (int ks = 0; ks < C::UD / 16; ++ks) {
+        const uint64_t off = ((uint32_t)(ks >> 2) * (kTile * 128) + (uint32_t)(ks & 3) * 32u) >> 4;
+        tc::mma_bf16(tb + scol, a + off, b + off, id_qk, u != 0 || ks != 0);
+      }
+    };
+    auto pv_unit = [&](int q, uint32_t pcol, int n, int u, bool acc) {
+      const uint64_t b = desc_v(ring0 + (n % C::STAGES) * C::UNIT);
+#pragma unroll
+      for (int ks = 0; ks < kTile / 16; ++ks)
+        tc::mma_bf16_ts(tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv, acc || ks != 0);
+    };
+    // a guarded V unit: from the guards, and its place's phase moves on here
+    auto v_ready = [&](int n, int j) {
+      if ((j + 1) * kTile <= t.least) return full(n);
+      const int k = guarded++;
+      if (!pre_wait(&sh.v_ok[k & 7], (uint32_t)(k >> 3) & 1, limit, fail)) return false;
+      mbar_arrive(&sh.full[n % C::STAGES]);
+      return true;
+    };
+    if constexpr (C::NQ == 1) {
+      ok = t.nkmax == 0 || pre_wait(&sh.q_full[0], 0, limit, fail);
+      auto qk = [&](int j) {
+        for (int u = 0; u < C::U; ++u, ++it) {
+          if (!full(it)) return false;
+          tc::fence_after_sync();
+          qk_unit(0, C::S0 + (j & 1) * 128, it, u);
+          tc::mma_commit(&sh.empty[it % C::STAGES]);
+        }
+        tc::mma_commit(&sh.s_full[j & 1]);
+        return true;
+      };
+      auto pv = [&](int j) {
+        if (!pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)) return false;
+        for (int u = 0; u < C::U; ++u, ++it) {
+          if (!v_ready(it, j)) return false;
+          tc::fence_after_sync();
+          pv_unit(0, C::S0 + (j & 1) * 128, it, u, j != 0);
+          tc::mma_commit(&sh.empty[it % C::STAGES]);
+        }
+        tc::mma_commit(&sh.o_done[0]);
+        return true;
+      };
+      if (ok && t.nkmax > 0) ok = qk(0);
+      if (ok && t.nkmax > 1) ok = qk(1);
+      for (int j = 0; ok && j < t.nkmax; ++j) ok = pv(j) && (j + 2 >= t.nkmax || qk(j + 2));
+    } else {
+      for (int q = 0; ok && q < 2; ++q) ok = t.nk[q] == 0 || pre_wait(&sh.q_full[q], 0, limit, fail);
+      if (ok && t.nkmax > 0) {
+        ok = full(0);
+        if (ok) {
+          tc::fence_after_sync();
+          for (int q = 0; q < 2; ++q)
+            if (t.nk[q] > 0) {
+              qk_unit(q, C::S0 + q * 128, 0, 0);
+              tc::mma_commit(&sh.s_full[q]);
+            }
+          tc::mma_commit(&sh.empty[0]);
+        }
+      }
+      for (int j = 0; ok && j < t.nkmax; ++j) {
+        const int nv = 1 + 2 * j, nkk = nv + 1;
+        const bool more = j + 1 < t.nkmax;
+        ok = v_ready(nv, j) && (!more || full(nkk));
+        for (int q = 0; ok && q < 2; ++q) {
+          if (j >= t.nk[q]) continue;
+          ok = pre_wait(&sh.p_full[q], (uint32_t)j & 1, limit, fail);
+          if (!ok) break;
+          tc::fence_after_sync();
+          pv_unit(q, C::S0 + q * 128, nv, 0, j != 0);
+          tc::mma_commit(&sh.o_done[q]);
+          if (j + 1 < t.nk[q]) {
+            qk_unit(q, C::S0 + q * 128, nkk, 0);
+            tc::mma_commit(&sh.s_full[q]);
+          }
+        }
+        if (!ok) break;
+        tc::mma_commit(&sh.empty[nv % C::STAGES]);
+        if (more) tc::mma_commit(&sh.empty[nkk % C::STAGES]);
+      }
+    }
+    // every product issued, and every arrival on a barrier, before the end
+    tc::mma_commit(&sh.drain);
+    if (!tc::mbar_wait_bounded(&sh.drain, 0, kPreWait)) *fail = 1;
+  } else if (warp >= C::NQ * 4 + 2) {
+    // ---- guards: in V tiles that some row sees in part, keys past the
+    // sequence become zero and so do NaN and infinities, which a weight of 0
+    // would not keep out of the product; where those were is noted by element
+    // for the rows that do see them ----
+    const int me = threadIdx.x - (C::NQ * 4 + 2) * 32;   // 0 .. 63
+    bool ok = true;
+    int done = 0;
+    for (int j = t.least / kTile; ok && j < t.nkmax; ++j) {
+      for (int u = 0; ok && u < C::U; ++u) {
+        // position of unit u of V tile j in the ring's order
+        int n;
+        if constexpr (C::NQ == 1) n = min(t.nkmax, j + 2) * C::U + j * C::U + u;
+        else n = 1 + 2 * j;
+        ok = pre_wait(&sh.v_raw[done & 7], (uint32_t)(done >> 3) & 1, limit, fail);
+        if (!ok) break;
+        ++done;
+        uint8_t* v = ring + (n % C::STAGES) * C::UNIT;
+        for (int x = me; x < (int)C::UNIT / 16; x += 64) {
+          const int blk = x / (kTile * 8), rest = x % (kTile * 8), row = rest >> 3, ch = rest & 7;
+          uint4* at = reinterpret_cast<uint4*>(v + x * 16);
+          const int key = j * kTile + row;
+          if (key >= t.L) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          uint4 w = *at;
+          const uint32_t e = 0x7f807f80u, one = 0x00800080u;
+          const uint32_t hit = (((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one)) & 0x80008000u;
+          if (hit) {
+            const int col = u * C::UD + blk * 64 + ((ch ^ (row & 7)) << 3);
+            for (int k = 0; k < 8; ++k) {
+              uint16_t* el = reinterpret_cast<uint16_t*>(at) + k;
+              const uint16_t b = *el;
+              if ((b & 0x7f80u) != 0x7f80u) continue;
+              min16(&sh.bad[(b & 0x7f) ? 0 : (b & 0x8000u) ? 2 : 1][col + k], key - t.least / kTile * kTile);
+              *el = 0;
+            }
+            *(volatile int*)&sh.bad_any = 1;
+          }
+        }
+        tc::fence_async_smem();
+        mbar_arrive(&sh.v_ok[(done - 1) & 7]);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (sh.fail) {
+    // a wait ran out: report, then give the copies in flight one more bounded
+    // wait each before their memory goes
+    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
+    if (warp == C::NQ * 4 && lane == 0)
+    {
+      for (int n = issued - 1, k = raw - 1; n >= 0 && n >= issued - C::STAGES; --n, raw_bits >>= 1) {
+        if (raw_bits & 1) {
+          tc::mbar_wait_bounded(&sh.v_raw[k & 7], (uint32_t)(k >> 3) & 1, kPreWait);
+          --k;
+        } else {
+          tc::mbar_wait_bounded(&sh.full[n % C::STAGES], (uint32_t)(n / C::STAGES) & 1, kPreWait);
+        }
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+  }
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tb, 512);
+}
+
+namespace {
+
+cudaError_t rows_map(CUtensorMap* map, const void* base, int d, int heads, int64_t rows, int64_t stride) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, kTile}, estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
+  using C = PreCfg<D>;
+  CUtensorMap kmap, vmap;
+  cudaError_t e = rows_map(&kmap, p.k, D, p.Hkv, p.Tk, p.k_stride);
+  if (e == cudaSuccess) e = rows_map(&vmap, p.v, D, p.Hkv, p.Tk, p.v_stride);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem<D>);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((int64_t)p.max_q * p.G + C::NQ * kTile - 1) / (C::NQ * kTile);
+  const int64_t grid = tiles * p.N * p.Hkv;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  attn_prefill_tc_kernel<D><<<(unsigned)grid, C::THREADS, kPreSmem<D>, st>>>(p, kmap, vmap);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_prefill_tc_supported(const AttnPrefillParams& p, int dtype) {
+  return dtype == GDN_BF16 && (p.d == 64 || p.d == 128 || p.d == 256) && p.Tk > 0 && p.k_stride < (1LL << 38) &&
+         p.v_stride < (1LL << 38);
+}
+
+cudaError_t launch_attn_prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
+  if (p.d == 64) return prefill_tc<64>(p, st);
+  if (p.d == 128) return prefill_tc<128>(p, st);
+  return prefill_tc<256>(p, st);
+}
+
+}  // namespace gdn

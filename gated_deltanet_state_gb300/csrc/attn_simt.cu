@@ -379,6 +379,7 @@ cudaError_t prefill_simt(const AttnPrefillParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStream_t st) {
+  if (attn_prefill_tc_supported(p, dtype)) return launch_attn_prefill_tc(p, st);
   return dtype == GDN_BF16 ? prefill_simt<__nv_bfloat16>(p, st) : prefill_simt<float>(p, st);
 }
 
