@@ -120,6 +120,9 @@ cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t st
 cudaError_t launch_kv_gather(const KvGatherParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_attn_decode(const AttnDecodeParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStream_t st);
+// The tensor-core decode (bf16, d a multiple of 32): the pieces, without the join.
+bool attn_decode_tc_supported(const AttnDecodeParams& p, int dtype);
+cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st);
 // The tensor-core prefill: bf16, d = 64, 128 or 256, at least one key row.
 bool attn_prefill_tc_supported(const AttnPrefillParams& p, int dtype);
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams& p, cudaStream_t st);

@@ -216,6 +216,12 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     }
     float m = -INFINITY, l = 0.f;
     const float c = p.scale_log2;
+    // O of tiles 0 .. j: with two score buffers two barriers in turn, since
+    // scores j only say that O of tile j - 2 is done
+    auto o_wait = [&](int j) {
+      return C::SLOTS == 2 ? pre_wait(&sh.o_done[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)
+                           : pre_wait(&sh.o_done[q], (uint32_t)j & 1, limit, fail);
+    };
     // keys that all of this warp's rows see: below it no mask
     int wlim = valid ? lim : 0x7fffffff;
 #pragma unroll
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       }
       if (__any_sync(0xffffffffu, grow)) {
         // O of the tiles before: wait for their products, scale this warp's rows
-        ok = pre_wait(&sh.o_done[q], (uint32_t)(j - 1) & 1, limit, fail);
+        ok = o_wait(j - 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::fence_after_sync();
 #pragma unroll 1
@@ -298,10 +304,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       mbar_arrive(&sh.p_full[b]);
     }
     // ---- outputs ----
-    // (with two score buffers the last scores only say that O of three tiles
-    // before is done: one phase at a time, so that none is taken for another)
-    if (ok && C::SLOTS == 2 && nk > 1) ok = pre_wait(&sh.o_done[q], (uint32_t)(nk - 2) & 1, limit, fail);
-    if (ok && nk > 0) ok = pre_wait(&sh.o_done[q], (uint32_t)(nk - 1) & 1, limit, fail);
+    if (ok && nk > 0) ok = o_wait(nk - 1);
     if (__all_sync(0xffffffffu, ok)) {
       tc::fence_after_sync();
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           pv_unit(0, C::S0 + (j & 1) * 128, it, u, j != 0);
           tc::mma_commit(&sh.empty[it % C::STAGES]);
         }
-        tc::mma_commit(&sh.o_done[0]);
+        tc::mma_commit(&sh.o_done[j & 1]);
         return true;
       };
       if (ok && t.nkmax > 0) ok = qk(0);

@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
 // w_i = 2^(m_i - max m).  A warp a (row, head).
 template <typename T>
 __global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeParams p) {
+  if (*p.err == GDN_ERR_TIMEOUT) return;   // a wait ran out: the pieces cannot be trusted
   const int s = blockIdx.y;
   const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
   if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
@@ -215,7 +216,12 @@ cudaError_t decode_simt(const AttnDecodeParams& p, cudaStream_t st) {
   const size_t sm_join = (size_t)(kDecWarps * kDecRows * (p.c.d + 2)) * 4;
   const size_t sm = sm_run > sm_join ? sm_run : sm_join;   // at most 33 KB
   attn_decode_simt_kernel<T><<<dim3(p.max_pieces, p.c.Hkv * groups, p.N), 32 * kDecWarps, sm, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
+  const cudaError_t e = attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st) : decode_simt<T>(p, st);
   if (e != cudaSuccess || !p.part_o) return e;
   attn_decode_join_kernel<T><<<dim3((unsigned)((p.max_q * p.Hq + 3) / 4), p.N), 128, 0, st>>>(p);
   return cudaGetLastError();
@@ -224,7 +230,7 @@ cudaError_t decode_simt(const AttnDecodeParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_decode(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
-  return dtype == GDN_BF16 ? decode_simt<__nv_bfloat16>(p, st) : decode_simt<float>(p, st);
+  return dtype == GDN_BF16 ? decode_dtype<__nv_bfloat16>(p, dtype, st) : decode_dtype<float>(p, dtype, st);
 }
 
 // ---- prefill ----------------------------------------------------------------------------
