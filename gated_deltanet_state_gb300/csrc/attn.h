@@ -91,28 +91,31 @@ struct AttnPrefillParams {
   int64_t wait_cycles;
 };
 
-// Keys of a decode sequence are cut into pieces by its own length alone, so a
-// row's sums are formed in the same order whatever batch it is in.  256-token
-// pieces spread a short context over more SMs; 512 keep the pieces' outputs
-// (4 G d bytes each, written and read once) under 3 % of the keys' bytes at
-// G = 6; beyond 38,912 tokens 76 pieces a head are one CTA on each of the 152
-// SMs for two kv heads.
+// Keys of a decode sequence are cut into pieces by its own length and number
+// of (row, head of the group) pairs alone, so a row's sums are formed in the
+// same order whatever batch it is in.  256-token pieces spread a short context
+// over more SMs; 512 keep a few rows' outputs (4 d bytes each for a piece,
+// written and read once) under 3 % of the keys' bytes at 6 rows; 1,024 do so
+// for drafts; beyond 38,912 tokens 76 pieces a head are one CTA on each of the
+// 152 SMs for two kv heads.
 constexpr int kMaxPieces = 76;
-__host__ __device__ inline int decode_piece_tokens(int L) {
-  if (L <= 2048) return 256;
-  if (L <= 512 * kMaxPieces) return 512;
+__host__ __device__ inline int decode_piece_tokens(int L, int rows) {
+  const int base = rows > 32 ? 1024 : 512;
+  if (L <= 2048) return base / 2;
+  if (L <= base * kMaxPieces) return base;
   return ((L + kMaxPieces - 1) / kMaxPieces + 127) / 128 * 128;
 }
-__host__ __device__ inline int decode_pieces(int L) {
-  const int c = decode_piece_tokens(L);
-  return (L + c - 1) / c;
+__host__ __device__ inline int decode_pieces(int L, int rows) {
+  const int c = decode_piece_tokens(L, rows);
+  return L < 1 ? 1 : (L + c - 1) / c;
 }
-// The most pieces of any length up to L (2,048 tokens make 8 pieces, 2,049 make 5).
+// The most pieces of any length up to L and any number of rows (2,048 tokens
+// make 8 pieces, 2,049 make 5).
 __host__ __device__ inline int decode_max_pieces(int L) {
-  int m = decode_pieces(L < 2048 ? L : 2048);
-  if (L > 2048 && decode_pieces(L < 512 * kMaxPieces ? L : 512 * kMaxPieces) > m)
-    m = decode_pieces(L < 512 * kMaxPieces ? L : 512 * kMaxPieces);
-  return m < 1 ? 1 : m;
+  const int s = decode_pieces(L < 2048 ? L : 2048, 1);
+  if (L <= 2048) return s;
+  const int m = decode_pieces(L < 512 * kMaxPieces ? L : 512 * kMaxPieces, 1);
+  return m > s ? m : s;
 }
 
 cudaError_t launch_kv_tables(const KvTablesParams& p, cudaStream_t st);

@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
     return;
   }
-  const int pt = decode_piece_tokens(L);
+  const int pt = decode_piece_tokens(L, n * p.G);
   const int k0 = piece * pt, k1 = min(L, k0 + pt);
   if (r0 >= n * p.G || (piece > 0 && k0 >= L)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeP
   const int s = blockIdx.y;
   const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
   if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
-  const int pieces = max(1, decode_pieces(L)), lane = threadIdx.x & 31, d = p.c.d;
+  const int pieces = decode_pieces(L, n * p.G), lane = threadIdx.x & 31, d = p.c.d;
   const int64_t R = p.T * p.Hq;
   for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n * p.Hq; i += gridDim.x * 4) {
     const int64_t rh = (int64_t)q0 * p.Hq + i;
