@@ -91,30 +91,31 @@ struct AttnPrefillParams {
   int64_t wait_cycles;
 };
 
-// Keys of a decode sequence are cut into pieces by its own length and number
-// of (row, head of the group) pairs alone, so a row's sums are formed in the
-// same order whatever batch it is in.  256-token pieces spread a short context
-// over more SMs; 512 keep a few rows' outputs (4 d bytes each for a piece,
-// written and read once) under 3 % of the keys' bytes at 6 rows; 1,024 do so
-// for drafts; beyond 38,912 tokens 76 pieces a head are one CTA on each of the
-// 152 SMs for two kv heads.
+// Keys of a decode sequence are cut into even pieces by its own length and
+// number of (row, head of the group) pairs alone, so a row's sums are formed in
+// the same order whatever batch it is in.  About 256 keys spread a short
+// context over more SMs; 512 keep a few rows' outputs (4 d bytes each for a
+// piece, written and read once) under 3 % of the keys' bytes at 6 rows; 1,024
+// do so for drafts; beyond 38,912 tokens 76 pieces a head are one CTA on each
+// of the 152 SMs for two kv heads.
 constexpr int kMaxPieces = 76;
+__host__ __device__ inline int decode_piece_target(int tiles, int rows) {   // pieces aimed at
+  const int per = (rows > 32 ? 8 : 4) / (tiles <= 16 ? 2 : 1);
+  const int n = (tiles + per / 2) / per;
+  return n < 1 ? 1 : n > kMaxPieces ? kMaxPieces : n;
+}
 __host__ __device__ inline int decode_piece_tokens(int L, int rows) {
-  const int base = rows > 32 ? 1024 : 512;
-  if (L <= 2048) return base / 2;
-  if (L <= base * kMaxPieces) return base;
-  return ((L + kMaxPieces - 1) / kMaxPieces + 127) / 128 * 128;
+  const int tiles = L < 1 ? 1 : (int)(((int64_t)L + 127) / 128), n = decode_piece_target(tiles, rows);
+  return (tiles + n - 1) / n * 128;
 }
 __host__ __device__ inline int decode_pieces(int L, int rows) {
   const int c = decode_piece_tokens(L, rows);
-  return L < 1 ? 1 : (L + c - 1) / c;
+  return L < 1 ? 1 : (int)(((int64_t)L + c - 1) / c);
 }
-// The most pieces of any length up to L and any number of rows (2,048 tokens
-// make 8 pieces, 2,049 make 5).
+// At least the pieces of any length up to L and any number of rows.
 __host__ __device__ inline int decode_max_pieces(int L) {
-  const int s = decode_pieces(L < 2048 ? L : 2048, 1);
-  if (L <= 2048) return s;
-  const int m = decode_pieces(L < 512 * kMaxPieces ? L : 512 * kMaxPieces, 1);
+  const int tiles = (int)(((int64_t)(L < 1 ? 1 : L) + 127) / 128);
+  const int s = decode_piece_target(tiles < 16 ? tiles : 16, 1), m = decode_piece_target(tiles, 1);
   return m > s ? m : s;
 }
 

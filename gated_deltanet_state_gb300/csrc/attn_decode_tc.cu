@@ -22,28 +22,30 @@ namespace {
 
 constexpr int kDtTok = 128;           // tokens of a tile
 constexpr int kDtBlocks = kDtTok / kKvBlock;
-constexpr int kDtSeqs = 512;         // sequences a launch
+constexpr int kDtSeqs = 256;         // sequences a launch
 constexpr int kDtMaxStages = 8;
 constexpr long long kDtWait = 4000000000LL;
-constexpr float kDtBase = 7.f;        // weights are scaled by 2^7 ...
-constexpr float kDtGrow = 1.75f;      // ... and may exceed that by 2^1.75: 430 < 448
+// Weights are scaled by 2^6 and may grow by 2^2.75 (430 < 448) before a
+// column's reference moves: a lower scale would lose small weights' bits (parts
+// vanish below 2^-16 of the reference), a higher one moves more often.
+constexpr float kDtBase = 6.f, kDtGrow = 2.75f;
 
-// NT columns; CW of them a softmax warpgroup (128 threads, a token each).
+// NT query rows; CW of them a softmax warpgroup (128 threads, a token each).
 template <int NT>
 struct DtCfg {
-  static constexpr int CW = NT < 32 ? NT : 32, WGS = NT / CW;
+  static constexpr int CW = NT < 32 ? NT : 32, WGS = NT / CW, CH = CW < 16 ? CW : 16;
+  static constexpr int N = NT < 16 ? 16 : NT;          // columns of a product; those past NT are not read
   static constexpr int THREADS = WGS * 128 + 96;       // and K loads, V loads, products
   // narrow tiles: two CTAs an SM, one's softmax under the other's products and loads
   static constexpr int CTAS = NT <= 32 ? 2 : 1;
-  static constexpr int PB = NT <= 64 ? 2 : 1;          // weights of two tiles while shared memory allows it
-  static constexpr uint32_t COLS = NT <= 16 ? 64 : NT <= 32 ? 128 : NT <= 64 ? 256 : 512;
-  static constexpr uint32_t O0 = 2 * NT;               // scores of two tiles, then O of 128 elements each
+  static constexpr uint32_t COLS = NT <= 16 ? 64 : NT <= 32 ? 128 : 512;
+  static constexpr uint32_t O0 = 2 * N;                // scores of two tiles, then O of 128 elements each
 };
 
 struct DtParams {
   AttnDecodeParams a;
   int32_t s0, ns;       // this launch's sequences
-  int32_t stages;
+  int32_t k_stages, v_stages;
   uint32_t k_off, v_off, q_off, p_off, misc_off;   // dynamic shared memory
 };
 
@@ -55,12 +57,13 @@ struct DtShared {
   float4 lsum[NT];
   float cmax[4][NT];        // largest score of each column, by warp
   float ref[NT], alpha[NT];
-  // of an item's columns, items alternate: score factor, keys seen, place among the outputs
+  // of a head's rows, heads alternate: score factor, keys seen, place among the outputs
   float fq[2][NT];
   int lim[2][NT];
-  int64_t out[2][NT];
-  int bad[2][256];          // first token with a NaN value that not every row sees, by element
-  int items[kDtSeqs + 1];   // running sum of the sequences' work items
+  uint32_t out[2][NT];      // (row, head) counted from the item's first row's head 0
+  int bad[2][256];          // (items alternate) first token with a NaN value that not every row sees, by element
+  int items[kDtSeqs + 1];   // running sums of the sequences' work items ...
+  int work[kDtSeqs + 1];    // ... and of their weights
   uint32_t tmem;
   int fail;
   unsigned grow[DtCfg<NT>::WGS];   // the last tile (from 1) that moved a column's reference
@@ -108,58 +111,126 @@ __device__ __forceinline__ uint64_t desc_tiles(uint32_t saddr, uint32_t lead, ui
 
 // Work item -> sequence, kv head, row tile, piece.
 struct DtItem {
-  int s, h, r0, rows, piece;   // rows: (row, head) pairs of this item, from r0
+  int s, h, r0, rows, piece, pieces, pt;   // rows: (row, head) pairs of this item, from r0
   int q0, n, L, k0, k1, tiles;
 };
 
+// Groups (kv head, row tile) of a sequence; 0: no rows, -1: out of bounds.
 template <int NT>
-__device__ __forceinline__ int dt_items(const AttnDecodeParams& p, int s) {
+__device__ __forceinline__ int dt_groups(const AttnDecodeParams& p, int s) {
   const int n = p.cu[s + 1] - p.cu[s], L = p.kv_len[s];
   if (n <= 0) return 0;
   if (n > p.max_q || L > p.max_kv || L < 0 || p.cu[s] < 0 || (int64_t)p.cu[s] + n > p.T) return -1;
-  return decode_pieces(L, n * p.G) * p.c.Hkv * ((n * p.G + NT - 1) / NT);
+  return p.c.Hkv * ((n * p.G + NT - 1) / NT);
+}
+// A tile of keys counts 1, an item's fixed cost as much again.
+__device__ __forceinline__ int dt_piece_work(const AttnDecodeParams& p, int s) {
+  return decode_piece_tokens(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G) / kDtTok + 1;
+}
+
+// The last s with sums[s] <= i.
+__device__ __forceinline__ int dt_find(const int* sums, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// First item of CTA b: the work before it is b / CTAs of all.
+template <int NT>
+__device__ __forceinline__ int dt_first(const DtParams& w, const int* items, const int* work, int b, int ctas) {
+  const int at = (int)((int64_t)work[w.ns] * b / ctas);
+  if (at >= work[w.ns]) return items[w.ns];
+  const int s = dt_find(work, w.ns, at);
+  const int groups = dt_groups<NT>(w.a, w.s0 + s), per = (work[s + 1] - work[s]) / groups, pieces = (items[s + 1] - items[s]) / groups;
+  const int g = (at - work[s]) / per;
+  return items[s] + g * pieces + min(pieces, (at - work[s] - g * per + dt_piece_work(w.a, w.s0 + s) - 1) / dt_piece_work(w.a, w.s0 + s));
 }
 
 template <int NT>
 __device__ __forceinline__ DtItem dt_item(const DtParams& w, const int* items, int i) {
   const AttnDecodeParams& p = w.a;
-  int lo = 0, hi = w.ns;   // the last s with items[s] <= i
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (items[mid] <= i) lo = mid;
-    else hi = mid;
-  }
+  const int lo = dt_find(items, w.ns, i);
   DtItem t;
   t.s = w.s0 + lo;
-  int k = i - items[lo];
+  const int k = i - items[lo];
   t.q0 = p.cu[t.s];
   t.n = p.cu[t.s + 1] - t.q0;
   t.L = p.kv_len[t.s];
+  // pieces of one head's rows one after another: a CTA's run of items loads
+  // its rows once a head
+  t.pieces = decode_pieces(t.L, t.n * p.G);
+  const int group = k / t.pieces;
+  t.piece = k - group * t.pieces;
   const int rt = (t.n * p.G + NT - 1) / NT;
-  t.r0 = k % rt * NT;
-  k /= rt;
-  t.h = k % p.c.Hkv;
-  t.piece = k / p.c.Hkv;
+  t.h = group / rt;
+  t.r0 = (group - t.h * rt) * NT;
   t.rows = min(NT, t.n * p.G - t.r0);
-  const int pt = decode_piece_tokens(t.L, t.n * p.G);
-  t.k0 = t.piece * pt;
-  t.k1 = min(t.L, t.k0 + pt);
+  t.pt = decode_piece_tokens(t.L, t.n * p.G);
+  t.k0 = t.piece * t.pt;
+  t.k1 = min(t.L, t.k0 + t.pt);
   t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
   return t;
 }
+// The item after it.
+template <int NT>
+__device__ __forceinline__ void dt_next(const DtParams& w, const int* items, int i, DtItem& t) {
+  if (t.piece + 1 < t.pieces) {
+    ++t.piece;
+    t.k0 += t.pt;
+    t.k1 = min(t.L, t.k0 + t.pt);
+    t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
+  } else {
+    t = dt_item<NT>(w, items, i);
+  }
+}
 
-// Sums of v[16] over 32 lanes: lane l ends with column l >> 1, 16 shuffles.
-__device__ __forceinline__ float sum16(float (&v)[16], int lane) {
+// CW or 16 columns of a product's sums.
+template <int CH>
+__device__ __forceinline__ void read_columns(uint32_t col, float (&x)[CH]) {
+  if constexpr (CH == 8) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(col));
+    tc::tmem_ld_wait();
 #pragma unroll
-  for (int half = 8, bit = 16; half >= 1; half >>= 1, bit >>= 1) {
+    for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(r[k]);
+  } else {
+    tc::tmem_ld16(col, x);
+  }
+}
+// One product's steps: KS of 32 elements, the operands' starts moving by a
+// step's tiles (constants, so that the issuing thread spends an add or two a
+// step: with run-time steps it takes 130 cycles a product, which takes 51 to 60).
+template <int KS>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint64_t astep, uint64_t bstep, bool acc) {
+#pragma unroll
+  for (int c = 0; c < KS; ++c) mma_e4m3(d, a + c * astep, b + c * bstep, id, acc || c != 0);
+}
+// Sums of l[CW] over a warp's lanes, into out[column] at its warp's place.  By
+// halves: after log2(CW) exchanges a lane holds one column of its part.
+template <int CW>
+__device__ __forceinline__ void column_sums(const float (&l)[CW], float4* out, int lane, int quad) {
+  float v[CW];
+#pragma unroll
+  for (int i = 0; i < CW; ++i) v[i] = l[i];
+  int bit = 16, at = 0;
+#pragma unroll
+  for (int half = CW / 2; half >= 1; half >>= 1, bit >>= 1) {
     const bool up = lane & bit;
+    at = 2 * at + (up ? 1 : 0);
 #pragma unroll
     for (int i = 0; i < half; ++i) {
       const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
       v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
     }
   }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+  for (; bit >= 1; bit >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+  if ((lane & (32 / CW - 1)) == 0) (&out[at].x)[quad] = v[0];
 }
 // Largest value of a warp (NaN falls out).
 __device__ __forceinline__ float warp_max(float x) {
@@ -187,20 +258,18 @@ __device__ __forceinline__ bool bar_and(bool ok, int id) {
 template <int NT>
 __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_decode_tc_kernel(const DtParams w) {
   using C = DtCfg<NT>;
-  constexpr int CW = C::CW, WARPS = C::WGS * 4;   // softmax warps; then K loads, V loads, products
+  constexpr int CW = C::CW, CH = C::CH, WARPS = C::WGS * 4;   // softmax warps; then K loads, V loads, products
   extern __shared__ uint8_t dyn[];
   const AttnDecodeParams& p = w.a;
   uint8_t* base = dyn + ((128u - (smem_u32(dyn) & 127u)) & 127u);
   DtShared<NT>& sh = *reinterpret_cast<DtShared<NT>*>(base + w.misc_off);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d, ST = w.stages, NS = ST + 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d;
+  const int KS = w.k_stages, VS = w.v_stages, NS = max(KS, VS) + 2;
   volatile int* fail = &sh.fail;
 
   if (threadIdx.x == 0) {
-    sh.items[0] = 0;
-    for (int i = 0; i < ST; ++i) {
-      tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], 1);
-      tc::mbar_init(&sh.v_full[i], 1), tc::mbar_init(&sh.v_empty[i], 1);
-    }
+    for (int i = 0; i < KS; ++i) tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], 1);
+    for (int i = 0; i < VS; ++i) tc::mbar_init(&sh.v_full[i], 1), tc::mbar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < NS; ++i) tc::mbar_init(&sh.sc_full[i], 2 * kDtBlocks);
     for (int i = 0; i < 2; ++i)
       tc::mbar_init(&sh.s_full[i], 1), tc::mbar_init(&sh.p_full[i], C::WGS * 128), tc::mbar_init(&sh.o_done[i], 1);
@@ -214,29 +283,42 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
     tc::tmem_alloc(&sh.tmem, C::COLS);
     tc::tmem_relinquish();
   }
-  // running sum of the items; lengths out of bounds are reported and have none
+  // running sums of the items; lengths out of bounds are reported and have none
   if (warp == 0) {
-    int sum = 0;
+    int sum = 0, sumw = 0;
+    if (lane == 0) sh.items[0] = sh.work[0] = 0;
     for (int c = 0; c < w.ns; c += 32) {
-      int v = c + lane < w.ns ? dt_items<NT>(p, w.s0 + c + lane) : 0;
-      if (v < 0) {
-        if (blockIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
-        v = 0;
+      int v = 0, x = 0;
+      if (c + lane < w.ns) {
+        const int s = w.s0 + c + lane;
+        int g = dt_groups<NT>(p, s);
+        if (g < 0) {
+          if (blockIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
+          g = 0;
+        }
+        if (g > 0) {
+          const int pieces = decode_pieces(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G);
+          v = g * pieces;
+          x = g * pieces * dt_piece_work(p, s);
+        }
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
+        const int a = __shfl_up_sync(0xffffffffu, v, o), b = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) v += a, x += b;
       }
-      if (c + lane < w.ns) sh.items[c + lane + 1] = sum + v;
+      if (c + lane < w.ns) sh.items[c + lane + 1] = sum + v, sh.work[c + lane + 1] = sumw + x;
       sum += __shfl_sync(0xffffffffu, v, 31);
+      sumw += __shfl_sync(0xffffffffu, x, 31);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tb = sh.tmem;
-  const int total = sh.items[w.ns];
+  // this CTA's run of items
+  const int i0 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
+  const int i1 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
   const uint32_t unit = (uint32_t)kDtTok * d;   // bytes of a tile's K (or V) codes
   int loaded = 0;                               // tiles loaded (a loading warp's)
 
@@ -245,10 +327,13 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
     const bool is_v = warp == WARPS + 1;
     uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
     uint8_t* ring = base + (is_v ? w.v_off : w.k_off);
+    const int ST = is_v ? VS : KS;
     int st = 0, ph = 0, sc = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
-      const DtItem t = dt_item<NT>(w, sh.items, i);
+    DtItem t{};
+    for (int i = i0; ok && i < i1; ++i) {
+      if (i == i0) t = dt_item<NT>(w, sh.items, i);
+      else dt_next<NT>(w, sh.items, i, t);
       const int32_t* bt = p.block_table + (int64_t)t.s * p.max_pages;
       auto page_of = [&](int j) {
         const int pos = t.k0 + j * kDtTok + lane * kKvBlock, at = pos / p.c.page_tokens;
@@ -302,48 +387,58 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
   } else if (warp == WARPS + 2) {
     // ---- products ----
     if (lane == 0) {
-      constexpr uint32_t id = idesc_e4m3(NT);
+      constexpr uint32_t id = idesc_e4m3(C::N);
       const uint32_t k0 = smem_u32(base + w.k_off), v0 = smem_u32(base + w.v_off), qa = smem_u32(base + w.q_off),
                      pa = smem_u32(base + w.p_off);
       const uint32_t rows8 = 8u * d;   // 8 tokens of K (or 8 rows of Q)
       const int halves = (d + 127) / 128;
-      int ks = 0, kp = 0, vs = 0, vp = 0, item = 0;
+      const uint64_t vstep = (uint64_t)(32u * d >> 4);
+      int ks = 0, kp = 0, vs = 0, vp = 0, heads = 0;
       unsigned T = 0;   // tiles multiplied
       bool ok = true;
       auto qk = [&](unsigned tt) {
         if (!dt_wait(&sh.k_full[ks], kp, fail)) return false;
         tc::fence_after_sync();
         const uint64_t a = desc_tiles(k0 + ks * unit, 128, rows8);
+#pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint64_t b = desc_tiles(qa + part * NT * d, 128, rows8);
-          for (int c = 0; c < d / 32; ++c) mma_e4m3(tb + (tt & 1) * NT, a + c * 16, b + c * 16, id, part | c);
+          const uint32_t dst = tb + (tt & 1) * C::N;
+          if (d == 256) {
+            mma_steps<8>(dst, a, b, id, 16, 16, part);
+          } else if (d == 128) {
+            mma_steps<4>(dst, a, b, id, 16, 16, part);
+          } else {
+            for (int c = 0; c < d / 32; ++c) mma_e4m3(dst, a + c * 16, b + c * 16, id, part | c);
+          }
         }
         tc::mma_commit(&sh.k_empty[ks]);
         tc::mma_commit(&sh.s_full[tt & 1]);
-        if (++ks == ST) ks = 0, kp ^= 1;
+        if (++ks == KS) ks = 0, kp ^= 1;
         return true;
       };
-      for (int i = blockIdx.x; ok && i < total; i += gridDim.x, ++item) {
-        const DtItem t = dt_item<NT>(w, sh.items, i);
-        ok = dt_wait(&sh.q_full, item & 1, fail);
+      DtItem t{};
+      for (int i = i0; ok && i < i1; ++i) {
+        if (i == i0) t = dt_item<NT>(w, sh.items, i);
+        else dt_next<NT>(w, sh.items, i, t);
+        if (i == i0 || t.piece == 0) ok = dt_wait(&sh.q_full, heads++ & 1, fail);
         if (ok && t.tiles > 0) ok = qk(T);
         for (int j = 0; ok && j < t.tiles; ++j, ++T) {
           if (j + 1 < t.tiles) ok = qk(T + 1);
           ok = ok && dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail);
           if (!ok) break;
           tc::fence_after_sync();
-          for (int hf = 0; hf < halves; ++hf)
-            for (int part = 0; part < 2; ++part) {
-              const uint64_t a = desc_tiles(v0 + vs * unit + hf * 2048u, 16u * d, 128);
-              // P: tokens of 16 columns (16 B), the next 16 columns a block of 128 tokens further
-              const uint64_t b = desc_tiles(pa + ((T & (C::PB - 1)) * 2 + part) * NT * kDtTok, 128, 16 * kDtTok);
+          for (int hf = 0; hf < halves; ++hf) {
+            const uint64_t a = desc_tiles(v0 + vs * unit + hf * 2048u, 16u * d, 128);
+            // P: tokens of 16 columns (16 B), the next 16 columns a block of 128 tokens further
 #pragma unroll
-              for (int c = 0; c < kDtTok / 32; ++c)
-                mma_e4m3(tb + C::O0 + hf * NT, a + ((uint32_t)c * 32u * d >> 4), b + c * 32, id | kTransposedB, j | part | c);
-            }
+            for (int part = 0; part < 2; ++part)
+              mma_steps<kDtTok / 32>(tb + C::O0 + hf * C::N, a, desc_tiles(pa + part * C::N * kDtTok, 128, 16 * kDtTok),
+                                     id | kTransposedB, vstep, 32, j | part);
+          }
           tc::mma_commit(&sh.v_empty[vs]);
           tc::mma_commit(&sh.o_done[T & 1]);
-          if (++vs == ST) vs = 0, vp ^= 1;
+          if (++vs == VS) vs = 0, vp ^= 1;
         }
       }
       // every product issued, and every arrival on a barrier, before the end
@@ -356,7 +451,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
     const uint32_t lanes = tb + ((uint32_t)quad << 21);
     uint8_t* qd = base + w.q_off;
     uint8_t* pd = base + w.p_off;
-    bool ok = true;
+    bool ok = true, okp = true;
     // an item's rows as hi and lo codes, a warp a row at a time, all loads first
     auto load_q = [&](const DtItem& t, int par) {
       const int e0 = lane * 8;
@@ -373,7 +468,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
                                                    (int64_t)(t.h * p.G + g) * d + e0);
           if (lane == 0) {
             sh.lim[par][n] = t.L - t.n + row + 1;
-            sh.out[par][n] = (int64_t)(t.q0 + row) * p.Hq + t.h * p.G + g;
+            sh.out[par][n] = (uint32_t)((row - t.r0 / p.G) * p.Hq + t.h * p.G + g);
           }
         }
       }
@@ -416,23 +511,23 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
       dt_arrive(&sh.q_full);
     };
     unsigned T = 0;
-    int st = 0, sc = 0, scp = 0, vp = 0, par = 0;   // V stage and its phase, scale slot and its phase, item
+    int st = 0, sc = 0, scp = 0, vp = 0, par = 0, ip = 0;   // V stage, scale slot and their phases; head, item
     DtItem t{};
-    if ((int)blockIdx.x < total) {
-      t = dt_item<NT>(w, sh.items, blockIdx.x);
+    if (i0 < i1) {
+      t = dt_item<NT>(w, sh.items, i0);
       load_q(t, 0);
     }
     bar_and(true, bar);
-    for (int i = blockIdx.x; i < total; i += gridDim.x, par ^= 1) {
+    for (int i = i0; i < i1; ++i) {
       float l[CW];
 #pragma unroll
       for (int n = 0; n < CW; ++n) l[n] = 0.f;
       float ref = -INFINITY;                          // of column c0 + tid
-      if (wg == 0) sh.bad[par][tid] = sh.bad[par][tid + 128] = 0x7fffffff;
+      if (wg == 0 && t.tiles > 0) sh.bad[ip][tid] = sh.bad[ip][tid + 128] = 0x7fffffff;
       const int least = t.L - t.n + 1;                // keys that every row sees
       for (int j = 0; j < t.tiles; ++j, ++T) {
         const int kb = t.k0 + j * kDtTok, pos = kb + tid;
-        const uint32_t scol = lanes + (T & 1) * NT + c0;
+        const uint32_t scol = lanes + (T & 1) * C::N + c0;
         ok = dt_wait(&sh.sc_full[sc], scp, fail) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail);
         __syncwarp();
         tc::fence_after_sync();
@@ -444,34 +539,31 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
         const float lv = (float)(ve - 127);
         const float rv = valid ? __uint_as_float((uint32_t)(254 - ve) << 23) : 0.f;
         const bool edge = kb + kDtTok > least;        // some row does not see some token
-        // weight exponents s + log2(vs) of 16 columns, -inf where masked
-        auto scores = [&](int ch, float (&x)[16]) {
-          tc::tmem_ld16(scol + ch * 16, x);
-          const float4* f4 = reinterpret_cast<const float4*>(&sh.fq[par][c0 + ch * 16]);
+        // weight exponents s + log2(vs), -inf where masked
+        float x[CW / CH][CH];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float4 f = f4[u];
+        for (int ch = 0; ch < CW / CH; ++ch) {
+          read_columns(scol + ch * CH, x[ch]);
+          const float4* f4 = reinterpret_cast<const float4*>(&sh.fq[par][c0 + ch * CH]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[4 * u + k] = fmaf(x[4 * u + k], kscale * (&f.x)[k], lv);
+          for (int k = 0; k < CH; k += 4) {
+            const float4 f = f4[k / 4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[ch][k + u] = fmaf(x[ch][k + u], kscale * (&f.x)[u], lv);
           }
           if (part || edge) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (!valid || pos >= sh.lim[par][c0 + ch * 16 + k]) x[k] = -INFINITY;
+            for (int k = 0; k < CH; ++k)
+              if (!valid || pos >= sh.lim[par][c0 + ch * CH + k]) x[ch][k] = -INFINITY;
           }
-        };
-        float x[CW / 16][16];
 #pragma unroll
-        for (int ch = 0; ch < CW / 16; ++ch) {
-          scores(ch, x[ch]);
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
+          for (int k = 0; k < CH; k += 4) {
             const float a = warp_max(x[ch][k]), b = warp_max(x[ch][k + 1]), c = warp_max(x[ch][k + 2]),
                         e = warp_max(x[ch][k + 3]);
-            if (lane == 0) *reinterpret_cast<float4*>(&sh.cmax[quad][c0 + ch * 16 + k]) = make_float4(a, b, c, e);
+            if (lane == 0) *reinterpret_cast<float4*>(&sh.cmax[quad][c0 + ch * CH + k]) = make_float4(a, b, c, e);
           }
         }
-        ok = bar_and(ok, bar);
+        ok = bar_and(ok && okp, bar);
         if (!ok) break;
         if (tid < CW) {
           const int n = c0 + tid;
@@ -492,49 +584,51 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
         bar_and(true, bar);
         if (*(volatile unsigned*)&sh.grow[wg] == T + 1) {
           // the products before this tile's: done, then scaled column by column
-          ok = bar_and(dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail), bar);
-          if (!ok) break;
+          // (one that runs out shows at the next barrier)
+          okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+          __syncwarp();
           tc::fence_after_sync();
 #pragma unroll
-          for (int ch = 0; ch < CW / 16; ++ch) {
-            float al[16];
+          for (int n = 0; n < CW; ++n) l[n] *= sh.alpha[c0 + n];
+          for (int hf = 0; hf < (d + 127) / 128; ++hf)
 #pragma unroll
-            for (int k = 0; k < 16; ++k) al[k] = sh.alpha[c0 + ch * 16 + k], l[ch * 16 + k] *= al[k];
-            for (int hf = 0; hf < (d + 127) / 128; ++hf) {
+            for (int ch = 0; ch < (CW + 15) / 16; ++ch) {
+              const uint32_t col = lanes + C::O0 + hf * C::N + c0 + ch * 16;
               float o[16];
-              tc::tmem_ld16(lanes + C::O0 + hf * NT + c0 + ch * 16, o);
+              tc::tmem_ld16(col, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= al[k];
-              tc::tmem_st16(lanes + C::O0 + hf * NT + c0 + ch * 16, o);
+              for (int k = 0; k < 16; ++k) o[k] *= sh.alpha[c0 + (ch * 16 + k) % CW];   // (of 8 rows the other 8 are not read)
+              tc::tmem_st16(col, o);
             }
-          }
           tc::tmem_st_wait();
         }
-        if (C::PB == 1 && j > 0) {   // one buffer of weights: the product before has read it
-          ok = bar_and(dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail), bar);
-          if (!ok) break;
-        }
-        uint8_t* pw = pd + (T & (C::PB - 1)) * 2 * NT * kDtTok + c0 * kDtTok + tid * 16;
+        // the weights' place: read by the product before
+        if (j > 0) okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail) && okp;
+        uint8_t* pw = pd + c0 * kDtTok + tid * 16;
 #pragma unroll
-        for (int ch = 0; ch < CW / 16; ++ch) {
-          uint4 hi, lo;
-          const float4* r4 = reinterpret_cast<const float4*>(&sh.ref[c0 + ch * 16]);
+        for (int ch = 0; ch < CW / CH; ++ch) {
+          uint32_t hi[CH / 4], lo[CH / 4];
+          const float4* r4 = reinterpret_cast<const float4*>(&sh.ref[c0 + ch * CH]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < CH / 4; ++u) {
             const float4 r = r4[u];
             float e[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               e[k] = dt_ex2(x[ch][4 * u + k] - (&r.x)[k]);
-              l[ch * 16 + 4 * u + k] = fmaf(e[k], rv, l[ch * 16 + 4 * u + k]);
+              l[ch * CH + 4 * u + k] = fmaf(e[k], rv, l[ch * CH + 4 * u + k]);
             }
-            const uint32_t h = e4m3x4(e[0], e[1], e[2], e[3]);
-            const float2 a = e4m3_f32x2(h), b = e4m3_f32x2(h >> 16);
-            (&hi.x)[u] = h;
-            (&lo.x)[u] = e4m3x4(e[0] - a.x, e[1] - a.y, e[2] - b.x, e[3] - b.y);
+            hi[u] = e4m3x4(e[0], e[1], e[2], e[3]);
+            const float2 a = e4m3_f32x2(hi[u]), b = e4m3_f32x2(hi[u] >> 16);
+            lo[u] = e4m3x4(e[0] - a.x, e[1] - a.y, e[2] - b.x, e[3] - b.y);
           }
-          *reinterpret_cast<uint4*>(pw + ch * 16 * kDtTok) = hi;
-          *reinterpret_cast<uint4*>(pw + ch * 16 * kDtTok + NT * kDtTok) = lo;
+          if constexpr (CH == 8) {
+            *reinterpret_cast<uint2*>(pw) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(pw + C::N * kDtTok) = make_uint2(lo[0], lo[1]);
+          } else {
+            *reinterpret_cast<uint4*>(pw + ch * 16 * kDtTok) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(pw + ch * 16 * kDtTok + C::N * kDtTok) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
         if (edge && wg == 0) {
           // values that some row may not see: past the sequence they become
@@ -554,7 +648,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
                   v[k] = 0;
                 } else if (at >= least && (v[k] & 0x7f) == 0x7f) {
                   v[k] = 0;
-                  sh.bad[par][e] = min(sh.bad[par][e], at);
+                  sh.bad[ip][e] = min(sh.bad[ip][e], at);
                 }
               }
             }
@@ -564,67 +658,68 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
         tc::fence_async_smem();
         tc::fence_before_sync();
         dt_arrive(&sh.p_full[T & 1]);
-        if (++st == ST) st = 0, vp ^= 1;
+        if (++st == VS) st = 0, vp ^= 1;
         if (++sc == NS) sc = 0, scp ^= 1;
       }
       if (!ok) break;
-      // the next item's rows: its scores may then start while this one ends
+      // the next head's rows: its scores may then start while this item ends
       const DtItem u = t;
-      if (i + (int)gridDim.x < total) {
-        t = dt_item<NT>(w, sh.items, i + gridDim.x);
-        load_q(t, par ^ 1);
+      const int was = par;
+      if (i + 1 < i1) {
+        dt_next<NT>(w, sh.items, i + 1, t);
+        if (t.piece == 0) load_q(t, par ^= 1);
       }
-#pragma unroll
-      for (int ch = 0; ch < CW / 16; ++ch) {
-        float x[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = l[ch * 16 + k];
-        const float sum = sum16(x, lane);
-        if (!(lane & 1)) (&sh.lsum[c0 + ch * 16 + (lane >> 1)].x)[quad] = sum;
-      }
+      column_sums<CW>(l, sh.lsum + c0, lane, quad);
       if (u.tiles > 0) ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
-      ok = bar_and(ok, bar);
+      ok = bar_and(ok && okp, bar);
       if (!ok) break;
       tc::fence_after_sync();
-      const int64_t R = p.T * p.Hq;
+      const int64_t R = p.T * p.Hq, rh0 = (int64_t)(u.q0 + u.r0 / p.G) * p.Hq;
       const int mine = min(CW, u.rows - c0);   // columns of this warpgroup that are rows
       if (tid < mine) {
         const float4 c = sh.lsum[c0 + tid];
         const float sum = (c.x + c.y) + (c.z + c.w), m = sum == 0.f ? -INFINITY : sh.ref[c0 + tid];
-        const int64_t rh = sh.out[par][c0 + tid];
+        const int64_t rh = rh0 + sh.out[was][c0 + tid];
         if (p.part_o) p.part_ml[u.piece * R + rh] = make_float2(m, sum);
         else if (p.lse) p.lse[rh] = sum == 0.f ? -INFINITY : m * 0.693147180559945309f + logf(sum);
       }
       __syncwarp();
-      const bool check = u.k0 + u.tiles * kDtTok > least;   // some tile had values that not every row sees
+      const bool check = u.tiles > 0 && u.k0 + u.tiles * kDtTok > least;   // some tile had values that not every row sees
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int e = hf * 128 + tid;
         if (hf * 128 >= d) break;
-        const int bad = check && e < d ? sh.bad[par][e] : 0x7fffffff;
-        float* po = p.part_o + u.piece * R * d + e;
+        const int e = hf * 128 + tid;
+        float* po = p.part_o + (u.piece * R + rh0) * d + e;
+        __nv_bfloat16* oo = static_cast<__nv_bfloat16*>(p.o) + rh0 * d + e;
 #pragma unroll
-        for (int ch = 0; ch < CW / 16; ++ch) {
-          if (ch * 16 >= mine) break;
-          float o[16];
+        for (int ch = 0; ch < CW / CH; ++ch) {
+          if (ch * CH >= mine) break;
+          float o[CH];
           if (u.tiles > 0) {
-            tc::tmem_ld16(lanes + C::O0 + hf * NT + c0 + ch * 16, o);
+            read_columns(lanes + C::O0 + hf * C::N + c0 + ch * CH, o);
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+            for (int k = 0; k < CH; ++k) o[k] = 0.f;
           }
           if (e < d) {
+            if (check) {
+              const int bad = sh.bad[ip][e];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int n = c0 + ch * 16 + k;
-              if (ch * 16 + k >= mine) break;
-              const float v = bad < sh.lim[par][n] ? __int_as_float(0x7fffffff) : o[k];
-              if (p.part_o) {
-                po[sh.out[par][n] * d] = v;
-              } else {
-                const float4 c = sh.lsum[n];
-                const float sum = (c.x + c.y) + (c.z + c.w);
-                static_cast<__nv_bfloat16*>(p.o)[sh.out[par][n] * d + e] = __float2bfloat16_rn(sum == 0.f ? 0.f : v / sum);
+              for (int k = 0; k < CH; ++k)
+                if (bad < sh.lim[was][c0 + ch * CH + k]) o[k] = __int_as_float(0x7fffffff);
+            }
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+              const int n = c0 + ch * CH + k;
+              const uint32_t at = sh.out[was][n] * (uint32_t)d;   // at most 32 rows of 1,024 heads of 256 elements
+              if (ch * CH + k < mine) {
+                if (p.part_o) {
+                  po[at] = o[k];
+                } else {
+                  const float4 c = sh.lsum[n];
+                  const float sum = (c.x + c.y) + (c.z + c.w);
+                  oo[at] = __float2bfloat16_rn(sum == 0.f ? 0.f : o[k] / sum);
+                }
               }
             }
           }
@@ -633,6 +728,8 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
       }
       tc::fence_before_sync();
       bar_and(true, bar);   // lsum, ref and O are free
+      // (a buffer comes back after an item whose tiles every warpgroup has passed)
+      if (u.tiles > 0) ip ^= 1;
     }
   }
   __syncwarp();
@@ -643,8 +740,11 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, DtCfg<NT>::CTAS) attn_deco
     // wait each before their memory goes
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
     if ((warp == WARPS || warp == WARPS + 1) && lane == 0)
+    {
+      const int ST = warp == WARPS ? KS : VS;
       for (int n = max(0, loaded - ST); n < loaded; ++n)
         tc::mbar_wait_bounded(warp == WARPS ? &sh.k_full[n % ST] : &sh.v_full[n % ST], (uint32_t)(n / ST) & 1, kDtWait);
+    }
     __syncwarp();
     __syncthreads();
   }
@@ -659,18 +759,20 @@ cudaError_t decode_tc(const AttnDecodeParams& p, int sms, cudaStream_t st) {
   using C = DtCfg<NT>;
   DtParams w{};
   w.a = p;
-  const uint32_t d = (uint32_t)p.c.d, unit = kDtTok * d, q = 2 * NT * d, pp = 2 * C::PB * NT * kDtTok;
+  const uint32_t d = (uint32_t)p.c.d, unit = kDtTok * d, q = 2 * NT * d, pp = 2 * C::N * kDtTok;
   // K and V stages in what is left of 227 KB (1 KB a CTA is the system's);
-  // below 128 elements the second product's 128 rows read up to 2 KB past a
-  // stage (their sums are not used)
+  // where d is no multiple of 128 the second product's 128 rows read up to
+  // 2 KB past a stage (their sums are not used)
+  const uint32_t past = d % 128 ? 2048 : 0;
   const uint32_t all = C::CTAS == 2 ? 115712 : 232448;
-  const uint32_t fixed = q + pp + (uint32_t)sizeof(DtShared<NT>) + 2048 + 512;
-  const uint32_t stages = (all - fixed) / (2 * unit);
-  w.stages = stages > kDtMaxStages ? kDtMaxStages : (int)stages;
-  if (w.stages < 1) return cudaErrorInvalidValue;
+  const uint32_t fixed = q + pp + (uint32_t)sizeof(DtShared<NT>) + past + 512;
+  const uint32_t units = (all - fixed) / unit;
+  if (units < 2) return cudaErrorInvalidValue;
+  w.k_stages = units / 2 + units % 2 > kDtMaxStages ? kDtMaxStages : (int)(units / 2 + units % 2);
+  w.v_stages = units / 2 > kDtMaxStages ? kDtMaxStages : (int)(units / 2);
   w.k_off = 0;
-  w.v_off = w.stages * unit;
-  w.q_off = (2 * w.stages * unit + 2048 + 127) / 128 * 128;
+  w.v_off = w.k_stages * unit;
+  w.q_off = ((w.k_stages + w.v_stages) * unit + past + 127) / 128 * 128;
   w.p_off = w.q_off + q;
   w.misc_off = (w.p_off + pp + 127) / 128 * 128;
   uint32_t smem = w.misc_off + (uint32_t)sizeof(DtShared<NT>) + 128;
@@ -704,9 +806,9 @@ cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // the narrowest tile that holds a sequence's (row, head) pairs of a kv head
   const int rows = p.max_q * p.G;
+  if (rows <= 8) return decode_tc<8>(p, sms, st);
   if (rows <= 16) return decode_tc<16>(p, sms, st);
   if (rows <= 32) return decode_tc<32>(p, sms, st);
-  if (rows <= 64) return decode_tc<64>(p, sms, st);
   return decode_tc<96>(p, sms, st);
 }
 

@@ -176,29 +176,44 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
 }
 
 // Joins the pieces of every row in their order: o = sum_i w_i O_i / sum_i w_i l_i,
-// w_i = 2^(m_i - max m).  A warp a (row, head).
+// w_i = 2^(m_i - max m).  A warp a (row, head): the lanes hold the pieces'
+// weights (76 at most), then an element of the head each.
 template <typename T>
 __global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeParams p) {
-  if (*p.err == GDN_ERR_TIMEOUT) return;   // a wait ran out: the pieces cannot be trusted
-  const int s = blockIdx.y;
+  const int s = blockIdx.y, lane = threadIdx.x & 31, d = p.c.d;
   const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the pieces' kernel before this one
   if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
-  const int pieces = decode_pieces(L, n * p.G), lane = threadIdx.x & 31, d = p.c.d;
+  if (*p.err == GDN_ERR_TIMEOUT) return;   // a wait ran out: the pieces cannot be trusted
+  const int pieces = decode_pieces(L, n * p.G);
   const int64_t R = p.T * p.Hq;
   for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n * p.Hq; i += gridDim.x * 4) {
     const int64_t rh = (int64_t)q0 * p.Hq + i;
+    float2 ml[3];
     float mx = -INFINITY;
-    for (int j = 0; j < pieces; ++j) mx = fmaxf(mx, p.part_ml[j * R + rh].x);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f, acc[8] = {};
-    for (int j = 0; j < pieces; ++j) {
-      const float2 ml = p.part_ml[j * R + rh];
-      const float w = fast_exp2(ml.x - ref);
-      sum += w * ml.y;
-      const float* o = p.part_o + (j * R + rh) * d;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < d) acc[e] += w * o[lane + 32 * e];
+    for (int k = 0; k < 3; ++k) {
+      ml[k] = lane + 32 * k < pieces ? p.part_ml[(lane + 32 * k) * R + rh] : make_float2(-INFINITY, 0.f);
+      mx = fmaxf(mx, ml[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float w[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) w[k] = fast_exp2(ml[k].x - ref);
+    float sum = 0.f, acc[8] = {};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll 4
+      for (int j = 0; j < min(32, pieces - 32 * k); ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w[k], j);
+        sum = fmaf(wj, __shfl_sync(0xffffffffu, ml[k].y, j), sum);
+        const float* o = p.part_o + ((j + 32 * k) * R + rh) * d;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (lane + 32 * e < d) acc[e] = fmaf(wj, o[lane + 32 * e], acc[e]);
+      }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -223,8 +238,17 @@ template <typename T>
 cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
   const cudaError_t e = attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st) : decode_simt<T>(p, st);
   if (e != cudaSuccess || !p.part_o) return e;
-  attn_decode_join_kernel<T><<<dim3((unsigned)((p.max_q * p.Hq + 3) / 4), p.N), 128, 0, st>>>(p);
-  return cudaGetLastError();
+  // launched while the pieces' kernel still runs, waiting on the device for its end
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((p.max_q * p.Hq + 3) / 4), p.N);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<T>, p);
 }
 
 }  // namespace
