@@ -99,8 +99,9 @@ struct AttnPrefillParams {
 // do so for drafts; beyond 38,912 tokens 76 pieces a head are one CTA on each
 // of the 152 SMs for two kv heads.
 constexpr int kMaxPieces = 76;
+constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows
 __host__ __device__ inline int decode_piece_target(int tiles, int rows) {   // pieces aimed at
-  const int per = (rows > 32 ? 8 : 4) / (tiles <= 16 ? 2 : 1);
+  const int per = (rows > kDtNarrow ? 8 : 4) / (tiles <= 16 ? 2 : 1);
   const int n = (tiles + per / 2) / per;
   return n < 1 ? 1 : n > kMaxPieces ? kMaxPieces : n;
 }
@@ -127,6 +128,7 @@ cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStrea
 // The tensor-core decode (bf16, d a multiple of 32): the pieces, without the join.
 bool attn_decode_tc_supported(const AttnDecodeParams& p, int dtype);
 cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st);
+cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, cudaStream_t st);
 // The tensor-core prefill: bf16, d = 64, 128 or 256, at least one key row.
 bool attn_prefill_tc_supported(const AttnPrefillParams& p, int dtype);
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams& p, cudaStream_t st);

@@ -1,0 +1,332 @@
+// attn_decode_tc.cuh — what the two decode kernels on the tensor cores share:
+// the work items, the loads of the cache's blocks, the products' forms.
+//
+// The cache's e4m3 codes are the products' operands as they lie in memory; no
+// code is converted.  Q and P enter as two e4m3 parts each, x = hi + lo: hi
+// keeps 4 significant bits, lo 4 more of what is left, which is all 8 of a
+// bf16 q (scaled by a power of two so that its largest element is in (224,
+// 448]; parts below 2^-9 vanish, 2^-18 of that element) and rounds p like bf16
+// would.  A block's K scale multiplies its scores; its V scale goes into the
+// weight's exponent, so a weight is 2^(s + log2(vs) - M) and the sum of the p
+// is the sum of the weights over vs.
+#pragma once
+
+#include "attn.h"
+#include "tc.cuh"
+
+namespace gdn {
+namespace dt {
+
+constexpr int kDtTok = 128;           // tokens of a tile
+constexpr int kDtBlocks = kDtTok / kKvBlock;
+constexpr int kDtSeqs = 256;         // sequences a launch
+constexpr int kDtMaxStages = 8;
+constexpr long long kDtWait = 4000000000LL;
+// Weights are scaled by 2^6 and may grow by 2^2.75 (430 < 448) before a
+// row's reference moves: a lower scale would lose small weights' bits (parts
+// vanish below 2^-16 of the reference), a higher one moves more often.
+constexpr float kDtBase = 6.f, kDtGrow = 2.75f;
+
+struct DtParams {
+  AttnDecodeParams a;
+  int32_t s0, ns;       // this launch's sequences ...
+  int32_t row_lo, row_hi;   // ... those with (row, head of the group) pairs in [row_lo, row_hi]
+  int32_t k_stages, v_stages;
+  uint32_t k_off, v_off, q_off, p_off, misc_off;   // dynamic shared memory
+};
+
+// Shared memory of either kernel.
+struct DtBase {
+  uint64_t k_full[kDtMaxStages], k_empty[kDtMaxStages], v_full[kDtMaxStages], v_empty[kDtMaxStages];
+  uint64_t sc_full[kDtMaxStages + 2], s_full[2], p_full[2], o_done[2], q_full, drain;
+  float ks[kDtMaxStages + 2][kDtBlocks], vs[kDtMaxStages + 2][kDtBlocks];
+  int bad[2][256];          // (items alternate) first token with a NaN value that not every row sees, by element
+  int items[kDtSeqs + 1];   // running sums of the sequences' work items ...
+  int work[kDtSeqs + 1];    // ... and of their weights
+  uint32_t tmem;
+  int fail;
+};
+
+__device__ __forceinline__ bool dt_wait(uint64_t* m, uint32_t parity, volatile int* fail) {
+  if (tc::mbar_test_wait(m, parity)) return true;
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait(m, parity)) {
+    if (*fail) return false;
+    if (clock64() - t0 > kDtWait) {
+      *fail = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void dt_arrive(uint64_t* m) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(m)) : "memory");
+}
+__device__ __forceinline__ float dt_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// e4m3 x e4m3 -> fp32: D[tmem] (+)= A[smem] B[smem]^T, 32 deep.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// Instruction descriptor: e4m3 A and B (both K-contiguous), fp32 sums, M = 128.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kDtTok >> 4) << 24);
+}
+constexpr uint32_t kTransposedB = 1u << 16;   // B's rows contiguous instead of the contraction
+// Operand of unswizzled 8-row x 16-byte tiles: `lead` bytes to the next 16
+// elements of the contraction, `stride` to the next 8 rows.
+__device__ __forceinline__ uint64_t desc_tiles(uint32_t saddr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// Work item -> sequence, kv head, row tile, piece.
+struct DtItem {
+  int s, h, r0, rows, piece, pieces, pt, rt;   // rows: (row, head) pairs of this item, from r0
+  int q0, n, L, k0, k1, tiles;
+};
+
+// Whether item t, the CTA's item i, has other rows than the one before it.
+__device__ __forceinline__ bool dt_new_rows(const DtItem& t, bool first) { return first || t.rt > 1 || t.piece == 0; }
+
+// Groups (kv head, row tile) of a sequence; 0: no rows, -1: out of bounds.
+template <int NT>
+__device__ __forceinline__ int dt_groups(const DtParams& w, int s) {
+  const AttnDecodeParams& p = w.a;
+  const int n = p.cu[s + 1] - p.cu[s], L = p.kv_len[s];
+  if (n <= 0) return 0;
+  if (n > p.max_q || L > p.max_kv || L < 0 || p.cu[s] < 0 || (int64_t)p.cu[s] + n > p.T) return -1;
+  if (n * p.G < w.row_lo || n * p.G > w.row_hi) return 0;
+  return p.c.Hkv * ((n * p.G + NT - 1) / NT);
+}
+// A tile of keys counts 1, an item's fixed cost as much again.
+__device__ __forceinline__ int dt_piece_work(const AttnDecodeParams& p, int s) {
+  return decode_piece_tokens(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G) / kDtTok + 1;
+}
+
+// The last s with sums[s] <= i.
+__device__ __forceinline__ int dt_find(const int* sums, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// First item of CTA b: the work before it is b / CTAs of all.
+template <int NT>
+__device__ __forceinline__ int dt_first(const DtParams& w, const int* items, const int* work, int b, int ctas) {
+  const int at = (int)((int64_t)work[w.ns] * b / ctas);
+  if (at >= work[w.ns]) return items[w.ns];
+  const int s = dt_find(work, w.ns, at);
+  const int per = dt_piece_work(w.a, w.s0 + s);   // of each of its items
+  return min(items[s + 1], items[s] + (at - work[s] + per - 1) / per);
+}
+
+template <int NT>
+__device__ __forceinline__ DtItem dt_item(const DtParams& w, const int* items, int i) {
+  const AttnDecodeParams& p = w.a;
+  const int lo = dt_find(items, w.ns, i);
+  DtItem t;
+  t.s = w.s0 + lo;
+  const int k = i - items[lo];
+  t.q0 = p.cu[t.s];
+  t.n = p.cu[t.s + 1] - t.q0;
+  t.L = p.kv_len[t.s];
+  // of one head: piece after piece, of a piece its row tiles (with one tile a
+  // CTA's run of items loads its rows once a head)
+  t.pieces = decode_pieces(t.L, t.n * p.G);
+  t.rt = (t.n * p.G + NT - 1) / NT;
+  t.h = k / (t.pieces * t.rt);
+  const int in = k - t.h * t.pieces * t.rt;
+  t.piece = in / t.rt;
+  t.r0 = (in - t.piece * t.rt) * NT;
+  t.rows = min(NT, t.n * p.G - t.r0);
+  t.pt = decode_piece_tokens(t.L, t.n * p.G);
+  t.k0 = t.piece * t.pt;
+  t.k1 = min(t.L, t.k0 + t.pt);
+  t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
+  return t;
+}
+// The item after it.
+template <int NT>
+__device__ __forceinline__ void dt_next(const DtParams& w, const int* items, int i, DtItem& t) {
+  if (t.rt == 1 && t.piece + 1 < t.pieces) {
+    ++t.piece;
+    t.k0 += t.pt;
+    t.k1 = min(t.L, t.k0 + t.pt);
+    t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
+  } else {
+    t = dt_item<NT>(w, items, i);
+  }
+}
+
+// One product's steps: KS of 32 elements, the operands' starts moving by a
+// step's tiles (constants, so that the issuing thread spends an add or two a
+// step: with run-time steps it takes 130 cycles a product, which takes 51 to 60).
+template <int KS>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint64_t astep, uint64_t bstep, bool acc) {
+#pragma unroll
+  for (int c = 0; c < KS; ++c) mma_e4m3(d, a + c * astep, b + c * bstep, id, acc || c != 0);
+}
+// Largest value of a warp (NaN falls out).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Running sums of the items (one warp); lengths out of bounds are reported and
+// have none.
+template <int NT>
+__device__ __forceinline__ void dt_sums(const DtParams& w, DtBase& sh, int lane) {
+  const AttnDecodeParams& p = w.a;
+  int sum = 0, sumw = 0;
+  if (lane == 0) sh.items[0] = sh.work[0] = 0;
+  for (int c = 0; c < w.ns; c += 32) {
+    int v = 0, x = 0;
+    if (c + lane < w.ns) {
+      const int s = w.s0 + c + lane;
+      int g = dt_groups<NT>(w, s);
+      if (g < 0) {
+        if (blockIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
+        g = 0;
+      }
+      if (g > 0) {
+        const int pieces = decode_pieces(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G);
+        v = g * pieces;
+        x = g * pieces * dt_piece_work(p, s);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, v, o), b = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) v += a, x += b;
+    }
+    if (c + lane < w.ns) sh.items[c + lane + 1] = sum + v, sh.work[c + lane + 1] = sumw + x;
+    sum += __shfl_sync(0xffffffffu, v, 31);
+    sumw += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
+
+// A warp's loads of the CTA's items [i0, i1), K's codes and scales or V's:
+// lane b < 8 the tile's block b.  Returns the tiles loaded.
+template <int NT>
+__device__ __forceinline__ int dt_load(const DtParams& w, DtBase& sh, uint8_t* base, int i0, int i1, bool is_v, int lane) {
+  const AttnDecodeParams& p = w.a;
+  volatile int* fail = &sh.fail;
+  uint64_t *full = is_v ? sh.v_full : sh.k_full, *empty = is_v ? sh.v_empty : sh.k_empty;
+  uint8_t* ring = base + (is_v ? w.v_off : w.k_off);
+  const int ST = is_v ? w.v_stages : w.k_stages, NS = max(w.k_stages, w.v_stages) + 2, d = p.c.d;
+  const uint32_t unit = (uint32_t)kDtTok * d;
+  int loaded = 0;
+  int st = 0, ph = 0, sc = 0;
+  bool ok = true;
+  DtItem t{};
+  for (int i = i0; ok && i < i1; ++i) {
+    if (i == i0) t = dt_item<NT>(w, sh.items, i);
+    else dt_next<NT>(w, sh.items, i, t);
+    const int32_t* bt = p.block_table + (int64_t)t.s * p.max_pages;
+    auto page_of = [&](int j) {
+      const int pos = t.k0 + j * kDtTok + lane * kKvBlock, at = pos / p.c.page_tokens;
+      return lane < kDtBlocks && pos < t.k1 && at < p.max_pages ? bt[at] : -1;
+    };
+    int next = t.tiles > 0 ? page_of(0) : -1;
+    for (int j = 0; j < t.tiles; ++j) {
+      const int page = next, pos = t.k0 + j * kDtTok + lane * kKvBlock;
+      if (j + 1 < t.tiles) next = page_of(j + 1);
+      const bool in = lane < kDtBlocks && pos < t.k1, good = in && page >= 0 && page < p.c.num_pages;
+      if (in && !good) set_error(p.err, GDN_ERR_PAGE_RANGE);
+      if (loaded >= ST) ok = dt_wait(&empty[st], ph ^ 1, fail);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      uint8_t* dst = ring + (uint32_t)st * unit;
+      const unsigned have = __ballot_sync(0xffffffffu, good);
+      if (have != (1u << kDtBlocks) - 1u) {
+        // blocks that are not loaded: their weights are 0, and so must V be
+        if (is_v)
+          for (unsigned miss = ~have & ((1u << kDtBlocks) - 1u); miss; miss &= miss - 1) {
+            uint4* z = reinterpret_cast<uint4*>(dst + (__ffs(miss) - 1) * kKvBlock * d);
+            for (int x = lane; x < d; x += 32) z[x] = make_uint4(0, 0, 0, 0);
+          }
+        tc::fence_async_smem();
+        if (lane < kDtBlocks && !good) {
+          if (is_v) sh.vs[sc][lane] = 1.f;
+          else sh.ks[sc][lane] = -1.f;   // a block to leave out
+        }
+        __syncwarp();
+      }
+      if (lane == 0) tc::mbar_expect_tx(&full[st], __popc(have) * kKvBlock * d);
+      __syncwarp();
+      if (lane < kDtBlocks) {
+        if (good) {
+          const int b = (pos - pos / p.c.page_tokens * p.c.page_tokens) / kKvBlock;
+          tc::bulk_load(dst + lane * kKvBlock * d, is_v ? kv_v_block(p.c, page, t.h, b) : kv_k_block(p.c, page, t.h, b),
+                        kKvBlock * d, &full[st]);
+          if (is_v) cp_async4(&sh.vs[sc][lane], kv_v_scale(p.c, page, t.h, b), 4);
+          else cp_async4(&sh.ks[sc][lane], kv_k_scale(p.c, page, t.h, b), 4);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(&sh.sc_full[sc])) : "memory");
+        } else {
+          dt_arrive(&sh.sc_full[sc]);
+        }
+      }
+      ++loaded;
+      if (++st == ST) st = 0, ph ^= 1;
+      if (++sc == NS) sc = 0;
+    }
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  return loaded;
+}
+
+// After a run-out: one more bounded wait for each copy in flight.
+__device__ __forceinline__ void dt_drain(const DtParams& w, DtBase& sh, int loaded, bool is_v) {
+  const int ST = is_v ? w.v_stages : w.k_stages;
+  for (int n = max(0, loaded - ST); n < loaded; ++n)
+    tc::mbar_wait_bounded(is_v ? &sh.v_full[n % ST] : &sh.k_full[n % ST], (uint32_t)(n / ST) & 1, kDtWait);
+}
+
+// Values of a tile (of its stage v) that some row may not see: past the
+// sequence they become zero, and so do NaN codes (a weight of 0 would not keep
+// them out of the product), noted by element for the rows that do see them.
+// 128 threads, elements tid and tid + 128.
+__device__ __forceinline__ void dt_clean(uint8_t* v, int* bad, const DtItem& t, int kb, int least, int d, int tid) {
+  for (int e = tid; e < d; e += 128)
+    for (int b = max(0, (least - kb) / kKvBlock); b < kDtBlocks && kb + b * kKvBlock < t.k1; ++b) {
+      uint8_t* at = v + (b * d + e) * kKvBlock;
+      for (int k = 0; k < kKvBlock; ++k) {
+        const int pos = kb + b * kKvBlock + k;
+        if (pos >= t.L) {
+          at[k] = 0;
+        } else if (pos >= least && (at[k] & 0x7f) == 0x7f) {
+          at[k] = 0;
+          bad[e] = min(bad[e], pos);
+        }
+      }
+    }
+}
+
+// The cache's share of dynamic shared memory: K and V stages in what `fixed`
+// leaves of `all` bytes; where d is no multiple of 128 a product's 128 rows of
+// V read up to 2 KB past a stage (their sums are not used).  The offset behind.
+inline uint32_t dt_rings(DtParams& w, uint32_t all, uint32_t fixed) {
+  const uint32_t d = (uint32_t)w.a.c.d, unit = kDtTok * d, past = d % 128 ? 2048 : 0;
+  const int units = all > fixed + past ? (int)((all - fixed - past) / unit) : 0;
+  w.k_stages = units / 2 + units % 2 > kDtMaxStages ? kDtMaxStages : units / 2 + units % 2;
+  w.v_stages = units / 2 > kDtMaxStages ? kDtMaxStages : units / 2;
+  w.k_off = 0;
+  w.v_off = w.k_stages * unit;
+  return ((w.k_stages + w.v_stages) * unit + past + 127) / 128 * 128;
+}
+
+}  // namespace dt
+}  // namespace gdn
