@@ -128,7 +128,7 @@ cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStrea
 // The tensor-core decode (bf16, d a multiple of 32): the pieces, without the join.
 bool attn_decode_tc_supported(const AttnDecodeParams& p, int dtype);
 cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st);
-cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, cudaStream_t st);
+cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overlap, cudaStream_t st);
 // The tensor-core prefill: bf16, d = 64, 128 or 256, at least one key row.
 bool attn_prefill_tc_supported(const AttnPrefillParams& p, int dtype);
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams& p, cudaStream_t st);

@@ -508,9 +508,9 @@ cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st) {
   // (row, head) pairs of a kv head here, more with the rows as the products'
   // 128 (attn_draft_tc.cu); a call that may have both launches both
   if (p.max_q * p.G > kDtNarrow) {
-    e = launch_attn_draft_tc(p, sms, st);
-    if (e != cudaSuccess || p.G > kDtNarrow) return e;
-    return decode_tc<16>(p, sms, st);
+    const bool few = p.G <= kDtNarrow;
+    if (few) e = decode_tc<16>(p, sms, st);
+    return e != cudaSuccess ? e : launch_attn_draft_tc(p, sms, few, st);
   }
   return p.max_q * p.G <= 8 ? decode_tc<8>(p, sms, st) : decode_tc<16>(p, sms, st);
 }

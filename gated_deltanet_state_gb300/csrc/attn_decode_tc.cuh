@@ -22,10 +22,11 @@ constexpr int kDtBlocks = kDtTok / kKvBlock;
 constexpr int kDtSeqs = 256;         // sequences a launch
 constexpr int kDtMaxStages = 8;
 constexpr long long kDtWait = 4000000000LL;
-// Weights are scaled by 2^6 and may grow by 2^2.75 (430 < 448) before a
-// row's reference moves: a lower scale would lose small weights' bits (parts
-// vanish below 2^-16 of the reference), a higher one moves more often.
-constexpr float kDtBase = 6.f, kDtGrow = 2.75f;
+// Weights are scaled by 2^4 and may grow by 2^4.75 (430 < 448) before a row's
+// reference moves (which costs a pass over its outputs).  Parts vanish below
+// 2^-14 of the reference, rounding errors of 2^-15 that a weight near it
+// outweighs: against 64 bits the outputs' error is bf16's own rounding.
+constexpr float kDtBase = 4.f, kDtGrow = 4.75f;
 
 struct DtParams {
   AttnDecodeParams a;

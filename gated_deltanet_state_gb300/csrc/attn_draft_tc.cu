@@ -23,7 +23,9 @@ constexpr int kDrRows = 128;
 constexpr int kDrThreads = 128 + 96;       // softmax; K loads, V loads, products
 constexpr uint32_t kDrO = 256;             // tensor memory: scores of two tiles, then O
 
-struct DrShared : DtBase {};
+struct DrShared : DtBase {
+  float turn[4][32][33];   // a warp's 32 rows x 32 elements on their way out
+};
 
 // D[tmem] (+)= A[tmem] B[smem]^T, e4m3, 32 deep: eight columns of A hold four codes each.
 __device__ __forceinline__ void mma_e4m3_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -352,12 +354,17 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
           for (int k = 0; k < 32; ++k)
             if (sh.bad[ip][e + k] < lim) o[k] = __int_as_float(0x7fffffff);
         }
-        if (mine) {
-          if (p.part_o) {
+        if (p.part_o) {
+          // through shared memory, so that a warp writes 128 bytes of one row at a time
 #pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(po + e + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-          } else {
+          for (int k = 0; k < 32; ++k) sh.turn[warp][lane][k] = o[k];
+          __syncwarp();
+          const int rows = min(32, u.rows - warp * 32);
+#pragma unroll 8
+          for (int k = 0; k < rows; ++k)
+            *reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(po + e), k) + 4 * lane) = sh.turn[warp][k][lane];
+        } else if (mine) {
+          {
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
               uint32_t b[4];
@@ -391,9 +398,11 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
   }
   tc::fence_after_sync();
   if (warp == 4) tc::tmem_dealloc(tb, 512);
+  // done when the kernel before this one (the call's other sequences) is
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
-cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, cudaStream_t st) {
+cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overlap, cudaStream_t st) {
   DtParams w{};
   w.a = p;
   w.row_lo = kDtNarrow + 1, w.row_hi = 0x7fffffff;
@@ -410,8 +419,18 @@ cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, cudaStream_
     w.s0 = s0;
     w.ns = p.N - s0 < kDtSeqs ? p.N - s0 : kDtSeqs;
     const int64_t most = (int64_t)w.ns * p.max_pieces * p.c.Hkv * rt;
-    attn_draft_tc_kernel<<<(unsigned)(most < sms ? most : sms), kDrThreads, smem, st>>>(w);
-    e = cudaGetLastError();
+    // behind the kernel of the sequences with few rows, which share nothing with these
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.blockDim = dim3(kDrThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = overlap ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, attn_draft_tc_kernel, w);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

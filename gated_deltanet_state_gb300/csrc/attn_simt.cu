@@ -202,22 +202,38 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeP
     float w[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) w[k] = fast_exp2(ml[k].x - ref);
-    float sum = 0.f, acc[8] = {};
+    float sum = 0.f;
+    float4 acc[2] = {};
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-#pragma unroll 4
-      for (int j = 0; j < min(32, pieces - 32 * k); ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w[k], j);
-        sum = fmaf(wj, __shfl_sync(0xffffffffu, ml[k].y, j), sum);
-        const float* o = p.part_o + ((j + 32 * k) * R + rh) * d;
+      const int most = min(32, pieces - 32 * k);
+      const float4* o = reinterpret_cast<const float4*>(p.part_o + (32 * k * R + rh) * d) + lane;
+      // eight pieces' loads at once; those past the last have weight 0
+#pragma unroll 1
+      for (int j0 = 0; j0 < most; j0 += 8) {
+        float4 v[8][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (lane + 32 * e < d) acc[e] = fmaf(wj, o[lane + 32 * e], acc[e]);
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            v[j][h] = j0 + j < most && lane * 4 + 128 * h < d ? o[(j0 + j) * (R * d / 4) + 32 * h] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float wj = __shfl_sync(0xffffffffu, w[k], j0 + j);
+          sum = fmaf(wj, __shfl_sync(0xffffffffu, ml[k].y, j0 + j), sum);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            acc[h].x = fmaf(wj, v[j][h].x, acc[h].x), acc[h].y = fmaf(wj, v[j][h].y, acc[h].y);
+            acc[h].z = fmaf(wj, v[j][h].z, acc[h].z), acc[h].w = fmaf(wj, v[j][h].w, acc[h].w);
+          }
+        }
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (lane + 32 * e < d) put1<T>(p.o, rh * d + lane + 32 * e, sum == 0.f ? 0.f : acc[e] / sum);
+    for (int h = 0; h < 2; ++h)
+      if (lane * 4 + 128 * h < d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put1<T>(p.o, rh * d + lane * 4 + 128 * h + e, sum == 0.f ? 0.f : (&acc[h].x)[e] / sum);
     if (p.lse && lane == 0) p.lse[rh] = sum == 0.f ? -INFINITY : mx * 0.693147180559945309f + logf(sum);
   }
 }
