@@ -4,7 +4,11 @@
 // S = Q K^T and O += P V are tcgen05 products of 128 query rows (row i of a
 // tile: token i / G, head i % G of the group, so that the group shares the
 // keys) with 128 keys, accumulated in tensor memory.  The softmax runs between
-// them with the running maximum and sum of a row held in one thread.
+// them with a row in one thread.  Two warpgroups of it share the products'
+// unit: up to d = 128 each has a row tile of its own; at d = 256, where the
+// outputs of one take half of tensor memory, they take that tile's key tiles in
+// turn, the running maximum passing from one to the other before the
+// exponentials, so that those of two key tiles overlap.
 #include <cuda.h>
 
 #include "attn.h"
@@ -28,14 +32,15 @@ struct PreCfg {
   static constexpr int STAGES = D == 64 ? 8 : 5;
   static constexpr uint32_t Q_BYTES = kTile * D * 2;
   static constexpr uint32_t DATA = NQ * Q_BYTES + STAGES * UNIT;
-  static constexpr int THREADS = NQ * 128 + 128;
+  static constexpr int THREADS = 384;                    // two softmax warpgroups; loads, products, guards
   // tensor memory columns: scores (the weights overwrite them), then outputs
   static constexpr uint32_t S0 = 0, O0 = 256;
   // registers: a softmax thread holds a row's 128 scores
 };
 
 struct PreShared {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], drain;
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], m_ready[2], fin[2], drain;
+  float m[2][kTile];   // d = 256: a warpgroup's reference of each row, its sum at the end
   uint32_t tmem;
   int fail, bad_any;
   // first key, counted from the first guarded tile's, with NaN, +inf, -inf in
@@ -43,7 +48,7 @@ struct PreShared {
   uint16_t bad[3][256];
 };
 template <int D>
-constexpr uint32_t kPreSmem = PreCfg<D>::DATA + sizeof(PreShared) + 1024;   // 1,024 to align the tiles
+constexpr uint32_t kPreSmem = PreCfg<D>::DATA + sizeof(PreShared);
 static_assert(kPreSmem<256> <= 232448 && kPreSmem<128> <= 232448, "227 KB a CTA");
 
 // Minimum of a 16-bit word in shared memory.
@@ -154,10 +159,15 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     attn_prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap) {
   using C = PreCfg<D>;
-  extern __shared__ uint8_t dyn[];
+  extern __shared__ __align__(1024) uint8_t base[];
   PreTile t;
   if (!pre_tile<D>(p, t, threadIdx.x == 0)) return;
-  uint8_t* base = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  // the swizzled tiles need the 1,024-byte alignment that shared memory without
+  // static variables starts with: there is no room to make it up
+  if (smem_u32(base) & 1023u) {
+    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_CUDA);
+    return;
+  }
   uint8_t* sq = base;
   uint8_t* ring = base + C::NQ * C::Q_BYTES;
   PreShared& sh = *reinterpret_cast<PreShared*>(base + C::DATA);
@@ -170,9 +180,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       tc::mbar_init(&sh.s_full[i], 1);
       tc::mbar_init(&sh.p_full[i], 128);
       tc::mbar_init(&sh.o_done[i], 1);
-      tc::mbar_init(&sh.q_full[i], 128);
+      tc::mbar_init(&sh.q_full[i], C::NQ == 1 ? 256 : 128);
+      tc::mbar_init(&sh.m_ready[i], 128);
     }
     for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], 64);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.fin[i], 128);
     tc::mbar_init(&sh.drain, 1);
     sh.fail = 0, sh.bad_any = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -190,9 +202,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
   int issued = 0, raw = 0;   // units loaded, those of them for the guards first (the loading thread's)
   uint32_t raw_bits = 0;     // which of the last 32 went to the guards
 
-  if (wg < C::NQ) {
-    // ---- softmax of row tile wg: one thread a row ----
-    const int q = wg, i = threadIdx.x & 127;
+  if (wg < 2) {
+    // ---- softmax: one thread a row, of row tile wg, or (d = 256) of every second key tile ----
+    constexpr bool ALT = C::SLOTS == 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+    const int q = ALT ? 0 : wg, i = threadIdx.x & 127;
     const int nk = t.nk[q];
     const int64_t rbase = t.r0 + q * kTile, r = rbase + i;
     const int tok = (int)(r / p.G), g = (int)(r - (int64_t)tok * p.G);
@@ -203,7 +217,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q);
     if (nk > 0) {
       constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a row, rows a warp loads at once
-      for (int rr = (warp & 3) * 32 + lane / CH; rr < (warp & 3) * 32 + 32; rr += RP) {
+      constexpr int WR = ALT ? 16 : 32;         // rows a warp loads
+      const int w0 = (ALT ? warp : warp & 3) * WR;
+      for (int rr = w0 + lane / CH; rr < w0 + WR; rr += RP) {
         const int64_t r2 = rbase + rr, tk = r2 / p.G;
         const int c = lane % CH;
         uint4 w = make_uint4(0, 0, 0, 0);
@@ -227,8 +243,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wlim = min(wlim, __shfl_xor_sync(0xffffffffu, wlim, o));
     bool ok = true;
-    for (int j = 0; j < nk; ++j) {
-      const int b = C::SLOTS == 2 ? (j & 1) : q;
+    for (int j = ALT ? wg : 0; j < nk; j += ALT ? 2 : 1) {
+      const int b = wg;
       const uint32_t par = C::SLOTS == 2 ? (uint32_t)(j >> 1) & 1 : (uint32_t)j & 1;
       ok = pre_wait(&sh.s_full[b], par, limit, fail);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -258,14 +274,24 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       // 2^8: weights stay below 2^8, and a row's choice depends on that row alone
       float alpha = 1.f;
       bool grow = false;
+      const float before = m;
+      if (ALT && j > 0) {   // the reference after the tile before, the other warpgroup's
+        ok = pre_wait(&sh.m_ready[wg ^ 1], (uint32_t)((j - 1) >> 1) & 1, limit, fail);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        m = sh.m[wg ^ 1][i];
+      }
       if (j == 0) {
         m = mt;
       } else if ((mt - m) * c > 8.f) {
         alpha = ex2((m - mt) * c);
         m = mt;
-        l *= alpha;
         grow = true;
       }
+      if (ALT) {
+        sh.m[wg][i] = m;
+        mbar_arrive(&sh.m_ready[wg]);
+      }
+      if (j > (ALT ? 1 : 0) && m != before) l *= ex2((before - m) * c);
       if (__any_sync(0xffffffffu, grow)) {
         // O of the tiles before: wait for their products, scale this warp's rows
         ok = o_wait(j - 1);
@@ -304,6 +330,27 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       mbar_arrive(&sh.p_full[b]);
     }
     // ---- outputs ----
+    if (ALT && nk > 0) {
+      // the row's sum: the warpgroup that had the last tile takes the other's,
+      // brought to its reference, and hands the total back; each then writes
+      // half of the row
+      const int last = (nk - 1) & 1;
+      if (!ok) *fail = 1;
+      if (wg != last) {
+        ok = pre_wait(&sh.m_ready[last], (uint32_t)((nk - 1) >> 1) & 1, limit, fail) && ok;
+        const float mine = m;
+        m = sh.m[last][i];
+        sh.m[wg][i] = l == 0.f ? 0.f : l * ex2((mine - m) * c);
+        mbar_arrive(&sh.fin[0]);
+        ok = pre_wait(&sh.fin[1], 0, limit, fail) && ok;
+        l = sh.m[last][i];
+      } else {
+        ok = pre_wait(&sh.fin[0], 0, limit, fail) && ok;
+        l += sh.m[wg ^ 1][i];
+        sh.m[wg][i] = l;
+        mbar_arrive(&sh.fin[1]);
+      }
+    }
     if (ok && nk > 0) ok = o_wait(nk - 1);
     if (__all_sync(0xffffffffu, ok)) {
       tc::fence_after_sync();
@@ -311,7 +358,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       const bool bad = nk > 0 && *(volatile int*)&sh.bad_any;
       __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.o) + row_off * D;
 #pragma unroll 1
-      for (int e = 0; e < D; e += 32) {
+      for (int e = ALT ? wg * (D / 2) : 0; e < (ALT ? (wg + 1) * (D / 2) : D); e += 32) {
         float o[32];
         if (nk > 0) {
           tc::tmem_ld32(lanes + C::O0 + (uint32_t)q * D + e, o);
@@ -344,9 +391,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           }
         }
       }
-      if (valid && p.lse) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
+      if (valid && p.lse && (!ALT || wg == 0)) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
     }
-  } else if (warp == C::NQ * 4 && lane == 0) {
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+  if (warp == 8 && lane == 0) {
     // ---- loads ----
     // a V tile that some row sees in part arrives on the guards' barriers, who
     // hand it on; they follow within the ring, so 8 barriers never alias
@@ -369,7 +418,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     constexpr int ahead = C::NQ == 1 ? 2 : 1;
     for (int j = 0; ok && j < t.nkmax; ++j) 
       ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + ahead >= t.nkmax || tile(&kmap, j + ahead, false));
-  } else if (warp == C::NQ * 4 + 1 && lane == 0) {
+  } else if (warp == 9 && lane == 0) {
     // ---- products ----
     const uint32_t ring0 = smem_u32(ring), sq0 = smem_u32(sq);
     constexpr uint32_t id_qk = tc::idesc_bf16_f32(kTile, kTile);
@@ -464,12 +513,12 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     // every product issued, and every arrival on a barrier, before the end
     tc::mma_commit(&sh.drain);
     if (!tc::mbar_wait_bounded(&sh.drain, 0, kPreWait)) *fail = 1;
-  } else if (warp >= C::NQ * 4 + 2) {
+  } else if (warp >= 10) {
     // ---- guards: in V tiles that some row sees in part, keys past the
     // sequence become zero and so do NaN and infinities, which a weight of 0
     // would not keep out of the product; where those were is noted by element
     // for the rows that do see them ----
-    const int me = threadIdx.x - (C::NQ * 4 + 2) * 32;   // 0 .. 63
+    const int me = threadIdx.x - 320;   // 0 .. 63
     bool ok = true;
     int done = 0;
     for (int j = t.least / kTile; ok && j < t.nkmax; ++j) {
@@ -510,6 +559,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       }
     }
   }
+  }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
@@ -517,7 +567,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
-    if (warp == C::NQ * 4 && lane == 0)
+    if (warp == 8 && lane == 0)
     {
       for (int n = issued - 1, k = raw - 1; n >= 0 && n >= issued - C::STAGES; --n, raw_bits >>= 1) {
         if (raw_bits & 1) {
