@@ -64,12 +64,7 @@ __device__ __forceinline__ void min16(uint16_t* at, uint32_t v) {
 }
 
 // Waits for a phase: bounded, and given up at once when another role has.
-__device__ __forceinline__ bool pre_wait(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
-  if (limit < 0) {
-    *fail = 1;
-    return false;
-  }
-  if (tc::mbar_test_wait(m, parity)) return true;
+__device__ __forceinline__ bool pre_wait_slow(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
   const long long t0 = clock64();
   while (!tc::mbar_try_wait(m, parity)) {
     if (*fail) return false;
@@ -79,6 +74,10 @@ __device__ __forceinline__ bool pre_wait(uint64_t* m, uint32_t parity, long long
     }
   }
   return true;
+}
+__device__ __forceinline__ bool pre_wait(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
+  if (tc::mbar_test_wait(m, parity)) return true;
+  return pre_wait_slow(m, parity, limit, fail);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], 64);
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.fin[i], 128);
     tc::mbar_init(&sh.drain, 1);
-    sh.fail = 0, sh.bad_any = 0;
+    sh.fail = limit < 0, sh.bad_any = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   for (int i = threadIdx.x; i < 3 * 256; i += C::THREADS) (&sh.bad[0][0])[i] = 0xffff;
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     const int64_t row_off = ((int64_t)(t.q0 + tok) * p.Hq + t.h * p.G + g);
     const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21);   // this warp's 32 lanes
     const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q);
-    if (nk > 0) {
+    if (nk > 0 && limit >= 0) {
       constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a row, rows a warp loads at once
       constexpr int WR = ALT ? 16 : 32;         // rows a warp loads
       const int w0 = (ALT ? warp : warp & 3) * WR;
@@ -242,8 +241,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     int wlim = valid ? lim : 0x7fffffff;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wlim = min(wlim, __shfl_xor_sync(0xffffffffu, wlim, o));
-    bool ok = true;
-    for (int j = ALT ? wg : 0; j < nk; j += ALT ? 2 : 1) {
+    bool ok = nk == 0 || limit >= 0;
+    for (int j = ALT ? wg : 0; ok && j < nk; j += ALT ? 2 : 1) {
       const int b = wg;
       const uint32_t par = C::SLOTS == 2 ? (uint32_t)(j >> 1) & 1 : (uint32_t)j & 1;
       ok = pre_wait(&sh.s_full[b], par, limit, fail);
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       mbar_arrive(&sh.p_full[b]);
     }
     // ---- outputs ----
-    if (ALT && nk > 0) {
+    if (ALT && nk > 0 && limit >= 0) {
       // the row's sum: the warpgroup that had the last tile takes the other's,
       // brought to its reference, and hands the total back; each then writes
       // half of the row
@@ -356,12 +355,17 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       tc::fence_after_sync();
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool bad = nk > 0 && *(volatile int*)&sh.bad_any;
-      __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.o) + row_off * D;
+      // Rows leave through shared memory (this tile's Q, which every product has
+      // read), so that a warp writes whole rows: 16-byte chunk ch of row i at
+      // place ch ^ (i % CH) of the row.
+      constexpr int W = ALT ? D / 2 : D, CH = W / 8, RP = 32 / CH;   // elements of a row here, its chunks, rows a pass
+      const int e0 = ALT ? wg * W : 0;
+      uint8_t* so = sq + (ALT ? wg : q) * (kTile * W * 2) + (warp & 3) * 32 * (W * 2);
 #pragma unroll 1
-      for (int e = ALT ? wg * (D / 2) : 0; e < (ALT ? (wg + 1) * (D / 2) : D); e += 32) {
+      for (int e = 0; e < W; e += 32) {
         float o[32];
         if (nk > 0) {
-          tc::tmem_ld32(lanes + C::O0 + (uint32_t)q * D + e, o);
+          tc::tmem_ld32(lanes + C::O0 + (uint32_t)q * D + e0 + e, o);
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
@@ -369,27 +373,36 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
         if (bad) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const int mine = lim - t.least / kTile * kTile;
-            const bool hi = sh.bad[1][e + k] < mine, lo = sh.bad[2][e + k] < mine;
+            const int mine = lim - t.least / kTile * kTile, at = e0 + e + k;
+            const bool hi = sh.bad[1][at] < mine, lo = sh.bad[2][at] < mine;
             if (hi) o[k] = INFINITY;
             if (lo) o[k] = -INFINITY;
-            if (sh.bad[0][e + k] < mine || (hi && lo)) o[k] = __int_as_float(0x7fffffff);
+            if (sh.bad[0][at] < mine || (hi && lo)) o[k] = __int_as_float(0x7fffffff);
           }
         }
-        if (valid) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            uint32_t w[4];
+        for (int k = 0; k < 32; k += 8) {
+          uint32_t w[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              // a row that sees no key is 0, whatever its lanes of O hold
-              const __nv_bfloat162 h2 = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
-                                                 : __floats2bfloat162_rn(o[k + 2 * u] * inv, o[k + 2 * u + 1] * inv);
-              w[u] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            *reinterpret_cast<uint4*>(og + e + k) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int u = 0; u < 4; ++u) {
+            // a row that sees no key is 0, whatever its lanes of O hold
+            const __nv_bfloat162 h2 = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
+                                               : __floats2bfloat162_rn(o[k + 2 * u] * inv, o[k + 2 * u + 1] * inv);
+            w[u] = *reinterpret_cast<const uint32_t*>(&h2);
           }
+          *reinterpret_cast<uint4*>(so + lane * (W * 2) + ((((e + k) >> 3) ^ (lane & (CH - 1))) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+      __syncwarp();
+      const int64_t mine = valid ? row_off : -1;
+      __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.o) + e0 + (lane % CH) * 8;
+#pragma unroll 4
+      for (int r0 = 0; r0 < 32; r0 += RP) {
+        const int rr = r0 + lane / CH;
+        const int64_t at = __shfl_sync(0xffffffffu, mine, rr);
+        if (at >= 0)
+          *reinterpret_cast<uint4*>(og + at * D) =
+              *reinterpret_cast<const uint4*>(so + rr * (W * 2) + (((lane % CH) ^ (rr & (CH - 1))) << 4));
       }
       if (valid && p.lse && (!ALT || wg == 0)) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
     }
@@ -418,102 +431,129 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     constexpr int ahead = C::NQ == 1 ? 2 : 1;
     for (int j = 0; ok && j < t.nkmax; ++j) 
       ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + ahead >= t.nkmax || tile(&kmap, j + ahead, false));
-  } else if (warp == 9 && lane == 0) {
-    // ---- products ----
-    const uint32_t ring0 = smem_u32(ring), sq0 = smem_u32(sq);
+  } else if (warp == 9 && limit >= 0) {
+    // ---- products: the whole warp, one lane issues ----
+    const uint32_t lead = tc::elect_one();
     constexpr uint32_t id_qk = tc::idesc_bf16_f32(kTile, kTile);
     constexpr uint32_t id_pv = tc::idesc_bf16_f32(kTile, C::UD) | kTransposedB;
-    int it = 0, guarded = 0;
+    const uint64_t qdesc = tc::desc_sw128(smem_u32(sq)), kdesc = tc::desc_sw128(smem_u32(ring)), vdesc = desc_v(smem_u32(ring));
+    int st = 0, guarded = 0;   // the ring's place that is taken next
+    uint32_t ph = 0;
     bool ok = true;
-    auto full = [&](int n) { return pre_wait(&sh.full[n % C::STAGES], (uint32_t)(n / C::STAGES) & 1, limit, fail); };
-    auto qk_unit = [&](int q, uint32_t scol, int n, int u) {
-      const uint64_t a = tc::desc_sw128(sq0 + q * C::Q_BYTES + u * (C::UD / 64) * (kTile * 128));
-      const uint64_t b = tc::desc_sw128(ring0 + (n % C::STAGES) * C::UNIT);
+    auto step = [&](int& s, uint32_t& p) {
+      if (++s == C::STAGES) s = 0, p ^= 1;
+    };
+    auto qk_unit = [&](int q, uint32_t scol, int s, int u) {
+      const uint64_t a = qdesc + ((q * C::Q_BYTES + u * (C::UD / 64) * (kTile * 128)) >> 4), b = kdesc + (s * C::UNIT >> 4);
 #pragma unroll
       for (int ks = 0; ks < C::UD / 16; ++ks) {
         const uint64_t off = ((uint32_t)(ks >> 2) * (kTile * 128) + (uint32_t)(ks & 3) * 32u) >> 4;
-        tc::mma_bf16(tb + scol, a + off, b + off, id_qk, u != 0 || ks != 0);
+        tc::mma_bf16_if(lead, tb + scol, a + off, b + off, id_qk, u != 0 || ks != 0);
       }
     };
-    auto pv_unit = [&](int q, uint32_t pcol, int n, int u, bool acc) {
-      const uint64_t b = desc_v(ring0 + (n % C::STAGES) * C::UNIT);
+    auto pv_unit = [&](int q, uint32_t pcol, int s, int u, bool acc) {
+      const uint64_t b = vdesc + (s * C::UNIT >> 4);
 #pragma unroll
       for (int ks = 0; ks < kTile / 16; ++ks)
-        tc::mma_bf16_ts(tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv, acc || ks != 0);
+        tc::mma_bf16_ts_if(lead, tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv,
+                           acc || ks != 0);
     };
+    auto full = [&](int s, uint32_t p) { return pre_wait(&sh.full[s], p, limit, fail); };
     // a guarded V unit: from the guards, and its place's phase moves on here
-    auto v_ready = [&](int n, int j) {
-      if ((j + 1) * kTile <= t.least) return full(n);
+    auto v_ready = [&](int s, uint32_t p, int j) {
+      if ((j + 1) * kTile <= t.least) return full(s, p);
       const int k = guarded++;
       if (!pre_wait(&sh.v_ok[k & 7], (uint32_t)(k >> 3) & 1, limit, fail)) return false;
-      mbar_arrive(&sh.full[n % C::STAGES]);
+      if (lead) mbar_arrive(&sh.full[s]);
+      __syncwarp();
       return true;
     };
+    // ok is the same in every lane: after each wait the warp agrees
+    auto all = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     if constexpr (C::NQ == 1) {
-      ok = t.nkmax == 0 || pre_wait(&sh.q_full[0], 0, limit, fail);
+      static_assert(C::U == 2, "two units a key tile");
+      ok = t.nkmax == 0 || all(pre_wait(&sh.q_full[0], 0, limit, fail));
       auto qk = [&](int j) {
-        for (int u = 0; u < C::U; ++u, ++it) {
-          if (!full(it)) return false;
-          tc::fence_after_sync();
-          qk_unit(0, C::S0 + (j & 1) * 128, it, u);
-          tc::mma_commit(&sh.empty[it % C::STAGES]);
-        }
-        tc::mma_commit(&sh.s_full[j & 1]);
+        int s1 = st;
+        uint32_t p1 = ph;
+        step(s1, p1);
+        if (!all(full(st, ph) && full(s1, p1))) return false;
+        tc::fence_after_sync();
+        qk_unit(0, C::S0 + (j & 1) * 128, st, 0);
+        tc::mma_commit_if(lead, &sh.empty[st]);
+        qk_unit(0, C::S0 + (j & 1) * 128, s1, 1);
+        tc::mma_commit_if(lead, &sh.empty[s1]);
+        tc::mma_commit_if(lead, &sh.s_full[j & 1]);
+        st = s1, ph = p1;
+        step(st, ph);
         return true;
       };
       auto pv = [&](int j) {
-        if (!pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)) return false;
-        for (int u = 0; u < C::U; ++u, ++it) {
-          if (!v_ready(it, j)) return false;
-          tc::fence_after_sync();
-          pv_unit(0, C::S0 + (j & 1) * 128, it, u, j != 0);
-          tc::mma_commit(&sh.empty[it % C::STAGES]);
-        }
-        tc::mma_commit(&sh.o_done[j & 1]);
+        int s1 = st;
+        uint32_t p1 = ph;
+        step(s1, p1);
+        if (!all(v_ready(st, ph, j) && pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail))) return false;
+        tc::fence_after_sync();
+        pv_unit(0, C::S0 + (j & 1) * 128, st, 0, j != 0);
+        tc::mma_commit_if(lead, &sh.empty[st]);
+        if (!all(v_ready(s1, p1, j))) return false;
+        tc::fence_after_sync();
+        pv_unit(0, C::S0 + (j & 1) * 128, s1, 1, j != 0);
+        tc::mma_commit_if(lead, &sh.empty[s1]);
+        tc::mma_commit_if(lead, &sh.o_done[j & 1]);
+        st = s1, ph = p1;
+        step(st, ph);
         return true;
       };
       if (ok && t.nkmax > 0) ok = qk(0);
       if (ok && t.nkmax > 1) ok = qk(1);
       for (int j = 0; ok && j < t.nkmax; ++j) ok = pv(j) && (j + 2 >= t.nkmax || qk(j + 2));
     } else {
-      for (int q = 0; ok && q < 2; ++q) ok = t.nk[q] == 0 || pre_wait(&sh.q_full[q], 0, limit, fail);
+      for (int q = 0; ok && q < 2; ++q) ok = t.nk[q] == 0 || all(pre_wait(&sh.q_full[q], 0, limit, fail));
       if (ok && t.nkmax > 0) {
-        ok = full(0);
+        ok = all(full(0, 0));
         if (ok) {
           tc::fence_after_sync();
           for (int q = 0; q < 2; ++q)
             if (t.nk[q] > 0) {
               qk_unit(q, C::S0 + q * 128, 0, 0);
-              tc::mma_commit(&sh.s_full[q]);
+              tc::mma_commit_if(lead, &sh.s_full[q]);
             }
-          tc::mma_commit(&sh.empty[0]);
+          tc::mma_commit_if(lead, &sh.empty[0]);
         }
+        step(st, ph);
       }
       for (int j = 0; ok && j < t.nkmax; ++j) {
-        const int nv = 1 + 2 * j, nkk = nv + 1;
+        int s1 = st;
+        uint32_t p1 = ph;
+        step(s1, p1);
         const bool more = j + 1 < t.nkmax;
-        ok = v_ready(nv, j) && (!more || full(nkk));
+        ok = all(v_ready(st, ph, j) && (!more || full(s1, p1)));
         for (int q = 0; ok && q < 2; ++q) {
           if (j >= t.nk[q]) continue;
-          ok = pre_wait(&sh.p_full[q], (uint32_t)j & 1, limit, fail);
+          ok = all(pre_wait(&sh.p_full[q], (uint32_t)j & 1, limit, fail));
           if (!ok) break;
           tc::fence_after_sync();
-          pv_unit(q, C::S0 + q * 128, nv, 0, j != 0);
-          tc::mma_commit(&sh.o_done[q]);
+          pv_unit(q, C::S0 + q * 128, st, 0, j != 0);
+          tc::mma_commit_if(lead, &sh.o_done[q]);
           if (j + 1 < t.nk[q]) {
-            qk_unit(q, C::S0 + q * 128, nkk, 0);
-            tc::mma_commit(&sh.s_full[q]);
+            qk_unit(q, C::S0 + q * 128, s1, 0);
+            tc::mma_commit_if(lead, &sh.s_full[q]);
           }
         }
         if (!ok) break;
-        tc::mma_commit(&sh.empty[nv % C::STAGES]);
-        if (more) tc::mma_commit(&sh.empty[nkk % C::STAGES]);
+        tc::mma_commit_if(lead, &sh.empty[st]);
+        if (more) {
+          tc::mma_commit_if(lead, &sh.empty[s1]);
+          step(st, ph);
+        }
+        step(st, ph);
       }
     }
     // every product issued, and every arrival on a barrier, before the end
-    tc::mma_commit(&sh.drain);
+    tc::mma_commit_if(lead, &sh.drain);
     if (!tc::mbar_wait_bounded(&sh.drain, 0, kPreWait)) *fail = 1;
-  } else if (warp >= 10) {
+  } else if (warp >= 10 && limit >= 0) {
     // ---- guards: in V tiles that some row sees in part, keys past the
     // sequence become zero and so do NaN and infinities, which a weight of 0
     // would not keep out of the product; where those were is noted by element
@@ -531,27 +571,31 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
         if (!ok) break;
         ++done;
         uint8_t* v = ring + (n % C::STAGES) * C::UNIT;
-        for (int x = me; x < (int)C::UNIT / 16; x += 64) {
-          const int blk = x / (kTile * 8), rest = x % (kTile * 8), row = rest >> 3, ch = rest & 7;
-          uint4* at = reinterpret_cast<uint4*>(v + x * 16);
-          const int key = j * kTile + row;
-          if (key >= t.L) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-          }
-          uint4 w = *at;
-          const uint32_t e = 0x7f807f80u, one = 0x00800080u;
-          const uint32_t hit = (((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one)) & 0x80008000u;
-          if (hit) {
-            const int col = u * C::UD + blk * 64 + ((ch ^ (row & 7)) << 3);
-            for (int k = 0; k < 8; ++k) {
-              uint16_t* el = reinterpret_cast<uint16_t*>(at) + k;
-              const uint16_t b = *el;
-              if ((b & 0x7f80u) != 0x7f80u) continue;
-              min16(&sh.bad[(b & 0x7f) ? 0 : (b & 0x8000u) ? 2 : 1][col + k], key - t.least / kTile * kTile);
-              *el = 0;
+        // 16-byte chunks x = me + 64 k: block x / 1024, key x / 8 % 128, eight at a time
+        for (int x0 = me; x0 < (int)C::UNIT / 16; x0 += 512) {
+          uint4 w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const uint4*>(v + (x0 + 64 * k) * 16);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int x = x0 + 64 * k, row = x >> 3 & (kTile - 1), key = j * kTile + row;
+            uint4* at = reinterpret_cast<uint4*>(v + x * 16);
+            if (key >= t.L) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
             }
-            *(volatile int*)&sh.bad_any = 1;
+            const uint32_t e = 0x7f807f80u, one = 0x00800080u;
+            if ((((w[k].x & e) + one) | ((w[k].y & e) + one) | ((w[k].z & e) + one) | ((w[k].w & e) + one)) & 0x80008000u) {
+              const int col = u * C::UD + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
+              for (int i = 0; i < 8; ++i) {
+                uint16_t* el = reinterpret_cast<uint16_t*>(at) + i;
+                const uint16_t b = *el;
+                if ((b & 0x7f80u) != 0x7f80u) continue;
+                min16(&sh.bad[(b & 0x7f) ? 0 : (b & 0x8000u) ? 2 : 1][col + i], key - t.least / kTile * kTile);
+                *el = 0;
+              }
+              *(volatile int*)&sh.bad_any = 1;
+            }
           }
         }
         tc::fence_async_smem();
