@@ -69,12 +69,13 @@ __device__ __forceinline__ float dt_ex2(float x) {
   return y;
 }
 
-// e4m3 x e4m3 -> fp32: D[tmem] (+)= A[smem] B[smem]^T, 32 deep.
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// e4m3 x e4m3 -> fp32: D[tmem] (+)= A[smem] B[smem]^T, 32 deep; a whole warp
+// runs it, the lane with `lead` issues (tc::elect_one).
+__device__ __forceinline__ void mma_e4m3(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 // Instruction descriptor: e4m3 A and B (both K-contiguous), fp32 sums, M = 128.
@@ -172,12 +173,12 @@ __device__ __forceinline__ void dt_next(const DtParams& w, const int* items, int
 }
 
 // One product's steps: KS of 32 elements, the operands' starts moving by a
-// step's tiles (constants, so that the issuing thread spends an add or two a
-// step: with run-time steps it takes 130 cycles a product, which takes 51 to 60).
+// step's tiles (constants: with run-time steps the issue takes 130 cycles a
+// product, which takes 41 at 16 columns and 67 at 128).
 template <int KS>
-__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint64_t astep, uint64_t bstep, bool acc) {
+__device__ __forceinline__ void mma_steps(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint64_t astep, uint64_t bstep, bool acc) {
 #pragma unroll
-  for (int c = 0; c < KS; ++c) mma_e4m3(d, a + c * astep, b + c * bstep, id, acc || c != 0);
+  for (int c = 0; c < KS; ++c) mma_e4m3(lead, d, a + c * astep, b + c * bstep, id, acc || c != 0);
 }
 // Largest value of a warp (NaN falls out).
 __device__ __forceinline__ float warp_max(float x) {

@@ -28,11 +28,11 @@ struct DrShared : DtBase {
 };
 
 // D[tmem] (+)= A[tmem] B[smem]^T, e4m3, 32 deep: eight columns of A hold four codes each.
-__device__ __forceinline__ void mma_e4m3_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_e4m3_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 
@@ -76,8 +76,10 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     // ---- loads, a warp for K and one for V ----
     loaded = dt_load<NT>(w, sh, base, i0, i1, warp == 5, lane);
   } else if (warp == 6) {
-    // ---- products ----
-    if (lane == 0) {
+    // ---- products: the whole warp, one lane issues ----
+    {
+      const uint32_t lead = tc::elect_one();
+      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
       constexpr uint32_t id_qk = idesc_e4m3(kDtTok);
       const uint32_t id_pv = idesc_e4m3(d);
       const uint32_t k0 = smem_u32(base + w.k_off), v0 = smem_u32(base + w.v_off), qa = smem_u32(base + w.q_off);
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       unsigned T = 0;   // tiles multiplied
       bool ok = true;
       auto qk = [&](unsigned tt) {
-        if (!dt_wait(&sh.k_full[ks], kp, fail)) return false;
+        if (!all(dt_wait(&sh.k_full[ks], kp, fail))) return false;
         tc::fence_after_sync();
         const uint64_t b = desc_tiles(k0 + ks * unit, 128, rows8);
         const uint32_t dst = tb + (tt & 1) * kDtTok;
@@ -95,15 +97,15 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         for (int part = 0; part < 2; ++part) {
           const uint64_t a = desc_tiles(qa + part * kDrRows * d, 128, rows8);
           if (d == 256) {
-            mma_steps<8>(dst, a, b, id_qk, 16, 16, part);
+            mma_steps<8>(lead, dst, a, b, id_qk, 16, 16, part);
           } else if (d == 128) {
-            mma_steps<4>(dst, a, b, id_qk, 16, 16, part);
+            mma_steps<4>(lead, dst, a, b, id_qk, 16, 16, part);
           } else {
-            for (int c = 0; c < d / 32; ++c) mma_e4m3(dst, a + c * 16, b + c * 16, id_qk, part | c);
+            for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id_qk, part | c);
           }
         }
-        tc::mma_commit(&sh.k_empty[ks]);
-        tc::mma_commit(&sh.s_full[tt & 1]);
+        tc::mma_commit_if(lead, &sh.k_empty[ks]);
+        tc::mma_commit_if(lead, &sh.s_full[tt & 1]);
         if (++ks == KS) ks = 0, kp ^= 1;
         return true;
       };
@@ -111,11 +113,11 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       for (int i = i0; ok && i < i1; ++i) {
         if (i == i0) t = dt_item<NT>(w, sh.items, i);
         else dt_next<NT>(w, sh.items, i, t);
-        if (dt_new_rows(t, i == i0)) ok = dt_wait(&sh.q_full, rows++ & 1, fail);
+        if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail));
         if (ok && t.tiles > 0) ok = qk(T);
         for (int j = 0; ok && j < t.tiles; ++j, ++T) {
           if (j + 1 < t.tiles) ok = qk(T + 1);
-          ok = ok && dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail);
+          ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail));
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t b = desc_tiles(v0 + vs * unit, 16u * d, 128);
@@ -123,14 +125,14 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int c = 0; c < kDtTok / 32; ++c)
-              mma_e4m3_ts(tb + kDrO, tb + (T & 1) * kDtTok + part * 32 + c * 8, b + c * vstep, id_pv, j | part | c);
-          tc::mma_commit(&sh.v_empty[vs]);
-          tc::mma_commit(&sh.o_done[T & 1]);
+              mma_e4m3_ts(lead, tb + kDrO, tb + (T & 1) * kDtTok + part * 32 + c * 8, b + c * vstep, id_pv, j | part | c);
+          tc::mma_commit_if(lead, &sh.v_empty[vs]);
+          tc::mma_commit_if(lead, &sh.o_done[T & 1]);
           if (++vs == VS) vs = 0, vp ^= 1;
         }
       }
       // every product issued, and every arrival on a barrier, before the end
-      tc::mma_commit(&sh.drain);
+      tc::mma_commit_if(lead, &sh.drain);
       if (!tc::mbar_wait_bounded(&sh.drain, 0, kDtWait)) *fail = 1;
     }
   } else {

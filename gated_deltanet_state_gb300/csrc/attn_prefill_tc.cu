@@ -88,6 +88,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Largest of three (NaN falls out).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
   f32x2 d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -267,8 +273,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[u][k]));
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int k = 0; k < 32; k += 2)
+          mx[k >> 1 & 3] = max3(mx[k >> 1 & 3], __uint_as_float(s[u][k]), __uint_as_float(s[u][k + 1]));
+      const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       // the reference of the weights moves only when the maximum has grown by
       // 2^8: weights stay below 2^8, and a row's choice depends on that row alone
       float alpha = 1.f;
@@ -473,36 +480,30 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     if constexpr (C::NQ == 1) {
       static_assert(C::U == 2, "two units a key tile");
       ok = t.nkmax == 0 || all(pre_wait(&sh.q_full[0], 0, limit, fail));
+      // a wait for each unit of 32 KB: the ring holds five, so the next one is
+      // often still on its way
       auto qk = [&](int j) {
-        int s1 = st;
-        uint32_t p1 = ph;
-        step(s1, p1);
-        if (!all(full(st, ph) && full(s1, p1))) return false;
-        tc::fence_after_sync();
-        qk_unit(0, C::S0 + (j & 1) * 128, st, 0);
-        tc::mma_commit_if(lead, &sh.empty[st]);
-        qk_unit(0, C::S0 + (j & 1) * 128, s1, 1);
-        tc::mma_commit_if(lead, &sh.empty[s1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (!all(full(st, ph))) return false;
+          tc::fence_after_sync();
+          qk_unit(0, C::S0 + (j & 1) * 128, st, u);
+          tc::mma_commit_if(lead, &sh.empty[st]);
+          step(st, ph);
+        }
         tc::mma_commit_if(lead, &sh.s_full[j & 1]);
-        st = s1, ph = p1;
-        step(st, ph);
         return true;
       };
       auto pv = [&](int j) {
-        int s1 = st;
-        uint32_t p1 = ph;
-        step(s1, p1);
-        if (!all(v_ready(st, ph, j) && pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail))) return false;
-        tc::fence_after_sync();
-        pv_unit(0, C::S0 + (j & 1) * 128, st, 0, j != 0);
-        tc::mma_commit_if(lead, &sh.empty[st]);
-        if (!all(v_ready(s1, p1, j))) return false;
-        tc::fence_after_sync();
-        pv_unit(0, C::S0 + (j & 1) * 128, s1, 1, j != 0);
-        tc::mma_commit_if(lead, &sh.empty[s1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (!all((u || pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)) && v_ready(st, ph, j))) return false;
+          tc::fence_after_sync();
+          pv_unit(0, C::S0 + (j & 1) * 128, st, u, j != 0);
+          tc::mma_commit_if(lead, &sh.empty[st]);
+          step(st, ph);
+        }
         tc::mma_commit_if(lead, &sh.o_done[j & 1]);
-        st = s1, ph = p1;
-        step(st, ph);
         return true;
       };
       if (ok && t.nkmax > 0) ok = qk(0);
@@ -571,32 +572,34 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
         if (!ok) break;
         ++done;
         uint8_t* v = ring + (n % C::STAGES) * C::UNIT;
-        // 16-byte chunks x = me + 64 k: block x / 1024, key x / 8 % 128, eight at a time
+        // 16-byte chunks x = me + 64 k: block x / 1024, key x / 8 % 128
+        const int left = t.L - j * kTile;   // keys of the tile in the sequence
+        if (left < kTile)
+          for (int x = me; x < (int)C::UNIT / 16; x += 64)
+            if ((x >> 3 & (kTile - 1)) >= left) *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
+        // eight chunks at a time: 0 times an infinity or NaN is NaN, and so is a sum with it
         for (int x0 = me; x0 < (int)C::UNIT / 16; x0 += 512) {
-          uint4 w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) w[k] = *reinterpret_cast<const uint4*>(v + (x0 + 64 * k) * 16);
+          __nv_bfloat162 sum[4] = {};
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int x = x0 + 64 * k, row = x >> 3 & (kTile - 1), key = j * kTile + row;
-            uint4* at = reinterpret_cast<uint4*>(v + x * 16);
-            if (key >= t.L) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            const uint32_t e = 0x7f807f80u, one = 0x00800080u;
-            if ((((w[k].x & e) + one) | ((w[k].y & e) + one) | ((w[k].z & e) + one) | ((w[k].w & e) + one)) & 0x80008000u) {
-              const int col = u * C::UD + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
-              for (int i = 0; i < 8; ++i) {
-                uint16_t* el = reinterpret_cast<uint16_t*>(at) + i;
-                const uint16_t b = *el;
-                if ((b & 0x7f80u) != 0x7f80u) continue;
-                min16(&sh.bad[(b & 0x7f) ? 0 : (b & 0x8000u) ? 2 : 1][col + i], key - t.least / kTile * kTile);
-                *el = 0;
-              }
-              *(volatile int*)&sh.bad_any = 1;
+            const uint4 w = *reinterpret_cast<const uint4*>(v + (x0 + 64 * k) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = __hfma2(reinterpret_cast<const __nv_bfloat162*>(&w)[i], zero, sum[i]);
+          }
+          const __nv_bfloat162 a = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
+          if (!__hisnan(a.x) && !__hisnan(a.y)) continue;
+          for (int x = x0; x < x0 + 512; x += 64) {
+            const int row = x >> 3 & (kTile - 1), col = u * C::UD + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
+            for (int i = 0; i < 8; ++i) {
+              uint16_t* el = reinterpret_cast<uint16_t*>(v + x * 16) + i;
+              const uint16_t b = *el;
+              if ((b & 0x7f80u) != 0x7f80u) continue;
+              min16(&sh.bad[(b & 0x7f) ? 0 : (b & 0x8000u) ? 2 : 1][col + i], j * kTile + row - t.least / kTile * kTile);
+              *el = 0;
             }
           }
+          *(volatile int*)&sh.bad_any = 1;
         }
         tc::fence_async_smem();
         mbar_arrive(&sh.v_ok[(done - 1) & 7]);
