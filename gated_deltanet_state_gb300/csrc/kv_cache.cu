@@ -160,25 +160,179 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// Largest magnitude of eight elements; NaN falls out, an infinity stays.
+__device__ __forceinline__ float max8(const Row8<__nv_bfloat16>& r) {
+  __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = (&r.w.x)[i] & 0x7fff7fffu;
+    m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w));
+  }
+  return fmaxf(__bfloat162float(m.x), __bfloat162float(m.y));
+}
+__device__ __forceinline__ float max8(const Row8<float>& r) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(r.get(e)));
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ float max8_finite(const Row8<T>& r) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = fabsf(r.get(e));
+    if (x < __int_as_float(0x7f800000)) m = fmaxf(m, x);
+  }
+  return m;
+}
+template <int LPT>
+__device__ __forceinline__ float lanes_max(float m, unsigned mask) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
+  return m;
+}
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Row8<T>& r, float inv) {
+  return make_uint2(e4m3x4(r.get(0) * inv, r.get(1) * inv, r.get(2) * inv, r.get(3) * inv),
+                    e4m3x4(r.get(4) * inv, r.get(5) * inv, r.get(6) * inv, r.get(7) * inv));
+}
+// Four codes times a power of two.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  const float2 a = e4m3_f32x2(w), b = e4m3_f32x2(w >> 16);
+  return e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+}
+
+// Where a task's lane writes: blk is its block of K or V, elements 8 lane .. 8 lane + 7.
+struct AppendAt {
+  uint8_t* blk;
+  float* scale;
+  int d, lane;
+  __device__ uint2* k(int t) const {   // token t of K
+    return reinterpret_cast<uint2*>(blk + (t >> 3) * (d / 16 * 128) + (t & 7) * 16 + (lane / 2) * 128 + (lane & 1) * 8);
+  }
+  __device__ uint8_t* v(int e) const { return blk + (lane * 8 + e) * kKvBlock; }   // element e's 16 tokens of V
+};
+
+// A whole block: its 16 rows into registers once, then the scale, then the codes.
+template <typename T, int LPT>
+__device__ __forceinline__ void append_block(const T* src, int64_t stride, const AppendAt& at, bool is_v, unsigned mask) {
+  const bool on = at.lane * 8 < at.d;
+  Row8<T> r[kKvBlock];
+#pragma unroll
+  for (int t = 0; t < kKvBlock; ++t) {
+    if (on) r[t].load(src + t * stride);
+    else r[t].zero();
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int t = 0; t < kKvBlock; ++t) m = fmaxf(m, max8(r[t]));
+  if (__any_sync(mask, !(m < __int_as_float(0x7f800000)))) {
+    m = 0.f;
+#pragma unroll
+    for (int t = 0; t < kKvBlock; ++t) m = fmaxf(m, max8_finite(r[t]));
+  }
+  const float now = pow2_scale(lanes_max<LPT>(m, mask)), inv = 1.0f / now;   // a power of two: exact
+  if (at.lane == 0) *at.scale = now;
+  if (!on) return;
+  if (!is_v) {
+#pragma unroll
+    for (int t = 0; t < kKvBlock; ++t) *at.k(t) = codes8(r[t], inv);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = e4m3x4(r[4 * i].get(e) * inv, r[4 * i + 1].get(e) * inv, r[4 * i + 2].get(e) * inv, r[4 * i + 3].get(e) * inv);
+      *reinterpret_cast<uint4*>(at.v(e)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Tokens [off, off + run) of a block that is not written whole (a decode
+// step's single tokens): row by row, in little code (a step's kernel is as long
+// as its instructions take to arrive).  The codes before the run are read only
+// when the scale rises.
+template <typename T, int LPT>
+__device__ __forceinline__ void append_part(const T* src, int64_t stride, const AppendAt& at, bool is_v, int off, int run,
+                                            unsigned mask) {
+  const bool on = at.lane * 8 < at.d;
+  const float before = off ? *at.scale : 0.f;
+  float m = 0.f;
+#pragma unroll 1
+  for (int t = 0; t < run; ++t) {
+    Row8<T> r;
+    r.zero();
+    if (on) r.load(src + t * stride);
+    const float x = max8(r);
+    m = fmaxf(m, x < __int_as_float(0x7f800000) ? x : max8_finite(r));
+  }
+  const float now = fmaxf(pow2_scale(lanes_max<LPT>(m, mask)), before), inv = 1.0f / now;
+  if (at.lane == 0) *at.scale = now;
+  if (!on) return;
+  if (off && now > before) {
+    const float ratio = before * inv;
+    if (!is_v) {
+#pragma unroll 1
+      for (int t = 0; t < off; ++t) {
+        const uint2 o = *at.k(t);
+        *at.k(t) = make_uint2(rescale4(o.x, ratio), rescale4(o.y, ratio));
+      }
+    } else {
+      // bytes of tokens before the run
+      const uint32_t full = off >> 2, rest = (1u << (8 * (off & 3))) - 1u;
+      uint4 o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = *reinterpret_cast<const uint4*>(at.v(e));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t& w = (&o[e].x)[i];
+          const uint32_t keep = i < (int)full ? 0xffffffffu : i == (int)full ? rest : 0u;
+          w = (rescale4(w, ratio) & keep) | (w & ~keep);
+        }
+        *reinterpret_cast<uint4*>(at.v(e)) = o[e];
+      }
+    }
+  }
+#pragma unroll 1
+  for (int t = 0; t < run; ++t) {
+    Row8<T> r;
+    r.load(src + t * stride);
+    const uint2 c = codes8(r, inv);
+    if (!is_v) {
+      *at.k(off + t) = c;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) at.v(e)[off + t] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+    }
+  }
+}
+
 }  // namespace
 
 // New rows into the cache.  A CTA takes W rows; a run of rows of one block of
 // 16 tokens is handled, for one kv head and K or V, by LPT lanes with 8
-// elements of the head each: the run's rows are read into registers once, give
-// the block's scale, and are written as codes in the operand layout.
-template <typename T, int LPT, int W>
-__global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) {
-  constexpr int kSlots = 256 / LPT;   // runs in work at once
+// elements of the head each.
+template <typename T, int LPT, int W, int THREADS>
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 / THREADS) kv_append_kernel(const KvAppendParams p) {
+  constexpr int kSlots = THREADS / LPT;   // runs in work at once
   __shared__ int64_t s_slot[W + kKvBlock];
   __shared__ int s_lead[W], s_len[W], s_n;
   const int64_t t0 = (int64_t)blockIdx.x * W;
-  for (int i = threadIdx.x; i < W + kKvBlock; i += 256) s_slot[i] = t0 + i < p.T ? p.slot_map[t0 + i] : -1;
-  if (threadIdx.x == 0) s_n = 0;
+  for (int i = threadIdx.x; i < W + kKvBlock; i += THREADS) s_slot[i] = t0 + i < p.T ? p.slot_map[t0 + i] : -1;
+  int64_t before0 = -1;
+  if (threadIdx.x == 0) {
+    s_n = 0;
+    if (t0 > 0) before0 = p.slot_map[t0 - 1];
+  }
   __syncthreads();
   if (threadIdx.x < W) {
     const int i = threadIdx.x;
     const int64_t slot = s_slot[i];
-    const int64_t before = i > 0 ? s_slot[i - 1] : t0 > 0 ? p.slot_map[t0 - 1] : -1;
+    const int64_t before = i > 0 ? s_slot[i - 1] : before0;
     if (slot >= 0 && !(before >= 0 && slot == before + 1 && slot % kKvBlock != 0)) {
       int n = 1;
       while (n < kKvBlock && (slot + n) % kKvBlock != 0 && s_slot[i + n] == slot + n) ++n;
@@ -190,12 +344,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) 
   __syncthreads();
   const int sub = threadIdx.x / LPT, lane = threadIdx.x % LPT;
   const unsigned mask = (LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (threadIdx.x % 32 / LPT * LPT));
-  const int e0 = lane * 8, d = p.c.d;
-  const bool on = e0 < d;
-  const int h = blockIdx.y;
-  for (int task = sub; task < 2 * s_n; task += kSlots) {
-    const int i = s_lead[task >> 1], run = s_len[task >> 1];
-    const bool is_v = task & 1;
+  const int d = p.c.d, h = blockIdx.y, runs = s_n;
+  for (int task = sub; task < 2 * runs; task += kSlots) {
+    const bool is_v = task >= runs;
+    const int i = s_lead[is_v ? task - runs : task], run = s_len[is_v ? task - runs : task];
     const int64_t slot = s_slot[i];
     const int64_t page = slot / p.c.page_tokens;
     if (page >= p.c.num_pages) {
@@ -203,84 +355,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) 
       continue;
     }
     const int in_page = (int)(slot - page * p.c.page_tokens), b = in_page / kKvBlock, off = in_page % kKvBlock;
-    const T* src = static_cast<const T*>(is_v ? p.v : p.k) + (t0 + i - off) * (is_v ? p.v_stride : p.k_stride) + (int64_t)h * d + e0;
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    Row8<T> r[kKvBlock];   // by token of the block
-    const float before = off ? *(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)) : 0.f;
-#pragma unroll
-    for (int t = 0; t < kKvBlock; ++t) {
-      if (on && t >= off && t < off + run) r[t].load(src + t * stride);
-      else r[t].zero();
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int t = 0; t < kKvBlock; ++t)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(r[t].get(e)));   // NaN falls out
-    if (__any_sync(mask, !(amax < __int_as_float(0x7f800000)))) {   // an infinity: finite values only
-      amax = 0.f;
-#pragma unroll
-      for (int t = 0; t < kKvBlock; ++t)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = fabsf(r[t].get(e));
-          if (x < __int_as_float(0x7f800000)) amax = fmaxf(amax, x);
-        }
-    }
-#pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-    const float now = fmaxf(pow2_scale(amax), before);
-    const float inv = 1.0f / now;   // a power of two: exact
-    if (lane == 0) *const_cast<float*>(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)) = now;
-    if (!on) continue;
-    const bool raise = off && now > before;
-    const float ratio = before * inv;
-    if (!is_v) {
-      uint8_t* dst = const_cast<uint8_t*>(kv_k_block(p.c, (int)page, h, b)) + (e0 / 16) * 128 + (e0 & 8);
-      const int half = d / 16 * 128;
-#pragma unroll
-      for (int t = 0; t < kKvBlock; ++t) {
-        uint2* q = reinterpret_cast<uint2*>(dst + (t >> 3) * half + (t & 7) * 16);
-        if (t >= off && t < off + run) {
-          *q = make_uint2(e4m3x4(r[t].get(0) * inv, r[t].get(1) * inv, r[t].get(2) * inv, r[t].get(3) * inv),
-                          e4m3x4(r[t].get(4) * inv, r[t].get(5) * inv, r[t].get(6) * inv, r[t].get(7) * inv));
-        } else if (raise && t < off) {
-          const uint2 o = *q;
-          const float2 a = e4m3_f32x2(o.x), b2 = e4m3_f32x2(o.x >> 16), c = e4m3_f32x2(o.y), f = e4m3_f32x2(o.y >> 16);
-          *q = make_uint2(e4m3x4(a.x * ratio, a.y * ratio, b2.x * ratio, b2.y * ratio),
-                          e4m3x4(c.x * ratio, c.y * ratio, f.x * ratio, f.y * ratio));
-        }
-      }
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(const_cast<uint8_t*>(kv_v_block(p.c, (int)page, h, b)) + e0 * kKvBlock);
-      const bool part = run < kKvBlock;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint4 old = make_uint4(0, 0, 0, 0), res;
-        if (part) old = dst[e];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t x = e4m3x4(r[4 * w].get(e) * inv, r[4 * w + 1].get(e) * inv, r[4 * w + 2].get(e) * inv,
-                              r[4 * w + 3].get(e) * inv);
-          if (part) {
-            uint32_t o = (&old.x)[w];
-            // bytes of tokens [lo, hi) of this word are new, those before are older tokens
-            const int lo = min(max(off - 4 * w, 0), 4), hi = min(max(off + run - 4 * w, 0), 4);
-            const uint32_t m_lo = lo == 4 ? 0xffffffffu : (1u << (8 * lo)) - 1u;
-            const uint32_t m_hi = hi == 4 ? 0xffffffffu : (1u << (8 * hi)) - 1u;
-            if (raise) {
-              const float2 a = e4m3_f32x2(o), c = e4m3_f32x2(o >> 16);
-              const uint32_t moved = e4m3x4(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio);
-              o = (moved & m_lo) | (o & ~m_lo);
-            }
-            const uint32_t fresh = m_hi & ~m_lo;
-            x = (x & fresh) | (o & ~fresh);
-          }
-          (&res.x)[w] = x;
-        }
-        dst[e] = res;
-      }
-    }
+    const T* src = static_cast<const T*>(is_v ? p.v : p.k) + (t0 + i) * stride + (int64_t)h * d + lane * 8;
+    const AppendAt at{const_cast<uint8_t*>(is_v ? kv_v_block(p.c, (int)page, h, b) : kv_k_block(p.c, (int)page, h, b)),
+                      const_cast<float*>(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)), d, lane};
+    if (run == kKvBlock) append_block<T, LPT>(src, stride, at, is_v, mask);
+    else append_part<T, LPT>(src, stride, at, is_v, off, run, mask);
   }
 }
 
@@ -288,12 +368,13 @@ namespace {
 
 template <typename T, int LPT>
 cudaError_t append_rows(const KvAppendParams& p, cudaStream_t st) {
-  // few rows (a decode step: every row a run of its own): 4 a CTA, so that the
-  // runs of a step spread over the SMs; many (prompts): 64, about four runs
+  // few rows (a decode step: every row a run of its own): 4 a CTA of 8 warps,
+  // so that the runs of a step spread over the SMs; many (prompts): 64 a CTA
+  // of 4 warps, about four runs of K and of V
   if (p.T <= 4096) {
-    kv_append_kernel<T, LPT, 4><<<dim3((unsigned)((p.T + 3) / 4), p.c.Hkv), 256, 0, st>>>(p);
+    kv_append_kernel<T, LPT, 4, 256><<<dim3((unsigned)((p.T + 3) / 4), p.c.Hkv), 256, 0, st>>>(p);
   } else {
-    kv_append_kernel<T, LPT, 64><<<dim3((unsigned)((p.T + 63) / 64), p.c.Hkv), 256, 0, st>>>(p);
+    kv_append_kernel<T, LPT, 64, 128><<<dim3((unsigned)((p.T + 63) / 64), p.c.Hkv), 128, 0, st>>>(p);
   }
   return cudaGetLastError();
 }
