@@ -128,6 +128,16 @@ class KVPool:
         return self._scales(1)
 
 
+# the current stream of a device as an integer (the public call makes a Stream object: 3 us of a 13 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(stream, t: torch.Tensor) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _stream(stream)
+
+
 def _rows(t: torch.Tensor, heads: int, shape: AttnShape, name: str):
     """(pointer, elements between rows) of [T, heads, d] rows that may be slices of wider ones."""
     if not t.is_cuda:
@@ -178,7 +188,7 @@ def gdn_kv_tables(shape: AttnShape, num_pages: int, *, kv_len, new_len, free_pag
                       _ints(kv_len_out, n, "kv_len_out"), _ints(positions, T, "positions", torch.int64),
                       _dev(slot_map, torch.int64, "slot_map"), _ints(pages_taken, 1, "pages_taken"),
                       _ints(dev_error, 1, "dev_error"))
-    st = load_library().gdn_kv_tables(make_attn_desc(shape), a, _stream(stream))
+    st = load_library().gdn_kv_tables(make_attn_desc(shape), a, _on(stream, kv_len))
     return _check(st, "gdn_kv_tables") if raise_on_error else st
 
 
@@ -192,7 +202,7 @@ def gdn_kv_append(shape: AttnShape, pool: KVPool, *, k, v, slot_map, dev_error, 
     if v.shape[0] != T:
         raise ValueError(f"v: expected {T} rows, got {v.shape[0]}")
     a = _KvAppendArgs(T, ks, vs, kp, vp, _ints(slot_map, T, "slot_map", torch.int64), _ints(dev_error, 1, "dev_error"))
-    st = load_library().gdn_kv_append(make_attn_desc(shape), pool.abi(), a, _stream(stream))
+    st = load_library().gdn_kv_append(make_attn_desc(shape), pool.abi(), a, _on(stream, k))
     return _check(st, "gdn_kv_append") if raise_on_error else st
 
 
@@ -205,7 +215,7 @@ def gdn_kv_gather(shape: AttnShape, pool: KVPool, *, cu_kv, block_table, k, v, d
     rows = (T, shape.num_kv_heads, shape.head_dim)
     a = _KvGatherArgs(n, cols, T, _dev(cu_kv, torch.int32, "cu_kv"), bt, _out(k, rows, shape.torch_dtype(), "k"),
                       _out(v, rows, shape.torch_dtype(), "v"), _ints(dev_error, 1, "dev_error"))
-    st = load_library().gdn_kv_gather(make_attn_desc(shape), pool.abi(), a, _stream(stream))
+    st = load_library().gdn_kv_gather(make_attn_desc(shape), pool.abi(), a, _on(stream, k))
     return _check(st, "gdn_kv_gather") if raise_on_error else st
 
 
@@ -236,7 +246,7 @@ def gdn_attn_decode(shape: AttnShape, pool: KVPool, *, q, cu_seqlens, kv_len, bl
                         _out(o, (T, shape.num_q_heads, shape.head_dim), shape.torch_dtype(), "o"),
                         _out(lse, (T, shape.num_q_heads), torch.float32, "lse"), _ints(dev_error, 1, "dev_error"))
     st = lib.gdn_attn_decode(desc, pool.abi(), a, _dev(workspace, None, "workspace"),
-                             workspace.numel() * workspace.element_size(), _stream(stream))
+                             workspace.numel() * workspace.element_size(), _on(stream, q))
     return _check(st, "gdn_attn_decode") if raise_on_error else st
 
 
@@ -257,5 +267,5 @@ def gdn_attn_prefill(shape: AttnShape, *, q, k, v, cu_seqlens, cu_kv, o, dev_err
                          _out(o, (Tq, shape.num_q_heads, shape.head_dim), shape.torch_dtype(), "o"),
                          _out(lse, (Tq, shape.num_q_heads), torch.float32, "lse"), _ints(dev_error, 1, "dev_error"),
                          int(wait_cycles))
-    st = load_library().gdn_attn_prefill(make_attn_desc(shape), a, _stream(stream))
+    st = load_library().gdn_attn_prefill(make_attn_desc(shape), a, _on(stream, q))
     return _check(st, "gdn_attn_prefill") if raise_on_error else st

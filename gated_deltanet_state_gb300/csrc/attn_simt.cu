@@ -276,17 +276,37 @@ cudaError_t launch_attn_decode(const AttnDecodeParams& p, int dtype, cudaStream_
 // ---- prefill ----------------------------------------------------------------------------
 namespace {
 
-constexpr int kPreRows = 64, kPreKeys = 32;
+constexpr int kPreKeys = 64, kPreLdP = kPreKeys + 4;
+// Rows of a tile, four threads' worth each: 32 up to D = 64, so that a small
+// model's prompts make more CTAs and their longest one is shorter (75 us with
+// 64, nine prompts of up to 1,000 tokens), 64 above, where the keys' tiles take
+// the shared memory.
+template <int D> constexpr int kPreRows = D <= 64 ? 32 : 64;
+
+// Four consecutive elements of a row as fp32.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
 
 }  // namespace
 
-// 64 query rows of one kv head's group (row i of the tile: token i / G, head
-// i % G, so that the group shares the keys) against its keys, 32 at a time.
-// 256 threads: 16 x 16, each 4 rows by 2 keys of the scores and 4 rows by
-// d / 16 elements of the outputs.
-template <typename T>
-__global__ void __launch_bounds__(256) attn_prefill_simt_kernel(const AttnPrefillParams p) {
+// A tile of query rows of one kv head's group (row i of the tile: token i / G, head
+// i % G, so that the group shares the keys) against its keys, 64 at a time.
+// 16 threads a row group: each 4 rows by 4 keys of the scores and 4 rows by
+// D / 16 elements of the outputs (D: the head size rounded up to 32, 64, 128
+// or 256).  Bound by fp32 arithmetic; a small model's prompts by the longest
+// tile's way through its keys, which the next keys' loads (up to D = 64 held in
+// registers while the present ones are used) leave.
+template <typename T, int D>
+__global__ void __launch_bounds__(4 * kPreRows<D>) attn_prefill_simt_kernel(const AttnPrefillParams p) {
   extern __shared__ float smem[];
+  constexpr int VW = D == 32 ? 2 : 4, VN = D / 16 / VW;   // a thread's elements: VN groups of VW
+  constexpr int ROWS = kPreRows<D>, THREADS = 4 * ROWS;
+  constexpr int NL = kPreKeys * D / 4 / THREADS;              // 4-element loads a thread for a tile of K (or V)
+  constexpr bool AHEAD = D <= 64;
   const int d = p.d, ld = d + 4;
   const int s = blockIdx.z, h = blockIdx.y;
   const int q0 = p.cu_q[s], n = p.cu_q[s + 1] - q0, k0 = p.cu_kv[s], L = p.cu_kv[s + 1] - k0;
@@ -296,23 +316,29 @@ __global__ void __launch_bounds__(256) attn_prefill_simt_kernel(const AttnPrefil
     return;
   }
   // the last tiles first: they see the most keys
-  const int tiles = (int)(((int64_t)n * p.G + kPreRows - 1) / kPreRows);
+  const int tiles = (int)(((int64_t)n * p.G + ROWS - 1) / ROWS);
   const int tile = tiles - 1 - (int)blockIdx.x;
   if (tile < 0) return;
-  const int64_t r0 = (int64_t)tile * kPreRows;
-  float* sq = smem;                       // [64][ld]
-  float* sk = sq + kPreRows * ld;         // [32][ld]
-  float* sv = sk + kPreKeys * ld;         // [32][ld]
-  float* sp = sv + kPreKeys * ld;         // [64][36]
+  const int64_t r0 = (int64_t)tile * ROWS;
+  float* sq = smem;                       // [ROWS][ld]
+  float* sk = sq + ROWS * ld;         // [64][ld]
+  float* sv = sk + kPreKeys * ld;         // [64][ld]
+  float* sp = sv + kPreKeys * ld;         // [ROWS][68]
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int i = threadIdx.x; i < kPreRows * d; i += 256) {
-    const int r = i / d, e = i - r * d;
+  // element group and row of this thread's loads: D / 4 groups a row
+  constexpr int LG = D / 4;
+  const int le = threadIdx.x % LG * 4, lr = threadIdx.x / LG, lstep = THREADS / LG;
+  for (int r = lr; r < ROWS; r += lstep) {
     const int64_t row = (r0 + r) / p.G;
-    const int g = (int)((r0 + r) % p.G);
-    sq[r * ld + e] = row < n ? p.scale_log2 * to_f32(static_cast<const T*>(p.q)[(q0 + row) * p.q_stride + (int64_t)(h * p.G + g) * d + e])
-                             : 0.f;
+    const int g = (int)((r0 + r) - row * p.G);
+    if (le < d) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (row < n) x = load4(static_cast<const T*>(p.q) + (q0 + row) * p.q_stride + (int64_t)(h * p.G + g) * d + le);
+      *reinterpret_cast<float4*>(sq + r * ld + le) =
+          make_float4(x.x * p.scale_log2, x.y * p.scale_log2, x.z * p.scale_log2, x.w * p.scale_log2);
+    }
   }
-  float O[4][16], m[4], l[4];
+  float O[4][VN * VW], m[4], l[4];
   int lim[4];   // keys that each of this thread's rows sees
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -320,77 +346,110 @@ __global__ void __launch_bounds__(256) attn_prefill_simt_kernel(const AttnPrefil
     const int64_t row = (r0 + 4 * ty + i) / p.G;
     lim[i] = row < n ? max(0, (int)(L - n + row + 1)) : 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) O[i][j] = 0.f;
+    for (int j = 0; j < VN * VW; ++j) O[i][j] = 0.f;
   }
-  const int last = (int)min((int64_t)n - 1, (r0 + kPreRows - 1) / p.G), most = max(0, L - n + last + 1);
+  const int last = (int)min((int64_t)n - 1, (r0 + ROWS - 1) / p.G), most = max(0, L - n + last + 1);
   const int least = max(0, (int)(L - n + r0 / p.G + 1));
+  const T* kg = static_cast<const T*>(p.k) + (int64_t)k0 * p.k_stride + (int64_t)h * d + le;
+  const T* vg = static_cast<const T*>(p.v) + (int64_t)k0 * p.v_stride + (int64_t)h * d + le;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 ak[AHEAD ? NL : 1], av[AHEAD ? NL : 1];
+  auto fetch = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < (AHEAD ? NL : 1); ++i) {
+      const int key = kb + lr + i * lstep;
+      const bool in = key < most && le < d;   // keys that no row sees may hold anything
+      ak[i] = in ? load4(kg + key * p.k_stride) : zero;
+      av[i] = in ? load4(vg + key * p.v_stride) : zero;
+    }
+  };
+  if (AHEAD) fetch(0);
   for (int kb = 0; kb < most; kb += kPreKeys) {
     __syncthreads();
-    for (int i = threadIdx.x; i < kPreKeys * d; i += 256) {
-      const int r = i / d, e = i - r * d;
-      const bool in = kb + r < L;
-      sk[r * ld + e] = in ? to_f32(static_cast<const T*>(p.k)[(int64_t)(k0 + kb + r) * p.k_stride + (int64_t)h * d + e]) : 0.f;
-      sv[r * ld + e] = in ? to_f32(static_cast<const T*>(p.v)[(int64_t)(k0 + kb + r) * p.v_stride + (int64_t)h * d + e]) : 0.f;
+    if (le < d) {
+      if (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          *reinterpret_cast<float4*>(sk + (lr + i * lstep) * ld + le) = ak[i];
+          *reinterpret_cast<float4*>(sv + (lr + i * lstep) * ld + le) = av[i];
+        }
+      } else {
+#pragma unroll 4
+        for (int i = 0; i < NL; ++i) {
+          const int key = kb + lr + i * lstep;
+          *reinterpret_cast<float4*>(sk + (lr + i * lstep) * ld + le) = key < most ? load4(kg + key * p.k_stride) : zero;
+          *reinterpret_cast<float4*>(sv + (lr + i * lstep) * ld + le) = key < most ? load4(vg + key * p.v_stride) : zero;
+        }
+      }
     }
     __syncthreads();
-    float x[4][2] = {};
+    if (AHEAD && kb + kPreKeys < most) fetch(kb + kPreKeys);
+    float x[4][4] = {};
+#pragma unroll 4
     for (int e = 0; e < d; e += 4) {
-      float4 a[4], b[2];
+      float4 a[4], b[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (4 * ty + i) * ld + e);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * ld + e);
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * ld + e);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
           x[i][j] = fmaf(a[i].x, b[j].x, x[i][j]);
           x[i][j] = fmaf(a[i].y, b[j].y, x[i][j]);
           x[i][j] = fmaf(a[i].z, b[j].z, x[i][j]);
           x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
         }
     }
+    const bool edge = kb + kPreKeys > least;   // some row does not see some key
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      if (edge) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (kb + tx + 16 * j >= lim[i]) x[i][j] = -INFINITY;
-      float mx = fmaxf(x[i][0], x[i][1]);
+        for (int j = 0; j < 4; ++j)
+          if (kb + tx + 16 * j >= lim[i]) x[i][j] = -INFINITY;
+      }
+      float mx = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float mn = fmaxf(m[i], mx), ref = mn == -INFINITY ? 0.f : mn;
       const float a = fast_exp2(m[i] - ref);
-      const float e0 = fast_exp2(x[i][0] - ref), e1 = fast_exp2(x[i][1] - ref);
-      float sum = e0 + e1;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float e = fast_exp2(x[i][j] - ref);
+        sum += e;
+        sp[(4 * ty + i) * kPreLdP + tx + 16 * j] = e;
+      }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       m[i] = mn, l[i] = l[i] * a + sum;
-      sp[(4 * ty + i) * 36 + tx] = e0;
-      sp[(4 * ty + i) * 36 + tx + 16] = e1;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) O[i][j] *= a;
+      for (int j = 0; j < VN * VW; ++j) O[i][j] *= a;
     }
     __syncwarp();   // a row's 16 threads are in one warp
-    const int keys = min(kPreKeys, L - kb);
-    const bool edge = kb + keys > least;
-    for (int k = 0; k < keys; ++k) {
-      float w[4];
-      bool see[4];
+#pragma unroll 2
+    for (int k = 0; k < kPreKeys; k += 4) {
+      float4 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = sp[(4 * ty + i) * 36 + k], see[i] = !edge || kb + k < lim[i];
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sp + (4 * ty + i) * kPreLdP + k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = 4 * tx + 64 * j;
-        if (e < d) {
-          const float4 v = *reinterpret_cast<const float4*>(sv + k * ld + e);
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int j = 0; j < VN; ++j) {
+          const int e = VW * (tx + 16 * j);
+          if (e >= d) continue;
+          float v[VW];
+#pragma unroll
+          for (int c = 0; c < VW; c += 2)
+            *reinterpret_cast<float2*>(v + c) = *reinterpret_cast<const float2*>(sv + (k + u) * ld + e + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (see[i]) {   // a masked key's value may be NaN
-              O[i][4 * j] = fmaf(w[i], v.x, O[i][4 * j]);
-              O[i][4 * j + 1] = fmaf(w[i], v.y, O[i][4 * j + 1]);
-              O[i][4 * j + 2] = fmaf(w[i], v.z, O[i][4 * j + 2]);
-              O[i][4 * j + 3] = fmaf(w[i], v.w, O[i][4 * j + 3]);
-            }
+            // a masked key's value may be NaN: it is left out, not times 0
+            const bool see = !edge || kb + k + u < lim[i];
+#pragma unroll
+            for (int c = 0; c < VW; ++c) O[i][j * VW + c] = fmaf((&w[i].x)[u], see ? v[c] : 0.f, O[i][j * VW + c]);
           }
         }
       }
@@ -400,33 +459,42 @@ __global__ void __launch_bounds__(256) attn_prefill_simt_kernel(const AttnPrefil
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + 4 * ty + i, row = r / p.G;
     if (row >= n) continue;
-    const int64_t rh = (q0 + row) * p.Hq + h * p.G + r % p.G;
+    const int64_t rh = (q0 + row) * p.Hq + h * p.G + (r - row * p.G);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int e = 4 * tx + 64 * (j >> 2) + (j & 3);
-      if (e < d) put1<T>(p.o, rh * d + e, l[i] == 0.f ? 0.f : O[i][j] / l[i]);
-    }
+    for (int j = 0; j < VN; ++j)
+#pragma unroll
+      for (int c = 0; c < VW; ++c) {
+        const int e = VW * (tx + 16 * j) + c;
+        if (e < d) put1<T>(p.o, rh * d + e, l[i] == 0.f ? 0.f : O[i][j * VW + c] / l[i]);
+      }
     if (p.lse && tx == 0) p.lse[rh] = l[i] == 0.f ? -INFINITY : m[i] * 0.693147180559945309f + logf(l[i]);
   }
 }
 
 namespace {
 
-template <typename T>
+template <typename T, int D>
 cudaError_t prefill_simt(const AttnPrefillParams& p, cudaStream_t st) {
-  const int64_t tiles = ((int64_t)p.max_q * p.G + kPreRows - 1) / kPreRows;
-  const size_t sm = (size_t)((kPreRows + 2 * kPreKeys) * (p.d + 4) + kPreRows * 36) * 4;   // 142,336 B at d = 256
-  cudaError_t e = cudaFuncSetAttribute(attn_prefill_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  const int64_t tiles = ((int64_t)p.max_q * p.G + kPreRows<D> - 1) / kPreRows<D>;
+  const size_t sm = (size_t)((kPreRows<D> + 2 * kPreKeys) * (p.d + 4) + kPreRows<D> * kPreLdP) * 4;   // 217,088 B at d = 256
+  cudaError_t e = cudaFuncSetAttribute(attn_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  attn_prefill_simt_kernel<T><<<dim3((unsigned)tiles, p.Hkv, p.N), 256, sm, st>>>(p);
+  attn_prefill_simt_kernel<T, D><<<dim3((unsigned)tiles, p.Hkv, p.N), 4 * kPreRows<D>, sm, st>>>(p);
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t prefill_dtype(const AttnPrefillParams& p, cudaStream_t st) {
+  if (p.d <= 32) return prefill_simt<T, 32>(p, st);
+  if (p.d <= 64) return prefill_simt<T, 64>(p, st);
+  if (p.d <= 128) return prefill_simt<T, 128>(p, st);
+  return prefill_simt<T, 256>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStream_t st) {
   if (attn_prefill_tc_supported(p, dtype)) return launch_attn_prefill_tc(p, st);
-  return dtype == GDN_BF16 ? prefill_simt<__nv_bfloat16>(p, st) : prefill_simt<float>(p, st);
+  return dtype == GDN_BF16 ? prefill_dtype<__nv_bfloat16>(p, st) : prefill_dtype<float>(p, st);
 }
 
 }  // namespace gdn
