@@ -142,14 +142,14 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     uint8_t* qd = base + w.q_off;
     bool ok = true;
     float fq = 0.f;   // this row's score factor
-    // the rows of this warp as hi and lo codes, a row at a time, four loads ahead
+    // the rows of this warp as hi and lo codes, a row at a time, eight loads ahead
     auto load_q = [&](const DtItem& t) {
       const int e0 = lane * 8;
 #pragma unroll 1
-      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 4) {
-        uint4 x[4];
+      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8) {
+        uint4 x[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
           const int n = r0 + u;
           x[u] = make_uint4(0, 0, 0, 0);
           if (n < t.rows && e0 < d) {
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
           }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
           const int n = r0 + u;
           float f[8], amax = 0.f;
 #pragma unroll

@@ -4,11 +4,13 @@
 // S = Q K^T and O += P V are tcgen05 products of 128 query rows (row i of a
 // tile: token i / G, head i % G of the group, so that the group shares the
 // keys) with 128 keys, accumulated in tensor memory.  The softmax runs between
-// them with a row in one thread.  Two warpgroups of it share the products'
-// unit: up to d = 128 each has a row tile of its own; at d = 256, where the
-// outputs of one take half of tensor memory, they take that tile's key tiles in
-// turn, the running maximum passing from one to the other before the
-// exponentials, so that those of two key tiles overlap.
+// them, the running maximum and sum of a row in the threads that hold it.  How
+// long that takes decides how idle the tensor cores are, so each of two row
+// tiles (up to d = 128) has two warpgroups, a row's 128 scores in two threads
+// which exchange their maxima; at d = 256, where the outputs of one row tile
+// take half of tensor memory, two warpgroups take its key tiles in turn, the
+// running maximum passing from one to the other before the exponentials, so
+// that those of two key tiles overlap.
 #include <cuda.h>
 
 #include "attn.h"
@@ -32,32 +34,36 @@ struct PreCfg {
   static constexpr int STAGES = D == 64 ? 8 : 5;
   static constexpr uint32_t Q_BYTES = kTile * D * 2;
   static constexpr uint32_t DATA = NQ * Q_BYTES + STAGES * UNIT;
-  static constexpr int THREADS = 384;                    // two softmax warpgroups; loads, products, guards
+  static constexpr bool ALT = D == 256;                  // key tiles in turn instead of rows in two halves
+  static constexpr int SW = ALT ? 8 : 16;                // softmax warps
+  static constexpr int THREADS = SW * 32 + 128;          // and loads, products, guards
+  // registers a thread: what the guards' group gives up goes to the softmax,
+  // together at most what the block starts with (168 x 384, 96 x 640)
+  static constexpr int REGS = ALT ? 216 : 104, REGS_REST = ALT ? 72 : 64;
   // tensor memory columns: scores (the weights overwrite them), then outputs
   static constexpr uint32_t S0 = 0, O0 = 256;
   // registers: a softmax thread holds a row's 128 scores
 };
 
+template <int D>
 struct PreShared {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], m_ready[2], fin[2], drain;
-  float m[2][kTile];   // d = 256: a warpgroup's reference of each row, its sum at the end
+  uint64_t full[PreCfg<D>::STAGES], empty[PreCfg<D>::STAGES], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], m_ready[4], fin[2], drain;
+  float m[PreCfg<D>::SW / 4][kTile];   // by warpgroup: d = 256: its reference of each row; else its scores' maxima; at the end its sums
   uint32_t tmem;
   int fail, bad_any;
-  // first key, counted from the first guarded tile's, with NaN, +inf, -inf in
-  // each element of V; 0xffff: none
-  uint16_t bad[3][256];
+  // by element of V the first key with +inf, -inf, NaN, counted from the first
+  // guarded tile's (a CTA's rows guard at most 512): 10 bits each, ones: none
+  uint32_t bad[D];
 };
 template <int D>
-constexpr uint32_t kPreSmem = PreCfg<D>::DATA + sizeof(PreShared);
-static_assert(kPreSmem<256> <= 232448 && kPreSmem<128> <= 232448, "227 KB a CTA");
+constexpr uint32_t kPreSmem = PreCfg<D>::DATA + sizeof(PreShared<D>);
+static_assert(kPreSmem<256> <= 232448 && kPreSmem<128> <= 232448 && kPreSmem<64> <= 232448, "227 KB a CTA");
 
-// Minimum of a 16-bit word in shared memory.
-__device__ __forceinline__ void min16(uint16_t* at, uint32_t v) {
-  unsigned* w = reinterpret_cast<unsigned*>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)3);
-  const int sft = (reinterpret_cast<uintptr_t>(at) & 2) * 8;
-  unsigned old = *w;
-  while (((old >> sft) & 0xffffu) > v) {
-    const unsigned seen = atomicCAS(w, old, (old & ~(0xffffu << sft)) | (v << sft));
+// Minimum of the 10-bit field of a word in shared memory that starts at bit `at`.
+__device__ __forceinline__ void min10(uint32_t* w, int at, uint32_t v) {
+  uint32_t old = *w;
+  while (((old >> at) & 0x3ffu) > v) {
+    const uint32_t seen = atomicCAS(w, old, (old & ~(0x3ffu << at)) | (v << at));
     if (seen == old) break;
     old = seen;
   }
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
   }
   uint8_t* sq = base;
   uint8_t* ring = base + C::NQ * C::Q_BYTES;
-  PreShared& sh = *reinterpret_cast<PreShared*>(base + C::DATA);
+  PreShared<D>& sh = *reinterpret_cast<PreShared<D>*>(base + C::DATA);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = p.wait_cycles > 0 ? p.wait_cycles : p.wait_cycles < 0 ? -1 : kPreWait;
   volatile int* fail = &sh.fail;
@@ -183,18 +189,18 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.s_full[i], 1);
-      tc::mbar_init(&sh.p_full[i], 128);
+      tc::mbar_init(&sh.p_full[i], C::ALT ? 128 : 256);
       tc::mbar_init(&sh.o_done[i], 1);
-      tc::mbar_init(&sh.q_full[i], C::NQ == 1 ? 256 : 128);
-      tc::mbar_init(&sh.m_ready[i], 128);
+      tc::mbar_init(&sh.q_full[i], 256);
     }
-    for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], 64);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.fin[i], 128);
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], C::U == 2 ? 32 : 64);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.m_ready[i], 128);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.fin[i], C::ALT ? 128 : 256);
     tc::mbar_init(&sh.drain, 1);
     sh.fail = limit < 0, sh.bad_any = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  for (int i = threadIdx.x; i < 3 * 256; i += C::THREADS) (&sh.bad[0][0])[i] = 0xffff;
+  for (int i = threadIdx.x; i < D; i += C::THREADS) sh.bad[i] = 0x3fffffffu;
   if (warp == 0) {
     tc::tmem_alloc(&sh.tmem, 512);
     tc::tmem_relinquish();
@@ -207,11 +213,12 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
   int issued = 0, raw = 0;   // units loaded, those of them for the guards first (the loading thread's)
   uint32_t raw_bits = 0;     // which of the last 32 went to the guards
 
-  if (wg < 2) {
-    // ---- softmax: one thread a row, of row tile wg, or (d = 256) of every second key tile ----
-    constexpr bool ALT = C::SLOTS == 2;
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
-    const int q = ALT ? 0 : wg, i = threadIdx.x & 127;
+  if (warp < C::SW) {
+    // ---- softmax: row i of tile q; its keys' half, or (d = 256) every second key tile ----
+    constexpr bool ALT = C::ALT;
+    constexpr int SC = ALT ? kTile : kTile / 2, NU = SC / 32;   // scores of a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::REGS));
+    const int q = ALT ? 0 : wg >> 1, half = wg & 1, i = threadIdx.x & 127;
     const int nk = t.nk[q];
     const int64_t rbase = t.r0 + q * kTile, r = rbase + i;
     const int tok = (int)(r / p.G), g = (int)(r - (int64_t)tok * p.G);
@@ -221,17 +228,22 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21);   // this warp's 32 lanes
     const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q);
     if (nk > 0 && limit >= 0) {
-      constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a row, rows a warp loads at once
-      constexpr int WR = ALT ? 16 : 32;         // rows a warp loads
-      const int w0 = (ALT ? warp : warp & 3) * WR;
-      for (int rr = w0 + lane / CH; rr < w0 + WR; rr += RP) {
-        const int64_t r2 = rbase + rr, tk = r2 / p.G;
-        const int c = lane % CH;
-        uint4 w = make_uint4(0, 0, 0, 0);
+      // 16 rows a warp, all their loads before the first store (one after
+      // another they take 19,000 cycles of a tile's 80,000)
+      constexpr int CH = D / 8, RP = 32 / CH, NP = 16 / RP;   // 16-byte chunks of a row, rows a pass, passes
+      const int w0 = (half * 4 + (warp & 3)) * 16 + lane / CH, c8 = lane % CH * 8;
+      const int tok0 = (int)(rbase / p.G), rem0 = (int)(rbase - (int64_t)tok0 * p.G);   // of the tile's first row
+      uint4 w[NP];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int x = rem0 + w0 + k * RP, tk = tok0 + x / p.G, gg = x % p.G;
+        w[k] = make_uint4(0, 0, 0, 0);
         if (tk < t.n)
-          w = *reinterpret_cast<const uint4*>(qg + (t.q0 + tk) * p.q_stride + (int64_t)(t.h * p.G + (int)(r2 - tk * p.G)) * D + c * 8);
-        *reinterpret_cast<uint4*>(sq + q * C::Q_BYTES + tc::sw128_offset(rr, c * 8, kTile)) = w;
+          w[k] = *reinterpret_cast<const uint4*>(qg + (int64_t)(t.q0 + tk) * p.q_stride + (int64_t)(t.h * p.G + gg) * D + c8);
       }
+#pragma unroll
+      for (int k = 0; k < NP; ++k)
+        *reinterpret_cast<uint4*>(sq + q * C::Q_BYTES + tc::sw128_offset(w0 + k * RP, c8, kTile)) = w[k];
       tc::fence_async_smem();
       mbar_arrive(&sh.q_full[q]);
     }
@@ -240,71 +252,79 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     // O of tiles 0 .. j: with two score buffers two barriers in turn, since
     // scores j only say that O of tile j - 2 is done
     auto o_wait = [&](int j) {
-      return C::SLOTS == 2 ? pre_wait(&sh.o_done[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)
-                           : pre_wait(&sh.o_done[q], (uint32_t)j & 1, limit, fail);
+      return ALT ? pre_wait(&sh.o_done[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)
+                 : pre_wait(&sh.o_done[q], (uint32_t)j & 1, limit, fail);
     };
     // keys that all of this warp's rows see: below it no mask
     int wlim = valid ? lim : 0x7fffffff;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) wlim = min(wlim, __shfl_xor_sync(0xffffffffu, wlim, o));
     bool ok = nk == 0 || limit >= 0;
-    for (int j = ALT ? wg : 0; ok && j < nk; j += ALT ? 2 : 1) {
-      const int b = wg;
-      const uint32_t par = C::SLOTS == 2 ? (uint32_t)(j >> 1) & 1 : (uint32_t)j & 1;
-      ok = pre_wait(&sh.s_full[b], par, limit, fail);
+    for (int j = ALT ? half : 0; ok && j < nk; j += ALT ? 2 : 1) {
+      const int b = ALT ? half : q;   // score buffer
+      ok = pre_wait(&sh.s_full[b], (uint32_t)(ALT ? j >> 1 : j) & 1, limit, fail);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc::fence_after_sync();
       const uint32_t scol = lanes + C::S0 + (uint32_t)b * 128;
-      uint32_t s[4][32];
+      uint32_t s[NU][32];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) tc::tmem_ld32_nowait(scol + u * 32, s[u]);
+      for (int u = 0; u < NU; ++u) tc::tmem_ld32_nowait(scol + (ALT ? 0 : half * SC) + u * 32, s[u]);
       tc::tmem_ld_wait();
 #pragma unroll
-      for (int u = 0; u < 4; ++u) tc::tmem_ld_fence(s[u]);
-      const int seen = lim - j * kTile;   // keys of this tile that the row sees
+      for (int u = 0; u < NU; ++u) tc::tmem_ld_fence(s[u]);
       if ((j + 1) * kTile > wlim) {
+        const int seen = lim - j * kTile - (ALT ? 0 : half * SC);   // of these scores, those that the row sees
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (u * 32 + k >= seen) s[u][k] = 0xff800000u;
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < NU; ++u)
 #pragma unroll
         for (int k = 0; k < 32; k += 2)
           mx[k >> 1 & 3] = max3(mx[k >> 1 & 3], __uint_as_float(s[u][k]), __uint_as_float(s[u][k + 1]));
-      const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-      // the reference of the weights moves only when the maximum has grown by
-      // 2^8: weights stay below 2^8, and a row's choice depends on that row alone
-      float alpha = 1.f;
-      bool grow = false;
+      float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       const float before = m;
-      if (ALT && j > 0) {   // the reference after the tile before, the other warpgroup's
+      if (!ALT) {
+        // the row's other half: its maximum, and that its scores have been read
+        // (the weights below overwrite them)
+        sh.m[wg][i] = mt;
+        mbar_arrive(&sh.m_ready[wg]);
+        ok = pre_wait(&sh.m_ready[wg ^ 1], (uint32_t)j & 1, limit, fail);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        mt = fmaxf(mt, sh.m[wg ^ 1][i]);
+      } else if (j > 0) {   // the reference after the tile before, the other warpgroup's
         ok = pre_wait(&sh.m_ready[wg ^ 1], (uint32_t)((j - 1) >> 1) & 1, limit, fail);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         m = sh.m[wg ^ 1][i];
       }
+      // the reference of the weights moves only when the maximum has grown by
+      // 2^8: weights stay below 2^8, and a row's choice depends on that row alone
+      float alpha = 1.f;
       if (j == 0) {
         m = mt;
       } else if ((mt - m) * c > 8.f) {
         alpha = ex2((m - mt) * c);
         m = mt;
-        grow = true;
       }
       if (ALT) {
         sh.m[wg][i] = m;
         mbar_arrive(&sh.m_ready[wg]);
+        if (j > 1 && m != before) l *= ex2((before - m) * c);
+      } else {
+        l *= alpha;
       }
-      if (j > (ALT ? 1 : 0) && m != before) l *= ex2((before - m) * c);
-      if (__any_sync(0xffffffffu, grow)) {
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {
         // O of the tiles before: wait for their products, scale this warp's rows
+        // (of two halves each half of the row)
         ok = o_wait(j - 1);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::fence_after_sync();
 #pragma unroll 1
-        for (int e = 0; e < D; e += 16) {
+        for (int e = ALT ? 0 : half * (D / 2); e < (ALT ? D : (half + 1) * (D / 2)); e += 16) {
           float o[16];
           const uint32_t col = lanes + C::O0 + (uint32_t)q * D + e;
           tc::tmem_ld16(col, o);
@@ -318,7 +338,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       const f32x2 cc = pack2(c, c), rr = pack2(ref, ref);
       f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < NU; ++u) {
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -328,7 +348,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b2);
           w[k] = *reinterpret_cast<const uint32_t*>(&h2);
         }
-        tc::tmem_st16u(scol + u * 16, w);
+        tc::tmem_st16u(scol + (ALT ? 0 : half * (SC / 2)) + u * 16, w);
       }
       l += sum2(add2(sum[0], sum[1]));
       tc::tmem_st_wait();
@@ -336,25 +356,33 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       mbar_arrive(&sh.p_full[b]);
     }
     // ---- outputs ----
-    if (ALT && nk > 0 && limit >= 0) {
-      // the row's sum: the warpgroup that had the last tile takes the other's,
-      // brought to its reference, and hands the total back; each then writes
-      // half of the row
-      const int last = (nk - 1) & 1;
+    if (nk > 0 && limit >= 0) {
       if (!ok) *fail = 1;
-      if (wg != last) {
-        ok = pre_wait(&sh.m_ready[last], (uint32_t)((nk - 1) >> 1) & 1, limit, fail) && ok;
-        const float mine = m;
-        m = sh.m[last][i];
-        sh.m[wg][i] = l == 0.f ? 0.f : l * ex2((mine - m) * c);
-        mbar_arrive(&sh.fin[0]);
-        ok = pre_wait(&sh.fin[1], 0, limit, fail) && ok;
-        l = sh.m[last][i];
-      } else {
-        ok = pre_wait(&sh.fin[0], 0, limit, fail) && ok;
-        l += sh.m[wg ^ 1][i];
+      if (!ALT) {
+        // the row's sum: the two halves' (the maxima's places are free: both
+        // have had the last tile's)
         sh.m[wg][i] = l;
-        mbar_arrive(&sh.fin[1]);
+        mbar_arrive(&sh.fin[q]);
+        ok = pre_wait(&sh.fin[q], 0, limit, fail) && ok;
+        l = sh.m[wg & ~1][i] + sh.m[wg | 1][i];
+      } else {
+        // the warpgroup that had the last tile takes the other's sum, brought to
+        // its reference, and hands the total back
+        const int last = (nk - 1) & 1;
+        if (wg != last) {
+          ok = pre_wait(&sh.m_ready[last], (uint32_t)((nk - 1) >> 1) & 1, limit, fail) && ok;
+          const float mine = m;
+          m = sh.m[last][i];
+          sh.m[wg][i] = l == 0.f ? 0.f : l * ex2((mine - m) * c);
+          mbar_arrive(&sh.fin[0]);
+          ok = pre_wait(&sh.fin[1], 0, limit, fail) && ok;
+          l = sh.m[last][i];
+        } else {
+          ok = pre_wait(&sh.fin[0], 0, limit, fail) && ok;
+          l += sh.m[wg ^ 1][i];
+          sh.m[wg][i] = l;
+          mbar_arrive(&sh.fin[1]);
+        }
       }
     }
     if (ok && nk > 0) ok = o_wait(nk - 1);
@@ -363,11 +391,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const bool bad = nk > 0 && *(volatile int*)&sh.bad_any;
       // Rows leave through shared memory (this tile's Q, which every product has
-      // read), so that a warp writes whole rows: 16-byte chunk ch of row i at
-      // place ch ^ (i % CH) of the row.
-      constexpr int W = ALT ? D / 2 : D, CH = W / 8, RP = 32 / CH;   // elements of a row here, its chunks, rows a pass
-      const int e0 = ALT ? wg * W : 0;
-      uint8_t* so = sq + (ALT ? wg : q) * (kTile * W * 2) + (warp & 3) * 32 * (W * 2);
+      // read), each warp its half of 32 rows, so that whole stretches of a row are
+      // written: 16-byte chunk ch of row i at place ch ^ (i % CH) of the row.
+      constexpr int W = D / 2, CH = W / 8, RP = 32 / CH;   // elements of a row here, its chunks, rows a pass
+      const int e0 = half * W;
+      uint8_t* so = sq + q * C::Q_BYTES + half * (kTile * W * 2) + (warp & 3) * 32 * (W * 2);
 #pragma unroll 1
       for (int e = 0; e < W; e += 32) {
         float o[32];
@@ -380,11 +408,12 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
         if (bad) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            const int mine = lim - t.least / kTile * kTile, at = e0 + e + k;
-            const bool hi = sh.bad[1][at] < mine, lo = sh.bad[2][at] < mine;
+            const int mine = lim - t.least / kTile * kTile;
+            const uint32_t w = sh.bad[e0 + e + k];
+            const bool hi = (int)(w & 0x3ffu) < mine, lo = (int)(w >> 10 & 0x3ffu) < mine;
             if (hi) o[k] = INFINITY;
             if (lo) o[k] = -INFINITY;
-            if (sh.bad[0][at] < mine || (hi && lo)) o[k] = __int_as_float(0x7fffffff);
+            if ((int)(w >> 20) < mine || (hi && lo)) o[k] = __int_as_float(0x7fffffff);
           }
         }
 #pragma unroll
@@ -411,11 +440,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           *reinterpret_cast<uint4*>(og + at * D) =
               *reinterpret_cast<const uint4*>(so + rr * (W * 2) + (((lane % CH) ^ (rr & (CH - 1))) << 4));
       }
-      if (valid && p.lse && (!ALT || wg == 0)) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
+      if (valid && p.lse && half == 0) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
     }
   } else {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-  if (warp == 8 && lane == 0) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::REGS_REST));
+  if (warp == C::SW && lane == 0) {
     // ---- loads ----
     // a V tile that some row sees in part arrives on the guards' barriers, who
     // hand it on; they follow within the ring, so 8 barriers never alias
@@ -438,7 +467,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     constexpr int ahead = C::NQ == 1 ? 2 : 1;
     for (int j = 0; ok && j < t.nkmax; ++j) 
       ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + ahead >= t.nkmax || tile(&kmap, j + ahead, false));
-  } else if (warp == 9 && limit >= 0) {
+  } else if (warp == C::SW + 1 && limit >= 0) {
     // ---- products: the whole warp, one lane issues ----
     const uint32_t lead = tc::elect_one();
     constexpr uint32_t id_qk = tc::idesc_bf16_f32(kTile, kTile);
@@ -465,6 +494,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
         tc::mma_bf16_ts_if(lead, tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv,
                            acc || ks != 0);
     };
+    // a look at a barrier ahead of its use, so that the answer is there when
+    // the products in between are issued
+    auto peek = [&](uint64_t* m, uint32_t p) { return __all_sync(0xffffffffu, tc::mbar_test_wait(m, p)) != 0; };
     auto full = [&](int s, uint32_t p) { return pre_wait(&sh.full[s], p, limit, fail); };
     // a guarded V unit: from the guards, and its place's phase moves on here
     auto v_ready = [&](int s, uint32_t p, int j) {
@@ -482,11 +514,18 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       ok = t.nkmax == 0 || all(pre_wait(&sh.q_full[0], 0, limit, fail));
       // a wait for each unit of 32 KB: the ring holds five, so the next one is
       // often still on its way
+      bool seen = false;   // whether the next unit has been seen to be there
+      auto unit = [&](bool last_unit) {   // the next unit's place is st; look at the one behind it
+        int s1 = st;
+        uint32_t p1 = ph;
+        step(s1, p1);
+        seen = !last_unit && peek(&sh.full[s1], p1);
+      };
       auto qk = [&](int j) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (!all(full(st, ph))) return false;
-          tc::fence_after_sync();
+          if (!seen && !all(full(st, ph))) return false;
+          unit(false);
           qk_unit(0, C::S0 + (j & 1) * 128, st, u);
           tc::mma_commit_if(lead, &sh.empty[st]);
           step(st, ph);
@@ -495,10 +534,13 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
         return true;
       };
       auto pv = [&](int j) {
+        const bool guards = (j + 1) * kTile > t.least;
+        if (!all(pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail))) return false;
+        tc::fence_after_sync();
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          if (!all((u || pre_wait(&sh.p_full[j & 1], (uint32_t)(j >> 1) & 1, limit, fail)) && v_ready(st, ph, j))) return false;
-          tc::fence_after_sync();
+          if ((guards || !seen) && !all(v_ready(st, ph, j))) return false;
+          unit(guards);
           pv_unit(0, C::S0 + (j & 1) * 128, st, u, j != 0);
           tc::mma_commit_if(lead, &sh.empty[st]);
           step(st, ph);
@@ -554,55 +596,58 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     // every product issued, and every arrival on a barrier, before the end
     tc::mma_commit_if(lead, &sh.drain);
     if (!tc::mbar_wait_bounded(&sh.drain, 0, kPreWait)) *fail = 1;
-  } else if (warp >= 10 && limit >= 0) {
+  } else if (warp >= C::SW + 2 && limit >= 0) {
     // ---- guards: in V tiles that some row sees in part, keys past the
     // sequence become zero and so do NaN and infinities, which a weight of 0
     // would not keep out of the product; where those were is noted by element
     // for the rows that do see them ----
-    const int me = threadIdx.x - 320;   // 0 .. 63
+    // (two units of a tile: a warp each; one: both warps)
+    constexpr int GT = C::U == 2 ? 32 : 64;
+    const int me = (threadIdx.x - (C::SW + 2) * 32) % GT;
     bool ok = true;
     int done = 0;
     for (int j = t.least / kTile; ok && j < t.nkmax; ++j) {
-      for (int u = 0; ok && u < C::U; ++u) {
+      for (int u = C::U == 2 ? warp - (C::SW + 2) : 0, one = 1; ok && one; one = 0) {
         // position of unit u of V tile j in the ring's order
         int n;
         if constexpr (C::NQ == 1) n = min(t.nkmax, j + 2) * C::U + j * C::U + u;
         else n = 1 + 2 * j;
-        ok = pre_wait(&sh.v_raw[done & 7], (uint32_t)(done >> 3) & 1, limit, fail);
+        const int k = done * C::U + u;   // of the guarded units
+        ok = pre_wait(&sh.v_raw[k & 7], (uint32_t)(k >> 3) & 1, limit, fail);
         if (!ok) break;
         ++done;
         uint8_t* v = ring + (n % C::STAGES) * C::UNIT;
-        // 16-byte chunks x = me + 64 k: block x / 1024, key x / 8 % 128
+        // 16-byte chunks x = me + GT k: block x / 1024, key x / 8 % 128
         const int left = t.L - j * kTile;   // keys of the tile in the sequence
         if (left < kTile)
-          for (int x = me; x < (int)C::UNIT / 16; x += 64)
+          for (int x = me; x < (int)C::UNIT / 16; x += GT)
             if ((x >> 3 & (kTile - 1)) >= left) *reinterpret_cast<uint4*>(v + x * 16) = make_uint4(0, 0, 0, 0);
         // eight chunks at a time: 0 times an infinity or NaN is NaN, and so is a sum with it
-        for (int x0 = me; x0 < (int)C::UNIT / 16; x0 += 512) {
+        for (int x0 = me; x0 < (int)C::UNIT / 16; x0 += 8 * GT) {
           __nv_bfloat162 sum[4] = {};
           const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint4 w = *reinterpret_cast<const uint4*>(v + (x0 + 64 * k) * 16);
+            const uint4 w = *reinterpret_cast<const uint4*>(v + (x0 + GT * k) * 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[i] = __hfma2(reinterpret_cast<const __nv_bfloat162*>(&w)[i], zero, sum[i]);
           }
           const __nv_bfloat162 a = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
           if (!__hisnan(a.x) && !__hisnan(a.y)) continue;
-          for (int x = x0; x < x0 + 512; x += 64) {
+          for (int x = x0; x < x0 + 8 * GT; x += GT) {
             const int row = x >> 3 & (kTile - 1), col = u * C::UD + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
             for (int i = 0; i < 8; ++i) {
               uint16_t* el = reinterpret_cast<uint16_t*>(v + x * 16) + i;
               const uint16_t b = *el;
               if ((b & 0x7f80u) != 0x7f80u) continue;
-              min16(&sh.bad[(b & 0x7f) ? 0 : (b & 0x8000u) ? 2 : 1][col + i], j * kTile + row - t.least / kTile * kTile);
+              min10(&sh.bad[col + i], (b & 0x7f) ? 20 : (b & 0x8000u) ? 10 : 0, j * kTile + row - t.least / kTile * kTile);
               *el = 0;
             }
           }
           *(volatile int*)&sh.bad_any = 1;
         }
         tc::fence_async_smem();
-        mbar_arrive(&sh.v_ok[(done - 1) & 7]);
+        mbar_arrive(&sh.v_ok[k & 7]);
       }
     }
   }
@@ -614,7 +659,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
-    if (warp == 8 && lane == 0)
+    if (warp == C::SW && lane == 0)
     {
       for (int n = issued - 1, k = raw - 1; n >= 0 && n >= issued - C::STAGES; --n, raw_bits >>= 1) {
         if (raw_bits & 1) {
