@@ -95,13 +95,14 @@ struct AttnPrefillParams {
 // number of (row, head of the group) pairs alone, so a row's sums are formed in
 // the same order whatever batch it is in.  About 256 keys spread a short
 // context over more SMs; 512 keep a few rows' outputs (4 d bytes each for a
-// piece, written and read once) under 3 % of the keys' bytes at 6 rows; 1,024
-// do so for drafts; beyond 38,912 tokens 76 pieces a head are one CTA on each
-// of the 152 SMs for two kv heads.
+// piece, written and read once) under 3 % of the keys' bytes at 6 rows; a
+// draft's take 1,024, and 2,048 from 8,192 keys on (16 drafts of 16 rows over
+// 2,048 to 32,768 keys: 262 us with 1,024, 226 with 2,048); beyond 38,912
+// tokens 76 pieces a head are one CTA on each of the 152 SMs for two kv heads.
 constexpr int kMaxPieces = 76;
 constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows
 __host__ __device__ inline int decode_piece_target(int tiles, int rows) {   // pieces aimed at
-  const int per = (rows > kDtNarrow ? 8 : 4) / (tiles <= 16 ? 2 : 1);
+  const int per = rows > kDtNarrow ? (tiles <= 16 ? 4 : tiles <= 64 ? 8 : 16) : tiles <= 16 ? 2 : 4;
   const int n = (tiles + per / 2) / per;
   return n < 1 ? 1 : n > kMaxPieces ? kMaxPieces : n;
 }

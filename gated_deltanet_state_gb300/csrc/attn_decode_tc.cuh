@@ -311,7 +311,7 @@ __device__ __forceinline__ void dt_clean(uint8_t* v, int* bad, const DtItem& t, 
           at[k] = 0;
         } else if (pos >= least && (at[k] & 0x7f) == 0x7f) {
           at[k] = 0;
-          bad[e] = min(bad[e], pos);
+          atomicMin(&bad[e], pos);
         }
       }
     }

@@ -7,10 +7,11 @@
 // with the cache's blocks as the second operands.  A softmax thread holds one
 // row, so no maximum or sum crosses lanes; the hi and lo parts of Q and P are
 // products of their own into the same sums, and P goes back to tensor memory
-// over the scores it comes from.  A tile of 128 tokens takes 24 products of 68
-// (scores) and 136 cycles (outputs), 2,180 in all, while its 64 KB at d = 256
-// take 2,700 cycles of the memory's rate: one CTA an SM, scores of two tiles in
-// tensor memory so that the products of one run under the softmax of the other.
+// over the scores it comes from.  A tile of 128 tokens takes 24 products of 67
+// (scores) and 134 cycles (outputs), 2,140 in all, while its 64 KB at d = 256
+// take 2,700 cycles of the memory's rate; the softmax of a tile takes 2,600, so
+// two warpgroups take the tiles in turn, the reference passing from one to the
+// other before the exponentials.
 #include "attn_decode_tc.cuh"
 
 namespace gdn {
@@ -20,11 +21,14 @@ using namespace dt;
 namespace {
 
 constexpr int kDrRows = 128;
-constexpr int kDrThreads = 128 + 96;       // softmax; K loads, V loads, products
+constexpr int kDrThreads = 256 + 128;      // softmax; K loads, V loads, products (and a warp that idles)
 constexpr uint32_t kDrO = 256;             // tensor memory: scores of two tiles, then O
 
 struct DrShared : DtBase {
-  float turn[4][32][33];   // a warp's 32 rows x 32 elements on their way out
+  uint64_t m_ready[2], fin[2];
+  float m[2][kDrRows];      // a warpgroup's reference of each row, its sum at the end
+  float fq[2][kDrRows];     // score factors (heads alternate)
+  float turn[8][32][17];    // a warp's 32 rows x 16 elements on their way out
 };
 
 // D[tmem] (+)= A[tmem] B[smem]^T, e4m3, 32 deep: eight columns of A hold four codes each.
@@ -53,12 +57,13 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     for (int i = 0; i < VS; ++i) tc::mbar_init(&sh.v_full[i], 1), tc::mbar_init(&sh.v_empty[i], 1);
     for (int i = 0; i < NS; ++i) tc::mbar_init(&sh.sc_full[i], 2 * kDtBlocks);
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.s_full[i], 1), tc::mbar_init(&sh.p_full[i], 128), tc::mbar_init(&sh.o_done[i], 1);
-    tc::mbar_init(&sh.q_full, 128);
+    tc::mbar_init(&sh.q_full, 256);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.m_ready[i], 128), tc::mbar_init(&sh.fin[i], 128);
     tc::mbar_init(&sh.drain, 1);
     sh.fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tc::tmem_alloc(&sh.tmem, 512);
     tc::tmem_relinquish();
   }
@@ -72,10 +77,307 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
   const uint32_t unit = (uint32_t)kDtTok * d;
   int loaded = 0;
 
-  if (warp == 4 || warp == 5) {
+  if (warp < 8) {
+    // registers: what the last warpgroup gives up goes to the softmax, together
+    // no more than the 168 x 384 that the block starts with
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+    // ---- softmax: a thread a row, a warpgroup every second tile ----
+    const int tid = threadIdx.x & 127, wg = warp >> 2;
+    const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21);
+    uint8_t* qd = base + w.q_off;
+    bool ok = true;
+    // the rows of this warp as hi and lo codes, a row at a time, eight loads ahead
+    auto load_q = [&](const DtItem& t, int par) {
+      const int e0 = lane * 8;
+#pragma unroll 1
+      for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += 8) {
+        uint4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int n = r0 + u;
+          x[u] = make_uint4(0, 0, 0, 0);
+          if (n < t.rows && e0 < d) {
+            const int row = (t.r0 + n) / p.G, g = t.r0 + n - row * p.G;
+            x[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(t.q0 + row) * p.q_stride +
+                                                   (int64_t)(t.h * p.G + g) * d + e0);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int n = r0 + u;
+          float f[8], amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t b = (&x[u].x)[k >> 1];
+            f[k] = __uint_as_float(k & 1 ? b & 0xffff0000u : b << 16);
+            amax = fmaxf(amax, fabsf(f[k]));
+          }
+          amax = warp_max(amax);
+          // largest element to (224, 448]; exponents kept where both factors are normal
+          int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
+          e = max(-100, min(100, e));
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float g4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g4[i] = f[4 * k + i] * inv;
+            hi[k] = e4m3x4(g4[0], g4[1], g4[2], g4[3]);
+            const float2 a = e4m3_f32x2(hi[k]), b = e4m3_f32x2(hi[k] >> 16);
+            lo[k] = e4m3x4(g4[0] - a.x, g4[1] - a.y, g4[2] - b.x, g4[3] - b.y);
+          }
+          if (e0 < d) {
+            uint8_t* at = qd + (n >> 3) * 8 * d + (e0 >> 4) * 128 + (n & 7) * 16 + (e0 & 8);
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + kDrRows * d) = make_uint2(lo[0], lo[1]);
+          }
+          // an infinite element makes the row NaN, as its codes would not
+          if (lane == 0)
+            sh.fq[par][n] = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
+        }
+      }
+      tc::fence_async_smem();
+      dt_arrive(&sh.q_full);
+    };
+    unsigned T = 0;
+    int ip = 0, par = 0, items = 0;   // item and head parity, items with tiles
+    DtItem t{};
+    if (i0 < i1) {
+      t = dt_item<NT>(w, sh.items, i0);
+      load_q(t, 0);
+    }
+    for (int i = i0; i < i1; ++i) {
+      float l = 0.f, ref = -INFINITY;
+      const int row = (t.r0 + tid) / p.G, g = t.r0 + tid - row * p.G;
+      const int lim = t.L - t.n + row + 1;            // keys that the row sees (rows past the last: masked as the last)
+      const int least = t.L - t.n + t.r0 / p.G + 1;   // keys that every row of the tile sees
+      for (int j = 0; j < t.tiles; ++j, ++T) {
+        if ((int)(T & 1) != wg) continue;
+        const int kb = t.k0 + j * kDtTok, sc = T % NS, st = T % VS;   // scale slot, V stage
+        const uint32_t scol = lanes + (T & 1) * kDtTok;
+        ok = dt_wait(&sh.sc_full[sc], T / NS & 1, fail) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc::fence_after_sync();
+        const float fq = sh.fq[par][tid];
+        if (j == 0) sh.bad[ip][tid] = sh.bad[ip][tid + 128] = 0x7fffffff;   // before the other warpgroup's next tile
+        uint32_t s[4][32];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tc::tmem_ld32_nowait(scol + u * 32, s[u]);
+        // factors of the tile's blocks
+        float kf[kDtBlocks], lv[kDtBlocks];
+        bool part = kb + kDtTok > t.k1;
+#pragma unroll
+        for (int b = 0; b < kDtBlocks; ++b) {
+          const float ks = sh.ks[sc][b], vs = sh.vs[sc][b];
+          part = part || !(ks >= 0.f);
+          // scales are powers of two from 2^-64 up: the exponent is exact
+          lv[b] = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+          kf[b] = ks * fq;
+          if (kf[b] < 1.2e-38f) kf[b] = 1.2e-38f;   // stays positive: times -inf is a mask (NaN stays)
+        }
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tc::tmem_ld_fence(s[u]);
+        const bool edge = kb + kDtTok > least;        // some row does not see some token
+        if (part || edge) {
+          const int seen = min(lim, t.k1) - kb;
+#pragma unroll
+          for (int b = 0; b < kDtBlocks; ++b) {
+            const bool out = !(sh.ks[sc][b] >= 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (out || b * 16 + k >= seen) s[b / 2][b % 2 * 16 + k] = 0xff800000u;
+          }
+        }
+        // the weight's exponent x = s kf + lv grows with s: the block's largest s gives its largest x
+        float mx = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kDtBlocks; ++b) {
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            m0 = fmaxf(m0, __uint_as_float(s[b / 2][b % 2 * 16 + k]));
+            m1 = fmaxf(m1, __uint_as_float(s[b / 2][b % 2 * 16 + k + 1]));
+          }
+          mx = fmaxf(mx, fmaf(fmaxf(m0, m1), kf[b], lv[b]));
+        }
+        float alpha = 1.f;
+        const float before = ref;
+        if (j > 0) {   // the reference after the tile before, the other warpgroup's
+          ok = dt_wait(&sh.m_ready[wg ^ 1], ((T - 1) >> 1) & 1, fail);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          ref = sh.m[wg ^ 1][tid];
+        }
+        if (j == 0) {
+          ref = mx;
+        } else if (mx - ref > kDtGrow) {
+          // the reference moves only past the codes' headroom: a row's choice
+          // depends on that row alone
+          alpha = dt_ex2(ref - mx);
+          ref = mx;
+        }
+        sh.m[wg][tid] = ref;
+        dt_arrive(&sh.m_ready[wg]);
+        if (j > 1 && ref != before) l *= dt_ex2(before - ref);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int e = 0; e < d; e += 32) {
+            uint32_t a[16], b[16];
+            float o[16], o2[16];
+            tc::tmem_ld16x2(lanes + kDrO + e, lanes + kDrO + e + 16, o, o2);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) a[k] = __float_as_uint(o[k] * alpha), b[k] = __float_as_uint(o2[k] * alpha);
+            tc::tmem_st16u(lanes + kDrO + e, a);
+            tc::tmem_st16u(lanes + kDrO + e + 16, b);
+          }
+          tc::tmem_st_wait();
+        }
+        const float r = (ref == -INFINITY ? 0.f : ref) - kDtBase;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {   // 64 tokens: 16 columns of hi codes, 16 of lo codes
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int blk = u * 4 + b;
+            const f32x2 kk = pack2(kf[blk], kf[blk]), rr = pack2(lv[blk] - r, lv[blk] - r);
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t* q4 = &s[blk / 2][blk % 2 * 16 + 4 * k];
+              const float2 x = unpack2(fma2(pack2(__uint_as_float(q4[0]), __uint_as_float(q4[1])), kk, rr));
+              const float2 y = unpack2(fma2(pack2(__uint_as_float(q4[2]), __uint_as_float(q4[3])), kk, rr));
+              const float e0 = dt_ex2(x.x), e1 = dt_ex2(x.y), e2 = dt_ex2(y.x), e3 = dt_ex2(y.y);
+              sum += (e0 + e1) + (e2 + e3);
+              const uint32_t h = e4m3x4(e0, e1, e2, e3);
+              const float2 f = e4m3_f32x2(h), f2 = e4m3_f32x2(h >> 16);
+              hi[b * 4 + k] = h;
+              lo[b * 4 + k] = e4m3x4(e0 - f.x, e1 - f.y, e2 - f2.x, e3 - f2.y);
+            }
+            l = fmaf(sum, __uint_as_float((uint32_t)(127 - (int)lv[blk]) << 23), l);   // over the V scale
+          }
+          tc::tmem_st16u(scol + u * 16, hi);
+          tc::tmem_st16u(scol + 32 + u * 16, lo);
+        }
+        tc::tmem_st_wait();
+        if (edge) {
+          ok = dt_wait(&sh.v_full[st], T / VS & 1, fail);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          dt_clean(base + w.v_off + (uint32_t)st * unit, sh.bad[ip], t, kb, least, d, tid);
+          tc::fence_async_smem();
+        }
+        __syncwarp();
+        tc::fence_before_sync();
+        dt_arrive(&sh.p_full[T & 1]);
+      }
+      if (!ok) break;
+      // the next head's rows: its scores may then start while this item ends
+      const DtItem u = t;
+      const unsigned last = T - 1;   // the item's last tile
+      if (i + 1 < i1) {
+        dt_next<NT>(w, sh.items, i + 1, t);
+        if (dt_new_rows(t, false)) {
+          // (the last scores, if the other warpgroup's, have to be done with the rows)
+          if (u.tiles > 0) ok = dt_wait(&sh.s_full[last & 1], (last >> 1) & 1, fail);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          load_q(t, par ^= 1);
+        }
+      }
+      if (u.tiles > 0) {
+        // the row's sum: the warpgroup that had the last tile takes the other's,
+        // brought to its reference, and hands the total back; each then writes
+        // every second 32 elements
+        const int w1 = (int)(last & 1);
+        if (wg != w1) {
+          ok = dt_wait(&sh.m_ready[w1], (last >> 1) & 1, fail);
+          const float mine = ref;
+          ref = sh.m[w1][tid];
+          sh.m[wg][tid] = l == 0.f ? 0.f : l * dt_ex2(mine - ref);
+          dt_arrive(&sh.fin[0]);
+          ok = dt_wait(&sh.fin[1], items & 1, fail) && ok;
+          l = sh.m[w1][tid];
+        } else {
+          ok = dt_wait(&sh.fin[0], items & 1, fail);
+          l += sh.m[wg ^ 1][tid];
+          sh.m[wg][tid] = l;
+          dt_arrive(&sh.fin[1]);
+        }
+        ++items;
+        ok = ok && dt_wait(&sh.o_done[last & 1], (last >> 1) & 1, fail);
+      }
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc::fence_after_sync();
+      const bool mine = tid < u.rows;
+      const int64_t R = p.T * p.Hq, rh = (int64_t)(u.q0 + row) * p.Hq + u.h * p.G + g;
+      const float m = l == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) - kDtBase;
+      if (mine && wg == 0) {
+        if (p.part_o) p.part_ml[u.piece * R + rh] = make_float2(m, l);
+        else if (p.lse) p.lse[rh] = l == 0.f ? -INFINITY : m * 0.693147180559945309f + logf(l);
+      }
+      __syncwarp();
+      const bool check = u.tiles > 0 && u.k0 + u.tiles * kDtTok > least;   // some tile had values that not every row sees
+      float* po = p.part_o + (u.piece * R + rh) * d;
+      __nv_bfloat16* oo = static_cast<__nv_bfloat16*>(p.o) + rh * d;
+#pragma unroll 1
+      for (int e = 32 * wg; e < d; e += 64) {
+        float o[32];
+        if (u.tiles > 0) {
+          tc::tmem_ld32(lanes + kDrO + e, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (check) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (sh.bad[ip][e + k] < lim) o[k] = __int_as_float(0x7fffffff);
+        }
+        if (p.part_o) {
+          // through shared memory, so that a warp writes 64 bytes of two rows at a time
+          const int rows = min(32, u.rows - (warp & 3) * 32), col = lane & 15;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sh.turn[warp][lane][k] = o[hf * 16 + k];
+            __syncwarp();
+#pragma unroll 8
+            for (int k = 0; k < 32; k += 2) {
+              const int r = k + (lane >> 4);
+              const uintptr_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(po + e + hf * 16), r);
+              if (r < rows) *reinterpret_cast<float*>(at + 4 * col) = sh.turn[warp][r][col];
+            }
+            __syncwarp();
+          }
+        } else if (mine) {
+          {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t b[4];
+#pragma unroll
+              for (int i2 = 0; i2 < 4; ++i2) {
+                const float x = l == 0.f ? 0.f : o[k + 2 * i2] / l, y = l == 0.f ? 0.f : o[k + 2 * i2 + 1] / l;
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                b[i2] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              *reinterpret_cast<uint4*>(oo + e + k) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      tc::fence_before_sync();
+      // (a buffer comes back after an item whose tiles every warp has passed)
+      if (u.tiles > 0) ip ^= 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+  if (warp == 8 || warp == 9) {
     // ---- loads, a warp for K and one for V ----
-    loaded = dt_load<NT>(w, sh, base, i0, i1, warp == 5, lane);
-  } else if (warp == 6) {
+    loaded = dt_load<NT>(w, sh, base, i0, i1, warp == 9, lane);
+  } else if (warp == 10) {
     // ---- products: the whole warp, one lane issues ----
     {
       const uint32_t lead = tc::elect_one();
@@ -135,256 +437,6 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       tc::mma_commit_if(lead, &sh.drain);
       if (!tc::mbar_wait_bounded(&sh.drain, 0, kDtWait)) *fail = 1;
     }
-  } else {
-    // ---- softmax: a thread a row ----
-    const int tid = threadIdx.x;
-    const uint32_t lanes = tb + ((uint32_t)warp << 21);
-    uint8_t* qd = base + w.q_off;
-    bool ok = true;
-    float fq = 0.f;   // this row's score factor
-    // the rows of this warp as hi and lo codes, a row at a time, eight loads ahead
-    auto load_q = [&](const DtItem& t) {
-      const int e0 = lane * 8;
-#pragma unroll 1
-      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8) {
-        uint4 x[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int n = r0 + u;
-          x[u] = make_uint4(0, 0, 0, 0);
-          if (n < t.rows && e0 < d) {
-            const int row = (t.r0 + n) / p.G, g = t.r0 + n - row * p.G;
-            x[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(t.q0 + row) * p.q_stride +
-                                                   (int64_t)(t.h * p.G + g) * d + e0);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int n = r0 + u;
-          float f[8], amax = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t b = (&x[u].x)[k >> 1];
-            f[k] = __uint_as_float(k & 1 ? b & 0xffff0000u : b << 16);
-            amax = fmaxf(amax, fabsf(f[k]));
-          }
-          amax = warp_max(amax);
-          // largest element to (224, 448]; exponents kept where both factors are normal
-          int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
-          e = max(-100, min(100, e));
-          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float g4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g4[i] = f[4 * k + i] * inv;
-            hi[k] = e4m3x4(g4[0], g4[1], g4[2], g4[3]);
-            const float2 a = e4m3_f32x2(hi[k]), b = e4m3_f32x2(hi[k] >> 16);
-            lo[k] = e4m3x4(g4[0] - a.x, g4[1] - a.y, g4[2] - b.x, g4[3] - b.y);
-          }
-          if (e0 < d) {
-            uint8_t* at = qd + (n >> 3) * 8 * d + (e0 >> 4) * 128 + (n & 7) * 16 + (e0 & 8);
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + kDrRows * d) = make_uint2(lo[0], lo[1]);
-          }
-          // an infinite element makes the row NaN, as its codes would not
-          if (lane == n - warp * 32)
-            fq = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
-        }
-      }
-      tc::fence_async_smem();
-      dt_arrive(&sh.q_full);
-    };
-    unsigned T = 0;
-    int st = 0, sc = 0, scp = 0, vp = 0, ip = 0;   // V stage, scale slot and their phases; item
-    DtItem t{};
-    if (i0 < i1) {
-      t = dt_item<NT>(w, sh.items, i0);
-      load_q(t);
-    }
-    for (int i = i0; i < i1; ++i) {
-      float l = 0.f, ref = -INFINITY;
-      const int row = (t.r0 + tid) / p.G, g = t.r0 + tid - row * p.G;
-      const int lim = t.L - t.n + row + 1;            // keys that the row sees (rows past the last: masked as the last)
-      const int least = t.L - t.n + t.r0 / p.G + 1;   // keys that every row of the tile sees
-      if (t.tiles > 0) sh.bad[ip][tid] = sh.bad[ip][tid + 128] = 0x7fffffff;
-      for (int j = 0; j < t.tiles; ++j, ++T) {
-        const int kb = t.k0 + j * kDtTok;
-        const uint32_t scol = lanes + (T & 1) * kDtTok;
-        ok = dt_wait(&sh.sc_full[sc], scp, fail) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        tc::fence_after_sync();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) tc::tmem_ld32_nowait(scol + u * 32, s[u]);
-        // factors of the tile's blocks
-        float kf[kDtBlocks], lv[kDtBlocks];
-        bool part = kb + kDtTok > t.k1;
-#pragma unroll
-        for (int b = 0; b < kDtBlocks; ++b) {
-          const float ks = sh.ks[sc][b], vs = sh.vs[sc][b];
-          part = part || !(ks >= 0.f);
-          // scales are powers of two from 2^-64 up: the exponent is exact
-          lv[b] = (float)((int)(__float_as_uint(vs) >> 23) - 127);
-          kf[b] = ks * fq;
-          if (kf[b] < 1.2e-38f) kf[b] = 1.2e-38f;   // stays positive: times -inf is a mask (NaN stays)
-        }
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) tc::tmem_ld_fence(s[u]);
-        const bool edge = kb + kDtTok > least;        // some row does not see some token
-        if (part || edge) {
-          const int seen = min(lim, t.k1) - kb;
-#pragma unroll
-          for (int b = 0; b < kDtBlocks; ++b) {
-            const bool out = !(sh.ks[sc][b] >= 0.f);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (out || b * 16 + k >= seen) s[b / 2][b % 2 * 16 + k] = 0xff800000u;
-          }
-        }
-        // the weight's exponent x = s kf + lv grows with s: the block's largest s gives its largest x
-        float mx = -INFINITY;
-#pragma unroll
-        for (int b = 0; b < kDtBlocks; ++b) {
-          float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            m0 = fmaxf(m0, __uint_as_float(s[b / 2][b % 2 * 16 + k]));
-            m1 = fmaxf(m1, __uint_as_float(s[b / 2][b % 2 * 16 + k + 1]));
-          }
-          mx = fmaxf(mx, fmaf(fmaxf(m0, m1), kf[b], lv[b]));
-        }
-        float alpha = 1.f;
-        if (j == 0) {
-          ref = mx;
-        } else if (mx - ref > kDtGrow) {
-          // the reference moves only past the codes' headroom: a row's choice
-          // depends on that row alone
-          alpha = dt_ex2(ref - mx);
-          ref = mx;
-          l *= alpha;
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-          ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int e = 0; e < d; e += 32) {
-            uint32_t a[16], b[16];
-            float o[16], o2[16];
-            tc::tmem_ld16x2(lanes + kDrO + e, lanes + kDrO + e + 16, o, o2);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) a[k] = __float_as_uint(o[k] * alpha), b[k] = __float_as_uint(o2[k] * alpha);
-            tc::tmem_st16u(lanes + kDrO + e, a);
-            tc::tmem_st16u(lanes + kDrO + e + 16, b);
-          }
-          tc::tmem_st_wait();
-        }
-        const float r = (ref == -INFINITY ? 0.f : ref) - kDtBase;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {   // 64 tokens: 16 columns of hi codes, 16 of lo codes
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int blk = u * 4 + b;
-            const f32x2 kk = pack2(kf[blk], kf[blk]), rr = pack2(lv[blk] - r, lv[blk] - r);
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t* q4 = &s[blk / 2][blk % 2 * 16 + 4 * k];
-              const float2 x = unpack2(fma2(pack2(__uint_as_float(q4[0]), __uint_as_float(q4[1])), kk, rr));
-              const float2 y = unpack2(fma2(pack2(__uint_as_float(q4[2]), __uint_as_float(q4[3])), kk, rr));
-              const float e0 = dt_ex2(x.x), e1 = dt_ex2(x.y), e2 = dt_ex2(y.x), e3 = dt_ex2(y.y);
-              sum += (e0 + e1) + (e2 + e3);
-              const uint32_t h = e4m3x4(e0, e1, e2, e3);
-              const float2 f = e4m3_f32x2(h), f2 = e4m3_f32x2(h >> 16);
-              hi[b * 4 + k] = h;
-              lo[b * 4 + k] = e4m3x4(e0 - f.x, e1 - f.y, e2 - f2.x, e3 - f2.y);
-            }
-            l = fmaf(sum, __uint_as_float((uint32_t)(127 - (int)lv[blk]) << 23), l);   // over the V scale
-          }
-          tc::tmem_st16u(scol + u * 16, hi);
-          tc::tmem_st16u(scol + 32 + u * 16, lo);
-        }
-        tc::tmem_st_wait();
-        if (edge) {
-          ok = dt_wait(&sh.v_full[st], vp, fail);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          dt_clean(base + w.v_off + (uint32_t)st * unit, sh.bad[ip], t, kb, least, d, tid);
-          tc::fence_async_smem();
-        }
-        __syncwarp();
-        tc::fence_before_sync();
-        dt_arrive(&sh.p_full[T & 1]);
-        if (++st == VS) st = 0, vp ^= 1;
-        if (++sc == NS) sc = 0, scp ^= 1;
-      }
-      if (!ok) break;
-      // the next head's rows: its scores may then start while this item ends
-      const DtItem u = t;
-      if (i + 1 < i1) {
-        dt_next<NT>(w, sh.items, i + 1, t);
-        if (dt_new_rows(t, false)) load_q(t);
-      }
-      if (u.tiles > 0) ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      tc::fence_after_sync();
-      const bool mine = tid < u.rows;
-      const int64_t R = p.T * p.Hq, rh = (int64_t)(u.q0 + row) * p.Hq + u.h * p.G + g;
-      const float m = l == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) - kDtBase;
-      if (mine) {
-        if (p.part_o) p.part_ml[u.piece * R + rh] = make_float2(m, l);
-        else if (p.lse) p.lse[rh] = l == 0.f ? -INFINITY : m * 0.693147180559945309f + logf(l);
-      }
-      __syncwarp();
-      const bool check = u.tiles > 0 && u.k0 + u.tiles * kDtTok > least;   // some tile had values that not every row sees
-      float* po = p.part_o + (u.piece * R + rh) * d;
-      __nv_bfloat16* oo = static_cast<__nv_bfloat16*>(p.o) + rh * d;
-#pragma unroll 1
-      for (int e = 0; e < d; e += 32) {
-        float o[32];
-        if (u.tiles > 0) {
-          tc::tmem_ld32(lanes + kDrO + e, o);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        }
-        if (check) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (sh.bad[ip][e + k] < lim) o[k] = __int_as_float(0x7fffffff);
-        }
-        if (p.part_o) {
-          // through shared memory, so that a warp writes 128 bytes of one row at a time
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sh.turn[warp][lane][k] = o[k];
-          __syncwarp();
-          const int rows = min(32, u.rows - warp * 32);
-#pragma unroll 8
-          for (int k = 0; k < rows; ++k)
-            *reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(po + e), k) + 4 * lane) = sh.turn[warp][k][lane];
-        } else if (mine) {
-          {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t b[4];
-#pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) {
-                const float x = l == 0.f ? 0.f : o[k + 2 * i2] / l, y = l == 0.f ? 0.f : o[k + 2 * i2 + 1] / l;
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                b[i2] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              *reinterpret_cast<uint4*>(oo + e + k) = make_uint4(b[0], b[1], b[2], b[3]);
-            }
-          }
-        }
-        __syncwarp();
-      }
-      tc::fence_before_sync();
-      // (a buffer comes back after an item whose tiles every warp has passed)
-      if (u.tiles > 0) ip ^= 1;
     }
   }
   __syncwarp();
@@ -394,12 +446,12 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
-    if ((warp == 4 || warp == 5) && lane == 0) dt_drain(w, sh, loaded, warp == 5);
+    if ((warp == 8 || warp == 9) && lane == 0) dt_drain(w, sh, loaded, warp == 9);
     __syncwarp();
     __syncthreads();
   }
   tc::fence_after_sync();
-  if (warp == 4) tc::tmem_dealloc(tb, 512);
+  if (warp == 8) tc::tmem_dealloc(tb, 512);
   // done when the kernel before this one (the call's other sequences) is
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
