@@ -8,7 +8,9 @@
 // long that takes decides how idle the tensor cores are, so each of two row
 // tiles (up to d = 128) has two warpgroups, a row's 128 scores in two threads
 // which exchange their maxima; at d = 256, where the outputs of one row tile
-// take half of tensor memory, two warpgroups take its key tiles in turn, the
+// take half of tensor memory and its keys and values more of L2 than there is,
+// two CTAs share every key tile (cta_group::2: half of its keys and half of its
+// values' elements in each) and two warpgroups take its key tiles in turn, the
 // running maximum passing from one to the other before the exponentials, so
 // that those of two key tiles overlap.
 #include <cuda.h>
@@ -24,14 +26,16 @@ namespace {
 constexpr int kTile = 128;          // rows and keys of a tile
 constexpr long long kPreWait = 4000000000LL;
 
-template <int D>
+template <int D, bool PAIR>
 struct PreCfg {
   static constexpr int NQ = D == 256 ? 1 : 2;            // row tiles a CTA
   static constexpr int SLOTS = D == 256 ? 2 : 1;         // score buffers a row tile
   static constexpr int UD = D < 128 ? D : 128;           // head elements of a staged unit
   static constexpr int U = D / UD;                       // units of a key tile
-  static constexpr uint32_t UNIT = kTile * UD * 2;
-  static constexpr int STAGES = D == 64 ? 8 : 5;
+  static constexpr int CTAS = PAIR ? 2 : 1;              // that share a key tile
+  static constexpr uint32_t UNIT = kTile * UD * 2 / CTAS;
+  static constexpr int STAGES = D == 64 ? 8 : 5 * CTAS;
+  static constexpr int KROWS = kTile / CTAS, VCOLS = UD / CTAS;   // of a unit of K, of V, in this CTA
   static constexpr uint32_t Q_BYTES = kTile * D * 2;
   static constexpr uint32_t DATA = NQ * Q_BYTES + STAGES * UNIT;
   static constexpr bool ALT = D == 256;                  // key tiles in turn instead of rows in two halves
@@ -42,22 +46,110 @@ struct PreCfg {
   static constexpr int REGS = ALT ? 216 : 104, REGS_REST = ALT ? 72 : 64;
   // tensor memory columns: scores (the weights overwrite them), then outputs
   static constexpr uint32_t S0 = 0, O0 = 256;
-  // registers: a softmax thread holds a row's 128 scores
 };
 
-template <int D>
+template <class C, int D>
 struct PreShared {
-  uint64_t full[PreCfg<D>::STAGES], empty[PreCfg<D>::STAGES], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], m_ready[4], fin[2], drain;
-  float m[PreCfg<D>::SW / 4][kTile];   // by warpgroup: d = 256: its reference of each row; else its scores' maxima; at the end its sums
+  uint64_t full[C::STAGES], empty[C::STAGES], s_full[2], p_full[2], o_done[2], q_full[2], v_raw[8], v_ok[8], m_ready[4], fin[2], drain;
+  float m[C::SW / 4][kTile];   // by warpgroup: d = 256: its reference of each row; else its scores' maxima; at the end its sums
   uint32_t tmem;
-  int fail, bad_any;
+  int fail, bad_any, issued[2];   // (issued: units loaded by each CTA of a pair)
   // by element of V the first key with +inf, -inf, NaN, counted from the first
-  // guarded tile's (a CTA's rows guard at most 512): 10 bits each, ones: none
+  // guarded tile's (a pair's rows guard at most 768): 10 bits each, ones: none
   uint32_t bad[D];
 };
-template <int D>
-constexpr uint32_t kPreSmem = PreCfg<D>::DATA + sizeof(PreShared<D>);
-static_assert(kPreSmem<256> <= 232448 && kPreSmem<128> <= 232448 && kPreSmem<64> <= 232448, "227 KB a CTA");
+template <int D, bool PAIR>
+constexpr uint32_t kPreSmem = PreCfg<D, PAIR>::DATA + sizeof(PreShared<PreCfg<D, PAIR>, D>);
+static_assert(kPreSmem<256, true> <= 232448 && kPreSmem<256, false> <= 232448 && kPreSmem<128, false> <= 232448 &&
+                  kPreSmem<64, false> <= 232448,
+              "227 KB a CTA");
+
+// ---- the two CTAs of a pair -----------------------------------------------------
+// The same place of shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_smem(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ T* peer_ptr(T* p, uint32_t rank) {   // for ordinary loads, stores and atomics
+  uint64_t r;
+  asm volatile("mapa.u64 %0, %1, %2;\n" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<T*>(r);
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
+// What orders tensor memory is the fence before it, not this.
+__device__ __forceinline__ void arrive_at_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// A tile load that reports to a barrier of either CTA.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Products of a pair: 256 rows, 128 in each CTA, against an operand of which
+// each CTA holds half; issued by one CTA for both.
+template <bool PAIR>
+__device__ __forceinline__ void pre_mma(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if constexpr (!PAIR) {
+    tc::mma_bf16_if(lead, d, a, b, id, acc);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+        : "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void pre_mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  if constexpr (!PAIR) {
+    tc::mma_bf16_ts_if(lead, d, a, b, id, acc);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+        : "memory");
+  }
+}
+// Arrival, on this barrier in every CTA of the pair, once the products so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void pre_commit(uint32_t lead, uint64_t* m) {
+  if constexpr (!PAIR) {
+    tc::mma_commit_if(lead, m);
+  } else {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}\n" ::"r"(
+            smem_u32(m)),
+        "r"(lead), "h"((uint16_t)3)
+        : "memory");
+  }
+}
+// As if bytes of a copy had arrived.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* m, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(m)), "r"(bytes) : "memory");
+}
+// The wait of one who then reads what the other CTA has written.
+__device__ __forceinline__ bool mbar_test_cluster(uint64_t* m, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(m)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 
 // Minimum of the 10-bit field of a word in shared memory that starts at bit `at`.
 __device__ __forceinline__ void min10(uint32_t* w, int at, uint32_t v) {
@@ -70,9 +162,11 @@ __device__ __forceinline__ void min10(uint32_t* w, int at, uint32_t v) {
 }
 
 // Waits for a phase: bounded, and given up at once when another role has.
-__device__ __forceinline__ bool pre_wait_slow(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool pre_wait(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
+  if (CLUSTER ? mbar_test_cluster(m, parity) : tc::mbar_test_wait(m, parity)) return true;
   const long long t0 = clock64();
-  while (!tc::mbar_try_wait(m, parity)) {
+  while (!(CLUSTER ? mbar_test_cluster(m, parity) : tc::mbar_try_wait(m, parity))) {
     if (*fail) return false;
     if (clock64() - t0 > limit) {
       *fail = 1;
@@ -80,10 +174,6 @@ __device__ __forceinline__ bool pre_wait_slow(uint64_t* m, uint32_t parity, long
     }
   }
   return true;
-}
-__device__ __forceinline__ bool pre_wait(uint64_t* m, uint32_t parity, long long limit, volatile int* fail) {
-  if (tc::mbar_test_wait(m, parity)) return true;
-  return pre_wait_slow(m, parity, limit, fail);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* m) {
@@ -108,7 +198,8 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 
 // Shared-memory descriptor of V as the N x K operand with N contiguous: rows of
 // 64 elements (128 B, swizzled) for one key, 8-key groups 1,024 B apart, the
-// next 64 elements a whole block of keys (128 x 128 B) further.
+// next 64 elements (which a CTA of a pair does not hold) a whole block of keys
+// (128 x 128 B) further.
 __device__ __forceinline__ uint64_t desc_v(uint32_t saddr) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
@@ -125,14 +216,14 @@ struct PreTile {
   int s, h, q0, n, k0, L;
   int64_t r0;            // first row (token * G + head) of the CTA's first tile
   int nk[2], nkmax;      // key tiles of each row tile
-  int least;             // keys that every row sees
+  int least;             // keys that every row sees (of the pair)
 };
 
-template <int D>
+template <class C>
 __device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t, bool report) {
-  constexpr int NQ = PreCfg<D>::NQ;
-  const int pairs = p.N * p.Hkv;
-  const int back = blockIdx.x / pairs, pr = blockIdx.x - back * pairs;
+  constexpr int NQ = C::NQ, ROWS = C::CTAS * NQ * kTile;   // rows of the CTA, or of the pair's
+  const int groups = p.N * p.Hkv, block = blockIdx.x / C::CTAS, rank = blockIdx.x % C::CTAS;
+  const int back = block / groups, pr = block - back * groups;
   t.s = pr / p.Hkv;
   t.h = pr - t.s * p.Hkv;
   t.q0 = p.cu_q[t.s];
@@ -146,33 +237,50 @@ __device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t,
     return false;
   }
   const int64_t rows = (int64_t)t.n * p.G;
-  const int tiles = (int)((rows + NQ * kTile - 1) / (NQ * kTile));
+  const int tiles = (int)((rows + ROWS - 1) / ROWS);
   if (back >= tiles) return false;
-  t.r0 = (int64_t)(tiles - 1 - back) * NQ * kTile;   // the last rows, which see the most keys, first
+  const int64_t first = (int64_t)(tiles - 1 - back) * ROWS;   // the last rows, which see the most keys, first
+  t.r0 = first + rank * NQ * kTile;
   t.nkmax = 0;
   for (int q = 0; q < 2; ++q) {
-    const int64_t r = t.r0 + q * kTile;
+    // key tiles of row tile q: of a pair's two the more (its products are one)
     t.nk[q] = 0;
-    if (q < NQ && r < rows) {
+    for (int c = 0; c < C::CTAS; ++c) {
+      const int64_t r = first + (c * NQ + q) * kTile;
+      if (q >= NQ || r >= rows) continue;
       const int last = (int)min((int64_t)t.n - 1, (r + kTile - 1) / p.G);
-      t.nk[q] = (max(0, t.L - t.n + last + 1) + kTile - 1) / kTile;
+      t.nk[q] = max(t.nk[q], (max(0, t.L - t.n + last + 1) + kTile - 1) / kTile);
     }
     t.nkmax = max(t.nkmax, t.nk[q]);
   }
-  t.least = max(0, t.L - t.n + (int)(t.r0 / p.G) + 1);
+  t.least = max(0, t.L - t.n + (int)(first / p.G) + 1);
   return true;
+}
+
+// Whether unit n in the ring's order (K 0, with one row tile K 1; then V j and
+// the next K in turn) is one of V for the guards.
+template <class C>
+__device__ __forceinline__ bool pre_guarded(const PreTile& t, int n) {
+  constexpr int ahead = C::NQ == 1 ? 2 : 1;
+  int tile = n / C::U;
+  const int lead = min(ahead, t.nkmax), both = 2 * (t.nkmax - lead);
+  if (tile < lead) return false;
+  tile -= lead;
+  if (tile < both && (tile & 1)) return false;
+  const int j = tile < both ? tile >> 1 : (both >> 1) + tile - both;
+  return (j + 1) * kTile > t.least;
 }
 
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
     attn_prefill_tc_kernel(const AttnPrefillParams p, const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap) {
-  using C = PreCfg<D>;
+  using C = PreCfg<D, PAIR>;
   extern __shared__ __align__(1024) uint8_t base[];
   PreTile t;
-  if (!pre_tile<D>(p, t, threadIdx.x == 0)) return;
+  if (!pre_tile<C>(p, t, threadIdx.x == 0)) return;   // (both CTAs of a pair)
   // the swizzled tiles need the 1,024-byte alignment that shared memory without
   // static variables starts with: there is no room to make it up
   if (smem_u32(base) & 1023u) {
@@ -181,7 +289,8 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
   }
   uint8_t* sq = base;
   uint8_t* ring = base + C::NQ * C::Q_BYTES;
-  PreShared<D>& sh = *reinterpret_cast<PreShared<D>*>(base + C::DATA);
+  PreShared<C, D>& sh = *reinterpret_cast<PreShared<C, D>*>(base + C::DATA);
+  const uint32_t rank = PAIR ? blockIdx.x & 1 : 0;   // 0: the CTA that issues the products
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = p.wait_cycles > 0 ? p.wait_cycles : p.wait_cycles < 0 ? -1 : kPreWait;
   volatile int* fail = &sh.fail;
@@ -189,11 +298,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sh.s_full[i], 1);
-      tc::mbar_init(&sh.p_full[i], C::ALT ? 128 : 256);
+      tc::mbar_init(&sh.p_full[i], (C::ALT ? 4 : 8) * C::CTAS);   // a warp arrives once
       tc::mbar_init(&sh.o_done[i], 1);
-      tc::mbar_init(&sh.q_full[i], 256);
+      tc::mbar_init(&sh.q_full[i], 8 * C::CTAS);
     }
-    for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], C::U == 2 ? 32 : 64);
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], (C::U == 2 ? 1 : 2) * C::CTAS);
     for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.m_ready[i], 128);
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.fin[i], C::ALT ? 128 : 256);
     tc::mbar_init(&sh.drain, 1);
@@ -202,16 +311,28 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
   }
   for (int i = threadIdx.x; i < D; i += C::THREADS) sh.bad[i] = 0x3fffffffu;
   if (warp == 0) {
-    tc::tmem_alloc(&sh.tmem, 512);
-    tc::tmem_relinquish();
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sh.tmem)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+    } else {
+      tc::tmem_alloc(&sh.tmem, 512);
+      tc::tmem_relinquish();
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
+  if (PAIR) cluster_sync();   // the other's barriers are there too
   tc::fence_after_sync();
+  // one arrival of a warp on a barrier of the CTA that issues the products
+  auto arrive_lead = [&](uint64_t* m) {
+    __syncwarp();
+    if (lane != 0) return;
+    if (PAIR) arrive_at(peer_smem(m, 0));
+    else mbar_arrive(m);
+  };
   const uint32_t tb = sh.tmem;
   const int wg = warp >> 2;
   int issued = 0, raw = 0;   // units loaded, those of them for the guards first (the loading thread's)
-  uint32_t raw_bits = 0;     // which of the last 32 went to the guards
 
   if (warp < C::SW) {
     // ---- softmax: row i of tile q; its keys' half, or (d = 256) every second key tile ----
@@ -245,7 +366,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       for (int k = 0; k < NP; ++k)
         *reinterpret_cast<uint4*>(sq + q * C::Q_BYTES + tc::sw128_offset(w0 + k * RP, c8, kTile)) = w[k];
       tc::fence_async_smem();
-      mbar_arrive(&sh.q_full[q]);
+      arrive_lead(&sh.q_full[q]);
     }
     float m = -INFINITY, l = 0.f;
     const float c = p.scale_log2;
@@ -353,14 +474,19 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       l += sum2(add2(sum[0], sum[1]));
       tc::tmem_st_wait();
       tc::fence_before_sync();
-      mbar_arrive(&sh.p_full[b]);
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) arrive_at_relaxed(peer_smem(&sh.p_full[b], 0));
+        else mbar_arrive(&sh.p_full[b]);
+      }
     }
     // ---- outputs ----
     if (nk > 0 && limit >= 0) {
       if (!ok) *fail = 1;
       if (!ALT) {
-        // the row's sum: the two halves' (the maxima's places are free: both
-        // have had the last tile's)
+        // the row's sum: the two halves', where the maxima were once the last
+        // products say that both halves have had those
+        ok = ok && o_wait(nk - 1);
         sh.m[wg][i] = l;
         mbar_arrive(&sh.fin[q]);
         ok = pre_wait(&sh.fin[q], 0, limit, fail) && ok;
@@ -386,6 +512,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       }
     }
     if (ok && nk > 0) ok = o_wait(nk - 1);
+    if (PAIR) asm volatile("fence.acq_rel.cluster;\n" ::: "memory");   // and what the other CTA noted of V
     if (__all_sync(0xffffffffu, ok)) {
       tc::fence_after_sync();
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -452,12 +579,28 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       for (int u = 0; u < C::U; ++u) {
         const int st = issued % C::STAGES;
         if (issued >= C::STAGES && !pre_wait(&sh.empty[st], (uint32_t)(issued / C::STAGES - 1) & 1, limit, fail)) return false;
-        uint64_t* bar = guarded ? &sh.v_raw[raw++ & 7] : &sh.full[st];
-        tc::mbar_expect_tx(bar, C::UNIT);
-        for (int b = 0; b < C::UD / 64; ++b)
-          tc::tma_load_3d(ring + st * C::UNIT + b * (kTile * 128), map, u * C::UD + b * 64, t.h, t.k0 + j * kTile, bar);
+        if constexpr (PAIR) {
+          // each CTA its half: keys of K, elements of V; the bytes of both count
+          // on the issuing CTA's barrier, what the guards take on their own CTA's
+          const bool is_v = map == &vmap;
+          uint64_t* bar = guarded ? &sh.v_raw[raw++ & 7] : &sh.full[st];
+          if (guarded) tc::mbar_expect_tx(bar, C::UNIT);
+          else if (rank == 0) tc::mbar_expect_tx(bar, 2 * C::UNIT);
+          const uint32_t at = guarded ? peer_smem(bar, rank) : peer_smem(bar, 0);
+          if (is_v) {
+            tma_load_3d_pair(ring + st * C::UNIT, map, u * C::UD + rank * C::VCOLS, t.h, t.k0 + j * kTile, at);
+          } else {
+            for (int b = 0; b < C::UD / 64; ++b)
+              tma_load_3d_pair(ring + st * C::UNIT + b * (C::KROWS * 128), map, u * C::UD + b * 64, t.h,
+                               t.k0 + j * kTile + rank * C::KROWS, at);
+          }
+        } else {
+          uint64_t* bar = guarded ? &sh.v_raw[raw++ & 7] : &sh.full[st];
+          tc::mbar_expect_tx(bar, C::UNIT);
+          for (int b = 0; b < C::UD / 64; ++b)
+            tc::tma_load_3d(ring + st * C::UNIT + b * (kTile * 128), map, u * C::UD + b * 64, t.h, t.k0 + j * kTile, bar);
+        }
         ++issued;
-        raw_bits = raw_bits << 1 | (guarded ? 1u : 0u);
       }
       return true;
     };
@@ -467,11 +610,11 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     constexpr int ahead = C::NQ == 1 ? 2 : 1;
     for (int j = 0; ok && j < t.nkmax; ++j) 
       ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + ahead >= t.nkmax || tile(&kmap, j + ahead, false));
-  } else if (warp == C::SW + 1 && limit >= 0) {
+  } else if (warp == C::SW + 1 && limit >= 0 && rank == 0) {
     // ---- products: the whole warp, one lane issues ----
     const uint32_t lead = tc::elect_one();
-    constexpr uint32_t id_qk = tc::idesc_bf16_f32(kTile, kTile);
-    constexpr uint32_t id_pv = tc::idesc_bf16_f32(kTile, C::UD) | kTransposedB;
+    constexpr uint32_t id_qk = tc::idesc_bf16_f32(C::CTAS * kTile, kTile);
+    constexpr uint32_t id_pv = tc::idesc_bf16_f32(C::CTAS * kTile, C::UD) | kTransposedB;
     const uint64_t qdesc = tc::desc_sw128(smem_u32(sq)), kdesc = tc::desc_sw128(smem_u32(ring)), vdesc = desc_v(smem_u32(ring));
     int st = 0, guarded = 0;   // the ring's place that is taken next
     uint32_t ph = 0;
@@ -483,15 +626,16 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
       const uint64_t a = qdesc + ((q * C::Q_BYTES + u * (C::UD / 64) * (kTile * 128)) >> 4), b = kdesc + (s * C::UNIT >> 4);
 #pragma unroll
       for (int ks = 0; ks < C::UD / 16; ++ks) {
-        const uint64_t off = ((uint32_t)(ks >> 2) * (kTile * 128) + (uint32_t)(ks & 3) * 32u) >> 4;
-        tc::mma_bf16_if(lead, tb + scol, a + off, b + off, id_qk, u != 0 || ks != 0);
+        const uint64_t oa = ((uint32_t)(ks >> 2) * (kTile * 128) + (uint32_t)(ks & 3) * 32u) >> 4;
+        const uint64_t ob = ((uint32_t)(ks >> 2) * (C::KROWS * 128) + (uint32_t)(ks & 3) * 32u) >> 4;
+        pre_mma<PAIR>(lead, tb + scol, a + oa, b + ob, id_qk, u != 0 || ks != 0);
       }
     };
     auto pv_unit = [&](int q, uint32_t pcol, int s, int u, bool acc) {
       const uint64_t b = vdesc + (s * C::UNIT >> 4);
 #pragma unroll
       for (int ks = 0; ks < kTile / 16; ++ks)
-        tc::mma_bf16_ts_if(lead, tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv,
+        pre_mma_ts<PAIR>(lead, tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv,
                            acc || ks != 0);
     };
     // a look at a barrier ahead of its use, so that the answer is there when
@@ -502,7 +646,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     auto v_ready = [&](int s, uint32_t p, int j) {
       if ((j + 1) * kTile <= t.least) return full(s, p);
       const int k = guarded++;
-      if (!pre_wait(&sh.v_ok[k & 7], (uint32_t)(k >> 3) & 1, limit, fail)) return false;
+      if (!pre_wait<PAIR>(&sh.v_ok[k & 7], (uint32_t)(k >> 3) & 1, limit, fail)) return false;
       if (lead) mbar_arrive(&sh.full[s]);
       __syncwarp();
       return true;
@@ -511,7 +655,7 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
     auto all = [&](bool x) { return __all_sync(0xffffffffu, x) != 0; };
     if constexpr (C::NQ == 1) {
       static_assert(C::U == 2, "two units a key tile");
-      ok = t.nkmax == 0 || all(pre_wait(&sh.q_full[0], 0, limit, fail));
+      ok = t.nkmax == 0 || all(pre_wait<PAIR>(&sh.q_full[0], 0, limit, fail));
       // a wait for each unit of 32 KB: the ring holds five, so the next one is
       // often still on its way
       bool seen = false;   // whether the next unit has been seen to be there
@@ -527,10 +671,10 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           if (!seen && !all(full(st, ph))) return false;
           unit(false);
           qk_unit(0, C::S0 + (j & 1) * 128, st, u);
-          tc::mma_commit_if(lead, &sh.empty[st]);
+          pre_commit<PAIR>(lead, &sh.empty[st]);
           step(st, ph);
         }
-        tc::mma_commit_if(lead, &sh.s_full[j & 1]);
+        pre_commit<PAIR>(lead, &sh.s_full[j & 1]);
         return true;
       };
       auto pv = [&](int j) {
@@ -542,17 +686,17 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           if ((guards || !seen) && !all(v_ready(st, ph, j))) return false;
           unit(guards);
           pv_unit(0, C::S0 + (j & 1) * 128, st, u, j != 0);
-          tc::mma_commit_if(lead, &sh.empty[st]);
+          pre_commit<PAIR>(lead, &sh.empty[st]);
           step(st, ph);
         }
-        tc::mma_commit_if(lead, &sh.o_done[j & 1]);
+        pre_commit<PAIR>(lead, &sh.o_done[j & 1]);
         return true;
       };
       if (ok && t.nkmax > 0) ok = qk(0);
       if (ok && t.nkmax > 1) ok = qk(1);
       for (int j = 0; ok && j < t.nkmax; ++j) ok = pv(j) && (j + 2 >= t.nkmax || qk(j + 2));
     } else {
-      for (int q = 0; ok && q < 2; ++q) ok = t.nk[q] == 0 || all(pre_wait(&sh.q_full[q], 0, limit, fail));
+      for (int q = 0; ok && q < 2; ++q) ok = t.nk[q] == 0 || all(pre_wait<PAIR>(&sh.q_full[q], 0, limit, fail));
       if (ok && t.nkmax > 0) {
         ok = all(full(0, 0));
         if (ok) {
@@ -560,9 +704,9 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           for (int q = 0; q < 2; ++q)
             if (t.nk[q] > 0) {
               qk_unit(q, C::S0 + q * 128, 0, 0);
-              tc::mma_commit_if(lead, &sh.s_full[q]);
+              pre_commit<PAIR>(lead, &sh.s_full[q]);
             }
-          tc::mma_commit_if(lead, &sh.empty[0]);
+          pre_commit<PAIR>(lead, &sh.empty[0]);
         }
         step(st, ph);
       }
@@ -578,23 +722,23 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           if (!ok) break;
           tc::fence_after_sync();
           pv_unit(q, C::S0 + q * 128, st, 0, j != 0);
-          tc::mma_commit_if(lead, &sh.o_done[q]);
+          pre_commit<PAIR>(lead, &sh.o_done[q]);
           if (j + 1 < t.nk[q]) {
             qk_unit(q, C::S0 + q * 128, s1, 0);
-            tc::mma_commit_if(lead, &sh.s_full[q]);
+            pre_commit<PAIR>(lead, &sh.s_full[q]);
           }
         }
         if (!ok) break;
-        tc::mma_commit_if(lead, &sh.empty[st]);
+        pre_commit<PAIR>(lead, &sh.empty[st]);
         if (more) {
-          tc::mma_commit_if(lead, &sh.empty[s1]);
+          pre_commit<PAIR>(lead, &sh.empty[s1]);
           step(st, ph);
         }
         step(st, ph);
       }
     }
     // every product issued, and every arrival on a barrier, before the end
-    tc::mma_commit_if(lead, &sh.drain);
+    pre_commit<PAIR>(lead, &sh.drain);
     if (!tc::mbar_wait_bounded(&sh.drain, 0, kPreWait)) *fail = 1;
   } else if (warp >= C::SW + 2 && limit >= 0) {
     // ---- guards: in V tiles that some row sees in part, keys past the
@@ -635,56 +779,88 @@ __global__ void __launch_bounds__(PreCfg<D>::THREADS, 1)
           const __nv_bfloat162 a = __hadd2(__hadd2(sum[0], sum[1]), __hadd2(sum[2], sum[3]));
           if (!__hisnan(a.x) && !__hisnan(a.y)) continue;
           for (int x = x0; x < x0 + 8 * GT; x += GT) {
-            const int row = x >> 3 & (kTile - 1), col = u * C::UD + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
+            const int row = x >> 3 & (kTile - 1), col = u * C::UD + rank * C::VCOLS + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
             for (int i = 0; i < 8; ++i) {
               uint16_t* el = reinterpret_cast<uint16_t*>(v + x * 16) + i;
               const uint16_t b = *el;
               if ((b & 0x7f80u) != 0x7f80u) continue;
-              min10(&sh.bad[col + i], (b & 0x7f) ? 20 : (b & 0x8000u) ? 10 : 0, j * kTile + row - t.least / kTile * kTile);
+              const int bit = (b & 0x7f) ? 20 : (b & 0x8000u) ? 10 : 0, key = j * kTile + row - t.least / kTile * kTile;
+              min10(&sh.bad[col + i], bit, key);
+              if (PAIR) min10(peer_ptr(&sh.bad[col + i], rank ^ 1), bit, key);
               *el = 0;
             }
           }
           *(volatile int*)&sh.bad_any = 1;
+          if (PAIR) *(volatile int*)peer_ptr(&sh.bad_any, rank ^ 1) = 1;
         }
         tc::fence_async_smem();
-        mbar_arrive(&sh.v_ok[k & 7]);
+        if (PAIR) asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+        arrive_lead(&sh.v_ok[k & 7]);
       }
     }
   }
   }
+  if constexpr (PAIR) {   // each CTA learns how far the other came
+    if (warp == C::SW && lane == 0) sh.issued[rank] = issued, *(volatile int*)peer_ptr(&sh.issued[rank], rank ^ 1) = issued;
+  }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
-  if (sh.fail) {
+  if constexpr (PAIR) {
+    if (threadIdx.x == 0 && *fail) *(volatile int*)peer_ptr(&sh.fail, rank ^ 1) = 1;
+    __syncwarp();
+    cluster_sync();
+    // the last arrival from the issuing CTA
+    if (rank == 1 && threadIdx.x == 0 && limit >= 0) tc::mbar_wait_bounded(&sh.drain, 0, kPreWait);
+    __syncwarp();
+  }
+  if (*fail) {
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
-    if (warp == C::SW && lane == 0)
-    {
-      for (int n = issued - 1, k = raw - 1; n >= 0 && n >= issued - C::STAGES; --n, raw_bits >>= 1) {
-        if (raw_bits & 1) {
-          tc::mbar_wait_bounded(&sh.v_raw[k & 7], (uint32_t)(k >> 3) & 1, kPreWait);
-          --k;
-        } else {
-          tc::mbar_wait_bounded(&sh.full[n % C::STAGES], (uint32_t)(n / C::STAGES) & 1, kPreWait);
+    if (warp == C::SW && lane == 0) {
+      // a pair's bytes of K and of whole V tiles count on the issuing CTA's
+      // barriers, which waits for both: with the same units on both sides
+      int first = issued, last = issued, k = raw - 1;
+      if (PAIR && rank == 0) {
+        const int other = *(volatile int*)&sh.issued[1];
+        first = min(first, other), last = max(last, other);
+      }
+      for (int n = last - 1; n >= 0 && n >= last - C::STAGES; --n) {
+        const bool mine = n < issued, guarded = pre_guarded<C>(t, n);
+        if (guarded) {
+          if (mine) tc::mbar_wait_bounded(&sh.v_raw[k & 7], (uint32_t)(k >> 3) & 1, kPreWait), --k;
+        } else if (rank == 0) {
+          uint64_t* bar = &sh.full[n % C::STAGES];
+          if (PAIR && n >= first) {
+            if (mine) mbar_complete_tx(bar, C::UNIT);   // the other's half does not come
+            else tc::mbar_expect_tx(bar, C::UNIT);      // only the other's half comes
+          }
+          tc::mbar_wait_bounded(bar, (uint32_t)(n / C::STAGES) & 1, kPreWait);
         }
       }
     }
     __syncwarp();
     __syncthreads();
   }
+  __syncwarp();
+  if (PAIR) cluster_sync();   // nobody leaves while the other may still reach it
   tc::fence_after_sync();
-  if (warp == 0) tc::tmem_dealloc(tb, 512);
+  if (warp == 0) {
+    if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tb) : "memory");
+    else tc::tmem_dealloc(tb, 512);
+  }
+  if (PAIR) cluster_sync();
 }
 
 namespace {
 
-cudaError_t rows_map(CUtensorMap* map, const void* base, int d, int heads, int64_t rows, int64_t stride) {
+cudaError_t rows_map(CUtensorMap* map, const void* base, int d, int heads, int64_t rows, int64_t stride, int box_rows) {
   auto encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, 1, kTile}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -692,20 +868,30 @@ cudaError_t rows_map(CUtensorMap* map, const void* base, int d, int heads, int64
              : cudaErrorInvalidValue;
 }
 
-template <int D>
+template <int D, bool PAIR>
 cudaError_t prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
-  using C = PreCfg<D>;
+  using C = PreCfg<D, PAIR>;
   CUtensorMap kmap, vmap;
-  cudaError_t e = rows_map(&kmap, p.k, D, p.Hkv, p.Tk, p.k_stride);
-  if (e == cudaSuccess) e = rows_map(&vmap, p.v, D, p.Hkv, p.Tk, p.v_stride);
+  cudaError_t e = rows_map(&kmap, p.k, D, p.Hkv, p.Tk, p.k_stride, C::KROWS);
+  if (e == cudaSuccess) e = rows_map(&vmap, p.v, D, p.Hkv, p.Tk, p.v_stride, kTile);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem<D>);
+    e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem<D, PAIR>);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)p.max_q * p.G + C::NQ * kTile - 1) / (C::NQ * kTile);
-  const int64_t grid = tiles * p.N * p.Hkv;
+  constexpr int ROWS = C::CTAS * C::NQ * kTile;
+  const int64_t grid = ((int64_t)p.max_q * p.G + ROWS - 1) / ROWS * p.N * p.Hkv * C::CTAS;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  attn_prefill_tc_kernel<D><<<(unsigned)grid, C::THREADS, kPreSmem<D>, st>>>(p, kmap, vmap);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = kPreSmem<D, PAIR>;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = C::CTAS;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_prefill_tc_kernel<D, PAIR>, p, kmap, vmap);
 }
 
 }  // namespace
@@ -716,9 +902,14 @@ bool attn_prefill_tc_supported(const AttnPrefillParams& p, int dtype) {
 }
 
 cudaError_t launch_attn_prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
-  if (p.d == 64) return prefill_tc<64>(p, st);
-  if (p.d == 128) return prefill_tc<128>(p, st);
-  return prefill_tc<256>(p, st);
+  // d = 256: a CTA's 128 rows take 128 KB of keys and values for 2,144 cycles of
+  // products, more than L2 gives (2 x 8,192 tokens: 1,235 us), so two share
+  // them (1,072 us) unless a sequence's rows fit one.  Two row tiles of d <= 128
+  // need half of that and only lose by moving together (d = 128, chunks of 101
+  // to 2,003 tokens: 525 us alone, 563 us in pairs).
+  if (p.d == 64) return prefill_tc<64, false>(p, st);
+  if (p.d == 128) return prefill_tc<128, false>(p, st);
+  return (int64_t)p.max_q * p.G > kTile ? prefill_tc<256, true>(p, st) : prefill_tc<256, false>(p, st);
 }
 
 }  // namespace gdn
