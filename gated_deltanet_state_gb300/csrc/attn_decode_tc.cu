@@ -9,6 +9,11 @@
 // and P stand side by side as 2 NT columns whose sums are added when read (a
 // product of up to 64 columns takes the time that reading the 128 rows of
 // codes takes, 52 cycles).
+//
+// Bound by HBM: 256 sequences over 1,024 to 8,192 tokens (24 heads, 4 kv heads,
+// d = 256: 2.45 GB) take 403 us with the join, 6.1 TB/s or 89 % of a copy's
+// rate; one over 777 tokens 12.3 us, two launches and the chain of a piece's
+// loads, two products and softmax.
 #include "attn_decode_tc.cuh"
 
 namespace gdn {

@@ -12,6 +12,11 @@
 // take 2,700 cycles of the memory's rate; the softmax of a tile takes 2,600, so
 // two warpgroups take the tiles in turn, the reference passing from one to the
 // other before the exponentials.
+//
+// Measured: 16 drafts of 16 rows over 2,048 to 32,768 tokens (606 MB of codes)
+// 226 us with the join, 2.7 TB/s: the softmax's hand-over, a piece's start and
+// its partial outputs (128 rows x 1 KB, 9,000 cycles) and the join's 22 us take
+// what is above the memory's 89 us.
 #include "attn_decode_tc.cuh"
 
 namespace gdn {

