@@ -33,7 +33,7 @@ struct DrShared : DtBase {
   uint64_t m_ready[2], fin[2];
   float m[2][kDrRows];      // a warpgroup's reference of each row, its sum at the end
   float fq[2][kDrRows];     // score factors (heads alternate)
-  float turn[8][32][17];    // a warp's 32 rows x 16 elements on their way out
+  float4 turn[8][32][5];    // a warp's 32 rows x 16 elements on their way out
 };
 
 // D[tmem] (+)= A[tmem] B[smem]^T, e4m3, 32 deep: eight columns of A hold four codes each.
@@ -341,34 +341,35 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
             if (sh.bad[ip][e + k] < lim) o[k] = __int_as_float(0x7fffffff);
         }
         if (p.part_o) {
-          // through shared memory, so that a warp writes 64 bytes of two rows at a time
-          const int rows = min(32, u.rows - (warp & 3) * 32), col = lane & 15;
+          // through shared memory, so that a warp writes 64 bytes of eight rows at a time
+          const int rows = min(32, u.rows - (warp & 3) * 32), c4 = lane & 3;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) sh.turn[warp][lane][k] = o[hf * 16 + k];
+            for (int k = 0; k < 4; ++k) {
+              const float* x = o + hf * 16 + 4 * k;
+              sh.turn[warp][lane][k] = make_float4(x[0], x[1], x[2], x[3]);
+            }
             __syncwarp();
-#pragma unroll 8
-            for (int k = 0; k < 32; k += 2) {
-              const int r = k + (lane >> 4);
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              const int r = k + (lane >> 2);
               const uintptr_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(po + e + hf * 16), r);
-              if (r < rows) *reinterpret_cast<float*>(at + 4 * col) = sh.turn[warp][r][col];
+              if (r < rows) reinterpret_cast<float4*>(at)[c4] = sh.turn[warp][r][c4];
             }
             __syncwarp();
           }
         } else if (mine) {
-          {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              uint32_t b[4];
+          for (int k = 0; k < 32; k += 8) {
+            uint32_t b[4];
 #pragma unroll
-              for (int i2 = 0; i2 < 4; ++i2) {
-                const float x = l == 0.f ? 0.f : o[k + 2 * i2] / l, y = l == 0.f ? 0.f : o[k + 2 * i2 + 1] / l;
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                b[i2] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              *reinterpret_cast<uint4*>(oo + e + k) = make_uint4(b[0], b[1], b[2], b[3]);
+            for (int i2 = 0; i2 < 4; ++i2) {
+              const float x = l == 0.f ? 0.f : o[k + 2 * i2] / l, y = l == 0.f ? 0.f : o[k + 2 * i2 + 1] / l;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+              b[i2] = *reinterpret_cast<const uint32_t*>(&h);
             }
+            *reinterpret_cast<uint4*>(oo + e + k) = make_uint4(b[0], b[1], b[2], b[3]);
           }
         }
         __syncwarp();
