@@ -30,7 +30,7 @@ constexpr int kDrThreads = 256 + 128;      // softmax; K loads, V loads, product
 constexpr uint32_t kDrO = 256;             // tensor memory: scores of two tiles, then O
 
 struct DrShared : DtBase {
-  uint64_t m_ready[2], fin[2];
+  uint64_t m_ready[2], fin[2], o_free;
   float m[2][kDrRows];      // a warpgroup's reference of each row, its sum at the end
   float fq[2][kDrRows];     // score factors (heads alternate)
   float4 turn[8][32][5];    // a warp's 32 rows x 16 elements on their way out
@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.s_full[i], 1), tc::mbar_init(&sh.p_full[i], 128), tc::mbar_init(&sh.o_done[i], 1);
     tc::mbar_init(&sh.q_full, 256);
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.m_ready[i], 128), tc::mbar_init(&sh.fin[i], 128);
+    tc::mbar_init(&sh.o_free, 256);
     tc::mbar_init(&sh.drain, 1);
     sh.fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         __syncwarp();
       }
       tc::fence_before_sync();
+      if (u.tiles > 0) dt_arrive(&sh.o_free);
       // (a buffer comes back after an item whose tiles every warp has passed)
       if (u.tiles > 0) ip ^= 1;
     }
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         return true;
       };
       DtItem t{};
+      int items = 0;   // with tiles
       for (int i = i0; ok && i < i1; ++i) {
         if (i == i0) t = dt_item<NT>(w, sh.items, i);
         else dt_next<NT>(w, sh.items, i, t);
@@ -426,6 +429,8 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         for (int j = 0; ok && j < t.tiles; ++j, ++T) {
           if (j + 1 < t.tiles) ok = qk(T + 1);
           ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail));
+          // O of the item before has been read, by both warpgroups
+          if (ok && j == 0 && items++ > 0) ok = all(dt_wait(&sh.o_free, items & 1, fail));
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t b = desc_tiles(v0 + vs * unit, 16u * d, 128);
