@@ -335,8 +335,8 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
 // elements of the head each.  The block's largest value decides its scale, so
 // the rows are held in registers from the load to the store: bound by that wait
 // and the conversions more than by HBM.  Measured (4 kv heads, d = 256, bf16):
-// five prompts, 29,500 rows, 181 MB read and written 50 us, 3.6 TB/s; 256 single rows
-// 8.0 us.
+// five prompts, 29,500 rows, 181 MB read and written 46 us, 3.9 TB/s; 256
+// single rows 8.0 us.
 template <typename T, int LPT, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 / THREADS) kv_append_kernel(const KvAppendParams p) {
   constexpr int kSlots = THREADS / LPT;   // runs in work at once
@@ -430,15 +430,16 @@ __device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
 
 }  // namespace
 
-// The cached rows of a prefix back as plain rows.  A CTA takes 64 output rows;
+// The cached rows of a prefix back as plain rows.  A CTA takes 16 output rows;
 // each block of 16 tokens that starts among them is read, for one head and K or
 // V, by LPT lanes with 8 elements each (V's operand tiles are transposed in
-// registers) and written as row pieces of 8 elements.  Bound by HBM: 1.06 GB
-// (two prefixes) 167 us, 6.4 TB/s or 93 % of a copy's rate; 19 ragged ones,
-// 242 MB, 50 us, of which the last CTAs' tail is a quarter.
+// registers) and written as row pieces of 8 elements.  Bound by HBM: two
+// prefixes, 1.06 GB (4 kv heads, d = 256), 160 us, 6.6 TB/s or 97 % of a copy's
+// rate; 19 ragged ones, 242 MB (8 kv heads, d = 128), 46 us (171 and 54 us with
+// 64 rows a CTA, whose last ones leave SMs idle).
 template <typename T, int LPT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherParams p) {
-  constexpr int kSlots = 256 / LPT, W = 64;
+  constexpr int kSlots = 256 / LPT, W = 16;
   __shared__ int s_row[W], s_len[W], s_page[W], s_blk[W], s_n;
   const int64_t t0 = (int64_t)blockIdx.x * W;
   if (threadIdx.x == 0) s_n = 0;
@@ -523,7 +524,7 @@ namespace {
 
 template <typename T>
 cudaError_t gather_dtype(const KvGatherParams& p, cudaStream_t st) {
-  const unsigned g = (unsigned)((p.T + 63) / 64);
+  const unsigned g = (unsigned)((p.T + 15) / 16);
   if (p.c.d > 128) kv_gather_kernel<T, 32><<<g, 256, 0, st>>>(p);
   else if (p.c.d > 64) kv_gather_kernel<T, 16><<<g, 256, 0, st>>>(p);
   else kv_gather_kernel<T, 8><<<g, 256, 0, st>>>(p);
