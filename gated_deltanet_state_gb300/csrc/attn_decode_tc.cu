@@ -11,8 +11,8 @@
 // codes takes, 52 cycles).
 //
 // Bound by HBM: 256 sequences over 1,024 to 8,192 tokens (24 heads, 4 kv heads,
-// d = 256: 2.45 GB) take 403 us with the join, 6.1 TB/s or 89 % of a copy's
-// rate; one over 777 tokens 12.3 us, two launches and the chain of a piece's
+// d = 256: 2.45 GB) take 405 us with the join, 6.0 TB/s or 89 % of a copy's
+// rate; one over 777 tokens 14.0 us, two launches and the chain of a piece's
 // loads, two products and softmax.
 #include "attn_decode_tc.cuh"
 
@@ -141,61 +141,59 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
     loaded = dt_load<NT>(w, sh, base, i0, i1, warp == WARPS + 1, lane);
   } else if (warp == WARPS + 2) {
     // ---- products: the whole warp, one lane issues ----
-    {
-      const uint32_t lead = tc::elect_one();
-      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-      constexpr uint32_t id = idesc_e4m3(C::N);
-      const uint32_t k0 = smem_u32(base + w.k_off), v0 = smem_u32(base + w.v_off), qa = smem_u32(base + w.q_off),
-                     pa = smem_u32(base + w.p_off);
-      const uint32_t rows8 = 8u * d;   // 8 tokens of K (or 8 rows of Q)
-      const int halves = (d + 127) / 128;
-      const uint64_t vstep = (uint64_t)(32u * d >> 4);
-      int ks = 0, kp = 0, vs = 0, vp = 0, rows = 0;
-      unsigned T = 0;   // tiles multiplied
-      bool ok = true;
-      auto qk = [&](unsigned tt) {
-        if (!all(dt_wait(&sh.k_full[ks], kp, fail))) return false;
-        tc::fence_after_sync();
-        const uint64_t a = desc_tiles(k0 + ks * unit, 128, rows8);
-        const uint64_t b = desc_tiles(qa, 128, rows8);
-        const uint32_t dst = tb + (tt & 1) * C::N;
-        if (d == 256) {
-          mma_steps<8>(lead, dst, a, b, id, 16, 16, false);
-        } else if (d == 128) {
-          mma_steps<4>(lead, dst, a, b, id, 16, 16, false);
-        } else {
-          for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id, c);
-        }
-        tc::mma_commit_if(lead, &sh.k_empty[ks]);
-        tc::mma_commit_if(lead, &sh.s_full[tt & 1]);
-        if (++ks == KS) ks = 0, kp ^= 1;
-        return true;
-      };
-      DtItem t{};
-      for (int i = i0; ok && i < i1; ++i) {
-        if (i == i0) t = dt_item<NT>(w, sh.items, i);
-        else dt_next<NT>(w, sh.items, i, t);
-        if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail));
-        if (ok && t.tiles > 0) ok = qk(T);
-        for (int j = 0; ok && j < t.tiles; ++j, ++T) {
-          if (j + 1 < t.tiles) ok = qk(T + 1);
-          ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail));
-          if (!ok) break;
-          tc::fence_after_sync();
-          for (int hf = 0; hf < halves; ++hf) {
-            const uint64_t a = desc_tiles(v0 + vs * unit + hf * 2048u, 16u * d, 128);
-            // P: tokens of 16 columns (16 B), the next 16 columns a block of 128 tokens further
-            mma_steps<kDtTok / 32>(lead, tb + C::O0 + hf * C::N, a, desc_tiles(pa, 128, 16 * kDtTok), id | kTransposedB, vstep, 32, j != 0);
-          }
-          tc::mma_commit_if(lead, &sh.v_empty[vs]);
-          tc::mma_commit_if(lead, &sh.o_done[T & 1]);
-          if (++vs == VS) vs = 0, vp ^= 1;
-        }
+    const uint32_t lead = tc::elect_one();
+    auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+    constexpr uint32_t id = idesc_e4m3(C::N);
+    const uint32_t k0 = smem_u32(base + w.k_off), v0 = smem_u32(base + w.v_off), qa = smem_u32(base + w.q_off),
+                   pa = smem_u32(base + w.p_off);
+    const uint32_t rows8 = 8u * d;   // 8 tokens of K (or 8 rows of Q)
+    const int halves = (d + 127) / 128;
+    const uint64_t vstep = (uint64_t)(32u * d >> 4);
+    int ks = 0, kp = 0, vs = 0, vp = 0, rows = 0;
+    unsigned T = 0;   // tiles multiplied
+    bool ok = true;
+    auto qk = [&](unsigned tt) {
+      if (!all(dt_wait(&sh.k_full[ks], kp, fail))) return false;
+      tc::fence_after_sync();
+      const uint64_t a = desc_tiles(k0 + ks * unit, 128, rows8);
+      const uint64_t b = desc_tiles(qa, 128, rows8);
+      const uint32_t dst = tb + (tt & 1) * C::N;
+      if (d == 256) {
+        mma_steps<8>(lead, dst, a, b, id, 16, 16, false);
+      } else if (d == 128) {
+        mma_steps<4>(lead, dst, a, b, id, 16, 16, false);
+      } else {
+        for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id, c);
       }
-      // every product issued, and every arrival on a barrier, before the end
-      tc::mma_commit_if(lead, &sh.drain);
-      if (!tc::mbar_wait_bounded(&sh.drain, 0, kDtWait)) *fail = 1;
+      tc::mma_commit_if(lead, &sh.k_empty[ks]);
+      tc::mma_commit_if(lead, &sh.s_full[tt & 1]);
+      if (++ks == KS) ks = 0, kp ^= 1;
+      return true;
+    };
+    DtItem t{};
+    for (int i = i0; ok && i < i1; ++i) {
+      if (i == i0) t = dt_item<NT>(w, sh.items, i);
+      else dt_next<NT>(w, sh.items, i, t);
+      if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail));
+      if (ok && t.tiles > 0) ok = qk(T);
+      for (int j = 0; ok && j < t.tiles; ++j, ++T) {
+        if (j + 1 < t.tiles) ok = qk(T + 1);
+        ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail));
+        if (!ok) break;
+        tc::fence_after_sync();
+        for (int hf = 0; hf < halves; ++hf) {
+          const uint64_t a = desc_tiles(v0 + vs * unit + hf * 2048u, 16u * d, 128);
+          // P: tokens of 16 columns (16 B), the next 16 columns a block of 128 tokens further
+          mma_steps<kDtTok / 32>(lead, tb + C::O0 + hf * C::N, a, desc_tiles(pa, 128, 16 * kDtTok), id | kTransposedB, vstep, 32, j != 0);
+        }
+        tc::mma_commit_if(lead, &sh.v_empty[vs]);
+        tc::mma_commit_if(lead, &sh.o_done[T & 1]);
+        if (++vs == VS) vs = 0, vp ^= 1;
+      }
     }
+    // every product issued, and every arrival on a barrier, before the end
+    tc::mma_commit_if(lead, &sh.drain);
+    if (!tc::mbar_wait_bounded(&sh.drain, 0, kDtWait)) *fail = 1;
   } else {
     // ---- softmax: a thread a token of the tile ----
     const int quad = warp, tid = threadIdx.x;

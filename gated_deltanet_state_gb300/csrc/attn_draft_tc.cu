@@ -14,9 +14,10 @@
 // other before the exponentials.
 //
 // Measured: 16 drafts of 16 rows over 2,048 to 32,768 tokens (606 MB of codes)
-// 226 us with the join, 2.7 TB/s: the softmax's hand-over, a piece's start and
-// its partial outputs (128 rows x 1 KB, 9,000 cycles) and the join's 22 us take
-// what is above the memory's 89 us.
+// 225 us with the join, 2.7 TB/s.  A CTA's items end one at a time (the sums'
+// way out, 128 rows x 1 KB, the next rows' way in: 25,000 of an item's 80,000
+// cycles), since their sums and two score tiles fill tensor memory; the join
+// takes 22 us.
 #include "attn_decode_tc.cuh"
 
 namespace gdn {
@@ -382,12 +383,11 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-  if (warp == 8 || warp == 9) {
-    // ---- loads, a warp for K and one for V ----
-    loaded = dt_load<NT>(w, sh, base, i0, i1, warp == 9, lane);
-  } else if (warp == 10) {
-    // ---- products: the whole warp, one lane issues ----
-    {
+    if (warp == 8 || warp == 9) {
+      // ---- loads, a warp for K and one for V ----
+      loaded = dt_load<NT>(w, sh, base, i0, i1, warp == 9, lane);
+    } else if (warp == 10) {
+      // ---- products: the whole warp, one lane issues ----
       const uint32_t lead = tc::elect_one();
       auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
       constexpr uint32_t id_qk = idesc_e4m3(kDtTok);
@@ -447,7 +447,6 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       // every product issued, and every arrival on a barrier, before the end
       tc::mma_commit_if(lead, &sh.drain);
       if (!tc::mbar_wait_bounded(&sh.drain, 0, kDtWait)) *fail = 1;
-    }
     }
   }
   __syncwarp();

@@ -631,7 +631,7 @@ int64_t gdn_kv_page_bytes(const gdn_attn_desc* desc);
  * and kv_len_out[s] = kv_len[s] (a negative one: 0).  So is, with slot -1, a
  * token whose page id is not in [0, num_pages).  No list is changed: the
  * caller drops the first *pages_taken entries of free_pages, and the same
- * call gives the same answer again. */
+ * call gives the same answer again.  The lengths' sums must fit in int32. */
 typedef struct gdn_kv_tables_args {
   int32_t num_seqs;              /* N >= 0                                    */
   int32_t max_pages;             /* row stride of block_table                 */
@@ -657,7 +657,7 @@ gdn_status gdn_kv_tables(const gdn_attn_desc* desc, const gdn_kv_tables_args* ar
 /* New K and V rows into the cache.  Row t goes to slot slot_map[t] = page *
  * page_tokens + offset (-1: skipped; a page outside the pool sets
  * GDN_ERR_PAGE_RANGE and is skipped).  Rows of one block of 16 tokens must
- * stand one after another in ascending order, and no two runs of rows may
+ * stand one after another in consecutive slots, and no two runs of rows may
  * share a block; a run that starts inside a block keeps the tokens before it.
  *
  * The scale of a block is the smallest power of two, at least 2^-64, with
@@ -705,9 +705,9 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
  * outside the pool, sets GDN_ERR_INVALID_ARG / GDN_ERR_PAGE_RANGE; its
  * outputs are not written (the page fault: that piece's keys are left out).
  *
- * The keys of a sequence are cut into pieces by its own kv_len alone, the
- * pieces run in parallel and are joined in order: a row's bits do not depend
- * on the batch around it. */
+ * The keys of a sequence are cut into pieces by its own kv_len and number of
+ * rows alone, the pieces run in parallel and are joined in order: a row's bits
+ * do not depend on the batch around it. */
 typedef struct gdn_attn_decode_args {
   int32_t num_seqs;              /* N >= 0                                    */
   int32_t max_pages;             /* row stride of block_table                 */
@@ -756,7 +756,8 @@ typedef struct gdn_attn_prefill_args {
   float* lse;                    /* [total_q][Hq] or NULL                     */
   int32_t* dev_error;
   int64_t wait_cycles;           /* bound of each device-side wait in SM
-                                    clocks; 0: the default (~2 s); < 0 makes
+                                    clocks (one may last as long as 128 rows
+                                    take); 0: the default (~2 s); < 0 makes
                                     every such wait of the tensor-core path
                                     report GDN_ERR_TIMEOUT at once (outputs
                                     are then not written)                     */

@@ -17,10 +17,11 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def test_example_serves():
-    """Every phase within the cache's rounding: e4m3 keeps 4 significant bits,
-    so a key's element is off by at most 2^-4 of itself (rms 2^-4 / sqrt(3) /
-    ... < 2.7 %), values alike; scores of unit normal rows move by ~0.027, and
-    outputs by the two together, below 6 %."""
+    """Every phase within the cache's rounding: e4m3 keeps 4 significant bits, so
+    an element is off by up to 2^-4 of itself and by 2.6 % in the root mean
+    square.  Values move the outputs by that; keys move the scores of unit
+    normal rows by about 0.026 and the weights, so the outputs, by as much.  The
+    two together are 3.7 %; bound: 6 %."""
     spec = importlib.util.spec_from_file_location("attention_layer", os.path.join(ROOT, "examples", "attention_layer.py"))
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
