@@ -281,10 +281,15 @@ namespace {
 
 constexpr int kPreKeys = 64, kPreLdP = kPreKeys + 4;
 // Rows of a tile, four threads' worth each: 32 up to D = 64, so that a small
-// model's prompts make more CTAs and their longest one is shorter (75 us with
-// 64, nine prompts of up to 1,000 tokens), 64 above, where the keys' tiles take
-// the shared memory.
+// model's prompts make more CTAs and their longest one is shorter (nine prompts
+// of up to 1,000 tokens: 75 us with 64, 53 with 32, one group each), 64 above,
+// where the keys' tiles take the shared memory.
 template <int D> constexpr int kPreRows = D <= 64 ? 32 : 64;
+// Groups of threads that take a tile's keys in turn, each with sums of its own:
+// at D = 32 the longest prompt's last tile, which decides, has twice the threads
+// (54 us with one group, 46 with two, 50 with four); at D = 64 two do not fit
+// their registers (four prompts of 2,000: 758 us with one, 809 with two).
+template <int D> constexpr int kPreGroups = D <= 32 ? 2 : 1;
 
 // Four consecutive elements of a row as fp32.
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -300,38 +305,48 @@ __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
 // i % G, so that the group shares the keys) against its keys, 64 at a time.
 // 16 threads a row group: each 4 rows by 4 keys of the scores and 4 rows by
 // D / 16 elements of the outputs (D: the head size rounded up to 32, 64, 128
-// or 256).  Bound by fp32 arithmetic; a small model's prompts by the longest
-// tile's way through its keys, which the next keys' loads (up to D = 64 held in
-// registers while the present ones are used) leave.
+// or 256).  Bound by fp32 arithmetic out of shared memory; a small model's
+// prompts by the longest tile's way through its keys, which the next keys' loads
+// (up to D = 64 held in registers while the present ones are used) leave.  Nine
+// fp32 prompts of up to 1,000 tokens (4 heads, 2 kv heads, d = 32; 0.47 GFLOP of
+// visible pairs): 43 us.
 template <typename T, int D>
-__global__ void __launch_bounds__(4 * kPreRows<D>) attn_prefill_simt_kernel(const AttnPrefillParams p) {
+__global__ void __launch_bounds__(4 * kPreRows<D> * kPreGroups<D>, D <= 32 ? 2 : 1) attn_prefill_simt_kernel(const AttnPrefillParams p) {
   extern __shared__ float smem[];
   constexpr int VW = D == 32 ? 2 : 4, VN = D / 16 / VW;   // a thread's elements: VN groups of VW
-  constexpr int ROWS = kPreRows<D>, THREADS = 4 * ROWS;
+  constexpr int ROWS = kPreRows<D>, THREADS = 4 * ROWS, GROUPS = kPreGroups<D>;   // threads of a group
   constexpr int NL = kPreKeys * D / 4 / THREADS;              // 4-element loads a thread for a tile of K (or V)
   constexpr bool AHEAD = D <= 64;
   const int d = p.d, ld = d + 4;
-  const int s = blockIdx.z, h = blockIdx.y;
+  // every sequence's last tile first, then the ones before: they see the most keys
+  const int pairs = p.N * p.Hkv, back = (int)(blockIdx.x / pairs), pr = (int)(blockIdx.x - (unsigned)back * pairs);
+  const int s = pr / p.Hkv, h = pr - s * p.Hkv;
   const int q0 = p.cu_q[s], n = p.cu_q[s + 1] - q0, k0 = p.cu_kv[s], L = p.cu_kv[s + 1] - k0;
   if (n <= 0) return;
   if (n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || k0 < 0 || (int64_t)q0 + n > p.Tq || (int64_t)k0 + L > p.Tk) {
     if (threadIdx.x == 0) set_error(p.err, GDN_ERR_INVALID_ARG);
     return;
   }
-  // the last tiles first: they see the most keys
   const int tiles = (int)(((int64_t)n * p.G + ROWS - 1) / ROWS);
-  const int tile = tiles - 1 - (int)blockIdx.x;
+  const int tile = tiles - 1 - back;
   if (tile < 0) return;
   const int64_t r0 = (int64_t)tile * ROWS;
   float* sq = smem;                       // [ROWS][ld]
-  float* sk = sq + ROWS * ld;         // [64][ld]
+  const int group = threadIdx.x / THREADS, tid = threadIdx.x % THREADS;
+  float* sk = sq + ROWS * ld + group * (2 * kPreKeys * ld + ROWS * kPreLdP);   // [64][ld]
   float* sv = sk + kPreKeys * ld;         // [64][ld]
   float* sp = sv + kPreKeys * ld;         // [ROWS][68]
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tx = tid & 15, ty = tid >> 4;
+  auto sync = [&] {   // of this group
+    if (GROUPS == 1) __syncthreads();
+    else if (group == 0) asm volatile("bar.sync 1, %0;\n" ::"n"(THREADS) : "memory");
+    else asm volatile("bar.sync 2, %0;\n" ::"n"(THREADS) : "memory");
+  };
+  static_assert(GROUPS <= 2, "a barrier each");
   // element group and row of this thread's loads: D / 4 groups a row
   constexpr int LG = D / 4;
-  const int le = threadIdx.x % LG * 4, lr = threadIdx.x / LG, lstep = THREADS / LG;
-  for (int r = lr; r < ROWS; r += lstep) {
+  const int le = tid % LG * 4, lr = tid / LG, lstep = THREADS / LG;
+  for (int r = lr + group * lstep; r < ROWS; r += GROUPS * lstep) {
     const int64_t row = (r0 + r) / p.G;
     const int g = (int)((r0 + r) - row * p.G);
     if (le < d) {
@@ -366,9 +381,10 @@ __global__ void __launch_bounds__(4 * kPreRows<D>) attn_prefill_simt_kernel(cons
       av[i] = in ? load4(vg + key * p.v_stride) : zero;
     }
   };
-  if (AHEAD) fetch(0);
-  for (int kb = 0; kb < most; kb += kPreKeys) {
-    __syncthreads();
+  if (AHEAD) fetch(group * kPreKeys);
+  __syncthreads();   // the rows are there
+  for (int kb = group * kPreKeys; kb < most; kb += GROUPS * kPreKeys) {
+    sync();
     if (le < d) {
       if (AHEAD) {
 #pragma unroll
@@ -385,8 +401,8 @@ __global__ void __launch_bounds__(4 * kPreRows<D>) attn_prefill_simt_kernel(cons
         }
       }
     }
-    __syncthreads();
-    if (AHEAD && kb + kPreKeys < most) fetch(kb + kPreKeys);
+    sync();
+    if (AHEAD && kb + GROUPS * kPreKeys < most) fetch(kb + GROUPS * kPreKeys);
     float x[4][4] = {};
 #pragma unroll 4
     for (int e = 0; e < d; e += 4) {
@@ -458,6 +474,41 @@ __global__ void __launch_bounds__(4 * kPreRows<D>) attn_prefill_simt_kernel(cons
       }
     }
   }
+  if constexpr (GROUPS > 1) {
+    // the groups' sums joined in their order, through where their keys were
+    constexpr int NO = VN * VW;
+    auto part = [&](int g) { return sq + ROWS * ld + g * (2 * kPreKeys * ld + ROWS * kPreLdP) + tid; };
+    sync();
+    if (group > 0) {
+      float* to = part(group);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        to[(2 * i) * THREADS] = m[i], to[(2 * i + 1) * THREADS] = l[i];
+#pragma unroll
+        for (int j = 0; j < NO; ++j) to[(8 + i * NO + j) * THREADS] = O[i][j];
+      }
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mn = m[i];
+#pragma unroll
+      for (int g = 1; g < GROUPS; ++g) mn = fmaxf(mn, part(g)[(2 * i) * THREADS]);
+      const float ref = mn == -INFINITY ? 0.f : mn, a = fast_exp2(m[i] - ref);
+      m[i] = mn, l[i] *= a;
+#pragma unroll
+      for (int j = 0; j < NO; ++j) O[i][j] *= a;
+#pragma unroll
+      for (int g = 1; g < GROUPS; ++g) {
+        const float* of = part(g);
+        const float b = fast_exp2(of[(2 * i) * THREADS] - ref);
+        l[i] = fmaf(of[(2 * i + 1) * THREADS], b, l[i]);
+#pragma unroll
+        for (int j = 0; j < NO; ++j) O[i][j] = fmaf(of[(8 + i * NO + j) * THREADS], b, O[i][j]);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = r0 + 4 * ty + i, row = r / p.G;
@@ -478,11 +529,13 @@ namespace {
 
 template <typename T, int D>
 cudaError_t prefill_simt(const AttnPrefillParams& p, cudaStream_t st) {
-  const int64_t tiles = ((int64_t)p.max_q * p.G + kPreRows<D> - 1) / kPreRows<D>;
-  const size_t sm = (size_t)((kPreRows<D> + 2 * kPreKeys) * (p.d + 4) + kPreRows<D> * kPreLdP) * 4;   // 217,088 B at d = 256
+  const int64_t grid = ((int64_t)p.max_q * p.G + kPreRows<D> - 1) / kPreRows<D> * p.N * p.Hkv;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  const size_t sm =   // 217,088 B at d = 256
+      (size_t)(kPreRows<D> * (p.d + 4) + kPreGroups<D> * (2 * kPreKeys * (p.d + 4) + kPreRows<D> * kPreLdP)) * 4;
   cudaError_t e = cudaFuncSetAttribute(attn_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  attn_prefill_simt_kernel<T, D><<<dim3((unsigned)tiles, p.Hkv, p.N), 4 * kPreRows<D>, sm, st>>>(p);
+  attn_prefill_simt_kernel<T, D><<<(unsigned)grid, 4 * kPreRows<D> * kPreGroups<D>, sm, st>>>(p);
   return cudaGetLastError();
 }
 template <typename T>
