@@ -267,23 +267,39 @@ __device__ __forceinline__ void append_block(const T* src, int64_t stride, const
   }
 }
 
-// Tokens [off, off + run) of a block that is not written whole (a decode
-// step's single tokens): row by row, in little code (a step's kernel is as long
-// as its instructions take to arrive).  The codes before the run are read only
-// when the scale rises.
-template <typename T, int LPT>
+// Tokens [off, off + run) of a block that is not written whole.  Prompts (HOLD):
+// the rows into registers at once, as a whole block's, or their ends' two
+// passes of one load after another hold up the last CTAs.  A decode step's
+// single tokens: row by row, in little code (a step's kernel is as long as its
+// instructions take to arrive).  The codes before the run are read only when the
+// scale rises.
+template <typename T, int LPT, bool HOLD>
 __device__ __forceinline__ void append_part(const T* src, int64_t stride, const AppendAt& at, bool is_v, int off, int run,
                                             unsigned mask) {
   const bool on = at.lane * 8 < at.d;
   const float before = off ? *at.scale : 0.f;
   float m = 0.f;
-#pragma unroll 1
-  for (int t = 0; t < run; ++t) {
-    Row8<T> r;
-    r.zero();
-    if (on) r.load(src + t * stride);
+  Row8<T> held[HOLD ? kKvBlock - 1 : 1];
+  auto most = [&](const Row8<T>& r) {
     const float x = max8(r);
     m = fmaxf(m, x < __int_as_float(0x7f800000) ? x : max8_finite(r));
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int t = 0; t < kKvBlock - 1; ++t) {
+      held[t].zero();
+      if (on && t < run) held[t].load(src + t * stride);
+    }
+#pragma unroll
+    for (int t = 0; t < kKvBlock - 1; ++t) most(held[t]);
+  } else {
+#pragma unroll 1
+    for (int t = 0; t < run; ++t) {
+      Row8<T> r;
+      r.zero();
+      if (on) r.load(src + t * stride);
+      most(r);
+    }
   }
   const float now = fmaxf(pow2_scale(lanes_max<LPT>(m, mask)), before), inv = 1.0f / now;
   if (at.lane == 0) *at.scale = now;
@@ -314,16 +330,25 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
       }
     }
   }
-#pragma unroll 1
-  for (int t = 0; t < run; ++t) {
-    Row8<T> r;
-    r.load(src + t * stride);
+  auto put = [&](int t, const Row8<T>& r) {
     const uint2 c = codes8(r, inv);
     if (!is_v) {
       *at.k(off + t) = c;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) at.v(e)[off + t] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+    }
+  };
+  if constexpr (HOLD) {
+#pragma unroll
+    for (int t = 0; t < kKvBlock - 1; ++t)
+      if (t < run) put(t, held[t]);
+  } else {
+#pragma unroll 1
+    for (int t = 0; t < run; ++t) {
+      Row8<T> r;
+      r.load(src + t * stride);
+      put(t, r);
     }
   }
 }
@@ -335,7 +360,7 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
 // elements of the head each.  The block's largest value decides its scale, so
 // the rows are held in registers from the load to the store: bound by that wait
 // and the conversions more than by HBM.  Measured (4 kv heads, d = 256, bf16):
-// five prompts, 29,500 rows, 181 MB read and written 46 us, 3.9 TB/s; 256
+// five prompts, 29,500 rows, 181 MB read and written 39 us, 4.6 TB/s; 256
 // single rows 8.0 us.
 template <typename T, int LPT, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 / THREADS) kv_append_kernel(const KvAppendParams p) {
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 
     const AppendAt at{const_cast<uint8_t*>(is_v ? kv_v_block(p.c, (int)page, h, b) : kv_k_block(p.c, (int)page, h, b)),
                       const_cast<float*>(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)), d, lane};
     if (run == kKvBlock) append_block<T, LPT>(src, stride, at, is_v, mask);
-    else append_part<T, LPT>(src, stride, at, is_v, off, run, mask);
+    else append_part<T, LPT, (W > kKvBlock)>(src, stride, at, is_v, off, run, mask);
   }
 }
 
@@ -391,7 +416,7 @@ template <typename T, int LPT>
 cudaError_t append_rows(const KvAppendParams& p, cudaStream_t st) {
   // few rows (a decode step: every row a run of its own): 4 a CTA of 8 warps,
   // so that the runs of a step spread over the SMs; many (prompts): 32 a CTA
-  // of 4 warps, about two runs of K and of V (five prompts of 29,500 rows: 54 us;
+  // of 4 warps, about two runs of K and of V (five prompts of 29,500 rows, before later steps: 54 us;
   // 56 with 64 rows, 60 with 16 on 2 warps)
   if (p.T <= 4096) {
     kv_append_kernel<T, LPT, 4, 256><<<dim3((unsigned)((p.T + 3) / 4), p.c.Hkv), 256, 0, st>>>(p);
