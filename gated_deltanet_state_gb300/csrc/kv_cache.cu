@@ -267,12 +267,12 @@ __device__ __forceinline__ void append_block(const T* src, int64_t stride, const
   }
 }
 
-// Tokens [off, off + run) of a block that is not written whole.  Prompts (HOLD):
-// the rows into registers at once, as a whole block's, or their ends' two
-// passes of one load after another hold up the last CTAs.  A decode step's
-// single tokens: row by row, in little code (a step's kernel is as long as its
-// instructions take to arrive).  The codes before the run are read only when the
-// scale rises.
+// Tokens [off, off + run) of a block that is not written whole.  More than two
+// (a prompt's ends, a draft; HOLD): the rows into registers at once, as a whole
+// block's, for one wait instead of one a row.  A decode step's single tokens: row
+// by row, in little code (a step's kernel is as long as its instructions take to
+// arrive: 256 of them 5.5 us, 6.1 through the other).  The codes before the run
+// are read only when the scale rises.
 template <typename T, int LPT, bool HOLD>
 __device__ __forceinline__ void append_part(const T* src, int64_t stride, const AppendAt& at, bool is_v, int off, int run,
                                             unsigned mask) {
@@ -361,7 +361,7 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
 // the rows are held in registers from the load to the store: bound by that wait
 // and the conversions more than by HBM.  Measured (4 kv heads, d = 256, bf16):
 // five prompts, 29,500 rows, 181 MB read and written 39 us, 4.6 TB/s; 256
-// single rows 8.0 us.
+// single rows 5.5 us.
 template <typename T, int LPT, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 / THREADS) kv_append_kernel(const KvAppendParams p) {
   constexpr int kSlots = THREADS / LPT;   // runs in work at once
@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 
     const AppendAt at{const_cast<uint8_t*>(is_v ? kv_v_block(p.c, (int)page, h, b) : kv_k_block(p.c, (int)page, h, b)),
                       const_cast<float*>(is_v ? kv_v_scale(p.c, (int)page, h, b) : kv_k_scale(p.c, (int)page, h, b)), d, lane};
     if (run == kKvBlock) append_block<T, LPT>(src, stride, at, is_v, mask);
-    else append_part<T, LPT, (W > kKvBlock)>(src, stride, at, is_v, off, run, mask);
+    else if (run > 2) append_part<T, LPT, true>(src, stride, at, is_v, off, run, mask);
+    else append_part<T, LPT, false>(src, stride, at, is_v, off, run, mask);
   }
 }
 
@@ -415,10 +416,11 @@ namespace {
 template <typename T, int LPT>
 cudaError_t append_rows(const KvAppendParams& p, cudaStream_t st) {
   // few rows (a decode step: every row a run of its own): 4 a CTA of 8 warps,
-  // so that the runs of a step spread over the SMs; many (prompts): 32 a CTA
-  // of 4 warps, about two runs of K and of V (five prompts of 29,500 rows, before later steps: 54 us;
-  // 56 with 64 rows, 60 with 16 on 2 warps)
-  if (p.T <= 4096) {
+  // so that the runs of a step spread over the SMs (256 single rows 5.5 us, 31
+  // with 32 rows a CTA); many (prompts): 32 a CTA of 4 warps, about two runs of K
+  // and of V (one prompt of 4,000 rows 9.5 us, 19 with 4 rows; 2,000 rows 9.9
+  // and 11.4)
+  if (p.T <= 2048) {
     kv_append_kernel<T, LPT, 4, 256><<<dim3((unsigned)((p.T + 3) / 4), p.c.Hkv), 256, 0, st>>>(p);
   } else {
     kv_append_kernel<T, LPT, 32, 128><<<dim3((unsigned)((p.T + 31) / 32), p.c.Hkv), 128, 0, st>>>(p);
