@@ -513,7 +513,8 @@ cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st) {
   // (row, head) pairs of a kv head here, more with the rows as the products'
   // 128 (attn_draft_tc.cu); a call that may have both launches both
   if (p.max_q * p.G > kDtNarrow) {
-    const bool few = p.G <= kDtNarrow;
+    // (none has few where all rows together say that each has max_q: a launch, 6 us, less)
+    const bool few = p.G <= kDtNarrow && (int64_t)p.N * p.max_q != p.T;
     if (few) e = decode_tc<16>(p, sms, st);
     return e != cudaSuccess ? e : launch_attn_draft_tc(p, sms, few, st);
   }

@@ -14,7 +14,7 @@
 // other before the exponentials.
 //
 // Measured: 16 drafts of 16 rows over 2,048 to 32,768 tokens (606 MB of codes)
-// 225 us with the join, 2.7 TB/s.  A CTA's items end one at a time (the sums'
+// 220 us with the join, 2.8 TB/s.  A CTA's items end one at a time (the sums'
 // way out, 128 rows x 1 KB, the next rows' way in: 25,000 of an item's 80,000
 // cycles), since their sums and two score tiles fill tensor memory; the join
 // takes 22 us.
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
 cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overlap, cudaStream_t st) {
   DtParams w{};
   w.a = p;
-  w.row_lo = kDtNarrow + 1, w.row_hi = 0x7fffffff;
+  w.row_lo = overlap ? kDtNarrow + 1 : 1, w.row_hi = 0x7fffffff;
   const uint32_t q = 2 * kDrRows * (uint32_t)p.c.d;
   w.q_off = dt_rings(w, 232448, q + (uint32_t)sizeof(DrShared) + 512);
   if (w.v_stages < 1) return cudaErrorInvalidValue;
