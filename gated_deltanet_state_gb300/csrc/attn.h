@@ -97,7 +97,7 @@ struct AttnPrefillParams {
 // context over more SMs; 512 keep a few rows' outputs (4 d bytes each for a
 // piece, written and read once) under 3 % of the keys' bytes at 6 rows; a
 // draft's take 1,024, and 2,048 from 8,192 keys on (16 drafts of 16 rows over
-// 2,048 to 32,768 keys: 262 us with 1,024, 225 with 2,048); beyond 38,912
+// 2,048 to 32,768 keys: 262 us with 1,024, 226 with 2,048); beyond 38,912
 // tokens 76 pieces a head are one CTA on each of the 152 SMs for two kv heads.
 constexpr int kMaxPieces = 76;
 constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows

@@ -11,8 +11,8 @@
 // codes takes, 52 cycles).
 //
 // Bound by HBM: 256 sequences over 1,024 to 8,192 tokens (24 heads, 4 kv heads,
-// d = 256: 2.45 GB) take 405 us with the join, 6.0 TB/s or 89 % of a copy's
-// rate; one over 777 tokens 14.0 us, two launches and the chain of a piece's
+// d = 256: 2.45 GB) take 406 us with the join, 6.0 TB/s or 89 % of a copy's
+// rate; one over 777 tokens 13.3 us, two launches and the chain of a piece's
 // loads, two products and softmax.
 #include "attn_decode_tc.cuh"
 

@@ -14,7 +14,7 @@
 // other before the exponentials.
 //
 // Measured: 16 drafts of 16 rows over 2,048 to 32,768 tokens (606 MB of codes)
-// 220 us with the join, 2.8 TB/s.  A CTA's items end one at a time (the sums'
+// 216 us with the join, 2.8 TB/s.  A CTA's items end one at a time (the sums'
 // way out, 128 rows x 1 KB, the next rows' way in: 25,000 of an item's 80,000
 // cycles), since their sums and two score tiles fill tensor memory; the join
 // takes 22 us.

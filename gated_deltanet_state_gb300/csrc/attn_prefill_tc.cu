@@ -6,26 +6,25 @@
 // keys) with 128 keys, accumulated in tensor memory; P = 2^(c S - m), rounded
 // to bf16 (as O is in the end), goes back over the scores it comes from; the
 // running maximum m and sum of a row stay in fp32 registers.  A key tile takes
-// 16 D / 2 products of 67 cycles, and everything else has to hide under them:
+// D / 8 products of 67 cycles, and everything else has to hide under them:
 //
-// * d = 128, 256: two warpgroups take the key tiles in turn (a row in a thread,
-//   1,900 cycles a tile), the reference m passing from one to the other before
-//   the exponentials, so that those of two key tiles overlap; two score buffers
-//   cover that at d = 256 (2,144 cycles of products), three at d = 128 (1,069).
-//   A CTA would load a key tile's 64 or 128 KB in that time, more than L2 gives,
-//   so two CTAs share it (cta_group::2: half of its keys and half of its values'
-//   elements in each, 256 query rows a product).
-// * d = 64: two row tiles, each with two warpgroups, a row's scores in two
-//   threads which exchange their maxima.
+// * Two warpgroups take the key tiles in turn (a row in a thread, 1,900 cycles a
+//   tile), the reference m passing from one to the other before the
+//   exponentials, so that those of two key tiles overlap; two score buffers
+//   cover that at d = 256 (2,144 cycles of products), three at d = 128 (1,069)
+//   and 64 (680, which the exponentials' 950 exceed).
+// * At d = 256 and 128 a CTA would load a key tile's 128 or 64 KB in that time,
+//   more than L2 gives, so two CTAs share it (cta_group::2: half of its keys and
+//   half of its values' elements in each, 256 query rows a product).
 // * Blocks take further row tiles while they run: what surrounds the key tiles
 //   (set-up, queries, outputs: 21,000 cycles of a block with one row tile, 33
 //   key tiles of 2,100 on average at 8,192 tokens) comes under the products of
 //   the tile before or after, about 9,000 of it still in the way.
 //
 // Measured (24 heads, 4 kv heads, d = 256; 32, 8, d = 128): two prompts of
-// 8,192 tokens 1,012 us, 1.63 PFLOP/s or 83 % of a library product's burst and 94 %
-// of its sustained rate (the power limit holds the clock at 1.63 GHz); six chunks of 101 to
-// 2,003 tokens after up to 6,007 keys 506 us, 1.26 PFLOP/s.
+// 8,192 tokens 995 us, 1.66 PFLOP/s or 85 % of a library product's burst and
+// 96 % of its sustained rate, under the power limit (893 us at 1.85 GHz); six
+// chunks of 101 to 2,003 tokens after up to 6,007 keys 496 us, 1.28 PFLOP/s.
 #include <cuda.h>
 
 #include "attn.h"

@@ -28,7 +28,7 @@ template <typename T> __device__ __forceinline__ void put1(void* o, int64_t i, f
 // of the head each (d / 32 of them) for the values; each warp keeps its own
 // softmax statistics, joined at the end.  Serves what the tensor-core kernels do
 // not (fp32 rows, d not a multiple of 32), bound by the conversions and fp32
-// arithmetic: 256 sequences of d = 256 took 5,070 us here against 405 there.
+// arithmetic: 256 sequences of d = 256 took 5,070 us here against 406 there.
 template <typename T>
 __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const AttnDecodeParams p) {
   extern __shared__ float smem[];
