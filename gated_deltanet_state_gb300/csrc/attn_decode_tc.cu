@@ -5,8 +5,8 @@
 // With 128 tokens as the rows of the first product and the head's elements as
 // the rows of the second,
 //   S^T [tokens x rows] = K Q^T,    O^T [elements x rows] += V^T P^T,
-// the few query rows are the products' narrow side; the hi and lo parts of Q
-// and P stand side by side as 2 NT columns whose sums are added when read (a
+// the few query rows are the products' narrow side; the two parts of Q and the
+// three of P stand side by side as columns whose sums are added when read (a
 // product of up to 64 columns takes the time that reading the 128 rows of
 // codes takes, 52 cycles).
 //
@@ -27,10 +27,12 @@ namespace {
 template <int NT>
 struct DtCfg {
   static constexpr int CW = NT;
-  static constexpr int N = 2 * NT;                     // columns of a product
+  static constexpr int NQ = 2 * NT;                    // columns of the scores' products
+  static constexpr int NP = NT <= 8 ? 32 : 48;         // of the outputs': 3 NT, in blocks of 16
   static constexpr int THREADS = 128 + 96;             // and K loads, V loads, products
-  static constexpr uint32_t COLS = NT <= 8 ? 64 : 128;
-  static constexpr uint32_t O0 = 2 * N;                // scores of two tiles, then O of 128 elements each
+  static constexpr uint32_t COLS = NT <= 8 ? 128 : 256;   // two CTAs an SM
+  static constexpr uint32_t O0 = 2 * NQ;               // scores of two tiles, then O of 128 elements each
+  static_assert(O0 + 2 * NP <= COLS, "tensor memory");
 };
 
 template <int NT>
@@ -45,17 +47,35 @@ struct DtShared : DtBase {
   unsigned grow;            // the last tile (from 1) that moved a column's reference
 };
 
-// CW columns of a product's sums: hi and lo parts added.
+// The rows' scores: hi and lo parts added.
 template <int CW>
-__device__ __forceinline__ void read_columns(uint32_t col, int NT, float (&x)[CW]) {
+__device__ __forceinline__ void read_scores(uint32_t col, float (&x)[CW]) {
   if constexpr (CW == 8) {
     float v[16];
     tc::tmem_ld16(col, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = v[k] + v[8 + k];
+    for (int k = 0; k < 8; ++k) x[k] = fmaf(v[8 + k], kDtLo, v[k]);
   } else {
     float v[16];
-    tc::tmem_ld16x2(col, col + NT, x, v);
+    tc::tmem_ld16x2(col, col + 16, x, v);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = fmaf(v[k], kDtLo, x[k]);
+  }
+}
+// The rows' outputs: three parts added.
+template <int CW>
+__device__ __forceinline__ void read_outputs(uint32_t col, float (&x)[CW]) {
+  float v[16];
+  if constexpr (CW == 8) {
+    float u[16];
+    tc::tmem_ld16x2(col, col + 16, u, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = u[k] + (u[8 + k] + v[k]);
+  } else {
+    tc::tmem_ld16x2(col + 16, col + 32, x, v);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] += v[k];
+    tc::tmem_ld16(col, v);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] += v[k];
   }
@@ -143,7 +163,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
     // ---- products: the whole warp, one lane issues ----
     const uint32_t lead = tc::elect_one();
     auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-    constexpr uint32_t id = idesc_e4m3(C::N);
+    constexpr uint32_t id_qk = idesc_e4m3(C::NQ), id_pv = idesc_e4m3(C::NP) | kE5m2B | kTransposedB;
     const uint32_t k0 = smem_u32(base + w.k_off), v0 = smem_u32(base + w.v_off), qa = smem_u32(base + w.q_off),
                    pa = smem_u32(base + w.p_off);
     const uint32_t rows8 = 8u * d;   // 8 tokens of K (or 8 rows of Q)
@@ -157,13 +177,13 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
       tc::fence_after_sync();
       const uint64_t a = desc_tiles(k0 + ks * unit, 128, rows8);
       const uint64_t b = desc_tiles(qa, 128, rows8);
-      const uint32_t dst = tb + (tt & 1) * C::N;
+      const uint32_t dst = tb + (tt & 1) * C::NQ;
       if (d == 256) {
-        mma_steps<8>(lead, dst, a, b, id, 16, 16, false);
+        mma_steps<8>(lead, dst, a, b, id_qk, 16, 16, false);
       } else if (d == 128) {
-        mma_steps<4>(lead, dst, a, b, id, 16, 16, false);
+        mma_steps<4>(lead, dst, a, b, id_qk, 16, 16, false);
       } else {
-        for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id, c);
+        for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id_qk, c);
       }
       tc::mma_commit_if(lead, &sh.k_empty[ks]);
       tc::mma_commit_if(lead, &sh.s_full[tt & 1]);
@@ -184,7 +204,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         for (int hf = 0; hf < halves; ++hf) {
           const uint64_t a = desc_tiles(v0 + vs * unit + hf * 2048u, 16u * d, 128);
           // P: tokens of 16 columns (16 B), the next 16 columns a block of 128 tokens further
-          mma_steps<kDtTok / 32>(lead, tb + C::O0 + hf * C::N, a, desc_tiles(pa, 128, 16 * kDtTok), id | kTransposedB, vstep, 32, j != 0);
+          mma_steps<kDtTok / 32>(lead, tb + C::O0 + hf * C::NP, a, desc_tiles(pa, 128, 16 * kDtTok), id_pv, vstep, 32, j != 0);
         }
         tc::mma_commit_if(lead, &sh.v_empty[vs]);
         tc::mma_commit_if(lead, &sh.o_done[T & 1]);
@@ -224,37 +244,14 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const int n = r * 4 + quad;
-        float f[8], amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t u = (&x[r].x)[k >> 1];
-          f[k] = __uint_as_float(k & 1 ? u & 0xffff0000u : u << 16);
-          amax = fmaxf(amax, fabsf(f[k]));
-        }
-        amax = warp_max(amax);
-        // largest element to (224, 448]; exponents kept where both factors are normal
-        int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = max(-100, min(100, e));
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float g4[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) g4[u] = f[4 * k + u] * inv;
-          hi[k] = e4m3x4(g4[0], g4[1], g4[2], g4[3]);
-          const float2 a = e4m3_f32x2(hi[k]), b = e4m3_f32x2(hi[k] >> 16);
-          lo[k] = e4m3x4(g4[0] - a.x, g4[1] - a.y, g4[2] - b.x, g4[3] - b.y);
-        }
+        uint2 hi, lo;
+        const float factor = split_row<false>(x[r], hi, lo);
         if (e0 < d) {
           uint8_t* at = qd + (n >> 3) * 8 * d + (e0 >> 4) * 128 + (n & 7) * 16 + (e0 & 8);
-          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(at + NT * d) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(at) = hi;
+          *reinterpret_cast<uint2*>(at + NT * d) = lo;
         }
-        // an infinite element makes the row NaN, as its codes would not
-        if (lane == 0)
-          sh.fq[par][n] = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23)
-                                          : __int_as_float(0x7fffffff);
+        if (lane == 0) sh.fq[par][n] = p.scale_log2 * factor;
       }
       tc::fence_async_smem();
       dt_arrive(&sh.q_full);
@@ -276,7 +273,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
       const int least = t.L - t.n + 1;                // keys that every row sees
       for (int j = 0; j < t.tiles; ++j, ++T) {
         const int kb = t.k0 + j * kDtTok, pos = kb + tid;
-        const uint32_t scol = lanes + (T & 1) * C::N;
+        const uint32_t scol = lanes + (T & 1) * C::NQ;
         ok = dt_wait(&sh.sc_full[sc], scp, fail) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail);
         __syncwarp();
         tc::fence_after_sync();
@@ -290,7 +287,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         const bool edge = kb + kDtTok > least;        // some row does not see some token
         // weight exponents s + log2(vs), -inf where masked
         float x[CW];
-        read_columns(scol, NT, x);
+        read_scores(scol, x);
         const float4* f4 = reinterpret_cast<const float4*>(&sh.fq[par][0]);
 #pragma unroll
         for (int k = 0; k < CW; k += 4) {
@@ -337,17 +334,14 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
 #pragma unroll
           for (int n = 0; n < CW; ++n) al[n] = sh.alpha[n], l[n] *= al[n];
           for (int hf = 0; hf < (d + 127) / 128; ++hf) {
-            const uint32_t col = lanes + C::O0 + hf * C::N;
-            float o[16];
-            tc::tmem_ld16(col, o);   // hi parts; of 8 rows both
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= al[k % CW];
-            tc::tmem_st16(col, o);
-            if constexpr (CW == 16) {
-              tc::tmem_ld16(col + NT, o);
+            for (int c = 0; c < C::NP; c += 16) {
+              const uint32_t col = lanes + C::O0 + hf * C::NP + c;
+              float o[16];
+              tc::tmem_ld16(col, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= al[k];
-              tc::tmem_st16(col + NT, o);
+              for (int k = 0; k < 16; ++k) o[k] *= al[k % CW];
+              tc::tmem_st16(col, o);
             }
           }
           tc::tmem_st_wait();
@@ -355,7 +349,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         // the weights' place: read by the product before
         if (j > 0) okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail) && okp;
         uint8_t* pw = pd + tid * 16;
-        uint32_t hi[CW / 4], lo[CW / 4];
+        uint32_t w4[3][CW / 4];
         const float4* r4 = reinterpret_cast<const float4*>(&sh.ref[0]);
 #pragma unroll
         for (int u = 0; u < CW / 4; ++u) {
@@ -366,15 +360,18 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
             e[k] = dt_ex2(x[4 * u + k] - (&r.x)[k]);
             l[4 * u + k] = fmaf(e[k], rv, l[4 * u + k]);
           }
-          hi[u] = e4m3x4(e[0], e[1], e[2], e[3]);
-          const float2 a = e4m3_f32x2(hi[u]), b = e4m3_f32x2(hi[u] >> 16);
-          lo[u] = e4m3x4(e[0] - a.x, e[1] - a.y, e[2] - b.x, e[3] - b.y);
+          uint32_t part[3];
+          split_weights(e[0], e[1], e[2], e[3], part);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) w4[k][u] = part[k];
         }
         if constexpr (CW == 8) {
-          *reinterpret_cast<uint4*>(pw) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+          *reinterpret_cast<uint4*>(pw) = make_uint4(w4[0][0], w4[0][1], w4[1][0], w4[1][1]);
+          *reinterpret_cast<uint4*>(pw + 16 * kDtTok) = make_uint4(w4[2][0], w4[2][1], 0, 0);
         } else {
-          *reinterpret_cast<uint4*>(pw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(pw + NT * kDtTok) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint4*>(pw + k * 16 * kDtTok) = make_uint4(w4[k][0], w4[k][1], w4[k][2], w4[k][3]);
         }
         if (edge) {
           ok = bar_and(dt_wait(&sh.v_full[st], vp, fail));
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         __nv_bfloat16* oo = static_cast<__nv_bfloat16*>(p.o) + rh0 * d + e;
         float o[CW];
         if (u.tiles > 0) {
-          read_columns(lanes + C::O0 + hf * C::N, NT, o);
+          read_outputs(lanes + C::O0 + hf * C::NP, o);
         } else {
 #pragma unroll
           for (int k = 0; k < CW; ++k) o[k] = 0.f;
@@ -477,7 +474,7 @@ cudaError_t decode_tc(const AttnDecodeParams& p, int sms, cudaStream_t st) {
   DtParams w{};
   w.a = p;
   w.row_lo = 1, w.row_hi = kDtNarrow;
-  const uint32_t q = C::N * (uint32_t)p.c.d, pp = C::N * kDtTok;
+  const uint32_t q = C::NQ * (uint32_t)p.c.d, pp = C::NP * kDtTok;
   // half of 227 KB a CTA, of which 1 KB is the system's
   w.q_off = dt_rings(w, 115712, q + pp + (uint32_t)sizeof(DtShared<NT>) + 512);
   if (w.v_stages < 1) return cudaErrorInvalidValue;

@@ -2,13 +2,23 @@
 // the work items, the loads of the cache's blocks, the products' forms.
 //
 // The cache's e4m3 codes are the products' operands as they lie in memory; no
-// code is converted.  Q and P enter as two e4m3 parts each, x = hi + lo: hi
-// keeps 4 significant bits, lo 4 more of what is left, which is all 8 of a
-// bf16 q (scaled by a power of two so that its largest element is in (224,
-// 448]; parts below 2^-9 vanish, 2^-18 of that element) and rounds p like bf16
-// would.  A block's K scale multiplies its scores; its V scale goes into the
-// weight's exponent, so a weight is 2^(s + log2(vs) - M) and the sum of the p
-// is the sum of the weights over vs.
+// code is converted.  Q and P enter in 8-bit parts whose products are added:
+//
+// * A row of Q, scaled by a power of two so that its largest element is in (224,
+//   448], as hi + lo: hi an e4m3 of 4 significant bits, lo what is left of the 8
+//   of a bf16 (at most 3 bits and a sign), as an e4m3 of 16 times it or as an
+//   e5m2.  All 8 bits are kept of elements down to 2^-14 of the largest; below,
+//   an element is off by at most 2^-21 of the largest.
+// * A weight p as three e5m2, of 3 significant bits each: 9 together, to at
+//   most 2^-9 of the weight, half of what a rounding to bf16 may do.  e5m2
+//   reaches down to 2^-16, and weights are scaled so that the reference is
+//   2^11, so this holds down to 2^-19 of it; smaller weights are off by at most
+//   2^-28 of the reference (and are not dropped: where one key takes most of
+//   the softmax and its values are small, the outputs are theirs).
+//
+// A block's K scale multiplies its scores; its V scale goes into the weight's
+// exponent, so a weight is 2^(s + log2(vs) - M) and the sum of the p is the sum
+// of the weights over vs (in fp32, of the weights as they were before the split).
 #pragma once
 
 #include "attn.h"
@@ -22,11 +32,9 @@ constexpr int kDtBlocks = kDtTok / kKvBlock;
 constexpr int kDtSeqs = 256;         // sequences a launch
 constexpr int kDtMaxStages = 8;
 constexpr long long kDtWait = 4000000000LL;
-// Weights are scaled by 2^4 and may grow by 2^4.75 (430 < 448) before a row's
-// reference moves (which costs a pass over its outputs).  Parts vanish below
-// 2^-14 of the reference, rounding errors of 2^-15 that a weight near it
-// outweighs: against 64 bits the outputs' error is bf16's own rounding.
-constexpr float kDtBase = 4.f, kDtGrow = 4.75f;
+// Weights are scaled by 2^11 and may grow by 2^4.75 (55,109 < 57,344, the largest
+// e5m2) before a row's reference moves (which costs a pass over its outputs).
+constexpr float kDtBase = 11.f, kDtGrow = 4.75f;
 
 struct DtParams {
   AttnDecodeParams a;
@@ -78,7 +86,9 @@ __device__ __forceinline__ void mma_e4m3(uint32_t lead, uint32_t d, uint64_t a, 
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
-// Instruction descriptor: e4m3 A and B (both K-contiguous), fp32 sums, M = 128.
+// Instruction descriptor: e4m3 A and B (both K-contiguous), fp32 sums, M = 128;
+// and what makes A or B e5m2.
+constexpr uint32_t kE5m2A = 1u << 7, kE5m2B = 1u << 10;
 __host__ __device__ constexpr uint32_t idesc_e4m3(int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kDtTok >> 4) << 24);
 }
@@ -185,6 +195,63 @@ __device__ __forceinline__ float warp_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));
   return r;
+}
+
+// ---- the parts of Q and P --------------------------------------------------------
+// Two f16 to e5m2, nearest even (x in the low byte).
+__device__ __forceinline__ uint32_t e5m2x2(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+// Four weights in three parts, four codes a word.  An e5m2 is the upper byte of
+// an f16, so the first two parts are cut off without a conversion; the last is
+// rounded.  (The differences are exact: f16 holds 11 bits.)
+__device__ __forceinline__ void split_weights(float e0, float e1, float e2, float e3, uint32_t (&part)[3]) {
+  __half2 a = __floats2half2_rn(e0, e1), b = __floats2half2_rn(e2, e3);
+  auto bits = [](__half2& x) -> uint32_t& { return *reinterpret_cast<uint32_t*>(&x); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    part[i] = __byte_perm(bits(a), bits(b), 0x7531);
+    __half2 u, v;
+    bits(u) = bits(a) & 0xff00ff00u, bits(v) = bits(b) & 0xff00ff00u;
+    a = __hsub2(a, u), b = __hsub2(b, v);
+  }
+  part[2] = e5m2x2(a) | e5m2x2(b) << 16;
+}
+// Eight elements of a row of Q (x; a warp holds the row) in two parts: LO_E5M2
+// or, for sums of its own, 16 times the rest as e4m3 (kDtLo undoes it).  Returns
+// the power of two that the codes are to be multiplied by; NaN where an element
+// is infinite, which makes the row's scores NaN, as its codes would not.
+constexpr float kDtLo = 1.f / 16.f;
+template <bool LO_E5M2>
+__device__ __forceinline__ float split_row(const uint4& x, uint2& hi, uint2& lo) {
+  float f[8], amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t u = (&x.x)[k >> 1];
+    f[k] = __uint_as_float(k & 1 ? u & 0xffff0000u : u << 16);
+    amax = fmaxf(amax, fabsf(f[k]));
+  }
+  amax = warp_max(amax);
+  // largest element to (224, 448]; exponents kept where both factors are normal
+  int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(-100, min(100, e));
+  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float g[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) g[u] = f[4 * k + u] * inv;
+    const uint32_t h = e4m3x4(g[0], g[1], g[2], g[3]);
+    const float2 a = e4m3_f32x2(h), b = e4m3_f32x2(h >> 16);
+    (&hi.x)[k] = h;
+    if constexpr (LO_E5M2)
+      (&lo.x)[k] = e5m2x2(__floats2half2_rn(g[0] - a.x, g[1] - a.y)) | e5m2x2(__floats2half2_rn(g[2] - b.x, g[3] - b.y)) << 16;
+    else
+      (&lo.x)[k] = e4m3x4((g[0] - a.x) * 16.f, (g[1] - a.y) * 16.f, (g[2] - b.x) * 16.f, (g[3] - b.y) * 16.f);
+  }
+  return amax < INFINITY ? __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
 }
 
 // Running sums of the items (one warp); lengths out of bounds are reported and

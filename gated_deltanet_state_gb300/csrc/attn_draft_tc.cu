@@ -5,19 +5,21 @@
 // The pairs are the 128 rows of both products,
 //   S [rows x tokens] = Q K^T,    O [rows x elements] += P V,
 // with the cache's blocks as the second operands.  A softmax thread holds one
-// row, so no maximum or sum crosses lanes; the hi and lo parts of Q and P are
-// products of their own into the same sums, and P goes back to tensor memory
-// over the scores it comes from.  A tile of 128 tokens takes 24 products of 67
-// (scores) and 134 cycles (outputs), 2,140 in all, while its 64 KB at d = 256
-// take 2,700 cycles of the memory's rate; the softmax of a tile takes 2,600, so
-// two warpgroups take the tiles in turn, the reference passing from one to the
-// other before the exponentials.
+// row, so no maximum or sum crosses lanes; the parts of Q (two) and of P (three)
+// are products of their own into the same sums, and P goes back to tensor
+// memory over the scores it comes from.  A tile of 128 tokens takes 16 products
+// of 67 cycles (scores) and 12 of 134 (outputs), 2,680 in all, as many as its
+// 64 KB at d = 256 take at the memory's rate (2,700); the softmax of a tile
+// takes 2,600, so two warpgroups take the tiles in turn, the reference passing
+// from one to the other before the exponentials.
 //
 // Measured: 16 drafts of 16 rows over 2,048 to 32,768 tokens (606 MB of codes)
-// 216 us with the join, 2.8 TB/s.  A CTA's items end one at a time (the sums'
-// way out, 128 rows x 1 KB, the next rows' way in: 25,000 of an item's 80,000
-// cycles), since their sums and two score tiles fill tensor memory; the join
-// takes 22 us.
+// 235 us with the join, 2.6 TB/s (with P in two e4m3 parts on one scale 216 us,
+// but then what lies below 2^-14 of the reference was lost).  A score buffer's
+// own chain (scores, softmax, outputs one after another, and what passes between
+// them) is the longest part of a tile; an item's end (128 rows x 1 KB on their
+// way out, the next rows' way in) takes about as long as seven tiles, since one
+// set of sums and two score tiles fill tensor memory; the join takes 22 us.
 #include "attn_decode_tc.cuh"
 
 namespace gdn {
@@ -112,36 +114,14 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int n = r0 + u;
-          float f[8], amax = 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t b = (&x[u].x)[k >> 1];
-            f[k] = __uint_as_float(k & 1 ? b & 0xffff0000u : b << 16);
-            amax = fmaxf(amax, fabsf(f[k]));
-          }
-          amax = warp_max(amax);
-          // largest element to (224, 448]; exponents kept where both factors are normal
-          int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
-          e = max(-100, min(100, e));
-          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float g4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g4[i] = f[4 * k + i] * inv;
-            hi[k] = e4m3x4(g4[0], g4[1], g4[2], g4[3]);
-            const float2 a = e4m3_f32x2(hi[k]), b = e4m3_f32x2(hi[k] >> 16);
-            lo[k] = e4m3x4(g4[0] - a.x, g4[1] - a.y, g4[2] - b.x, g4[3] - b.y);
-          }
+          uint2 hi, lo;
+          const float factor = split_row<true>(x[u], hi, lo);
           if (e0 < d) {
             uint8_t* at = qd + (n >> 3) * 8 * d + (e0 >> 4) * 128 + (n & 7) * 16 + (e0 & 8);
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + kDrRows * d) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(at) = hi;
+            *reinterpret_cast<uint2*>(at + kDrRows * d) = lo;
           }
-          // an infinite element makes the row NaN, as its codes would not
-          if (lane == 0)
-            sh.fq[par][n] = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
+          if (lane == 0) sh.fq[par][n] = p.scale_log2 * factor;
         }
       }
       tc::fence_async_smem();
@@ -245,11 +225,11 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         }
         const float r = (ref == -INFINITY ? 0.f : ref) - kDtBase;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {   // 64 tokens: 16 columns of hi codes, 16 of lo codes
-          uint32_t hi[16], lo[16];
+        for (int u = 0; u < 4; ++u) {   // 32 tokens: 8 columns of codes of each part
+          uint32_t code[3][8];
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int blk = u * 4 + b;
+          for (int b = 0; b < 2; ++b) {
+            const int blk = u * 2 + b;
             const f32x2 kk = pack2(kf[blk], kf[blk]), rr = pack2(lv[blk] - r, lv[blk] - r);
             float sum = 0.f;
 #pragma unroll
@@ -259,15 +239,15 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
               const float2 y = unpack2(fma2(pack2(__uint_as_float(q4[2]), __uint_as_float(q4[3])), kk, rr));
               const float e0 = dt_ex2(x.x), e1 = dt_ex2(x.y), e2 = dt_ex2(y.x), e3 = dt_ex2(y.y);
               sum += (e0 + e1) + (e2 + e3);
-              const uint32_t h = e4m3x4(e0, e1, e2, e3);
-              const float2 f = e4m3_f32x2(h), f2 = e4m3_f32x2(h >> 16);
-              hi[b * 4 + k] = h;
-              lo[b * 4 + k] = e4m3x4(e0 - f.x, e1 - f.y, e2 - f2.x, e3 - f2.y);
+              uint32_t part[3];
+              split_weights(e0, e1, e2, e3, part);
+#pragma unroll
+              for (int i2 = 0; i2 < 3; ++i2) code[i2][b * 4 + k] = part[i2];
             }
             l = fmaf(sum, __uint_as_float((uint32_t)(127 - (int)lv[blk]) << 23), l);   // over the V scale
           }
-          tc::tmem_st16u(scol + u * 16, hi);
-          tc::tmem_st16u(scol + 32 + u * 16, lo);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) tc::tmem_st8(scol + 32 * k + u * 8, code[k]);
         }
         tc::tmem_st_wait();
         if (edge) {
@@ -391,7 +371,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       const uint32_t lead = tc::elect_one();
       auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
       constexpr uint32_t id_qk = idesc_e4m3(kDtTok);
-      const uint32_t id_pv = idesc_e4m3(d);
+      const uint32_t id_pv = idesc_e4m3(d) | kE5m2A;
       const uint32_t k0 = smem_u32(base + w.k_off), v0 = smem_u32(base + w.v_off), qa = smem_u32(base + w.q_off);
       const uint32_t rows8 = 8u * d;
       const uint64_t vstep = (uint64_t)(32u * d >> 4);
@@ -405,13 +385,14 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         const uint32_t dst = tb + (tt & 1) * kDtTok;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
+          const uint32_t id = id_qk | (part ? kE5m2A : 0u);
           const uint64_t a = desc_tiles(qa + part * kDrRows * d, 128, rows8);
           if (d == 256) {
-            mma_steps<8>(lead, dst, a, b, id_qk, 16, 16, part);
+            mma_steps<8>(lead, dst, a, b, id, 16, 16, part);
           } else if (d == 128) {
-            mma_steps<4>(lead, dst, a, b, id_qk, 16, 16, part);
+            mma_steps<4>(lead, dst, a, b, id, 16, 16, part);
           } else {
-            for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id_qk, part | c);
+            for (int c = 0; c < d / 32; ++c) mma_e4m3(lead, dst, a + c * 16, b + c * 16, id, part | c);
           }
         }
         tc::mma_commit_if(lead, &sh.k_empty[ks]);
@@ -435,7 +416,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
           tc::fence_after_sync();
           const uint64_t b = desc_tiles(v0 + vs * unit, 16u * d, 128);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 3; ++part)
 #pragma unroll
             for (int c = 0; c < kDtTok / 32; ++c)
               mma_e4m3_ts(lead, tb + kDrO, tb + (T & 1) * kDtTok + part * 32 + c * 8, b + c * vstep, id_pv, j | part | c);
