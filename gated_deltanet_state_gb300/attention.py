@@ -43,7 +43,7 @@ class _KvGatherArgs(ctypes.Structure):
 class _AttnDecodeArgs(ctypes.Structure):
     _fields_ = [("num_seqs", _i32), ("max_pages", _i32), ("max_q_len", _i32), ("max_kv_len", _i32),
                 ("total_tokens", _i64), ("q_stride", _i64), ("cu_seqlens", _P), ("kv_len", _P), ("block_table", _P),
-                ("q", _P), ("o", _P), ("lse", _P), ("dev_error", _P)]
+                ("q", _P), ("o", _P), ("lse", _P), ("dev_error", _P), ("wait_cycles", _i64)]
 
 
 class _AttnPrefillArgs(ctypes.Structure):
@@ -224,12 +224,13 @@ def gdn_attn_decode_workspace_size(shape: AttnShape, num_seqs: int, total_tokens
 
 
 def gdn_attn_decode(shape: AttnShape, pool: KVPool, *, q, cu_seqlens, kv_len, block_table, o, dev_error, lse=None,
-                    max_q_len: int = 1, max_kv_len: Optional[int] = None, workspace=None, stream=None,
-                    raise_on_error: bool = True) -> int:
+                    max_q_len: int = 1, max_kv_len: Optional[int] = None, workspace=None, wait_cycles: int = 0,
+                    stream=None, raise_on_error: bool = True) -> int:
     """Attention of 1 to 32 new rows a sequence over the 8-bit cache (gdn.h:
     gdn_attn_decode).  max_kv_len bounds kv_len (None: what the block table
     can hold).  Without `workspace` one of gdn_attn_decode_workspace_size
-    bytes is taken from PyTorch's allocator for the call."""
+    bytes is taken from PyTorch's allocator for the call.  wait_cycles bounds
+    the device-side waits (gdn.h)."""
     lib = load_library()
     n = int(kv_len.numel())
     qp, qs = _rows(q, shape.num_q_heads, shape, "q")
@@ -244,7 +245,8 @@ def gdn_attn_decode(shape: AttnShape, pool: KVPool, *, q, cu_seqlens, kv_len, bl
     a = _AttnDecodeArgs(n, cols, int(max_q_len), int(max_kv_len), T, qs, _ints(cu_seqlens, n + 1, "cu_seqlens"),
                         _dev(kv_len, torch.int32, "kv_len"), bt, qp,
                         _out(o, (T, shape.num_q_heads, shape.head_dim), shape.torch_dtype(), "o"),
-                        _out(lse, (T, shape.num_q_heads), torch.float32, "lse"), _ints(dev_error, 1, "dev_error"))
+                        _out(lse, (T, shape.num_q_heads), torch.float32, "lse"), _ints(dev_error, 1, "dev_error"),
+                        int(wait_cycles))
     st = lib.gdn_attn_decode(desc, pool.abi(), a, _dev(workspace, None, "workspace"),
                              workspace.numel() * workspace.element_size(), _on(stream, q))
     return _check(st, "gdn_attn_decode") if raise_on_error else st

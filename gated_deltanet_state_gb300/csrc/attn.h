@@ -74,6 +74,7 @@ struct AttnDecodeParams {
   float* part_o;      // [max_pieces][T * Hq][d] sums of p v (nullptr: one piece, written to o)
   float2* part_ml;    // [max_pieces][T * Hq] (m, l) of the pieces
   int32_t* err;
+  int64_t wait_cycles;
 };
 
 struct AttnPrefillParams {

@@ -172,6 +172,7 @@ gdn_status gdn_attn_decode(const gdn_attn_desc* desc, const gdn_pool* pool, cons
     p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + part_o_bytes(desc, a->total_tokens, pieces));
   }
   p.err = a->dev_error;
+  p.wait_cycles = a->wait_cycles;
   return cuda_status(launch_attn_decode(p, desc->dtype, static_cast<cudaStream_t>(stream)));
 }
 

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d;
   const int KS = w.k_stages, VS = w.v_stages, NS = max(KS, VS) + 2;
   volatile int* fail = &sh.fail;
+  const long long limit = w.wait;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], 1);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
       tc::mbar_init(&sh.s_full[i], 1), tc::mbar_init(&sh.p_full[i], 128), tc::mbar_init(&sh.o_done[i], 1);
     tc::mbar_init(&sh.q_full, 128);
     tc::mbar_init(&sh.drain, 1);
-    sh.fail = 0;
+    sh.fail = limit < 0;
     sh.grow = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
   const uint32_t tb = sh.tmem;
   // this CTA's run of items
   const int i0 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
-  const int i1 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int i1 = limit < 0 ? i0 : dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
   const uint32_t unit = (uint32_t)kDtTok * d;   // bytes of a tile's K (or V) codes
   int loaded = 0;                               // tiles loaded (a loading warp's)
 
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
     unsigned T = 0;   // tiles multiplied
     bool ok = true;
     auto qk = [&](unsigned tt) {
-      if (!all(dt_wait(&sh.k_full[ks], kp, fail))) return false;
+      if (!all(dt_wait(&sh.k_full[ks], kp, fail, limit))) return false;
       tc::fence_after_sync();
       const uint64_t a = desc_tiles(k0 + ks * unit, 128, rows8);
       const uint64_t b = desc_tiles(qa, 128, rows8);
@@ -194,11 +195,11 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
     for (int i = i0; ok && i < i1; ++i) {
       if (i == i0) t = dt_item<NT>(w, sh.items, i);
       else dt_next<NT>(w, sh.items, i, t);
-      if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail));
+      if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail, limit));
       if (ok && t.tiles > 0) ok = qk(T);
       for (int j = 0; ok && j < t.tiles; ++j, ++T) {
         if (j + 1 < t.tiles) ok = qk(T + 1);
-        ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail));
+        ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail, limit) && dt_wait(&sh.v_full[vs], vp, fail, limit));
         if (!ok) break;
         tc::fence_after_sync();
         for (int hf = 0; hf < halves; ++hf) {
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
       for (int j = 0; j < t.tiles; ++j, ++T) {
         const int kb = t.k0 + j * kDtTok, pos = kb + tid;
         const uint32_t scol = lanes + (T & 1) * C::NQ;
-        ok = dt_wait(&sh.sc_full[sc], scp, fail) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail);
+        ok = dt_wait(&sh.sc_full[sc], scp, fail, limit) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail, limit);
         __syncwarp();
         tc::fence_after_sync();
         const float kscale = sh.ks[sc][tid >> 4], vscale = sh.vs[sc][tid >> 4];
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         if (*(volatile unsigned*)&sh.grow == T + 1) {
           // the products before this tile's: done, then scaled column by column
           // (one that runs out shows at the next barrier)
-          okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+          okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit);
           __syncwarp();
           tc::fence_after_sync();
           float al[CW];
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
           tc::tmem_st_wait();
         }
         // the weights' place: read by the product before
-        if (j > 0) okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail) && okp;
+        if (j > 0) okp = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit) && okp;
         uint8_t* pw = pd + tid * 16;
         uint32_t w4[3][CW / 4];
         const float4* r4 = reinterpret_cast<const float4*>(&sh.ref[0]);
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
             *reinterpret_cast<uint4*>(pw + k * 16 * kDtTok) = make_uint4(w4[k][0], w4[k][1], w4[k][2], w4[k][3]);
         }
         if (edge) {
-          ok = bar_and(dt_wait(&sh.v_full[st], vp, fail));
+          ok = bar_and(dt_wait(&sh.v_full[st], vp, fail, limit));
           if (!ok) break;
           dt_clean(base + w.v_off + (uint32_t)st * unit, sh.bad[ip], t, kb, least, d, tid);
         }
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         if (dt_new_rows(t, false)) load_q(t, par ^= 1);
       }
       column_sums<CW>(l, sh.lsum, lane, quad);
-      if (u.tiles > 0) ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+      if (u.tiles > 0) ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit);
       ok = bar_and(ok && okp);
       if (!ok) break;
       tc::fence_after_sync();
@@ -473,6 +474,7 @@ cudaError_t decode_tc(const AttnDecodeParams& p, int sms, cudaStream_t st) {
   using C = DtCfg<NT>;
   DtParams w{};
   w.a = p;
+  w.wait = dt_limit(p);
   w.row_lo = 1, w.row_hi = kDtNarrow;
   const uint32_t q = C::NQ * (uint32_t)p.c.d, pp = C::NP * kDtTok;
   // half of 227 KB a CTA, of which 1 KB is the system's

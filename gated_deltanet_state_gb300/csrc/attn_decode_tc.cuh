@@ -41,6 +41,7 @@ struct DtParams {
   int32_t s0, ns;       // this launch's sequences ...
   int32_t row_lo, row_hi;   // ... those with (row, head of the group) pairs in [row_lo, row_hi]
   int32_t k_stages, v_stages;
+  long long wait;       // SM clocks that a wait may take; < 0: every one has run out
   uint32_t k_off, v_off, q_off, p_off, misc_off;   // dynamic shared memory
 };
 
@@ -56,12 +57,12 @@ struct DtBase {
   int fail;
 };
 
-__device__ __forceinline__ bool dt_wait(uint64_t* m, uint32_t parity, volatile int* fail) {
+__device__ __forceinline__ bool dt_wait(uint64_t* m, uint32_t parity, volatile int* fail, long long limit) {
   if (tc::mbar_test_wait(m, parity)) return true;
   const long long t0 = clock64();
   while (!tc::mbar_try_wait(m, parity)) {
     if (*fail) return false;
-    if (clock64() - t0 > kDtWait) {
+    if (clock64() - t0 > limit) {
       *fail = 1;
       return false;
     }
@@ -315,7 +316,7 @@ __device__ __forceinline__ int dt_load(const DtParams& w, DtBase& sh, uint8_t* b
       if (j + 1 < t.tiles) next = page_of(j + 1);
       const bool in = lane < kDtBlocks && pos < t.k1, good = in && page >= 0 && page < p.c.num_pages;
       if (in && !good) set_error(p.err, GDN_ERR_PAGE_RANGE);
-      if (loaded >= ST) ok = dt_wait(&empty[st], ph ^ 1, fail);
+      if (loaded >= ST) ok = dt_wait(&empty[st], ph ^ 1, fail, w.wait);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       uint8_t* dst = ring + (uint32_t)st * unit;
       const unsigned have = __ballot_sync(0xffffffffu, good);
@@ -382,6 +383,10 @@ __device__ __forceinline__ void dt_clean(uint8_t* v, int* bad, const DtItem& t, 
         }
       }
     }
+}
+
+inline long long dt_limit(const AttnDecodeParams& p) {
+  return p.wait_cycles > 0 ? p.wait_cycles : p.wait_cycles < 0 ? -1 : kDtWait;
 }
 
 // The cache's share of dynamic shared memory: K and V stages in what `fixed`

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d;
   const int KS = w.k_stages, VS = w.v_stages, NS = max(KS, VS) + 2;
   volatile int* fail = &sh.fail;
+  const long long limit = w.wait;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], 1);
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     for (int i = 0; i < 2; ++i) tc::mbar_init(&sh.m_ready[i], 128), tc::mbar_init(&sh.fin[i], 128);
     tc::mbar_init(&sh.o_free, 256);
     tc::mbar_init(&sh.drain, 1);
-    sh.fail = 0;
+    sh.fail = limit < 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 8) {
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
   tc::fence_after_sync();
   const uint32_t tb = sh.tmem;
   const int i0 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
-  const int i1 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int i1 = limit < 0 ? i0 : dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
   const uint32_t unit = (uint32_t)kDtTok * d;
   int loaded = 0;
 
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         if ((int)(T & 1) != wg) continue;
         const int kb = t.k0 + j * kDtTok, sc = T % NS, st = T % VS;   // scale slot, V stage
         const uint32_t scol = lanes + (T & 1) * kDtTok;
-        ok = dt_wait(&sh.sc_full[sc], T / NS & 1, fail) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail);
+        ok = dt_wait(&sh.sc_full[sc], T / NS & 1, fail, limit) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail, limit);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc::fence_after_sync();
         const float fq = sh.fq[par][tid];
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         float alpha = 1.f;
         const float before = ref;
         if (j > 0) {   // the reference after the tile before, the other warpgroup's
-          ok = dt_wait(&sh.m_ready[wg ^ 1], ((T - 1) >> 1) & 1, fail);
+          ok = dt_wait(&sh.m_ready[wg ^ 1], ((T - 1) >> 1) & 1, fail, limit);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           ref = sh.m[wg ^ 1][tid];
         }
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         dt_arrive(&sh.m_ready[wg]);
         if (j > 1 && ref != before) l *= dt_ex2(before - ref);
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
-          ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail);
+          ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc::fence_after_sync();
 #pragma unroll 1
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         }
         tc::tmem_st_wait();
         if (edge) {
-          ok = dt_wait(&sh.v_full[st], T / VS & 1, fail);
+          ok = dt_wait(&sh.v_full[st], T / VS & 1, fail, limit);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           dt_clean(base + w.v_off + (uint32_t)st * unit, sh.bad[ip], t, kb, least, d, tid);
           tc::fence_async_smem();
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         dt_next<NT>(w, sh.items, i + 1, t);
         if (dt_new_rows(t, false)) {
           // (the last scores, if the other warpgroup's, have to be done with the rows)
-          if (u.tiles > 0) ok = dt_wait(&sh.s_full[last & 1], (last >> 1) & 1, fail);
+          if (u.tiles > 0) ok = dt_wait(&sh.s_full[last & 1], (last >> 1) & 1, fail, limit);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           load_q(t, par ^= 1);
         }
@@ -279,21 +280,21 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
         // every second 32 elements
         const int w1 = (int)(last & 1);
         if (wg != w1) {
-          ok = dt_wait(&sh.m_ready[w1], (last >> 1) & 1, fail);
+          ok = dt_wait(&sh.m_ready[w1], (last >> 1) & 1, fail, limit);
           const float mine = ref;
           ref = sh.m[w1][tid];
           sh.m[wg][tid] = l == 0.f ? 0.f : l * dt_ex2(mine - ref);
           dt_arrive(&sh.fin[0]);
-          ok = dt_wait(&sh.fin[1], items & 1, fail) && ok;
+          ok = dt_wait(&sh.fin[1], items & 1, fail, limit) && ok;
           l = sh.m[w1][tid];
         } else {
-          ok = dt_wait(&sh.fin[0], items & 1, fail);
+          ok = dt_wait(&sh.fin[0], items & 1, fail, limit);
           l += sh.m[wg ^ 1][tid];
           sh.m[wg][tid] = l;
           dt_arrive(&sh.fin[1]);
         }
         ++items;
-        ok = ok && dt_wait(&sh.o_done[last & 1], (last >> 1) & 1, fail);
+        ok = ok && dt_wait(&sh.o_done[last & 1], (last >> 1) & 1, fail, limit);
       }
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc::fence_after_sync();
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       unsigned T = 0;   // tiles multiplied
       bool ok = true;
       auto qk = [&](unsigned tt) {
-        if (!all(dt_wait(&sh.k_full[ks], kp, fail))) return false;
+        if (!all(dt_wait(&sh.k_full[ks], kp, fail, limit))) return false;
         tc::fence_after_sync();
         const uint64_t b = desc_tiles(k0 + ks * unit, 128, rows8);
         const uint32_t dst = tb + (tt & 1) * kDtTok;
@@ -405,13 +406,13 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       for (int i = i0; ok && i < i1; ++i) {
         if (i == i0) t = dt_item<NT>(w, sh.items, i);
         else dt_next<NT>(w, sh.items, i, t);
-        if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail));
+        if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail, limit));
         if (ok && t.tiles > 0) ok = qk(T);
         for (int j = 0; ok && j < t.tiles; ++j, ++T) {
           if (j + 1 < t.tiles) ok = qk(T + 1);
-          ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail) && dt_wait(&sh.v_full[vs], vp, fail));
+          ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail, limit) && dt_wait(&sh.v_full[vs], vp, fail, limit));
           // O of the item before has been read, by both warpgroups
-          if (ok && j == 0 && items++ > 0) ok = all(dt_wait(&sh.o_free, items & 1, fail));
+          if (ok && j == 0 && items++ > 0) ok = all(dt_wait(&sh.o_free, items & 1, fail, limit));
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t b = desc_tiles(v0 + vs * unit, 16u * d, 128);
@@ -450,6 +451,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
 cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overlap, cudaStream_t st) {
   DtParams w{};
   w.a = p;
+  w.wait = dt_limit(p);
   w.row_lo = overlap ? kDtNarrow + 1 : 1, w.row_hi = 0x7fffffff;
   const uint32_t q = 2 * kDrRows * (uint32_t)p.c.d;
   w.q_off = dt_rings(w, 232448, q + (uint32_t)sizeof(DrShared) + 512);

@@ -726,6 +726,11 @@ typedef struct gdn_attn_decode_args {
   void* o;                       /* [T][Hq][d] dtype                          */
   float* lse;                    /* [T][Hq] or NULL                           */
   int32_t* dev_error;
+  int64_t wait_cycles;           /* bound of each device-side wait of the
+                                    tensor-core kernels in SM clocks; 0: the
+                                    default (~2 s); < 0: every one reports
+                                    GDN_ERR_TIMEOUT at once (outputs are then
+                                    not written)                              */
 } gdn_attn_decode_args;
 
 /* Device workspace bytes (256-byte aligned scratch, as the prefill's): the

@@ -1,0 +1,71 @@
+"""Bounded waits of the attention kernels that run out: the call returns, says
+so, and the next one is as always.  No fault is made: wait_cycles < 0 has every
+wait report at once, and a bound of a few clocks ends waits that would have
+been served a moment later."""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_state_gb300 as gdn
+from gated_deltanet_state_gb300.inputs import AttnShape
+
+from attn_harness import err_word, fill_cache, table_for
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = gdn.STATUS_CODE["GDN_ERR_TIMEOUT"]
+
+# (rows, keys) of each sequence: 6 (row, head) pairs a row and kv head
+BATCHES = {
+    "few rows, one piece": [(1, 100), (2, 7), (1, 0)],
+    "few rows, pieces": [(1, 5000), (2, 700), (1, 31)],
+    "drafts, one piece": [(16, 200), (32, 90)],
+    "drafts, pieces": [(16, 5000), (24, 9000)],
+    "both": [(16, 3000), (1, 4000), (2, 60), (32, 700), (0, 50), (1, 9000)],
+}
+
+
+class Decode:
+    def __init__(self, batch, d=128):
+        self.sh = AttnShape(12, 2, d, 64)
+        news, lens = [n for n, _ in batch], [k for _, k in batch]
+        pages = sum(-(-k // 64) for k in lens) + 1
+        self.pool = gdn.KVPool(self.sh, pages, fill=0xFF)
+        table = table_for(lens, 64, pages, 2)
+        fill_cache(self.pool, table, lens, 3)
+        self.q = torch.randn(sum(news), 12, d, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+        i32 = dict(dtype=torch.int32, device="cuda")
+        self.cu, self.kv = torch.tensor([0] + np.cumsum(news).tolist(), **i32), torch.tensor(lens, **i32)
+        self.table, self.top = table.cuda(), (max(news), max(lens))
+
+    def __call__(self, wait=0, err=None):
+        o, lse = torch.full_like(self.q, 7.0), torch.full(self.q.shape[:2], 7.0, device="cuda")
+        err = err_word() if err is None else err
+        gdn.gdn_attn_decode(self.sh, self.pool, q=self.q, cu_seqlens=self.cu, kv_len=self.kv, block_table=self.table, o=o,
+                            lse=lse, max_q_len=self.top[0], max_kv_len=self.top[1], wait_cycles=wait, dev_error=err)
+        return o, lse, err.item()
+
+
+@pytest.mark.parametrize("batch", list(BATCHES))
+def test_decode_waits_that_run_out_write_nothing(batch):
+    call = Decode(BATCHES[batch])
+    want, want_lse, err = call()
+    assert err == 0
+    o, lse, err = call(-1)
+    assert err == TIMEOUT and bool((o == 7).all()) and bool((lse == 7).all())
+    o, lse, err = call()
+    assert err == 0 and torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("batch", list(BATCHES))
+def test_decode_waits_that_run_out_midway(batch):
+    """Whatever wait gives up first, the call returns and the context is intact."""
+    call = Decode(BATCHES[batch], d=256)
+    want, want_lse, err = call()
+    assert err == 0
+    for wait in (1, 1, 3000, 10000, 30000):
+        o, lse, err = call(wait)
+        assert err in (0, TIMEOUT)
+        assert err == TIMEOUT or (torch.equal(o, want) and torch.equal(lse, want_lse))
+    o, lse, err = call()
+    assert err == 0 and torch.equal(o, want) and torch.equal(lse, want_lse)
