@@ -122,6 +122,9 @@ __host__ __device__ inline int decode_max_pieces(int L) {
   return m > s ? m : s;
 }
 
+// In place of a row's sum (never negative) in a piece that was not finished.
+constexpr float kLostPiece = -1.f;
+
 cudaError_t launch_kv_tables(const KvTablesParams& p, cudaStream_t st);
 cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_kv_gather(const KvGatherParams& p, int dtype, cudaStream_t st);

@@ -153,7 +153,8 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
   const uint32_t tb = sh.tmem;
   // this CTA's run of items
   const int i0 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
-  const int i1 = limit < 0 ? i0 : dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int last_item = dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int i1 = limit < 0 ? i0 : last_item;
   const uint32_t unit = (uint32_t)kDtTok * d;   // bytes of a tile's K (or V) codes
   int loaded = 0;                               // tiles loaded (a loading warp's)
 
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
   if (sh.fail) {
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
-    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
+    dt_report<NT>(w, sh, i0, last_item);
     if ((warp == WARPS || warp == WARPS + 1) && lane == 0) dt_drain(w, sh, loaded, warp == WARPS + 1);
     __syncwarp();
     __syncthreads();

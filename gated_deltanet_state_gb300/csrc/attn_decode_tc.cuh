@@ -365,6 +365,22 @@ __device__ __forceinline__ void dt_drain(const DtParams& w, DtBase& sh, int load
     tc::mbar_wait_bounded(is_v ? &sh.v_full[n % ST] : &sh.k_full[n % ST], (uint32_t)(n / ST) & 1, kDtWait);
 }
 
+// Reports a run-out and marks the rows of the pieces that this CTA had, items
+// [i0, i1): what it has not written of them must not be joined.
+template <int NT>
+__device__ __forceinline__ void dt_report(const DtParams& w, const DtBase& sh, int i0, int i1) {
+  const AttnDecodeParams& p = w.a;
+  if (threadIdx.x == 0) atomicExch(p.err, GDN_ERR_TIMEOUT);   // over an earlier code
+  if (!p.part_o) return;
+  for (int i = i0; i < i1; ++i) {
+    const DtItem t = dt_item<NT>(w, sh.items, i);
+    for (int n = threadIdx.x; n < t.rows; n += blockDim.x) {
+      const int row = (t.r0 + n) / p.G, g = t.r0 + n - row * p.G;
+      p.part_ml[t.piece * (p.T * p.Hq) + (int64_t)(t.q0 + row) * p.Hq + t.h * p.G + g] = make_float2(0.f, kLostPiece);
+    }
+  }
+}
+
 // Values of a tile (of its stage v) that some row may not see: past the
 // sequence they become zero, and so do NaN codes (a weight of 0 would not keep
 // them out of the product), noted by element for the rows that do see them.

@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
   tc::fence_after_sync();
   const uint32_t tb = sh.tmem;
   const int i0 = dt_first<NT>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
-  const int i1 = limit < 0 ? i0 : dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int last_item = dt_first<NT>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int i1 = limit < 0 ? i0 : last_item;
   const uint32_t unit = (uint32_t)kDtTok * d;
   int loaded = 0;
 
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
   if (sh.fail) {
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
-    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
+    dt_report<NT>(w, sh, i0, last_item);
     if ((warp == 8 || warp == 9) && lane == 0) dt_drain(w, sh, loaded, warp == 9);
     __syncwarp();
     __syncthreads();

@@ -181,13 +181,14 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
 // w_i = 2^(m_i - max m).  A warp a (row, head): the lanes hold the pieces'
 // weights (76 at most), then an element of the head each.  Bound by the pieces'
 // bytes: 15.6 us after 256 single rows (24 heads, d = 256), 22 us after 16 drafts of 16.
+// (Four CTAs an SM leave 128 registers, which hold eight pieces' loads; with the
+// bound open the compiler loads one by one: 417 us for the 256 rows' call, 405.)
 template <typename T>
-__global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeParams p) {
+__global__ void __launch_bounds__(128, 4) attn_decode_join_kernel(const AttnDecodeParams p) {
   const int s = blockIdx.y, lane = threadIdx.x & 31, d = p.c.d;
   const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the pieces' kernel before this one
   if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
-  if (*p.err == GDN_ERR_TIMEOUT) return;   // a wait ran out: the pieces cannot be trusted
   const int pieces = decode_pieces(L, n * p.G);
   const int64_t R = p.T * p.Hq;
   for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n * p.Hq; i += gridDim.x * 4) {
@@ -199,6 +200,8 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeP
       ml[k] = lane + 32 * k < pieces ? p.part_ml[(lane + 32 * k) * R + rh] : make_float2(-INFINITY, 0.f);
       mx = fmaxf(mx, ml[k].x);
     }
+    // a wait ran out in a piece of this row: the row is not written
+    const bool lost = __any_sync(0xffffffffu, ml[0].y == kLostPiece || ml[1].y == kLostPiece || ml[2].y == kLostPiece);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float ref = mx == -INFINITY ? 0.f : mx;
@@ -234,10 +237,10 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const AttnDecodeP
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (lane * 4 + 128 * h < d)
+      if (lane * 4 + 128 * h < d && !lost)
 #pragma unroll
         for (int e = 0; e < 4; ++e) put1<T>(p.o, rh * d + lane * 4 + 128 * h + e, sum == 0.f ? 0.f : (&acc[h].x)[e] / sum);
-    if (p.lse && lane == 0) p.lse[rh] = sum == 0.f ? -INFINITY : mx * 0.693147180559945309f + logf(sum);
+    if (p.lse && lane == 0 && !lost) p.lse[rh] = sum == 0.f ? -INFINITY : mx * 0.693147180559945309f + logf(sum);
   }
 }
 

@@ -729,8 +729,11 @@ typedef struct gdn_attn_decode_args {
   int64_t wait_cycles;           /* bound of each device-side wait of the
                                     tensor-core kernels in SM clocks; 0: the
                                     default (~2 s); < 0: every one reports
-                                    GDN_ERR_TIMEOUT at once (outputs are then
-                                    not written)                              */
+                                    GDN_ERR_TIMEOUT (over any earlier code) at
+                                    once, outputs are then not written.  After
+                                    a later run-out the outputs are not
+                                    complete; what dev_error held before the
+                                    call has no effect on it                  */
 } gdn_attn_decode_args;
 
 /* Device workspace bytes (256-byte aligned scratch, as the prefill's): the

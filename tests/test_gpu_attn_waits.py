@@ -69,3 +69,16 @@ def test_decode_waits_that_run_out_midway(batch):
         assert err == TIMEOUT or (torch.equal(o, want) and torch.equal(lse, want_lse))
     o, lse, err = call()
     assert err == 0 and torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("batch", list(BATCHES))
+def test_decode_goes_by_its_own_run_outs(batch):
+    """A code that dev_error holds from an earlier call neither stops this one
+    nor hides that its waits have run out."""
+    call = Decode(BATCHES[batch])
+    want, want_lse, _ = call()
+    word = lambda code: torch.tensor([code], dtype=torch.int32, device="cuda")  # noqa: E731
+    o, lse, err = call(err=word(TIMEOUT))
+    assert err == TIMEOUT and torch.equal(o, want) and torch.equal(lse, want_lse)
+    o, lse, err = call(-1, err=word(gdn.STATUS_CODE["GDN_ERR_PAGE_RANGE"]))
+    assert err == TIMEOUT and bool((o == 7).all()) and bool((lse == 7).all())
