@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
   if (*fail) {
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
-    if (threadIdx.x == 0) set_error(p.err, GDN_ERR_TIMEOUT);
+    if (threadIdx.x == 0) atomicExch(p.err, GDN_ERR_TIMEOUT);   // over an earlier code
     if (warp == C::SW && lane == 0) {
       // a pair's bytes of K and of whole V tiles count on the issuing CTA's
       // barriers, which waits for both: with the same units on both sides

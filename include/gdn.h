@@ -771,8 +771,10 @@ typedef struct gdn_attn_prefill_args {
                                     clocks (one may last as long as 128 rows
                                     take); 0: the default (~2 s); < 0 makes
                                     every such wait of the tensor-core path
-                                    report GDN_ERR_TIMEOUT at once (outputs
-                                    are then not written)                     */
+                                    report GDN_ERR_TIMEOUT (over any earlier
+                                    code) at once, outputs are then not
+                                    written; after a later run-out they are
+                                    not complete                              */
 } gdn_attn_prefill_args;
 
 gdn_status gdn_attn_prefill(const gdn_attn_desc* desc, const gdn_attn_prefill_args* args, void* stream);

@@ -82,3 +82,15 @@ def test_decode_goes_by_its_own_run_outs(batch):
     assert err == TIMEOUT and torch.equal(o, want) and torch.equal(lse, want_lse)
     o, lse, err = call(-1, err=word(gdn.STATUS_CODE["GDN_ERR_PAGE_RANGE"]))
     assert err == TIMEOUT and bool((o == 7).all()) and bool((lse == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prefill_reports_a_run_out_over_an_earlier_code(d):
+    sh = AttnShape(4, 2, d, 16)
+    g = torch.Generator().manual_seed(d)
+    q, k, v = (torch.randn(300, h, d, generator=g).bfloat16().cuda() for h in (4, 2, 2))
+    cu = torch.tensor([0, 300], dtype=torch.int32).cuda()
+    o = torch.full((300, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.tensor([gdn.STATUS_CODE["GDN_ERR_PAGE_RANGE"]], dtype=torch.int32, device="cuda")
+    gdn.gdn_attn_prefill(sh, q=q, k=k, v=v, cu_seqlens=cu, cu_kv=cu, o=o, dev_error=err, wait_cycles=-1)
+    assert err.item() == TIMEOUT and bool((o == 7).all())
