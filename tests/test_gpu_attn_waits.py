@@ -94,3 +94,29 @@ def test_prefill_reports_a_run_out_over_an_earlier_code(d):
     err = torch.tensor([gdn.STATUS_CODE["GDN_ERR_PAGE_RANGE"]], dtype=torch.int32, device="cuda")
     gdn.gdn_attn_prefill(sh, q=q, k=k, v=v, cu_seqlens=cu, cu_kv=cu, o=o, dev_error=err, wait_cycles=-1)
     assert err.item() == TIMEOUT and bool((o == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prefill_waits_that_run_out_midway(d):
+    """Several row tiles a CTA, alone and in pairs; whatever wait gives up
+    first, the call returns and the context is intact."""
+    sh = AttnShape(6, 2, d, 16)
+    lens = [40 + 97 * s % 700 for s in range(30)]
+    T = sum(lens)
+    g = torch.Generator().manual_seed(d)
+    q, k, v = (torch.randn(T, h, d, generator=g).bfloat16().cuda() for h in (6, 2, 2))
+    cu = torch.tensor([0] + np.cumsum(lens).tolist(), dtype=torch.int32, device="cuda")
+
+    def call(wait):
+        o, err = torch.full_like(q, 7.0), err_word()
+        gdn.gdn_attn_prefill(sh, q=q, k=k, v=v, cu_seqlens=cu, cu_kv=cu, o=o, dev_error=err, max_q_len=max(lens),
+                             max_kv_len=max(lens), wait_cycles=wait)
+        return o, err.item()
+
+    want, err = call(0)
+    assert err == 0
+    for wait in (1, 1, 3000, 10000, 30000):
+        o, err = call(wait)
+        assert err in (0, TIMEOUT) and (err == TIMEOUT or torch.equal(o, want))
+    o, err = call(0)
+    assert err == 0 and torch.equal(o, want)
