@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
     for (int i = i0; ok && i < i1; ++i) {
       if (i == i0) t = dt_item<NT>(w, sh.items, i);
       else dt_next<NT>(w, sh.items, i, t);
-      if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail, limit));
+      if (dt_load_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail, limit));
       if (ok && t.tiles > 0) ok = qk(T);
       for (int j = 0; ok && j < t.tiles; ++j, ++T) {
         if (j + 1 < t.tiles) ok = qk(T + 1);
@@ -223,7 +223,8 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
     uint8_t* qd = base + w.q_off;
     uint8_t* pd = base + w.p_off;
     bool ok = true, okp = true;
-    // an item's rows as hi and lo codes, a warp a row at a time, all loads first
+    // an item's rows as hi and lo codes, a warp a row at a time, all loads first;
+    // where they belong is noted for an item without keys too
     auto load_q = [&](const DtItem& t, int par) {
       const int e0 = lane * 8;
       constexpr int NR = CW / 4;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
         x[r] = make_uint4(0, 0, 0, 0);
         if (n < t.rows) {
           const int row = (t.r0 + n) / p.G, g = t.r0 + n - row * p.G;
-          if (e0 < d)
+          if (t.tiles > 0 && e0 < d)
             x[r] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(t.q0 + row) * p.q_stride +
                                                    (int64_t)(t.h * p.G + g) * d + e0);
           if (lane == 0) {
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(DtCfg<NT>::THREADS, 2) attn_decode_tc_kernel(c
           }
         }
       }
+      if (t.tiles == 0) return;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const int n = r * 4 + quad;

@@ -106,8 +106,12 @@ struct DtItem {
   int q0, n, L, k0, k1, tiles;
 };
 
-// Whether item t, the CTA's item i, has other rows than the one before it.
+// Whether item t has other rows than the one before it.
 __device__ __forceinline__ bool dt_new_rows(const DtItem& t, bool first) { return first || t.rt > 1 || t.piece == 0; }
+// Whether its rows then enter a product.  (Those of an item without keys do not,
+// and no role waits for them: two such loads in a row would pass the product
+// warp's wait by, since only an item's scores tell that it has seen them.)
+__device__ __forceinline__ bool dt_load_rows(const DtItem& t, bool first) { return t.tiles > 0 && dt_new_rows(t, first); }
 
 // Groups (kv head, row tile) of a sequence; 0: no rows, -1: out of bounds.
 template <int NT>

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
     DtItem t{};
     if (i0 < i1) {
       t = dt_item<NT>(w, sh.items, i0);
-      load_q(t, 0);
+      if (dt_load_rows(t, true)) load_q(t, 0);
     }
     for (int i = i0; i < i1; ++i) {
       float l = 0.f, ref = -INFINITY;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       const unsigned last = T - 1;   // the item's last tile
       if (i + 1 < i1) {
         dt_next<NT>(w, sh.items, i + 1, t);
-        if (dt_new_rows(t, false)) {
+        if (dt_load_rows(t, false)) {
           // (the last scores, if the other warpgroup's, have to be done with the rows)
           if (u.tiles > 0) ok = dt_wait(&sh.s_full[last & 1], (last >> 1) & 1, fail, limit);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kDrThreads, 1) attn_draft_tc_kernel(const DtPa
       for (int i = i0; ok && i < i1; ++i) {
         if (i == i0) t = dt_item<NT>(w, sh.items, i);
         else dt_next<NT>(w, sh.items, i, t);
-        if (dt_new_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail, limit));
+        if (dt_load_rows(t, i == i0)) ok = all(dt_wait(&sh.q_full, rows++ & 1, fail, limit));
         if (ok && t.tiles > 0) ok = qk(T);
         for (int j = 0; ok && j < t.tiles; ++j, ++T) {
           if (j + 1 < t.tiles) ok = qk(T + 1);
