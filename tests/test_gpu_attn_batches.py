@@ -1,5 +1,6 @@
-"""Decode attention over large batches: sequences without keys between others.
-A sequence gives the bits that it gives alone."""
+"""Decode attention over large batches: sequences without keys or without rows
+between others, more sequences than one launch takes, few rows and drafts in
+one call.  A sequence gives the bits that it gives alone."""
 import numpy as np
 import pytest
 import torch
@@ -68,3 +69,16 @@ def test_many_sequences_without_keys(rows):
 @pytest.mark.parametrize("rows", [1, 16])
 def test_no_sequence_has_keys(rows):
     Batch(AttnShape(48, 8, 64, 64), [rows] * 400, [0] * 399 + [1], seed=rows).check(every=399)
+
+
+@pytest.mark.parametrize("N", [257, 600])
+def test_more_sequences_than_a_launch_takes(N):
+    """0, 1 and 32 rows mixed: both kernels, each launched more than once."""
+    news = [(0, 1, 32, 2, 1)[s * 7 % 5] for s in range(N)]
+    lens = [(0, 700, 33, 1500, 128, 1)[s * 5 % 6] + s % 3 for s in range(N)]
+    Batch(AttnShape(12, 2, 64, 64), news, lens, seed=N).check(every=29)
+
+
+@pytest.mark.parametrize("G", [1, 16, 24])
+def test_more_sequences_than_a_launch_takes_one_row_each(G):
+    Batch(AttnShape(G, 1, 64, 64), [1] * 520, [s * 17 % 900 for s in range(520)], seed=G).check(every=37)
