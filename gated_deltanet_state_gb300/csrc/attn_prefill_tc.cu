@@ -849,7 +849,9 @@ __global__ void __launch_bounds__(PreCfg<D, PAIR>::THREADS, 1)
             const long long t0 = clock64();
             while (*(volatile int*)&sh.out_done < k * C::SW * C::CTAS && !*fail)
               if (clock64() - t0 > limit) *fail = 1;
-            __threadfence_block();
+            // (the other CTA's clearing, before notes go there)
+            if (PAIR) asm volatile("fence.acq_rel.cluster;\n" ::: "memory");
+            else __threadfence_block();
             for (int x = x0; x < x0 + 8 * GT; x += GT) {
               const int row = x >> 3 & (kTile - 1), col = u * C::UD + rank * C::VCOLS + (x >> 10) * 64 + (((x & 7) ^ (row & 7)) << 3);
               for (int i = 0; i < 8; ++i) {
