@@ -138,6 +138,13 @@ def _on(stream, t: torch.Tensor) -> int:
     return _stream(stream)
 
 
+def _stream_object(stream, device):
+    """The stream of a call for torch's own calls (None: the current one)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
 def _rows(t: torch.Tensor, heads: int, shape: AttnShape, name: str):
     """(pointer, elements between rows) of [T, heads, d] rows that may be slices of wider ones."""
     if not t.is_cuda:
@@ -179,7 +186,9 @@ def gdn_kv_tables(shape: AttnShape, num_pages: int, *, kv_len, new_len, free_pag
                   raise_on_error: bool = True) -> int:
     """Block tables, slot map and positions of a step from request lengths
     (gdn.h: gdn_kv_tables).  slot_map and positions may have more rows than
-    the step has tokens: the rest get slot -1."""
+    the step has tokens: the rest get slot -1.  A step without requests gives
+    sums of 0, no pages taken and only such rows (the C entry launches nothing
+    for it and leaves the outputs alone)."""
     n, T = int(kv_len.numel()), int(slot_map.numel())
     bt, cols = _table(block_table, n)
     a = _KvTablesArgs(n, cols, int(free_pages.numel()), int(num_pages), T, _dev(kv_len, torch.int32, "kv_len"),
@@ -188,6 +197,11 @@ def gdn_kv_tables(shape: AttnShape, num_pages: int, *, kv_len, new_len, free_pag
                       _ints(kv_len_out, n, "kv_len_out"), _ints(positions, T, "positions", torch.int64),
                       _dev(slot_map, torch.int64, "slot_map"), _ints(pages_taken, 1, "pages_taken"),
                       _ints(dev_error, 1, "dev_error"))
+    if n == 0:
+        with torch.cuda.stream(_stream_object(stream, slot_map.device)):
+            for t in (cu_seqlens, cu_kv, pages_taken, positions):
+                t.zero_()
+            slot_map.fill_(-1)
     st = load_library().gdn_kv_tables(make_attn_desc(shape), a, _on(stream, kv_len))
     return _check(st, "gdn_kv_tables") if raise_on_error else st
 

@@ -631,7 +631,9 @@ int64_t gdn_kv_page_bytes(const gdn_attn_desc* desc);
  * and kv_len_out[s] = kv_len[s] (a negative one: 0).  So is, with slot -1, a
  * token whose page id is not in [0, num_pages).  No list is changed: the
  * caller drops the first *pages_taken entries of free_pages, and the same
- * call gives the same answer again.  The lengths' sums must fit in int32. */
+ * call gives the same answer again.  The lengths' sums must fit in int32.
+ * With num_seqs = 0 nothing is launched and nothing written: no page is taken,
+ * whatever *pages_taken holds. */
 typedef struct gdn_kv_tables_args {
   int32_t num_seqs;              /* N >= 0                                    */
   int32_t max_pages;             /* row stride of block_table                 */
