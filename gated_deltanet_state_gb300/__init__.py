@@ -201,6 +201,13 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _stream_object(stream, device):
+    """The stream of a call for torch's own calls (None: the current one)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
 def _dev(t: Optional[torch.Tensor], dtype=None, name: str = "") -> Optional[int]:
     """Device pointer of a contiguous CUDA tensor (None -> NULL)."""
     if t is None:
@@ -340,9 +347,14 @@ def gdn_replay_workspace_size(shape: LayerShape, num_reqs: int) -> int:
     return int(load_library().gdn_replay_workspace_size(ctypes.byref(make_desc(shape)), num_reqs))
 
 
-def workspace_for(nbytes: int, device="cuda") -> torch.Tensor:
-    """A device scratch buffer of at least nbytes (PyTorch owns the memory)."""
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+def workspace_for(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
+    """A device scratch buffer of at least nbytes (PyTorch owns the memory).
+    `stream`: the one that a call will use it on, if not the current one, so
+    that the memory is not given to others before that call is done."""
+    t = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if stream is not None and _stream(stream) != torch.cuda.current_stream(t.device).cuda_stream:
+        t.record_stream(_stream_object(stream, t.device))
+    return t
 
 
 # --------------------------------------------------------------------------- device entry points
@@ -380,7 +392,7 @@ def gdn_prefill_chunked(shape: LayerShape, pool: StatePool, *, cu_seqlens, start
     lib = load_library()
     n = int(cu_seqlens.numel()) - 1
     if workspace is None:
-        workspace = workspace_for(gdn_prefill_workspace_size(shape, n, int(x.shape[0])), x.device)
+        workspace = workspace_for(gdn_prefill_workspace_size(shape, n, int(x.shape[0])), x.device, stream)
     a, keep = _prefill_args(shape, cu_seqlens=cu_seqlens, start_pos=start_pos, init_page=init_page,
                             block_table=block_table, out_slot=out_slot, x=x, g=g, beta=beta, conv_w=conv_w,
                             o=o, dev_error=dev_error, start_pos_host=start_pos_host,
@@ -434,7 +446,7 @@ def gdn_core_prefill(shape: LayerShape, pool: StatePool, *, cu_seqlens, start_po
     n = int(cu_seqlens.numel()) - 1
     T = int(qkvz.shape[0])
     if workspace is None:
-        workspace = workspace_for(gdn_core_prefill_workspace_size(shape, n, T), qkvz.device)
+        workspace = workspace_for(gdn_core_prefill_workspace_size(shape, n, T), qkvz.device, stream)
     sph, keep1 = _host(start_pos_host, torch.int64, "start_pos_host")
     iph, keep2 = _host(init_page_host, torch.int32, "init_page_host")
     bt = block_table
@@ -482,7 +494,7 @@ def gdn_mixed_step(shape: LayerShape, pool: StatePool, *, cu_seqlens, is_decode,
     n = int(cu_seqlens.numel()) - 1
     T = int(x.shape[0])
     if workspace is None:
-        workspace = workspace_for(gdn_mixed_workspace_size(shape, n, T), x.device)
+        workspace = workspace_for(gdn_mixed_workspace_size(shape, n, T), x.device, stream)
     cuh, k1 = _host(cu_seqlens, torch.int32, "cu_seqlens_host")
     dh, k2 = _host(is_decode, torch.int8, "is_decode_host")
     sph, k3 = _host(start_pos_host, torch.int64, "start_pos_host")
@@ -541,9 +553,9 @@ def gdn_checkpoint_save(shape: LayerShape, pool: StatePool, src_page, dst_page, 
 
 def _replay_args(shape, *, ckpt_slot, log_x, log_g, log_beta, log_len, conv_w, dev_error,
                  x_new=None, g_new=None, beta_new=None, o=None, num_new=0, workspace=None,
-                 boundary_rows=None, boundary_page=None):
+                 boundary_rows=None, boundary_page=None, stream=None):
     if workspace is None:
-        workspace = workspace_for(gdn_replay_workspace_size(shape, int(ckpt_slot.numel())), log_x.device)
+        workspace = workspace_for(gdn_replay_workspace_size(shape, int(ckpt_slot.numel())), log_x.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     return workspace, _ReplayArgs(int(ckpt_slot.numel()), int(num_new), _dev(ckpt_slot, torch.int32, "ckpt_slot"),
                        _dev(log_x, shape.torch_in(), "log_x"), _dev(log_g, torch.float32, "log_g"),
@@ -563,7 +575,7 @@ def gdn_replay_append(shape: LayerShape, pool: StatePool, *, ckpt_slot, log_x, l
     lib = load_library()
     keep, a = _replay_args(shape, ckpt_slot=ckpt_slot, log_x=log_x, log_g=log_g, log_beta=log_beta,
                            log_len=log_len, conv_w=conv_w, dev_error=dev_error, x_new=x_new, g_new=g_new,
-                           beta_new=beta_new, o=o, num_new=int(x_new.shape[1]), workspace=workspace)
+                           beta_new=beta_new, o=o, num_new=int(x_new.shape[1]), workspace=workspace, stream=stream)
     st = lib.gdn_replay_append(ctypes.byref(make_desc(shape)), ctypes.byref(pool.abi()), ctypes.byref(a),
                                _stream(stream))
     return _check(st, "gdn_replay_append") if raise_on_error else st
@@ -588,7 +600,7 @@ def gdn_replay_flush(shape: LayerShape, pool: StatePool, *, ckpt_slot, log_x, lo
     lib = load_library()
     keep, a = _replay_args(shape, ckpt_slot=ckpt_slot, log_x=log_x, log_g=log_g, log_beta=log_beta,
                            log_len=log_len, conv_w=conv_w, dev_error=dev_error, workspace=workspace,
-                           boundary_rows=boundary_rows, boundary_page=boundary_page)
+                           boundary_rows=boundary_rows, boundary_page=boundary_page, stream=stream)
     st = lib.gdn_replay_flush(ctypes.byref(make_desc(shape)), ctypes.byref(pool.abi()), ctypes.byref(a),
                               _stream(stream))
     return _check(st, "gdn_replay_flush") if raise_on_error else st

@@ -9,7 +9,7 @@ from typing import Optional
 
 import torch
 
-from . import _check, _dev, _P, _Pool, _stream, load_library
+from . import _check, _dev, _P, _Pool, _stream, _stream_object, load_library, workspace_for
 from .inputs import AttnShape
 
 ATTN_DECODE_ROWS = 32    # GDN_ATTN_DECODE_ROWS
@@ -138,13 +138,6 @@ def _on(stream, t: torch.Tensor) -> int:
     return _stream(stream)
 
 
-def _stream_object(stream, device):
-    """The stream of a call for torch's own calls (None: the current one)."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
 def _rows(t: torch.Tensor, heads: int, shape: AttnShape, name: str):
     """(pointer, elements between rows) of [T, heads, d] rows that may be slices of wider ones."""
     if not t.is_cuda:
@@ -255,7 +248,7 @@ def gdn_attn_decode(shape: AttnShape, pool: KVPool, *, q, cu_seqlens, kv_len, bl
     desc = make_attn_desc(shape)
     if workspace is None:
         size = lib.gdn_attn_decode_workspace_size(desc, n, T, max_kv_len)
-        workspace = torch.empty(max(int(size), 256), dtype=torch.uint8, device=q.device)
+        workspace = workspace_for(size, q.device, stream)
     a = _AttnDecodeArgs(n, cols, int(max_q_len), int(max_kv_len), T, qs, _ints(cu_seqlens, n + 1, "cu_seqlens"),
                         _dev(kv_len, torch.int32, "kv_len"), bt, qp,
                         _out(o, (T, shape.num_q_heads, shape.head_dim), shape.torch_dtype(), "o"),

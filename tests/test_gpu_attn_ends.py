@@ -7,7 +7,7 @@ import torch
 import gated_deltanet_state_gb300 as gdn
 from gated_deltanet_state_gb300.inputs import AttnShape
 
-from attn_harness import err_word
+from attn_harness import err_word, fill_cache, table_for
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +27,37 @@ def test_tables_of_a_step_without_requests(stream):
     torch.cuda.synchronize()
     assert cu.tolist() == [0] and cu_kv.tolist() == [0] and taken.tolist() == [0] and err.item() == 0
     assert pos.tolist() == [0] * 5 and slot.tolist() == [-1] * 5 and free.tolist() == [77] * 9
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_scratch_of_a_call_on_another_stream_is_its_own(handle):
+    """A call on a stream that is still busy takes its scratch from the
+    allocator; what the current stream allocates and writes meanwhile is other
+    memory."""
+    sh, L = AttnShape(24, 4, 128, 64), 9000
+    pages = -(-L // 64)
+    pool = gdn.KVPool(sh, pages, fill=0xFF)
+    table = table_for([L], 64, pages, 1)
+    fill_cache(pool, table, [L], 1)
+    q = torch.randn(1, 24, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    cu, kv, bt = (torch.tensor(x, dtype=torch.int32).cuda() for x in ([0, 1], [L], table.tolist()))
+    err = err_word()
+    size = gdn.gdn_attn_decode_workspace_size(sh, 1, 1, L)
+
+    def call(stream):
+        o = torch.zeros_like(q)
+        gdn.gdn_attn_decode(sh, pool, q=q, cu_seqlens=cu, kv_len=kv, block_table=bt, o=o, max_kv_len=L, dev_error=err,
+                            stream=stream)
+        return o
+
+    want = call(None)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)          # about 10 ms
+    o = call(st.cuda_stream if handle else st)
+    done = st.record_event()
+    while not done.query():
+        torch.full((size,), 0x7F, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and err.item() == 0
