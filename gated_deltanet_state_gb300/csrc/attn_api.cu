@@ -9,6 +9,9 @@ using namespace gdn;
 namespace {
 
 constexpr int32_t kMaxSeqs = 65535;   // grid y / z limit used for sequences
+// Keys of a sequence: the kernels count in tiles of up to 512 keys in 32 bits,
+// past the last key by less than two of them.
+constexpr int32_t kMaxKeys = 0x7fffffff - 1023;
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 gdn_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
@@ -156,7 +159,7 @@ gdn_status gdn_attn_decode(const gdn_attn_desc* desc, const gdn_pool* pool, cons
   p.Hq = desc->num_q_heads;
   p.G = desc->num_q_heads / desc->num_kv_heads;
   p.max_q = a->max_q_len;
-  p.max_kv = a->max_kv_len;
+  p.max_kv = a->max_kv_len < kMaxKeys ? a->max_kv_len : kMaxKeys;
   p.max_pieces = pieces;
   p.T = a->total_tokens;
   p.q_stride = a->q_stride;
@@ -196,6 +199,7 @@ gdn_status gdn_attn_prefill(const gdn_attn_desc* desc, const gdn_attn_prefill_ar
   p.d = desc->head_dim;
   p.max_q = a->max_q_len > 0 ? a->max_q_len : (int32_t)a->total_q;
   p.max_kv = a->max_kv_len > 0 ? a->max_kv_len : (int32_t)a->total_kv;
+  if (p.max_kv > kMaxKeys) p.max_kv = kMaxKeys;
   p.Tq = a->total_q;
   p.Tk = a->total_kv;
   p.q_stride = a->q_stride;

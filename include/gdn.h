@@ -718,7 +718,8 @@ typedef struct gdn_attn_decode_args {
   int32_t num_seqs;              /* N >= 0                                    */
   int32_t max_pages;             /* row stride of block_table                 */
   int32_t max_q_len;             /* host bound on new rows a sequence, 1..32  */
-  int32_t max_kv_len;            /* host bound on kv_len                      */
+  int32_t max_kv_len;            /* host bound on kv_len (one above 2^31 -
+                                    1,024 counts as that)                     */
   int64_t total_tokens;          /* T = cu_seqlens[N]                         */
   int64_t q_stride;              /* elements between rows of q, >= Hq*d       */
   const int32_t* cu_seqlens;     /* [N+1] rows of q                           */
@@ -750,8 +751,8 @@ gdn_status gdn_attn_decode(const gdn_attn_desc* desc, const gdn_pool* pool, cons
  * (a whole prompt: both alike; a chunk after a prefix: more keys than rows).
  * The desc's page_tokens is not used.  Rows of q, k, v are q_stride,
  * k_stride, v_stride elements apart.  max_q_len and max_kv_len bound a
- * sequence's rows and keys (0: total_q / total_kv); a longer one sets
- * GDN_ERR_INVALID_ARG and is skipped.  A row's bits depend on its own keys
+ * sequence's rows and keys (0: total_q / total_kv; more than 2^31 - 1,024 keys
+ * counts as that); a longer one sets GDN_ERR_INVALID_ARG and is skipped.  A row's bits depend on its own keys
  * only: not on the batch, nor on how a prompt was cut into chunks. */
 typedef struct gdn_attn_prefill_args {
   int32_t num_seqs;              /* N >= 0                                    */

@@ -5,11 +5,13 @@ import pytest
 import torch
 
 import gated_deltanet_state_gb300 as gdn
-from gated_deltanet_state_gb300.inputs import AttnShape
+from gated_deltanet_state_gb300.inputs import BF16, F32, AttnShape
 
 from attn_harness import err_word, fill_cache, table_for
 
 pytestmark = pytest.mark.gpu
+
+INVALID = gdn.STATUS_CODE["GDN_ERR_INVALID_ARG"]
 
 
 @pytest.mark.parametrize("stream", ["current", "other", "handle"])
@@ -61,3 +63,26 @@ def test_scratch_of_a_call_on_another_stream_is_its_own(handle):
         torch.full((size,), 0x7F, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(o, want) and err.item() == 0
+
+
+@pytest.mark.parametrize("rows,dtype", [(1, BF16), (16, BF16), (1, F32)])
+def test_decode_refuses_lengths_that_its_counts_do_not_hold(rows, dtype):
+    """Contexts within a few tiles of 2^31 tokens; the others of the batch are as always."""
+    sh = AttnShape(6, 1, 64, 64, dtype=dtype)
+    pool = gdn.KVPool(sh, 3, fill=0xFF)
+    table = torch.tensor([[0], [1], [2]], dtype=torch.int32)
+    fill_cache(pool, table, [64, 64, 64], 2)
+    q = torch.randn(3 * rows, 6, 64, generator=torch.Generator().manual_seed(2)).to(sh.torch_dtype()).cuda()
+    cu = torch.arange(0, 3 * rows + 1, rows, dtype=torch.int32).cuda()
+
+    def call(lens):
+        o, err = torch.full_like(q, 7.0), err_word()
+        gdn.gdn_attn_decode(sh, pool, q=q, cu_seqlens=cu, kv_len=torch.tensor(lens, dtype=torch.int32).cuda(),
+                            block_table=table.cuda(), o=o, max_q_len=rows, max_kv_len=0x7fffffff, dev_error=err)
+        return o.unflatten(0, (3, rows)), err.item()
+
+    want, err = call([64, 64, 64])
+    assert err == 0
+    for far in (0x7fffffff, 0x7fffffff - 1022):
+        o, err = call([64, far, 64])
+        assert err == INVALID and bool((o[1] == 7).all()) and torch.equal(o[0], want[0]) and torch.equal(o[2], want[2])
