@@ -52,7 +52,7 @@ struct DtBase {
   float ks[kDtMaxStages + 2][kDtBlocks], vs[kDtMaxStages + 2][kDtBlocks];
   int bad[2][256];          // (items alternate) first token with a NaN value that not every row sees, by element
   int items[kDtSeqs + 1];   // running sums of the sequences' work items ...
-  int work[kDtSeqs + 1];    // ... and of their weights
+  long long work[kDtSeqs + 1];   // ... and of their weights (tiles of every head: past 32 bits for long shared contexts)
   uint32_t tmem;
   int fail;
 };
@@ -129,7 +129,8 @@ __device__ __forceinline__ int dt_piece_work(const AttnDecodeParams& p, int s) {
 }
 
 // The last s with sums[s] <= i.
-__device__ __forceinline__ int dt_find(const int* sums, int n, int i) {
+template <typename I>
+__device__ __forceinline__ int dt_find(const I* sums, int n, I i) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -141,12 +142,12 @@ __device__ __forceinline__ int dt_find(const int* sums, int n, int i) {
 
 // First item of CTA b: the work before it is b / CTAs of all.
 template <int NT>
-__device__ __forceinline__ int dt_first(const DtParams& w, const int* items, const int* work, int b, int ctas) {
-  const int at = (int)((int64_t)work[w.ns] * b / ctas);
+__device__ __forceinline__ int dt_first(const DtParams& w, const int* items, const long long* work, int b, int ctas) {
+  const long long at = work[w.ns] * b / ctas;
   if (at >= work[w.ns]) return items[w.ns];
   const int s = dt_find(work, w.ns, at);
   const int per = dt_piece_work(w.a, w.s0 + s);   // of each of its items
-  return min(items[s + 1], items[s] + (at - work[s] + per - 1) / per);
+  return min(items[s + 1], items[s] + (int)((at - work[s] + per - 1) / per));
 }
 
 template <int NT>
@@ -264,10 +265,12 @@ __device__ __forceinline__ float split_row(const uint4& x, uint2& hi, uint2& lo)
 template <int NT>
 __device__ __forceinline__ void dt_sums(const DtParams& w, DtBase& sh, int lane) {
   const AttnDecodeParams& p = w.a;
-  int sum = 0, sumw = 0;
+  int sum = 0;
+  long long sumw = 0;
   if (lane == 0) sh.items[0] = sh.work[0] = 0;
   for (int c = 0; c < w.ns; c += 32) {
-    int v = 0, x = 0;
+    int v = 0;
+    long long x = 0;
     if (c + lane < w.ns) {
       const int s = w.s0 + c + lane;
       int g = dt_groups<NT>(w, s);
@@ -278,12 +281,13 @@ __device__ __forceinline__ void dt_sums(const DtParams& w, DtBase& sh, int lane)
       if (g > 0) {
         const int pieces = decode_pieces(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G);
         v = g * pieces;
-        x = g * pieces * dt_piece_work(p, s);
+        x = (long long)v * dt_piece_work(p, s);
       }
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, v, o), b = __shfl_up_sync(0xffffffffu, x, o);
+      const int a = __shfl_up_sync(0xffffffffu, v, o);
+      const long long b = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) v += a, x += b;
     }
     if (c + lane < w.ns) sh.items[c + lane + 1] = sum + v, sh.work[c + lane + 1] = sumw + x;

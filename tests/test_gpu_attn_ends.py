@@ -11,7 +11,7 @@ from attn_harness import err_word, fill_cache, table_for
 
 pytestmark = pytest.mark.gpu
 
-INVALID = gdn.STATUS_CODE["GDN_ERR_INVALID_ARG"]
+INVALID, TIMEOUT = (gdn.STATUS_CODE[c] for c in ("GDN_ERR_INVALID_ARG", "GDN_ERR_TIMEOUT"))
 
 
 @pytest.mark.parametrize("stream", ["current", "other", "handle"])
@@ -86,3 +86,20 @@ def test_decode_refuses_lengths_that_its_counts_do_not_hold(rows, dtype):
     for far in (0x7fffffff, 0x7fffffff - 1022):
         o, err = call([64, far, 64])
         assert err == INVALID and bool((o[1] == 7).all()) and torch.equal(o[0], want[0]) and torch.equal(o[2], want[2])
+
+
+def test_decode_shares_out_more_than_2_31_tiles():
+    """256 requests of 64 kv heads over 20 million tokens: every row's pieces
+    belong to some CTA.  With every wait run out nothing is computed, each CTA
+    only marks the rows of its pieces, and no row is joined."""
+    sh = AttnShape(64, 64, 32, 64)
+    N, L = 256, 20_000_000
+    pool = gdn.KVPool(sh, 1, fill=0)
+    q = torch.zeros(N, 64, 32, dtype=torch.bfloat16, device="cuda")
+    o, lse, err = torch.full_like(q, 7.0), torch.full((N, 64), 7.0, device="cuda"), err_word()
+    ws = gdn.workspace_for(gdn.gdn_attn_decode_workspace_size(sh, N, N, L)).zero_()
+    gdn.gdn_attn_decode(sh, pool, q=q, cu_seqlens=torch.arange(N + 1, dtype=torch.int32).cuda(),
+                        kv_len=torch.full((N,), L, dtype=torch.int32).cuda(),
+                        block_table=torch.full((N, 1), -1, dtype=torch.int32).cuda(), o=o, lse=lse, max_kv_len=L, workspace=ws,
+                        wait_cycles=-1, dev_error=err)
+    assert err.item() == TIMEOUT and bool((o == 7).all()) and bool((lse == 7).all())
