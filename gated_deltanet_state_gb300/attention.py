@@ -263,7 +263,9 @@ def gdn_attn_prefill(shape: AttnShape, *, q, k, v, cu_seqlens, cu_kv, o, dev_err
                      max_kv_len: int = 0, wait_cycles: int = 0, stream=None, raise_on_error: bool = True) -> int:
     """Causal attention of packed rows q [Tq, Hq, d] over k, v [Tk, Hkv, d]
     (slices of wider rows are fine; gdn.h: gdn_attn_prefill).  max_q_len and
-    max_kv_len (the longest sequence; 0: the call's totals) size the launch."""
+    max_kv_len (the longest sequence; 0: the call's totals) bound a sequence;
+    with the longest one's rows the launch starts the tiles with the most keys
+    first."""
     n = int(cu_seqlens.numel()) - 1
     qp, qs = _rows(q, shape.num_q_heads, shape, "q")
     kp, ks = _rows(k, shape.num_kv_heads, shape, "k")

@@ -90,7 +90,25 @@ struct AttnPrefillParams {
   float* lse;
   int32_t* err;
   int64_t wait_cycles;
+  int32_t flat;       // the order of the row tiles (prefill_grid)
 };
+
+// Row tiles of a prefill, `rows` rows each, as blocks (times kv heads).  Where
+// max_q is about the longest sequence: every sequence's last tile, then the ones
+// before, and so on, as many as the longest may have, so that those with the
+// most keys start first.  Where that is `times` the tiles that total_q rows can
+// make or more (max_q left at total_q; one long prompt among many short ones),
+// sequence s has the places from cu_q[s] G / rows + s on, which are as many as
+// its tiles or one more.  A place without a tile costs the tensor-core kernel, a
+// CTA an SM, more than the search for a place, the fp32 one less (24 prompts of
+// 500 tokens, 24 heads, 4 kv heads, d = 256, bound of 500: 152 us even, 147 flat;
+// of 4,000: 210, 147; of all: 360, 147.  4 heads, 2, d = 32, fp32: 107, 122; 119,
+// 123; 156, 123.  One of 4,000 and 60 of 50: 366, 179; 276, 232), hence 2 and 8.
+inline int64_t prefill_grid(AttnPrefillParams& p, int rows, int times) {
+  const int64_t even = ((int64_t)p.max_q * p.G + rows - 1) / rows * p.N, flat = p.Tq * p.G / rows + p.N;
+  p.flat = even >= times * flat;
+  return (p.flat ? flat : even) * p.Hkv;
+}
 
 // Keys of a decode sequence are cut into even pieces by its own length and
 // number of (row, head of the group) pairs alone, so a row's sums are formed in
@@ -168,6 +186,30 @@ __device__ __forceinline__ void e4m3_f32x16(const uint4& v, float (&f)[16]) {
     const float2 a = e4m3_f32x2(w[i]), b = e4m3_f32x2(w[i] >> 16);
     f[4 * i] = a.x, f[4 * i + 1] = a.y, f[4 * i + 2] = b.x, f[4 * i + 3] = b.y;
   }
+}
+
+// ---- a prefill's row tiles ---------------------------------------------------------
+// Block -> sequence, kv head, and which of the sequence's tiles, counted from its last.
+__device__ __forceinline__ void prefill_place(const AttnPrefillParams& p, int rows, int block, int& s, int& h, int& back) {
+  if (!p.flat) {
+    const int groups = p.N * p.Hkv;
+    back = block / groups;
+    const int pr = block - back * groups;
+    s = pr / p.Hkv;
+    h = pr - s * p.Hkv;
+    return;
+  }
+  const int i = block / p.Hkv;
+  h = block - i * p.Hkv;
+  auto first = [&](int k) { return (int64_t)p.cu_q[k] * p.G / rows + k; };
+  int lo = 0, hi = p.N;   // the last s with first(s) <= i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first(mid) <= i) lo = mid;
+    else hi = mid;
+  }
+  s = lo;
+  back = (int)(i - first(lo));
 }
 
 // ---- cache addressing ------------------------------------------------------------

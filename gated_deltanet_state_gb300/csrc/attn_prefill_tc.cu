@@ -270,11 +270,8 @@ __device__ __forceinline__ int next_block(const uint4* answer) {
 template <class C>
 __device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t, int block, int rank, bool report) {
   constexpr int ROWS = C::CTAS * kTile;
-  const int groups = p.N * p.Hkv;
-  block /= C::CTAS;
-  const int back = block / groups, pr = block - back * groups;
-  t.s = pr / p.Hkv;
-  t.h = pr - t.s * p.Hkv;
+  int back;
+  prefill_place(p, ROWS, block / C::CTAS, t.s, t.h, back);
   t.q0 = p.cu_q[t.s];
   t.n = p.cu_q[t.s + 1] - t.q0;
   t.k0 = p.cu_kv[t.s];
@@ -287,7 +284,7 @@ __device__ __forceinline__ bool pre_tile(const AttnPrefillParams& p, PreTile& t,
   }
   const int64_t rows = (int64_t)t.n * p.G;
   const int tiles = (int)((rows + ROWS - 1) / ROWS);
-  if (back >= tiles) return false;
+  if (back < 0 || back >= tiles) return false;
   const int64_t first = (int64_t)(tiles - 1 - back) * ROWS;   // the last rows, which see the most keys, first
   t.r0 = first + rank * kTile;
   // the key tiles of the last row (a pair's two have the same: its products are one)
@@ -959,7 +956,7 @@ cudaError_t rows_map(CUtensorMap* map, const void* base, int d, int heads, int64
 }
 
 template <int D, bool PAIR>
-cudaError_t prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
+cudaError_t prefill_tc(AttnPrefillParams p, cudaStream_t st) {
   using C = PreCfg<D, PAIR>;
   CUtensorMap kmap, vmap;
   cudaError_t e = rows_map(&kmap, p.k, D, p.Hkv, p.Tk, p.k_stride, C::KROWS);
@@ -968,7 +965,7 @@ cudaError_t prefill_tc(const AttnPrefillParams& p, cudaStream_t st) {
     e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem<D, PAIR>);
   if (e != cudaSuccess) return e;
   constexpr int ROWS = C::CTAS * kTile;
-  const int64_t grid = ((int64_t)p.max_q * p.G + ROWS - 1) / ROWS * p.N * p.Hkv * C::CTAS;
+  const int64_t grid = prefill_grid(p, ROWS, 2) * C::CTAS;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);

@@ -321,9 +321,8 @@ __global__ void __launch_bounds__(4 * kPreRows<D> * kPreGroups<D>, D <= 32 ? 2 :
   constexpr int NL = kPreKeys * D / 4 / THREADS;              // 4-element loads a thread for a tile of K (or V)
   constexpr bool AHEAD = D <= 64;
   const int d = p.d, ld = d + 4;
-  // every sequence's last tile first, then the ones before: they see the most keys
-  const int pairs = p.N * p.Hkv, back = (int)(blockIdx.x / pairs), pr = (int)(blockIdx.x - (unsigned)back * pairs);
-  const int s = pr / p.Hkv, h = pr - s * p.Hkv;
+  int s, h, back;
+  prefill_place(p, ROWS, (int)blockIdx.x, s, h, back);
   const int q0 = p.cu_q[s], n = p.cu_q[s + 1] - q0, k0 = p.cu_kv[s], L = p.cu_kv[s + 1] - k0;
   if (n <= 0) return;
   if (n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || k0 < 0 || (int64_t)q0 + n > p.Tq || (int64_t)k0 + L > p.Tk) {
@@ -332,7 +331,7 @@ __global__ void __launch_bounds__(4 * kPreRows<D> * kPreGroups<D>, D <= 32 ? 2 :
   }
   const int tiles = (int)(((int64_t)n * p.G + ROWS - 1) / ROWS);
   const int tile = tiles - 1 - back;
-  if (tile < 0) return;
+  if (tile < 0 || back < 0) return;
   const int64_t r0 = (int64_t)tile * ROWS;
   float* sq = smem;                       // [ROWS][ld]
   const int group = threadIdx.x / THREADS, tid = threadIdx.x % THREADS;
@@ -531,8 +530,8 @@ __global__ void __launch_bounds__(4 * kPreRows<D> * kPreGroups<D>, D <= 32 ? 2 :
 namespace {
 
 template <typename T, int D>
-cudaError_t prefill_simt(const AttnPrefillParams& p, cudaStream_t st) {
-  const int64_t grid = ((int64_t)p.max_q * p.G + kPreRows<D> - 1) / kPreRows<D> * p.N * p.Hkv;
+cudaError_t prefill_simt(AttnPrefillParams p, cudaStream_t st) {
+  const int64_t grid = prefill_grid(p, kPreRows<D>, 8);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   const size_t sm =   // 217,088 B at d = 256
       (size_t)(kPreRows<D> * (p.d + 4) + kPreGroups<D> * (2 * kPreKeys * (p.d + 4) + kPreRows<D> * kPreLdP)) * 4;

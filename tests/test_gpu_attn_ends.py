@@ -103,3 +103,45 @@ def test_decode_shares_out_more_than_2_31_tiles():
                         block_table=torch.full((N, 1), -1, dtype=torch.int32).cuda(), o=o, lse=lse, max_kv_len=L, workspace=ws,
                         wait_cycles=-1, dev_error=err)
     assert err.item() == TIMEOUT and bool((o == 7).all()) and bool((lse == 7).all())
+
+
+def prefill(sh, q, k, v, lens, **kw):
+    cu = torch.tensor([0] + lens, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    o, err = torch.full_like(q, 7.0), err_word()
+    gdn.gdn_attn_prefill(sh, q=q, k=k, v=v, cu_seqlens=cu, cu_kv=cu, o=o, dev_error=err, **kw)
+    return o, err.item()
+
+
+def test_prefill_of_65535_prompts_without_a_bound():
+    """One token each: every output is its own value row."""
+    N, H, G, d = 65535, 4, 8, 16
+    sh = AttnShape(H * G, H, d, 16, dtype=F32)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn(N, h, d, generator=g, device="cuda") for h in (H * G, H, H))
+    o, err = prefill(sh, q, k, v, [1] * N)
+    assert err == 0 and torch.equal(o, v.repeat_interleave(G, 1))
+
+
+@pytest.mark.parametrize("H,G,d,dtype", [(2, 6, 256, BF16), (4, 4, 128, BF16), (1, 3, 64, BF16), (2, 2, 96, BF16), (2, 2, 32, F32),
+                                         (1, 40, 64, BF16)])
+@pytest.mark.parametrize("lens", [[37 * s % 201 for s in range(60)], [1] * 40 + [1500] + [0, 1] * 30, [3000], [1] * 300])
+def test_prefill_gives_the_same_bits_whatever_bound_it_has(lens, H, G, d, dtype):
+    """The longest prompt as the bound, the call's rows (0) and more than those."""
+    sh = AttnShape(H * G, H, d, 16, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    T = sum(lens)
+    q, k, v = (torch.randn(T, h, d, generator=g, device="cuda").to(sh.torch_dtype()) for h in (H * G, H, H))
+    want, err = prefill(sh, q, k, v, lens, max_q_len=max(lens), max_kv_len=max(lens))
+    assert err == 0
+    for s in (0, len(lens) // 2, len(lens) - 1):           # alone
+        a, n = sum(lens[:s]), lens[s]
+        if n:
+            r = slice(a, a + n)
+            o, err = prefill(sh, q[r], k[r], v[r], [n], max_q_len=n)
+            assert err == 0 and torch.equal(o, want[r])
+    for bound in (0, 50 * T):
+        o, err = prefill(sh, q, k, v, lens, max_q_len=bound)
+        assert err == 0 and torch.equal(o, want)
+    if max(lens) > 1:
+        o, err = prefill(sh, q, k, v, lens, max_q_len=max(lens) - 1)
+        assert err == INVALID
