@@ -302,6 +302,7 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
     }
   }
   const float now = fmaxf(pow2_scale(lanes_max<LPT>(m, mask)), before), inv = 1.0f / now;
+  __syncwarp(mask);   // the scale before has been read by every lane
   if (at.lane == 0) *at.scale = now;
   if (!on) return;
   if (off && now > before) {
