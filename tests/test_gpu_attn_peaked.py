@@ -137,3 +137,24 @@ def test_scores_that_keep_growing(n):
     o, lse = attend(sh, pool, table, q, L)
     kk, vv = sequence_rows(pool, table[0], L)
     assert_attention(o, lse, attention64(q, kk, vv, sh.softmax_scale), inputs.BF16)
+
+
+@pytest.mark.parametrize("d,G,dtype", [(64, 3, inputs.BF16), (128, 4, inputs.BF16), (256, 6, inputs.BF16), (96, 2, inputs.BF16),
+                                       (32, 2, inputs.F32)])
+@pytest.mark.parametrize("weight", [0.9, 0.999])
+def test_prefill_one_key_takes_most_of_the_weight(d, G, dtype, weight):
+    """The same over plain rows: every row of a prompt sees the first key, whose
+    values are small."""
+    T = 700
+    sh = AttnShape(G, 1, d, 16, dtype=dtype)
+    g = torch.Generator().manual_seed(d)
+    q, k, v = (torch.randn(T, h, d, generator=g) for h in (G, 1, 1))
+    q[..., 0], k[..., 0], k[0] = 1.0, 0.0, 0.0
+    k[0, 0, 0] = (math.log(weight / (1 - weight)) + math.log(T - 1) + 0.5) * d ** 0.5
+    v[0] *= 0.02
+    q, k, v = (x.to(sh.torch_dtype()).cuda() for x in (q, k, v))
+    cu = torch.tensor([0, T], dtype=torch.int32).cuda()
+    o, lse, err = torch.empty_like(q), torch.empty(T, G, device="cuda"), err_word()
+    gdn.gdn_attn_prefill(sh, q=q, k=k, v=v, cu_seqlens=cu, cu_kv=cu, o=o, lse=lse, dev_error=err)
+    assert err.item() == 0
+    assert_attention(o, lse, attention64(q, k, v, sh.softmax_scale), dtype)
