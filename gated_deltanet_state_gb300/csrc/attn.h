@@ -93,20 +93,22 @@ struct AttnPrefillParams {
   int32_t flat;       // the order of the row tiles (prefill_grid)
 };
 
-// Row tiles of a prefill, `rows` rows each, as blocks (times kv heads).  Where
-// max_q is about the longest sequence: every sequence's last tile, then the ones
-// before, and so on, as many as the longest may have, so that those with the
-// most keys start first.  Where that is `times` the tiles that total_q rows can
-// make or more (max_q left at total_q; one long prompt among many short ones),
-// sequence s has the places from cu_q[s] G / rows + s on, which are as many as
-// its tiles or one more.  A place without a tile costs the tensor-core kernel, a
-// CTA an SM, more than the search for a place, the fp32 one less (24 prompts of
-// 500 tokens, 24 heads, 4 kv heads, d = 256, bound of 500: 152 us even, 147 flat;
-// of 4,000: 210, 147; of all: 360, 147.  4 heads, 2, d = 32, fp32: 107, 122; 119,
-// 123; 156, 123.  One of 4,000 and 60 of 50: 366, 179; 276, 232), hence 2 and 8.
+// Row tiles of a prefill, `rows` rows each, as blocks (times kv heads), in one of
+// two orders.  Even: every sequence's last tile, then the ones before, and so on,
+// as many as max_q allows the longest, so that those with the most keys start
+// first.  Flat: sequence after sequence, s at the places from cu_q[s] G / rows + s
+// on, which are as many as its tiles or one more, whatever max_q is.  A place
+// without a tile costs the tensor-core kernel, a CTA an SM, more than the search
+// for a place and the worse order, so it takes the order with fewer places
+// (24 heads, 4 kv heads, d = 256, even and flat: 24 prompts of 1 to 600 tokens
+// after up to 2,000 keys 207 and 187 us; 24 of 500 under a bound of 4,000, 210
+// and 147; one of 4,000 and 60 of 50, 366 and 180; 256 of 64, which are even's,
+// 32 heads, 8, d = 128, 165 and 190).  The fp32 kernel's empty blocks cost less:
+// flat from `times` = 8 (4 heads, 2, d = 32, 24 prompts of 500 under a bound of
+// 500: 107 and 122; of 4,000: 119 and 121; of all rows: 156 and 123).
 inline int64_t prefill_grid(AttnPrefillParams& p, int rows, int times) {
   const int64_t even = ((int64_t)p.max_q * p.G + rows - 1) / rows * p.N, flat = p.Tq * p.G / rows + p.N;
-  p.flat = even >= times * flat;
+  p.flat = even > times * flat;
   return (p.flat ? flat : even) * p.Hkv;
 }
 
@@ -191,16 +193,13 @@ __device__ __forceinline__ void e4m3_f32x16(const uint4& v, float (&f)[16]) {
 // ---- a prefill's row tiles ---------------------------------------------------------
 // Block -> sequence, kv head, and which of the sequence's tiles, counted from its last.
 __device__ __forceinline__ void prefill_place(const AttnPrefillParams& p, int rows, int block, int& s, int& h, int& back) {
-  if (!p.flat) {
-    const int groups = p.N * p.Hkv;
-    back = block / groups;
-    const int pr = block - back * groups;
-    s = pr / p.Hkv;
-    h = pr - s * p.Hkv;
-    return;
-  }
-  const int i = block / p.Hkv;
-  h = block - i * p.Hkv;
+  const int groups = p.N * p.Hkv;
+  back = block / groups;
+  const int pr = block - back * groups;
+  s = pr / p.Hkv;
+  h = pr - s * p.Hkv;
+  if (!p.flat) return;
+  const int i = back * p.N + s;   // block / Hkv
   auto first = [&](int k) { return (int64_t)p.cu_q[k] * p.G / rows + k; };
   int lo = 0, hi = p.N;   // the last s with first(s) <= i
   while (hi - lo > 1) {

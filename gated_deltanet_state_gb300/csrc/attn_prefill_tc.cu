@@ -965,7 +965,7 @@ cudaError_t prefill_tc(AttnPrefillParams p, cudaStream_t st) {
     e = cudaFuncSetAttribute(attn_prefill_tc_kernel<D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPreSmem<D, PAIR>);
   if (e != cudaSuccess) return e;
   constexpr int ROWS = C::CTAS * kTile;
-  const int64_t grid = prefill_grid(p, ROWS, 2) * C::CTAS;
+  const int64_t grid = prefill_grid(p, ROWS, 1) * C::CTAS;
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
