@@ -25,7 +25,7 @@ __host__ __device__ inline int64_t kv_codes_bytes(const KvCache& c) { return (in
 
 struct KvTablesParams {
   int32_t N, max_pages, num_free, num_pages, page_tokens;
-  int32_t seqs_per_cta, slices;
+  int32_t seqs_per_cta;
   int64_t T;
   const int32_t* kv_len;
   const int32_t* new_len;

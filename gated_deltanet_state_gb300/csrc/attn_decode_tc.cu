@@ -11,9 +11,11 @@
 // codes takes, 52 cycles).
 //
 // Bound by HBM: 256 sequences over 1,024 to 8,192 tokens (24 heads, 4 kv heads,
-// d = 256: 2.45 GB) take 406 us with the join, 6.0 TB/s or 89 % of a copy's
-// rate; one over 777 tokens 13.3 us, two launches and the chain of a piece's
-// loads, two products and softmax.
+// d = 256: 2.45 GB) take 403 to 407 us with the join, 6.0 TB/s or 89 % of a
+// copy's rate; one over 777 tokens 13.5 to 14 us, two launches and the chain of a
+// piece's loads, two products and softmax.  The third part of P doubles the
+// columns of 8 rows' output products (16 to 32): nothing at d = 256, 7 to 10 % at
+// narrow heads (64 sequences of 1,024 to 8,192 tokens, 32 heads, 8, d = 64: 113 us).
 #include "attn_decode_tc.cuh"
 
 namespace gdn {

@@ -7,7 +7,7 @@
 // * A row of Q, scaled by a power of two so that its largest element is in (224,
 //   448], as hi + lo: hi an e4m3 of 4 significant bits, lo what is left of the 8
 //   of a bf16 (at most 3 bits and a sign), as an e4m3 of 16 times it or as an
-//   e5m2.  All 8 bits are kept of elements down to 2^-14 of the largest; below,
+//   e5m2.  All 8 bits are kept of elements down to 2^-13 of the largest; below,
 //   an element is off by at most 2^-21 of the largest.
 // * A weight p as three e5m2, of 3 significant bits each: 9 together, to at
 //   most 2^-9 of the weight, half of what a rounding to bf16 may do.  e5m2

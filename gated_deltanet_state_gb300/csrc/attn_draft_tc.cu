@@ -14,7 +14,7 @@
 // from one to the other before the exponentials.
 //
 // Measured: 16 drafts of 16 rows over 2,048 to 32,768 tokens (606 MB of codes)
-// 235 us with the join, 2.6 TB/s (with P in two e4m3 parts on one scale 216 us,
+// 225 to 235 us with the join, 2.6 TB/s (with P in two e4m3 parts on one scale 216 us,
 // but then what lies below 2^-14 of the reference was lost).  A score buffer's
 // own chain (scores, softmax, outputs one after another, and what passes between
 // them) is the longest part of a tile; an item's end (128 rows x 1 KB on their

@@ -11,8 +11,10 @@
 // * Two warpgroups take the key tiles in turn (a row in a thread, 1,900 cycles a
 //   tile), the reference m passing from one to the other before the
 //   exponentials, so that those of two key tiles overlap; two score buffers
-//   cover that at d = 256 (2,144 cycles of products), three at d = 128 (1,069)
-//   and 64 (680, which the exponentials' 950 exceed).
+//   cover that at d = 256 (2,144 cycles of products), three at d = 128 (1,069,
+//   of about 1,400 that a key tile takes in the six chunks below: latency, since
+//   neither the tensor pipe nor the issue slots are full) and 64 (680, which the
+//   exponentials' 950 exceed).
 // * At d = 256 and 128 a CTA would load a key tile's 128 or 64 KB in that time,
 //   more than L2 gives, so two CTAs share it (cta_group::2: half of its keys and
 //   half of its values' elements in each, 256 query rows a product).
@@ -22,9 +24,11 @@
 //   the tile before or after, about 9,000 of it still in the way.
 //
 // Measured (24 heads, 4 kv heads, d = 256; 32, 8, d = 128): two prompts of
-// 8,192 tokens 995 us, 1.66 PFLOP/s or 85 % of a library product's burst and
-// 96 % of its sustained rate, under the power limit (893 us at 1.85 GHz); six
-// chunks of 101 to 2,003 tokens after up to 6,007 keys 496 us, 1.28 PFLOP/s.
+// 8,192 tokens 1,002 to 1,017 us, 1.62 to 1.65 PFLOP/s or 83 to 84 % of a library
+// product's burst, 94 to 95 % of its sustained rate, under the power limit (900 us
+// at 1.85 GHz); six chunks of 101 to 2,003 tokens after up to 6,007 keys 457 to
+// 465 us, 1.37 to 1.39 PFLOP/s; two prompts of 8,192 at d = 64 (32 heads, 8)
+// 666 us, 0.83 PFLOP/s.
 #include <cuda.h>
 
 #include "attn.h"

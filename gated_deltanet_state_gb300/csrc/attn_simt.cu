@@ -28,7 +28,8 @@ template <typename T> __device__ __forceinline__ void put1(void* o, int64_t i, f
 // of the head each (d / 32 of them) for the values; each warp keeps its own
 // softmax statistics, joined at the end.  Serves what the tensor-core kernels do
 // not (fp32 rows, d not a multiple of 32), bound by the conversions and fp32
-// arithmetic: 256 sequences of d = 256 took 5,070 us here against 406 there.
+// arithmetic: 256 sequences over 1,024 to 8,192 tokens (24 heads, 4 kv heads) take
+// 5,045 us at d = 256 in fp32, against 404 there in bf16, and 1,823 at d = 80.
 template <typename T>
 __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const AttnDecodeParams p) {
   extern __shared__ float smem[];
@@ -260,7 +261,8 @@ template <typename T>
 cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
   const cudaError_t e = attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st) : decode_simt<T>(p, st);
   if (e != cudaSuccess || !p.part_o) return e;
-  // launched while the pieces' kernel still runs, waiting on the device for its end
+  // launched as the last CTAs of the pieces' kernel leave, waiting on the device for
+  // its end
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((p.max_q * p.Hq + 3) / 4), p.N);
   cfg.blockDim = dim3(128);

@@ -359,10 +359,11 @@ __device__ __forceinline__ void append_part(const T* src, int64_t stride, const 
 // New rows into the cache.  A CTA takes W rows; a run of rows of one block of
 // 16 tokens is handled, for one kv head and K or V, by LPT lanes with 8
 // elements of the head each.  The block's largest value decides its scale, so
-// the rows are held in registers from the load to the store: bound by that wait
-// and the conversions more than by HBM.  Measured (4 kv heads, d = 256, bf16):
-// five prompts, 29,500 rows, 181 MB read and written 39 us, 4.6 TB/s; 256
-// single rows 5.5 us.
+// the rows are held in registers from the load to the store.  Prompts are bound
+// by what a CTA does before its first row arrives (slots, list, two barriers) and
+// by whole waves of CTAs more than by HBM.  Measured (4 kv heads, d = 256, bf16):
+// five prompts, 29,500 rows (6.05 waves of 608 CTAs), 181 MB read and written
+// 39 us, 4.6 TB/s (fp32: 301 MB 65 us); 256 single rows 5.5 us.
 template <typename T, int LPT, int W, int THREADS>
 __global__ void __launch_bounds__(THREADS, sizeof(T) == 2 ? 512 / THREADS : 256 / THREADS) kv_append_kernel(const KvAppendParams p) {
   constexpr int kSlots = THREADS / LPT;   // runs in work at once
@@ -462,8 +463,8 @@ __device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
 // each block of 16 tokens that starts among them is read, for one head and K or
 // V, by LPT lanes with 8 elements each (V's operand tiles are transposed in
 // registers) and written as row pieces of 8 elements.  Bound by HBM: two
-// prefixes, 1.06 GB (4 kv heads, d = 256), 160 us, 6.6 TB/s or 97 % of a copy's
-// rate; 19 ragged ones, 242 MB (8 kv heads, d = 128), 46 us (171 and 54 us with
+// prefixes, 1.06 GB (4 kv heads, d = 256), 159 us, 6.6 TB/s or 97 % of a copy's
+// rate; 19 ragged ones, 242 MB (8 kv heads, d = 128), 44 us (171 and 54 us with
 // 64 rows a CTA, whose last ones leave SMs idle).
 template <typename T, int LPT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherParams p) {

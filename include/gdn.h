@@ -701,15 +701,16 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
                          const gdn_kv_gather_args* args, void* stream);
 
 /* Attention of 1 to 32 new rows a sequence over the 8-bit cache: a decode
- * step, or the rows of a draft being verified.  In bf16 all 8 bits of an
- * element of q count down to 2^-14 of its row's largest (smaller ones to 2^-21
- * of that), and 9 of a weight down to 2^-19 of the largest of its piece
- * (smaller ones to 2^-28 of that); sums and statistics are fp32.  The new
- * rows' own K and V are in the cache already (kv_len[s] counts them).  A
- * sequence with more rows than max_q_len or more keys than max_kv_len, or
- * whose table holds a page outside the pool, sets GDN_ERR_INVALID_ARG /
- * GDN_ERR_PAGE_RANGE; its outputs are not written (the page fault: that
- * piece's keys are left out).
+ * step, or the rows of a draft being verified.  The new rows' own K and V are
+ * in the cache already (kv_len[s] counts them).  A sequence with more rows
+ * than max_q_len or more keys than max_kv_len, or whose table holds a page
+ * outside the pool, sets GDN_ERR_INVALID_ARG / GDN_ERR_PAGE_RANGE; its
+ * outputs are not written (the page fault: that piece's keys are left out).
+ *
+ * Sums and statistics are fp32.  In bf16 all 8 bits of an element of q count
+ * down to 2^-13 of its row's largest (smaller ones to 2^-21 of that), and 9 of
+ * a weight (times its block's V scale) down to 2^-19 of the largest of its
+ * piece (smaller ones to 2^-28 of that).
  *
  * The keys of a sequence are cut into pieces by its own kv_len and number of
  * rows alone, the pieces run in parallel and are joined in order: a row's bits
