@@ -34,7 +34,7 @@ __all__ = [
     "gdn_core_prefill_workspace_size", "gdn_core_prefill", "gdn_core_decode",
     "gdn_decode_step", "gdn_checkpoint_resume", "gdn_checkpoint_save", "gdn_replay_append",
     "gdn_replay_rollback", "gdn_replay_flush", "AttnShape", "KVPool", "make_attn_desc", "gdn_kv_page_bytes", "gdn_kv_tables", "gdn_kv_append", "gdn_kv_gather",
-    "gdn_attn_decode_workspace_size", "gdn_attn_decode", "gdn_attn_prefill", "ATTN_DECODE_ROWS", "KV_BLOCK",
+    "gdn_attn_decode_workspace_size", "gdn_attn_decode", "gdn_attn_prefill", "ATTN_DECODE_ROWS", "KV_BLOCK", "KV4_GROUP",
     "REPLAY_LOG_SLOTS", "PREFILL_AUTO", "PREFILL_FUSED", "PREFILL_TWO_KERNELS", "STATUS",
 ]
 
@@ -610,5 +610,5 @@ def gdn_replay_flush(shape: LayerShape, pool: StatePool, *, ckpt_slot, log_x, lo
 
 from . import attention  # noqa: E402  (needs the names above)
 from .attention import (  # noqa: E402
-    ATTN_DECODE_ROWS, KV_BLOCK, KVPool, gdn_attn_decode, gdn_attn_decode_workspace_size, gdn_attn_prefill,
+    ATTN_DECODE_ROWS, KV4_GROUP, KV_BLOCK, KVPool, gdn_attn_decode, gdn_attn_decode_workspace_size, gdn_attn_prefill,
     gdn_kv_append, gdn_kv_gather, gdn_kv_page_bytes, gdn_kv_tables, make_attn_desc)

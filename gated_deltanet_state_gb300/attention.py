@@ -1,5 +1,5 @@
 """Binding of the attention layers' entry points (``include/gdn.h``): the
-tables of a step, the paged 8-bit K / V cache and the attention that reads it.
+tables of a step, the paged K / V cache of 8 or 4 bits and the attention that reads it.
 Imported into the package's namespace, like the GDN layers' functions."""
 from __future__ import annotations
 
@@ -14,13 +14,14 @@ from .inputs import AttnShape
 
 ATTN_DECODE_ROWS = 32    # GDN_ATTN_DECODE_ROWS
 KV_BLOCK = 16            # GDN_KV_BLOCK
+KV4_GROUP = 32           # GDN_KV4_GROUP
 
 _i32, _i64 = ctypes.c_int32, ctypes.c_int64
 
 
 class _AttnDesc(ctypes.Structure):
     _fields_ = [("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("page_tokens", _i32),
-                ("dtype", _i32), ("scale", ctypes.c_float), ("reserved", _i32)]
+                ("dtype", _i32), ("scale", ctypes.c_float), ("kv_bits", _i32)]
 
 
 class _KvTablesArgs(ctypes.Structure):
@@ -69,7 +70,7 @@ def _signatures() -> dict:
 @lru_cache(maxsize=256)
 def make_attn_desc(shape: AttnShape) -> _AttnDesc:
     return _AttnDesc(shape.num_q_heads, shape.num_kv_heads, shape.head_dim, shape.page_tokens, shape.dtype,
-                     shape.softmax_scale, 0)
+                     shape.softmax_scale, shape.kv_bits)
 
 
 def gdn_kv_page_bytes(shape: AttnShape) -> int:
@@ -107,24 +108,33 @@ class KVPool:
         return self.shape.num_kv_heads, self.shape.page_tokens // KV_BLOCK
 
     def k_codes(self) -> torch.Tensor:
-        """e4m3 [pages][Hkv][blocks][2][d/16][8][16]"""
+        """e4m3 [pages][Hkv][blocks][2][d/16][8][16]; 4 bits: bytes [pages][Hkv][blocks][d/32][16][16]"""
         n, d = self.shape.codes_bytes, self.shape.head_dim
+        if self.shape.kv_bits == 4:
+            return self.buf[:, :n].unflatten(1, self._blocks() + (d // KV4_GROUP, KV_BLOCK, 16))
         return self.buf[:, :n].unflatten(1, self._blocks() + (2, d // 16, 8, 16)).view(torch.float8_e4m3fn)
 
     def v_codes(self) -> torch.Tensor:
-        """e4m3 [pages][Hkv][blocks][d][16]"""
+        """e4m3 [pages][Hkv][blocks][d][16]; 4 bits: bytes [pages][Hkv][blocks][d][8]"""
         n, d = self.shape.codes_bytes, self.shape.head_dim
+        if self.shape.kv_bits == 4:
+            return self.buf[:, n:2 * n].unflatten(1, self._blocks() + (d, 8))
         return self.buf[:, n:2 * n].unflatten(1, self._blocks() + (d, KV_BLOCK)).view(torch.float8_e4m3fn)
 
     def _scales(self, i: int) -> torch.Tensor:
+        if self.shape.kv_bits == 4:
+            n, o = self.shape.scales_bytes[i], 2 * self.shape.codes_bytes + i * self.shape.scales_bytes[0]
+            groups = () if i else (self.shape.head_dim // KV4_GROUP,)
+            return self.buf[:, o:o + n].unflatten(1, self._blocks() + groups + (KV_BLOCK,))
         o, n = self.shape.codes_bytes // 2, self._blocks()[0] * self._blocks()[1]
         return self.buf.view(torch.float32)[:, o + i * n:o + (i + 1) * n].unflatten(1, self._blocks())
 
     def k_scales(self) -> torch.Tensor:
-        """fp32 [pages][Hkv][blocks]"""
+        """fp32 [pages][Hkv][blocks]; 4 bits: bytes [pages][Hkv][blocks][d/32][16]"""
         return self._scales(0)
 
     def v_scales(self) -> torch.Tensor:
+        """fp32 [pages][Hkv][blocks]; 4 bits: bytes [pages][Hkv][blocks][16]"""
         return self._scales(1)
 
 
@@ -202,7 +212,7 @@ def gdn_kv_tables(shape: AttnShape, num_pages: int, *, kv_len, new_len, free_pag
 def gdn_kv_append(shape: AttnShape, pool: KVPool, *, k, v, slot_map, dev_error, stream=None,
                   raise_on_error: bool = True) -> int:
     """New K and V rows [T, Hkv, d] (slices of wider rows are fine) into the
-    8-bit cache at slot_map's slots (gdn.h: gdn_kv_append)."""
+    cache at slot_map's slots (gdn.h: gdn_kv_append)."""
     kp, ks = _rows(k, shape.num_kv_heads, shape, "k")
     vp, vs = _rows(v, shape.num_kv_heads, shape, "v")
     T = int(k.shape[0])
@@ -233,7 +243,7 @@ def gdn_attn_decode_workspace_size(shape: AttnShape, num_seqs: int, total_tokens
 def gdn_attn_decode(shape: AttnShape, pool: KVPool, *, q, cu_seqlens, kv_len, block_table, o, dev_error, lse=None,
                     max_q_len: int = 1, max_kv_len: Optional[int] = None, workspace=None, wait_cycles: int = 0,
                     stream=None, raise_on_error: bool = True) -> int:
-    """Attention of 1 to 32 new rows a sequence over the 8-bit cache (gdn.h:
+    """Attention of 1 to 32 new rows a sequence over the cache (gdn.h:
     gdn_attn_decode).  max_kv_len bounds kv_len (None: what the block table
     can hold).  Without `workspace` one of gdn_attn_decode_workspace_size
     bytes is taken from PyTorch's allocator for the call.  wait_cycles bounds

@@ -1,5 +1,5 @@
 // attn.h — parameters and launchers of the attention layers' kernels (the
-// 8-bit K / V cache and the attention that reads it; not exported).
+// 8-bit and 4-bit K / V caches and the attention that reads them; not exported).
 #pragma once
 
 #include "common.cuh"
@@ -15,6 +15,7 @@ struct KvCache {
   int32_t num_pages;
   int32_t page_tokens;
   int32_t Hkv, d;
+  int32_t bits;   // 8 or 4
 };
 
 // Offsets within a page: block b of head h.
@@ -148,6 +149,8 @@ constexpr float kLostPiece = -1.f;
 cudaError_t launch_kv_tables(const KvTablesParams& p, cudaStream_t st);
 cudaError_t launch_kv_append(const KvAppendParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_kv_gather(const KvGatherParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_kv4_append(const KvAppendParams& p, int dtype, cudaStream_t st);
+cudaError_t launch_kv4_gather(const KvGatherParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_attn_decode(const AttnDecodeParams& p, int dtype, cudaStream_t st);
 cudaError_t launch_attn_prefill(const AttnPrefillParams& p, int dtype, cudaStream_t st);
 // The tensor-core decode (bf16, d a multiple of 32): the pieces, without the join.

@@ -21,10 +21,12 @@ gdn_status check_desc(const gdn_attn_desc* d) {
   if (!d || d->num_q_heads <= 0 || d->num_kv_heads <= 0 || d->head_dim <= 0 || d->page_tokens <= 0)
     return GDN_ERR_INVALID_ARG;
   if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
-  if (!(d->scale > 0.0f) || !std::isfinite(d->scale) || d->reserved != 0) return GDN_ERR_INVALID_ARG;
+  if (!(d->scale > 0.0f) || !std::isfinite(d->scale)) return GDN_ERR_INVALID_ARG;
+  if (d->kv_bits != 0 && d->kv_bits != 8 && d->kv_bits != 4) return GDN_ERR_INVALID_ARG;
   if (d->head_dim % 16 != 0 || d->head_dim > 256 || d->page_tokens % GDN_KV_BLOCK != 0 ||
       d->page_tokens > (1 << 24) || d->num_q_heads % d->num_kv_heads != 0 || d->num_q_heads > 1024)
     return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (d->kv_bits == 4 && d->head_dim % GDN_KV4_GROUP != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
   return GDN_OK;
 }
 
@@ -37,7 +39,7 @@ gdn_status check_pool(const gdn_attn_desc* d, const gdn_pool* pool) {
 
 KvCache make_cache(const gdn_attn_desc* d, const gdn_pool* pool) {
   return KvCache{static_cast<char*>(pool->base), pool->page_bytes, pool->num_pages, d->page_tokens, d->num_kv_heads,
-                 d->head_dim};
+                 d->head_dim, d->kv_bits == 4 ? 4 : 8};
 }
 
 // Rows of `heads` heads, `stride` elements apart, each 16-byte aligned.
@@ -59,7 +61,9 @@ extern "C" {
 
 int64_t gdn_kv_page_bytes(const gdn_attn_desc* d) {
   if (check_desc(d) != GDN_OK) return -1;
-  const int64_t per = 2 * (int64_t)d->head_dim * GDN_KV_BLOCK + 2 * (int64_t)sizeof(float);   // a block, K and V
+  // a block, K and V
+  const int64_t per = d->kv_bits == 4 ? GDN_KV_BLOCK * (int64_t)(d->head_dim + d->head_dim / GDN_KV4_GROUP + 1)
+                                      : 2 * (int64_t)d->head_dim * GDN_KV_BLOCK + 2 * (int64_t)sizeof(float);
   return (d->num_kv_heads * (int64_t)(d->page_tokens / GDN_KV_BLOCK) * per + 255) / 256 * 256;
 }
 
@@ -107,7 +111,7 @@ gdn_status gdn_kv_append(const gdn_attn_desc* desc, const gdn_pool* pool, const 
   if (st != GDN_OK) return st;
   const KvAppendParams p{make_cache(desc, pool), a->total_tokens, a->k_stride, a->v_stride, a->k, a->v, a->slot_map,
                          a->dev_error};
-  return cuda_status(launch_kv_append(p, desc->dtype, static_cast<cudaStream_t>(stream)));
+  return cuda_status((desc->kv_bits == 4 ? launch_kv4_append : launch_kv_append)(p, desc->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool, const gdn_kv_gather_args* a, void* stream) {
@@ -123,7 +127,7 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool, const 
     return GDN_ERR_INVALID_ARG;
   const KvGatherParams p{make_cache(desc, pool), a->num_seqs, a->max_pages, a->total_tokens, a->cu_kv, a->block_table,
                          a->k, a->v, a->dev_error};
-  return cuda_status(launch_kv_gather(p, desc->dtype, static_cast<cudaStream_t>(stream)));
+  return cuda_status((desc->kv_bits == 4 ? launch_kv4_gather : launch_kv_gather)(p, desc->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_attn_decode_workspace_size(const gdn_attn_desc* desc, int32_t num_seqs, int64_t total_tokens,

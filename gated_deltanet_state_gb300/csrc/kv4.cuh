@@ -1,0 +1,76 @@
+// kv4.cuh — the 4-bit form of the attention layers' cache (layout and rules:
+// include/gdn.h): addresses, scales, codes.
+#pragma once
+
+#include "attn.h"
+
+namespace gdn {
+
+constexpr int kKv4Group = GDN_KV4_GROUP;   // channels of K that share a scale
+constexpr uint32_t kKv4Nan = 255;          // the scale byte of NaN
+constexpr float kKv4Most = 25088.f;        // the largest magnitude that no scale cuts off: 7 * 14 * 2^8
+
+// Bytes of a block of 16 tokens of a head: K's codes (V's are as many), K's scales, V's scales.
+__host__ __device__ inline int kv4_codes(int d) { return kKvBlock * d / 2; }
+__host__ __device__ inline int kv4_k_scales(int d) { return kKvBlock * (d / kKv4Group); }
+
+}  // namespace gdn
+
+#ifdef __CUDACC__
+namespace gdn {
+
+__device__ __forceinline__ uint8_t* kv4_page(const KvCache& c, int page) {
+  return reinterpret_cast<uint8_t*>(c.base) + (int64_t)page * c.page_bytes;
+}
+__device__ __forceinline__ uint8_t* kv4_k_block(const KvCache& c, int page, int h, int b) {
+  return kv4_page(c, page) + kv_block_index(c, h, b) * kv4_codes(c.d);
+}
+__device__ __forceinline__ uint8_t* kv4_v_block(const KvCache& c, int page, int h, int b) {
+  return kv4_k_block(c, page, h, b) + kv_codes_bytes(c) / 2;
+}
+__device__ __forceinline__ uint8_t* kv4_k_scale(const KvCache& c, int page, int h, int b) {
+  return kv4_page(c, page) + kv_codes_bytes(c) + kv_block_index(c, h, b) * kv4_k_scales(c.d);
+}
+__device__ __forceinline__ uint8_t* kv4_v_scale(const KvCache& c, int page, int h, int b) {
+  return kv4_page(c, page) + kv_codes_bytes(c) + (int64_t)c.Hkv * c.page_tokens * (c.d / kKv4Group) +
+         kv_block_index(c, h, b) * kKvBlock;
+}
+
+// Value of a scale byte: (8 + b % 8) 2^(b / 8 - 23), whose fp32 bits are the byte
+// next to an exponent of 107; its bf16 bits the upper half of those (4
+// significant bits: exact).
+__device__ __forceinline__ float kv4_scale(uint32_t b) {
+  return b == kKv4Nan ? __int_as_float(0x7fffffff) : __uint_as_float((b << 20) + (107u << 23));
+}
+__device__ __forceinline__ uint32_t kv4_scale_bf16(uint32_t b) { return b == kKv4Nan ? 0x7fffu : (b << 4) + (107u << 7); }
+
+// The least byte whose scale times 7 (exact: 7 bits) reaches a magnitude, given by its bits.
+__device__ __forceinline__ uint32_t kv4_byte(uint32_t amax_bits) {
+  const float amax = __uint_as_float(amax_bits), y = amax * (1.f / 7.f);
+  int b = ((int)__float_as_uint(y) - (107 << 23) + 0xfffff) >> 20;
+  b = max(0, min(254, b));
+  // (the quotient's rounding can be off by one step at a scale's own value)
+  if (b > 0 && 7.f * kv4_scale(b - 1) >= amax) --b;
+  if (b < 254 && 7.f * kv4_scale(b) < amax) ++b;
+  return b;
+}
+
+// Two neighbouring elements of a word of eight, already shifted to bits 0 .. 3 and
+// 16 .. 19, as bf16 of 128 + n: the codes become the mantissas' last bits.
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
+// (128 + n) s - 136 s = (n - 8) s: exact, since 136 s has 17 times s's 4 bits,
+// 8 at most, and the product is not rounded on its way.
+__device__ __forceinline__ uint32_t kv4_fma(uint32_t a, uint32_t s, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(s), "r"(c));
+  return r;
+}
+// -136 s of a pair of scales in bf16.
+__device__ __forceinline__ uint32_t kv4_offset(uint32_t s) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xc308c308u));
+  return r;
+}
+
+}  // namespace gdn
+#endif

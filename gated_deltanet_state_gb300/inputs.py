@@ -81,13 +81,14 @@ QWEN4B = LayerShape(16, 32, 128, 128, block_size=640, chunk_size=64, page_bytes=
 
 @dataclass(frozen=True)
 class AttnShape:
-    """Shape of one attention layer plus the geometry of its 8-bit cache."""
+    """Shape of one attention layer plus the geometry of its cache."""
     num_q_heads: int
     num_kv_heads: int
     head_dim: int
     page_tokens: int             # tokens of a KV page, a multiple of 16
     dtype: int = BF16
     scale: float = 0.0           # of the scores; 0: 1 / sqrt(head_dim)
+    kv_bits: int = 8             # of a cached value: 8, or 4 (head_dim a multiple of 32)
 
     @property
     def softmax_scale(self) -> float:
@@ -96,12 +97,19 @@ class AttnShape:
     @property
     def codes_bytes(self) -> int:
         """Bytes of a page's K codes (and of its V codes)."""
-        return self.num_kv_heads * self.page_tokens * self.head_dim
+        return self.num_kv_heads * self.page_tokens * self.head_dim * self.kv_bits // 8
+
+    @property
+    def scales_bytes(self) -> tuple[int, int]:
+        """Bytes of a page's K scales and of its V scales."""
+        if self.kv_bits == 4:    # a byte for 32 channels of a token, a byte for a token
+            tokens = self.num_kv_heads * self.page_tokens
+            return tokens * (self.head_dim // 32), tokens
+        return (self.num_kv_heads * (self.page_tokens // 16) * 4,) * 2
 
     @property
     def page_bytes(self) -> int:
-        scales = self.num_kv_heads * (self.page_tokens // 16) * 4
-        return (2 * self.codes_bytes + 2 * scales + 255) // 256 * 256
+        return (2 * self.codes_bytes + sum(self.scales_bytes) + 255) // 256 * 256
 
     def torch_dtype(self) -> torch.dtype:
         return _TORCH_DTYPE[self.dtype]

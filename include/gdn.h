@@ -558,8 +558,8 @@ gdn_status gdn_replay_flush(const gdn_layer_desc* desc, const gdn_pool* pool,
                             const gdn_replay_args* args, void* stream);
 
 /* ---------------------------------------------------------------------------
- * The attention layers of a hybrid model: a paged 8-bit K / V cache and the
- * attention that reads it.
+ * The attention layers of a hybrid model: a paged K / V cache of 8 or 4 bits a
+ * value and the attention that reads it.
  *
  * A hybrid model interleaves its GDN layers with full-attention layers whose
  * cache is paged too ("Hybrid linear attention (gated DeltaNet)", "Why this
@@ -599,10 +599,30 @@ gdn_status gdn_replay_flush(const gdn_layer_desc* desc, const gdn_pool* pool,
  * gdn_kv_page_bytes, so KV pages and GDN state pages can share one pool).  A
  * block table row maps a sequence's token t to the page
  * block_table[s][t / page_tokens].
+ *
+ * In 4 bits (gdn_attn_desc.kv_bits = 4; head_dim a multiple of 32) a page holds
+ * twice the tokens: a value is (n - 8) * scale with a code n of 1 .. 15.  K has
+ * a scale for each GDN_KV4_GROUP = 32 channels of a token and head, since a few
+ * channels of K are much larger than the others; V has one for a token and head.
+ * A scale is a byte b that stands for (8 + b % 8) * 2^(b / 8 - 23), from 2^-20 to
+ * 3,584, and 255 for NaN.  Every value is exact in bf16.  Page layout:
+ *
+ *   K codes  [Hkv][page_tokens/16][d/32][16][16]   token, 16 bytes: 32 channels
+ *   V codes  [Hkv][page_tokens/16][d][8]           channel, 8 bytes: 16 tokens
+ *   K scales [Hkv][page_tokens/16][d/32][16]       bytes
+ *   V scales [Hkv][page_tokens/16][16]             bytes
+ *   padding up to page_bytes
+ *
+ * where eight codes of consecutive channels (tokens) are a little-endian 32-bit
+ * word, element 2 i in bits 4 i .. 4 i + 3 and element 2 i + 1 in bits 16 + 4 i ..
+ * 19 + 4 i, so that a shift and a mask leave a pair of neighbours in a word's
+ * halves.  A token's scales are its own: no block's scale ever rises.
  * ------------------------------------------------------------------------- */
 
-/* Tokens that share a scale. */
+/* Tokens of a cache block (that share a scale in 8 bits). */
 #define GDN_KV_BLOCK 16
+/* Channels of K that share a scale in 4 bits. */
+#define GDN_KV4_GROUP 32
 /* Most new rows a sequence in one gdn_attn_decode call: the replay log's. */
 #define GDN_ATTN_DECODE_ROWS GDN_REPLAY_LOG_SLOTS
 
@@ -610,11 +630,11 @@ gdn_status gdn_replay_flush(const gdn_layer_desc* desc, const gdn_pool* pool,
 typedef struct gdn_attn_desc {
   int32_t num_q_heads;   /* Hq, a multiple of Hkv                            */
   int32_t num_kv_heads;  /* Hkv                                              */
-  int32_t head_dim;      /* d: a multiple of 16, 16 .. 256                   */
+  int32_t head_dim;      /* d: a multiple of 16, 16 .. 256 (4 bits: of 32)   */
   int32_t page_tokens;   /* tokens of a KV page: a multiple of 16            */
   int32_t dtype;         /* GDN_F32 or GDN_BF16: q, k, v, o                  */
   float scale;           /* of the scores, finite and > 0 (1 / sqrt(d))      */
-  int32_t reserved;      /* must be 0                                        */
+  int32_t kv_bits;       /* of a cached value: 0 or 8, or 4                  */
 } gdn_attn_desc;
 
 /* Bytes of one KV page of this layer, a multiple of 256; -1 for a malformed
@@ -666,7 +686,15 @@ gdn_status gdn_kv_tables(const gdn_attn_desc* desc, const gdn_kv_tables_args* ar
  * max |x| / scale <= 448 over the run's finite values; where tokens stand
  * before the run it is at least their scale, and when it rises their codes
  * are converted to it.  Values beyond (infinities) saturate at 448 * scale,
- * NaN stays NaN.  k and v rows are [Hkv][d] dense, k_stride / v_stride
+ * NaN stays NaN.
+ *
+ * In 4 bits a scale is the least with 7 * scale >= max |x| over the finite values
+ * that it covers (the greatest, 3,584, if none has), a code the nearest to x /
+ * scale, halves away from zero; values beyond 7 * scale saturate, and a NaN makes
+ * the values that share its scale NaN.  Other tokens of the block, before the run
+ * and after it, stay as they are.
+ *
+ * k and v rows are [Hkv][d] dense, k_stride / v_stride
  * elements apart (multiples of 16 bytes), so slices of a fused projection's
  * rows can be given as they are. */
 typedef struct gdn_kv_append_args {
@@ -707,7 +735,7 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
  * outside the pool, sets GDN_ERR_INVALID_ARG / GDN_ERR_PAGE_RANGE; its
  * outputs are not written (the page fault: that piece's keys are left out).
  *
- * Sums and statistics are fp32.  In bf16 all 8 bits of an element of q count
+ * Sums and statistics are fp32.  Over 8 bits, in bf16 all 8 bits of an element of q count
  * down to 2^-13 of its row's largest (smaller ones to 2^-21 of that), and 9 of
  * a weight (times its block's V scale) down to 2^-19 of the largest of its
  * piece (smaller ones to 2^-28 of that).
