@@ -1,7 +1,8 @@
-// attn_decode_tc.cuh — what the two decode kernels on the tensor cores share:
-// the work items, the loads of the cache's blocks, the products' forms.
+// attn_decode_tc.cuh — what the decode kernels on the tensor cores share: the
+// work items of a CTA and its waits; and, of the two over the 8-bit cache, the
+// loads of its blocks and the products' forms.
 //
-// The cache's e4m3 codes are the products' operands as they lie in memory; no
+// There the cache's e4m3 codes are the products' operands as they lie in memory; no
 // code is converted.  Q and P enter in 8-bit parts whose products are added:
 //
 // * A row of Q, scaled by a power of two so that its largest element is in (224,
@@ -45,16 +46,20 @@ struct DtParams {
   uint32_t k_off, v_off, q_off, p_off, misc_off;   // dynamic shared memory
 };
 
-// Shared memory of either kernel.
-struct DtBase {
-  uint64_t k_full[kDtMaxStages], k_empty[kDtMaxStages], v_full[kDtMaxStages], v_empty[kDtMaxStages];
-  uint64_t sc_full[kDtMaxStages + 2], s_full[2], p_full[2], o_done[2], q_full, drain;
-  float ks[kDtMaxStages + 2][kDtBlocks], vs[kDtMaxStages + 2][kDtBlocks];
-  int bad[2][256];          // (items alternate) first token with a NaN value that not every row sees, by element
+// A CTA's share of the work, in shared memory.
+struct DtItems {
   int items[kDtSeqs + 1];   // running sums of the sequences' work items ...
   long long work[kDtSeqs + 1];   // ... and of their weights (tiles of every head: past 32 bits for long shared contexts)
   uint32_t tmem;
   int fail;
+};
+
+// Shared memory of either kernel over 8 bits.
+struct DtBase : DtItems {
+  uint64_t k_full[kDtMaxStages], k_empty[kDtMaxStages], v_full[kDtMaxStages], v_empty[kDtMaxStages];
+  uint64_t sc_full[kDtMaxStages + 2], s_full[2], p_full[2], o_done[2], q_full, drain;
+  float ks[kDtMaxStages + 2][kDtBlocks], vs[kDtMaxStages + 2][kDtBlocks];
+  int bad[2][256];          // (items alternate) first token with a NaN value that not every row sees, by element
 };
 
 __device__ __forceinline__ bool dt_wait(uint64_t* m, uint32_t parity, volatile int* fail, long long limit) {
@@ -263,7 +268,7 @@ __device__ __forceinline__ float split_row(const uint4& x, uint2& hi, uint2& lo)
 // Running sums of the items (one warp); lengths out of bounds are reported and
 // have none.
 template <int NT>
-__device__ __forceinline__ void dt_sums(const DtParams& w, DtBase& sh, int lane) {
+__device__ __forceinline__ void dt_sums(const DtParams& w, DtItems& sh, int lane) {
   const AttnDecodeParams& p = w.a;
   int sum = 0;
   long long sumw = 0;
@@ -367,7 +372,8 @@ __device__ __forceinline__ int dt_load(const DtParams& w, DtBase& sh, uint8_t* b
 }
 
 // After a run-out: one more bounded wait for each copy in flight.
-__device__ __forceinline__ void dt_drain(const DtParams& w, DtBase& sh, int loaded, bool is_v) {
+template <typename SH>
+__device__ __forceinline__ void dt_drain(const DtParams& w, SH& sh, int loaded, bool is_v) {
   const int ST = is_v ? w.v_stages : w.k_stages;
   for (int n = max(0, loaded - ST); n < loaded; ++n)
     tc::mbar_wait_bounded(is_v ? &sh.v_full[n % ST] : &sh.k_full[n % ST], (uint32_t)(n / ST) & 1, kDtWait);
@@ -376,7 +382,7 @@ __device__ __forceinline__ void dt_drain(const DtParams& w, DtBase& sh, int load
 // Reports a run-out and marks the rows of the pieces that this CTA had, items
 // [i0, i1): what it has not written of them must not be joined.
 template <int NT>
-__device__ __forceinline__ void dt_report(const DtParams& w, const DtBase& sh, int i0, int i1) {
+__device__ __forceinline__ void dt_report(const DtParams& w, const DtItems& sh, int i0, int i1) {
   const AttnDecodeParams& p = w.a;
   if (threadIdx.x == 0) atomicExch(p.err, GDN_ERR_TIMEOUT);   // over an earlier code
   if (!p.part_o) return;

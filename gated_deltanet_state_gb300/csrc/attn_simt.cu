@@ -1,7 +1,7 @@
 // attn_simt.cu — attention over the 8-bit cache and over packed prompts with
 // fp32 arithmetic on the CUDA cores: every dtype, head size and group size;
 // and the kernel that joins the pieces of a decode row.
-#include "kv4.cuh"
+#include "attn.h"
 
 namespace gdn {
 
@@ -30,7 +30,7 @@ template <typename T> __device__ __forceinline__ void put1(void* o, int64_t i, f
 // not (fp32 rows, d not a multiple of 32), bound by the conversions and fp32
 // arithmetic: 256 sequences over 1,024 to 8,192 tokens (24 heads, 4 kv heads) take
 // 5,045 us at d = 256 in fp32, against 404 there in bf16, and 1,823 at d = 80.
-template <typename T, bool B4>
+template <typename T>
 __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const AttnDecodeParams p) {
   extern __shared__ float smem[];
   const int d = p.c.d, piece = blockIdx.x, s = blockIdx.z;
@@ -74,18 +74,11 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
       if (lane == 0) set_error(p.err, GDN_ERR_PAGE_RANGE);
       continue;
     }
-    const uint8_t* kp = B4 ? kv4_k_block(p.c, page, h, b) + t * 16 : kv_k_block(p.c, page, h, b) + (t >> 3) * (d / 16) * 128 + (t & 7) * 16;
+    const uint8_t* kp = kv_k_block(p.c, page, h, b) + (t >> 3) * (d / 16) * 128 + (t & 7) * 16;
     float acc[kDecRows] = {};
     for (int c = hf; c < d / 16; c += 2) {
       float f[16];
-      if constexpr (B4) {
-        const uint2 w = *reinterpret_cast<const uint2*>(kp + (c >> 1) * 256 + (c & 1) * 8);
-        const float s4 = kv4_scale(kv4_k_scale(p.c, page, h, b)[(c >> 1) * 16 + t]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = s4 * (float)((int)((i < 8 ? w.x : w.y) >> (4 * (i % 8 / 2) + 16 * (i % 2)) & 15u) - 8);
-      } else {
-        e4m3_f32x16(*reinterpret_cast<const uint4*>(kp + c * 128), f);
-      }
+      e4m3_f32x16(*reinterpret_cast<const uint4*>(kp + c * 128), f);
 #pragma unroll
       for (int r = 0; r < kDecRows; ++r) {
         const float4* q4 = reinterpret_cast<const float4*>(sq + r * d + c * 16);
@@ -99,7 +92,7 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
         }
       }
     }
-    const float ks = B4 ? 1.f : *kv_k_scale(p.c, page, h, b), vs = B4 ? kv4_scale(kv4_v_scale(p.c, page, h, b)[t]) : *kv_v_scale(p.c, page, h, b);
+    const float ks = *kv_k_scale(p.c, page, h, b), vs = *kv_v_scale(p.c, page, h, b);
     const int pos = kb + t;
 #pragma unroll
     for (int r = 0; r < kDecRows; ++r) {
@@ -120,23 +113,17 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
       l[r] = l[r] * a + sum;
 #pragma unroll
       for (int i = 0; i < 8; ++i) O[r][i] *= a;
-      if (hf == 0) sp[r * 16 + t] = x == -INFINITY ? 0.f : e * vs;
+      if (hf == 0) sp[r * 16 + t] = e * vs;
     }
     __syncwarp();
-    const uint8_t* vp = B4 ? kv4_v_block(p.c, page, h, b) : kv_v_block(p.c, page, h, b);
+    const uint8_t* vp = kv_v_block(p.c, page, h, b);
     const bool edge = kb + kKvBlock > L - n + 1;   // some row does not see some token
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane + 32 * i;
       if (e < d) {
         float f[16];
-        if constexpr (B4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(vp + e * 8);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) f[k] = (float)((int)((k < 8 ? w.x : w.y) >> (4 * (k % 8 / 2) + 16 * (k % 2)) & 15u) - 8);
-        } else {
-          e4m3_f32x16(*reinterpret_cast<const uint4*>(vp + e * kKvBlock), f);
-        }
+        e4m3_f32x16(*reinterpret_cast<const uint4*>(vp + e * kKvBlock), f);
 #pragma unroll
         for (int r = 0; r < kDecRows; ++r) {
           const int seen = L - n + (r0 + r) / p.G + 1 - kb;
@@ -266,13 +253,15 @@ cudaError_t decode_simt(const AttnDecodeParams& p, cudaStream_t st) {
   const size_t sm_run = (size_t)(kDecRows * p.c.d + kDecWarps * kDecRows * 16) * 4;
   const size_t sm_join = (size_t)(kDecWarps * kDecRows * (p.c.d + 2)) * 4;
   const size_t sm = sm_run > sm_join ? sm_run : sm_join;   // at most 33 KB
-  (p.c.bits == 4 ? attn_decode_simt_kernel<T, true> : attn_decode_simt_kernel<T, false>)<<<dim3(p.max_pieces, p.c.Hkv * groups, p.N), 32 * kDecWarps, sm, st>>>(p);
+  attn_decode_simt_kernel<T><<<dim3(p.max_pieces, p.c.Hkv * groups, p.N), 32 * kDecWarps, sm, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
-  const cudaError_t e = p.c.bits == 8 && attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st) : decode_simt<T>(p, st);
+  const cudaError_t e = p.c.bits == 4                      ? launch_attn_decode4_tc(p, dtype, st)
+                        : attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st)
+                                                             : decode_simt<T>(p, st);
   if (e != cudaSuccess || !p.part_o) return e;
   // launched as the last CTAs of the pieces' kernel leave, waiting on the device for
   // its end
