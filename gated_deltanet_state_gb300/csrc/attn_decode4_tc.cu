@@ -4,15 +4,18 @@
 // The products have the cache as their 128 rows,
 //   S^T [tokens x rows] = K Q^T,    O^T [elements x rows] += V^T P^T,
 // and K and V^T come from tensor memory: two kinds of warps stand between the
-// codes and the products, one that unpacks codes of shared memory into bf16
-// operands of 64 tokens or channels there, one that makes the weights.  A code
-// under its scale is exact in bf16, so K and V enter as they are cached and Q as
-// it is given (fp32 rows in three bf16 parts, which hold their 24 bits).  V's
-// scale, one for a token and head, multiplies the token's weight.
+// codes and the products, one that unpacks codes of shared memory into operands
+// there, one that makes the weights.  A code under its scale is exact in bf16, so
+// K enters as it is cached, in bf16, and Q as it is given (fp32 rows in three bf16
+// parts, which hold their 24 bits).  V's codes enter as whole numbers, subnormals
+// of f16; V's scale, one for a token and head, goes into the token's weight, an
+// f16 (two parts for fp32 rows).
 //
-// A weight is 2^(s - M) for a reference M of its row that is the first tile's
-// maximum and moves only for a weight above 2^kGrow: bf16 has fp32's range,
-// so the reference need not follow, and a tile costs the softmax one vote.
+// A weight times its V scale is 2^(s + log2(vs) - M) for a reference M of its row:
+// the first tile's maximum, which moves only when a weight would pass f16's range,
+// so a tile costs the softmax one vote.  Weights keep 11 bits down to 2^-20 of the
+// reference and are off by at most 2^-31 of it below (fp32 rows: 23 bits down to
+// 2^-10, 2^-33 of it below).
 #include "attn_decode_tc.cuh"
 #include "kv4.cuh"
 
@@ -22,28 +25,29 @@ using namespace dt;
 
 namespace {
 
-// Weights stay below 2^16, so that the join, whose factors go by the pieces'
-// references, loses nothing above 2^-110 of the largest (2^-126 is fp32's end).
-constexpr float kGrow = 16.f;
-constexpr float kUnset = 3e38f;    // minus the reference of a row that has seen no key
-constexpr int kChunk = 64;         // tokens or channels of an operand: 32 columns of tensor memory
+// A weight at its row's reference is 2^BASE, and none passes 2^kTop (f16 ends at
+// 2^16); a token whose codes stand four bits up (kv4_halves) has 2^-4 of that.
+constexpr float kTop = 15.75f;
+constexpr float kCodes = 16777216.f;   // the outputs' products count in 2^-24
+constexpr float kUnset = 3e38f;        // the offset of a row that has seen no key
 
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
 
 // NT rows a tile, QP parts of Q and PP of P side by side as columns, SWG softmax
-// and UWG unpacking warpgroups, CTAS on an SM.
-template <typename T_, int NT_, int QP_, int PP_, int SWG_, int UWG_, int CTAS_>
+// and UWG unpacking warpgroups, operands of CH tokens or channels, CTAS on an SM.
+template <typename T_, int NT_, int QP_, int PP_, int SWG_, int UWG_, int CH_, int CTAS_>
 struct D4Cfg {
   using T = T_;
-  static constexpr int NT = NT_, QP = QP_, PP = PP_, SWG = SWG_, UWG = UWG_, CTAS = CTAS_;
+  static constexpr int NT = NT_, QP = QP_, PP = PP_, SWG = SWG_, UWG = UWG_, CH = CH_, CTAS = CTAS_;
+  static constexpr float BASE = sizeof(T) == 2 ? 10.f : 12.f;
   static constexpr int CW = NT / SWG;                      // columns (rows) of a softmax warpgroup
   static constexpr int NQ = round16(NT * QP), NP = round16(NT * PP);
   static constexpr int SOFT = 128 * SWG, UNPACK = 128 * UWG;
   static constexpr int THREADS = SOFT + UNPACK + (CTAS == 1 ? 128 : 96);   // and K loads, V loads, products
   static constexpr uint32_t COLS = CTAS == 1 ? 512 : 256;
   static constexpr uint32_t O0 = 2 * NQ, R0 = O0 + 2 * NP; // tensor memory: scores of two tiles, O of 128 elements each, operands
-  static constexpr int RING = (COLS - R0) / (kChunk / 2);
-  static_assert(RING >= 3 && NT % SWG == 0 && CW % 8 == 0, "tensor memory");
+  static constexpr int SLOT = CH / 2, RING = (COLS - R0) / SLOT;   // columns of an operand, operands
+  static_assert(RING >= 2 && RING <= 8 && NT % SWG == 0 && CW % 8 == 0, "tensor memory");
 };
 
 template <typename C>
@@ -53,7 +57,7 @@ struct D4Shared : DtItems {
   uint32_t have[kDtMaxStages];    // blocks of a tile that were loaded, by V stage
   float4 lsum[C::NT];
   float cmax[4][C::NT];           // largest score of each column, by warp
-  float nref[C::NT], alpha[C::NT];
+  float off[C::NT], alpha[C::NT];   // what a row's exponents are moved by: BASE less its reference
   // of a head's rows, heads alternate: keys seen, place among the outputs
   int lim[2][C::NT];
   uint32_t out[2][C::NT];         // (row, head) counted from the item's first row's head 0
@@ -73,17 +77,22 @@ __device__ __forceinline__ bool soft_any(bool x) {
   return r != 0;
 }
 
-// 32-bit words of bf16 pairs: hi, and what it leaves, PARTS times.
-template <int PARTS>
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&w)[PARTS]) {
+// 32-bit words of pairs (f16, or bf16): a rounding, and what it leaves, PARTS times.
+template <int PARTS, bool BF16>
+__device__ __forceinline__ void split_pairs(float a, float b, uint32_t (&w)[PARTS]) {
 #pragma unroll
   for (int i = 0; i < PARTS; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    if (i + 1 < PARTS) {
-      const float2 r = unpack2(sub2(pack2(a, b), pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u))));
-      a = r.x, b = r.y;
+    float2 back;
+    if constexpr (BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      back = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+      const __half2 h = __floats2half2_rn(a, b);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      back = __half22float2(h);
     }
+    a -= back.x, b -= back.y;
   }
 }
 
@@ -135,6 +144,11 @@ __device__ __forceinline__ void sums16(const float* l, float4* out, int n, int l
   }
   v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
   if ((lane & 1) == 0 && at < n) (&out[at].x)[quad] = v[0];
+}
+
+// Instruction descriptor: f16 A and B, fp32 sums, M = 128.
+__host__ __device__ constexpr uint32_t idesc_f16(int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kDtTok >> 4) << 24);
 }
 
 // A warp's loads of the CTA's items [i0, i1), K's codes and scales or V's: lane b
@@ -203,13 +217,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
   D4Shared<C>& sh = *reinterpret_cast<D4Shared<C>*>(base + w.misc_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d, quad = warp & 3;
   const int KS = w.k_stages, VS = w.v_stages;
-  const int nk = (d + kChunk - 1) / kChunk, halves = (d + 127) / 128;   // operands of K and of V (halves x 2 of 64 tokens) a tile
+  constexpr int CH = C::CH, VC = 128 / CH;
+  const int nk = (d + CH - 1) / CH, halves = (d + 127) / 128;   // operands of K, and of V (VC for each half), a tile
   volatile int* fail = &sh.fail;
   const long long limit = w.wait;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < KS; ++i) tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], 4 * nk);
-    for (int i = 0; i < VS; ++i) tc::mbar_init(&sh.v_full[i], 1), tc::mbar_init(&sh.v_empty[i], 8 * halves + SW);
+    for (int i = 0; i < KS; ++i) tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], UW);
+    for (int i = 0; i < VS; ++i) tc::mbar_init(&sh.v_full[i], 1), tc::mbar_init(&sh.v_empty[i], UW + SW);
     for (int i = 0; i < C::RING; ++i) tc::mbar_init(&sh.a_full[i], 4), tc::mbar_init(&sh.a_empty[i], 1);
     for (int i = 0; i < 2; ++i)
       tc::mbar_init(&sh.s_full[i], 1), tc::mbar_init(&sh.p_full[i], C::SOFT), tc::mbar_init(&sh.o_done[i], 1);
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       // ---- products: the whole warp, one lane issues ----
       const uint32_t lead = tc::elect_one();
       auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-      constexpr uint32_t id_qk = tc::idesc_bf16_f32(128, C::NQ), id_pv = tc::idesc_bf16_f32(128, C::NP) | kTransposedB;
+      constexpr uint32_t id_qk = tc::idesc_bf16_f32(128, C::NQ), id_pv = idesc_f16(C::NP) | kTransposedB;
       const uint64_t qd = desc_tiles(smem_u32(base + w.q_off), 128, 16u * d);
       // P: tokens of 8 columns (16 B), the next 8 columns a block of 128 tokens further
       const uint64_t pd = desc_tiles(smem_u32(base + w.p_off), 128, 16 * kDtTok);
@@ -253,10 +268,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       auto operand = [&](uint32_t dst, uint64_t b, uint32_t id, int steps, bool acc) {
         if (!all(dt_wait(&sh.a_full[r], rp, fail, limit))) return false;
         tc::fence_after_sync();
-        const uint32_t a = tb + C::R0 + r * (kChunk / 2);
-        if (steps == 4) {
+        const uint32_t a = tb + C::R0 + r * C::SLOT;
+        if (steps == CH / 16) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tc::mma_bf16_ts_if(lead, dst, a + 8 * k, b + 16 * k, id, acc || k != 0);
+          for (int k = 0; k < CH / 16; ++k) tc::mma_bf16_ts_if(lead, dst, a + 8 * k, b + 16 * k, id, acc || k != 0);
         } else {
           for (int k = 0; k < steps; ++k) tc::mma_bf16_ts_if(lead, dst, a + 8 * k, b + 16 * k, id, acc || k != 0);
         }
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       };
       auto qk = [&](unsigned tt) {
         for (int c = 0; c < nk; ++c)
-          if (!operand(tb + (tt & 1) * C::NQ, qd + c * 64, id_qk, min(4, (d - c * kChunk) / 16), c != 0)) return false;
+          if (!operand(tb + (tt & 1) * C::NQ, qd + c * CH, id_qk, min(CH, d - c * CH) / 16, c != 0)) return false;
         tc::mma_commit_if(lead, &sh.s_full[tt & 1]);
         return true;
       };
@@ -282,9 +297,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail, limit));
           if (!ok) break;
           tc::fence_after_sync();
-          for (int c = 0; ok && c < 2; ++c)
+          for (int c = 0; ok && c < VC; ++c)
             for (int hf = 0; ok && hf < halves; ++hf)
-              ok = operand(tb + C::O0 + hf * C::NP, pd + (T & 1) * (C::NP * kDtTok * 2 / 16) + c * 64, id_pv, 4, j != 0 || c != 0);
+              ok = operand(tb + C::O0 + hf * C::NP, pd + (T & 1) * (C::NP * kDtTok * 2 / 16) + c * CH, id_pv, CH / 16, j != 0 || c != 0);
           tc::mma_commit_if(lead, &sh.o_done[T & 1]);
         }
       }
@@ -330,58 +345,57 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           const uint8_t* sc = kr + (uint32_t)ks * k_unit + kDtBlocks * codes + (row >> 4) * kv4_k_scales(d) + (row & 15);
           for (int c = 0; ok && c < nk; ++c, next()) {
             if (!mine()) continue;
-            const int groups = min(2, (d - c * kChunk) / kKv4Group);
-            uint4 x[2];
-            uint32_t s[2];
+            const int groups = min(CH, d - c * CH) / kKv4Group;
+            uint4 x[CH / 32];
+            uint32_t s[CH / 32];
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
-              if (g < groups) x[g] = *reinterpret_cast<const uint4*>(blk + (2 * c + g) * 256), s[g] = sc[(2 * c + g) * 16];
-            __syncwarp();
-            if (lane == 0) dt_arrive(&sh.k_empty[ks]);
+            for (int g = 0; g < CH / 32; ++g)
+              if (g < groups) x[g] = *reinterpret_cast<const uint4*>(blk + (c * (CH / 32) + g) * 256), s[g] = sc[(c * (CH / 32) + g) * 16];
             ok = free_wait();
             if (!ok) break;
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+            for (int g = 0; g < CH / 32; ++g)
               if (g < groups) {
                 const uint32_t s1 = kv4_scale_bf16(s[g]), s2 = s1 << 16 | s1, off = kv4_offset(s2);
                 uint32_t y[16];
 #pragma unroll
                 for (int u = 0; u < 16; ++u) y[u] = kv4_fma(kv4_pair((&x[g].x)[u >> 2] >> (4 * (u & 3))), s2, off);
-                tc::tmem_st16u(lanes + r * (kChunk / 2) + g * 16, y);
+                tc::tmem_st16u(lanes + r * C::SLOT + g * 16, y);
               }
             done();
           }
+          __syncwarp();
+          if (lane == 0) dt_arrive(&sh.k_empty[ks]);
           if (++ks == KS) ks = 0, kp ^= 1;
         }
         if (ok && j > 0) {
           ok = __all_sync(0xffffffffu, dt_wait(&sh.v_full[vs], vp, fail, limit));
           const uint8_t* blk = vr + (uint32_t)vs * v_unit + row * 8;
-          for (int c = 0; ok && c < 2; ++c)
+          for (int c = 0; ok && c < VC; ++c)
             for (int hf = 0; ok && hf < halves; ++hf, next()) {
               if (!mine()) continue;
               const bool live = hf * 128 + quad * 32 < d;   // (channels past the head's: rows of O that no one reads)
-              uint2 x[4];
+              uint2 x[CH / 16];
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (live) x[b] = *reinterpret_cast<const uint2*>(blk + (4 * c + b) * codes + hf * 1024);
-              __syncwarp();
-              if (lane == 0) dt_arrive(&sh.v_empty[vs]);
+              for (int b = 0; b < CH / 16; ++b)
+                if (live) x[b] = *reinterpret_cast<const uint2*>(blk + (c * (CH / 16) + b) * codes + hf * 1024);
               ok = free_wait();
               if (!ok) break;
               if (live) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                  uint32_t y[16];
+                for (int g = 0; g < CH / 32; ++g) {
+                  uint32_t y[4][4], z[16];
 #pragma unroll
-                  for (int u = 0; u < 16; ++u) {
-                    const uint2& q = x[2 * g + (u >> 3)];
-                    y[u] = kv4_fma(kv4_pair((u & 4 ? q.y : q.x) >> (4 * (u & 3))), 0x3f803f80u, 0xc308c308u);   // n - 8
-                  }
-                  tc::tmem_st16u(lanes + r * (kChunk / 2) + g * 16, y);
+                  for (int u = 0; u < 4; ++u) kv4_halves(u & 1 ? x[2 * g + (u >> 1)].y : x[2 * g + (u >> 1)].x, y[u]);
+#pragma unroll
+                  for (int u = 0; u < 16; ++u) z[u] = y[u >> 2][u & 3];
+                  tc::tmem_st16u(lanes + r * C::SLOT + g * 16, z);
                 }
               }
               done();
             }
+          __syncwarp();
+          if (lane == 0) dt_arrive(&sh.v_empty[vs]);
           if (++vs == VS) vs = 0, vp ^= 1;
         }
       }
@@ -431,7 +445,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint4& f = x[u][k >> 1];
-              split_bf16<C::QP>(__uint_as_float(k & 1 ? f.z : f.x), __uint_as_float(k & 1 ? f.w : f.y), part[k]);
+              split_pairs<C::QP, true>(__uint_as_float(k & 1 ? f.z : f.x), __uint_as_float(k & 1 ? f.w : f.y), part[k]);
             }
 #pragma unroll
             for (int v = 0; v < C::QP; ++v) *at(v * NT + n) = make_uint4(part[0][v], part[1][v], part[2][v], part[3][v]);
@@ -445,7 +459,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
     unsigned T = 0;
     int st = 0, vp = 0, par = 0;   // V stage and its phase; head
     DtItem t{};
-    if (threadIdx.x < NT) sh.nref[threadIdx.x] = kUnset;
+    if (threadIdx.x < NT) sh.off[threadIdx.x] = kUnset;
     if (i0 < i1) {
       t = dt_item<NT>(w, sh.items, i0);
       load_q(t, 0);
@@ -464,43 +478,45 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         tc::fence_after_sync();
         const float vscale = kv4_scale((base + w.v_off + (uint32_t)st * v_unit + kDtBlocks * codes)[tid]);
         const bool valid = pos < t.k1 && (sh.have[st] >> (tid >> 4) & 1);
+        // of this token: the exponent of its V scale, and what undoes it in the sums of
+        // weights (a NaN scale makes weights NaN; masked ones stay 0)
+        const float lv = __log2f(vscale) - (tid & 2 ? 4.f : 0.f);
+        const float rv = vscale == vscale ? __fdividef(tid & 2 ? 16.f : 1.f, vscale) : 1.f;
         __syncwarp();
         if (lane == 0) dt_arrive(&sh.v_empty[st]);
         const bool part = !__all_sync(0xffffffffu, valid), edge = kb + kDtTok > least;   // some row does not see some token
         float x[CW];
-        auto scores = [&]() {
+        // s + log2(vs) + off, where off is the rows' offsets or nothing; masked -inf
+        auto scores = [&](bool against) {
           read_columns<CW, NT, C::QP>(scol, x);
+          const float4* r4 = reinterpret_cast<const float4*>(&sh.off[c0]);
+          const f32x2 cc = pack2(cs, cs), ll = pack2(lv, lv);
+#pragma unroll
+          for (int k = 0; k < CW; k += 4) {
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (against) r = r4[k / 4];
+            const float2 a = unpack2(fma2(pack2(x[k], x[k + 1]), cc, add2(pack2(r.x, r.y), ll)));
+            const float2 b = unpack2(fma2(pack2(x[k + 2], x[k + 3]), cc, add2(pack2(r.z, r.w), ll)));
+            x[k] = a.x, x[k + 1] = a.y, x[k + 2] = b.x, x[k + 3] = b.y;
+          }
           if (part || edge) {
 #pragma unroll
             for (int k = 0; k < CW; ++k)
               if (!valid || pos >= sh.lim[par][c0 + k]) x[k] = -INFINITY;
           }
         };
-        // exponents of the weights against the rows' references
-        auto exponents = [&]() {
-          const float4* r4 = reinterpret_cast<const float4*>(&sh.nref[c0]);
-          const f32x2 cc = pack2(cs, cs);
-#pragma unroll
-          for (int k = 0; k < CW; k += 4) {
-            const float4 r = r4[k / 4];
-            const float2 a = unpack2(fma2(pack2(x[k], x[k + 1]), cc, pack2(r.x, r.y)));
-            const float2 b = unpack2(fma2(pack2(x[k + 2], x[k + 3]), cc, pack2(r.z, r.w)));
-            x[k] = a.x, x[k + 1] = a.y, x[k + 2] = b.x, x[k + 3] = b.y;
-          }
-        };
-        scores();
-        exponents();
+        scores(true);
         float top = x[0];
 #pragma unroll
         for (int k = 1; k < CW; ++k) top = fmaxf(top, x[k]);
-        if (soft_any<C::SOFT>(top > kGrow || !ok)) {
+        if (soft_any<C::SOFT>(top > kTop || !ok)) {
           // a row's first keys, or one far above its reference (or a wait that ran
           // out): a row's reference moves by that row's scores alone
-          scores();
+          scores(false);
 #pragma unroll
           for (int k = 0; k < CW; k += 4) {
             const float a = warp_max(x[k]), b = warp_max(x[k + 1]), c = warp_max(x[k + 2]), e = warp_max(x[k + 3]);
-            if (lane == 0) *reinterpret_cast<float4*>(&sh.cmax[quad][c0 + k]) = make_float4(a * cs, b * cs, c * cs, e * cs);
+            if (lane == 0) *reinterpret_cast<float4*>(&sh.cmax[quad][c0 + k]) = make_float4(a, b, c, e);
           }
           // the products before this tile's are done with O
           if (j > 0) ok = ok && dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit);
@@ -508,13 +524,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           if (tid < CW) {
             const int n = c0 + tid;
             const float mx = fmaxf(fmaxf(sh.cmax[0][n], sh.cmax[1][n]), fmaxf(sh.cmax[2][n], sh.cmax[3][n]));
-            const float nref = sh.nref[n];
+            const float off = sh.off[n];
             float alpha = 1.f;
-            if (nref == kUnset) {
-              if (mx > -INFINITY) sh.nref[n] = -mx;
-            } else if (mx + nref > kGrow) {
-              alpha = dt_ex2(-nref - mx);
-              sh.nref[n] = -mx;
+            if (off == kUnset) {
+              if (mx > -INFINITY) sh.off[n] = C::BASE - mx;
+            } else if (mx + off > kTop) {
+              alpha = dt_ex2(C::BASE - mx - off);
+              sh.off[n] = C::BASE - mx;
             }
             sh.alpha[n] = alpha;
           }
@@ -539,13 +555,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
             }
             tc::tmem_st_wait();
           }
-          exponents();
+          scores(true);
         }
-        // the weights: their sums as they are, their products' parts times V's
-        // scale (the products of two tiles ago, which read this place, were done
+        // the weights (the products of two tiles ago, which read this place, were done
         // before this tile's scores)
         uint8_t* pw = ps + (T & 1) * (C::NP * kDtTok * 2) + tid * 16;
-        const f32x2 vv = pack2(valid ? vscale : 0.f, valid ? vscale : 0.f);
+        const f32x2 rr = pack2(rv, rv);
 #pragma unroll
         for (int k = 0; k < CW; k += 8) {
           uint32_t word[4][C::PP];
@@ -553,14 +568,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           for (int u = 0; u < 4; ++u) {
             const int n = k + 2 * u;
             const float a = dt_ex2(x[n]), b = dt_ex2(x[n + 1]);
-            const f32x2 e = pack2(a, b);
-            l[n] += a, l[n + 1] += b;
-            float2 q = unpack2(mul2(e, vv));
-            if (edge) {   // a NaN scale keeps to the rows that see its token
-              if (pos >= sh.lim[par][c0 + n]) q.x = 0.f;
-              if (pos >= sh.lim[par][c0 + n + 1]) q.y = 0.f;
-            }
-            split_bf16<C::PP>(q.x, q.y, word[u]);
+            const float2 sum = unpack2(fma2(pack2(a, b), rr, pack2(l[n], l[n + 1])));
+            l[n] = sum.x, l[n + 1] = sum.y;
+            split_pairs<C::PP, false>(a, b, word[u]);
           }
 #pragma unroll
           for (int v = 0; v < C::PP; ++v)
@@ -594,7 +604,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       };
       if (tid < rows) {
         const int n = c0 + tid;
-        const float sum = u.tiles > 0 ? total(n) : 0.f, m = sum == 0.f ? -INFINITY : -sh.nref[n];
+        const float sum = u.tiles > 0 ? total(n) : 0.f, m = sum == 0.f ? -INFINITY : -sh.off[n];
         const int64_t rh = rh0 + sh.out[was][n];
         if (p.part_o) p.part_ml[u.piece * R + rh] = make_float2(m, sum);
         else if (p.lse) p.lse[rh] = sum == 0.f ? -INFINITY : m * 0.693147180559945309f + logf(sum);
@@ -620,10 +630,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
               if (k0 + k < rows) {
                 const uint32_t at = sh.out[was][c0 + k0 + k] * (uint32_t)d;   // at most 32 rows of 1,024 heads of 256 elements
                 if (p.part_o) {
-                  po[at] = o[k];
+                  po[at] = o[k] * kCodes;
                 } else {
                   const float sum = u.tiles > 0 ? total(c0 + k0 + k) : 0.f;
-                  oo[at] = from_f32<E>(sum == 0.f ? 0.f : o[k] / sum);
+                  oo[at] = from_f32<E>(sum == 0.f ? 0.f : o[k] * kCodes / sum);
                 }
               }
             }
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       }
       tc::fence_before_sync();
       soft_any<C::SOFT>(false);   // lsum, references and O are free
-      if (threadIdx.x < NT) sh.nref[threadIdx.x] = kUnset;
+      if (threadIdx.x < NT) sh.off[threadIdx.x] = kUnset;
       soft_any<C::SOFT>(false);
     }
   }
@@ -691,10 +701,10 @@ cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, int hi, cudaStre
   return cudaSuccess;
 }
 
-using Few8 = D4Cfg<__nv_bfloat16, 8, 1, 2, 1, 1, 2>;
-using Few16 = D4Cfg<__nv_bfloat16, 16, 1, 2, 1, 1, 2>;
-using Many = D4Cfg<__nv_bfloat16, 96, 1, 1, 2, 2, 1>;
-using Full8 = D4Cfg<float, 8, 3, 3, 1, 1, 2>;
+using Few8 = D4Cfg<__nv_bfloat16, 8, 1, 1, 1, 1, 128, 2>;
+using Few16 = D4Cfg<__nv_bfloat16, 16, 1, 1, 1, 1, 128, 2>;
+using Many = D4Cfg<__nv_bfloat16, 96, 1, 1, 2, 2, 64, 1>;
+using Full8 = D4Cfg<float, 8, 3, 2, 1, 1, 128, 2>;
 
 }  // namespace
 

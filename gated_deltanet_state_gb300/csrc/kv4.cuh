@@ -56,8 +56,13 @@ __device__ __forceinline__ uint32_t kv4_byte(uint32_t amax_bits) {
 }
 
 // Two neighbouring elements of a word of eight, already shifted to bits 0 .. 3 and
-// 16 .. 19, as bf16 of 128 + n: the codes become the mantissas' last bits.
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
+// 16 .. 19, as bf16 of 128 + n: the codes become the mantissas' last bits.  (One
+// instruction, where the compiler makes two of (w & a) | b with constants.)
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(0x000f000fu), "r"(0x43004300u));
+  return r;
+}
 // (128 + n) s - 136 s = (n - 8) s: exact, since 136 s has 17 times s's 4 bits,
 // 8 at most, and the product is not rounded on its way.
 __device__ __forceinline__ uint32_t kv4_fma(uint32_t a, uint32_t s, uint32_t c) {
@@ -70,6 +75,20 @@ __device__ __forceinline__ uint32_t kv4_offset(uint32_t s) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(s), "r"(0xc308c308u));
   return r;
+}
+
+// The eight elements of a word in f16, where a code is a subnormal's last bits:
+// pairs 0 and 2 as (n - 8) 2^-24, pairs 1 and 3, whose codes stay four bits
+// further up, as (n - 8) 2^-20 (exact: whole multiples of 2^-24).
+__device__ __forceinline__ uint32_t kv4_half(uint32_t masked, uint32_t eight) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(masked), "r"(eight));
+  return r;
+}
+__device__ __forceinline__ void kv4_halves(uint32_t w, uint32_t (&y)[4]) {
+  const uint32_t v = w >> 8;
+  y[0] = kv4_half(w & 0x000f000fu, 0x80088008u), y[1] = kv4_half(w & 0x00f000f0u, 0x80808080u);
+  y[2] = kv4_half(v & 0x000f000fu, 0x80088008u), y[3] = kv4_half(v & 0x00f000f0u, 0x80808080u);
 }
 
 }  // namespace gdn
