@@ -23,7 +23,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v"]
 CU_SOURCES = ["api.cu", "prefill.cu", "replay.cu", "decode.cu", "checkpoint.cu", "noalloc.cu", "tc_replay.cu", "tc_prefill.cu", "tc_chain.cu",
-              "kv_cache.cu", "kv4_cache.cu", "attn_simt.cu", "attn_prefill_tc.cu", "attn_decode_tc.cu", "attn_draft_tc.cu", "attn_decode4_tc.cu",
+              "kv_cache.cu", "kv4_cache.cu", "attn_simt.cu", "attn_prefill_tc.cu", "attn_decode_tc.cu", "attn_draft_tc.cu", "attn_decode4_tc.cu", "attn_decode4_few.cu",
               "attn_api.cu"]
 C_SOURCES = ["gdn_host.c"]
 

@@ -1,0 +1,518 @@
+// attn_decode4_few.cu — attention over the 4-bit cache of up to 8 (row, head of
+// the group) pairs a kv head, bf16 rows: a decode step.
+//
+// With so few rows the products are small and what decides is the way of the
+// codes into them: 65,536 of a 128-token tile at d = 256, for which the memory
+// takes 1,500 cycles an SM.  They go from shared memory into registers and, as
+// operands of warp-wide products, nowhere else.  (By way of tensor memory, where
+// the larger products take their operands from, the same step costs stores,
+// hand-overs and waits on top: 256 sequences of 1,024 to 8,192 tokens, 24 heads, 4
+// kv heads, d = 256, 425 us.)
+//
+//   S^T [16 tokens x 8 rows] = K Q^T,    O^T [16 channels x 8 rows] += V^T P^T
+//
+// Codes are f16 subnormals as they stand: four of a word's eight after one mask,
+// n 2^-24 (pairs 0 and 2) or n 2^-20 (pairs 1 and 3, whose partners in Q and P
+// carry 2^-4).  K's offset of 8 is in the products' start value, -8 sum(q) of a
+// group of 32 channels; a group's product is its own and is added under its
+// tokens' scales in fp32.  V's is taken off in f16 (exact).  Which token or channel
+// stands in which row or step of a product is chosen so that a lane's word is its
+// operand: a lane holds eight channels of K, or eight tokens of V.
+//
+// Q is scaled by a power of two for each row: 8 bits of elements down to 2^-27 of
+// the largest, off by 2^-35 of it at most below.  A weight times its V scale is an
+// f16 against a reference of its row that is the first chunk's maximum and moves
+// only when a weight would pass f16's range: 11 bits down to 2^-20 of it, off by
+// 2^-31 at most below.
+//
+// A warp takes every fourth chunk of 32 tokens of a piece, with statistics and
+// sums of its own, which the four bring together in a fixed order at its end; it
+// waits for nothing but its chunk.
+#include "attn_decode_tc.cuh"
+#include "kv4.cuh"
+
+namespace gdn {
+
+using namespace dt;
+
+namespace {
+
+constexpr int kFewRows = 8, kFewWarps = 4, kFewThreads = 32 * (kFewWarps + 1);   // and the loads' warp
+constexpr int kFewTok = 32, kFewBlocks = kFewTok / kKvBlock;                     // of a chunk
+constexpr int kFewStages = 8;
+constexpr float kFewBase = 10.f, kFewTop = 15.75f;   // a weight at its reference is 2^10, none passes 2^15.75
+constexpr float kFewUnset = 3e38f;                   // the offset of a row that has seen no key
+constexpr float kFewUnit = 16777216.f;               // the products count in 2^-24
+
+// A chunk in shared memory: blocks further apart than they are long, so that the
+// lanes of two blocks do not meet in a bank.
+struct FewStage {
+  uint32_t kp, ksp, v, vp, vs, bytes;   // pitch of K's codes and scales, V's codes from here, their pitch, V's scales
+};
+__host__ __device__ inline FewStage few_stage(int d) {
+  FewStage s;
+  s.kp = kv4_codes(d) + 64, s.ksp = kv4_k_scales(d) + 16;
+  s.v = kFewBlocks * (s.kp + s.ksp), s.vp = kv4_codes(d) + 64;
+  s.vs = s.v + kFewBlocks * s.vp;
+  s.bytes = (s.vs + kFewBlocks * kKvBlock + 127) / 128 * 128;
+  return s;
+}
+
+struct FewShared : DtItems {
+  uint64_t full[kFewStages], empty[kFewStages];
+  uint32_t have[kFewStages];            // blocks of a chunk that were loaded
+  float2 stat[kFewWarps][kFewRows];     // a warp's offset and sum of each row
+  uint4 q[8][32];                       // Q of row g, eight channels of a group, by lane
+  float2 start[8][4];                   // a group's start value for rows 2 t, 2 t + 1
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+// D = A B + C: 16 x 16 by 16 x 8 in f16, fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                        float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ float few_log2(float x) {   // (normal numbers and NaN)
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Largest and sum over the lanes of a column (every fourth lane).
+__device__ __forceinline__ float column_max(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float column_sum(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// Barrier of the four warps, with a vote.
+__device__ __forceinline__ bool few_any(bool x) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
+      " selp.s32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((int)x)
+      : "memory");
+  __syncwarp();
+  return r != 0;
+}
+
+// The loads of the CTA's items [i0, i1), four chunks at a time: lane 8 x + b has
+// part x (K's codes and scales, V's) of their block b.  Returns the chunks loaded.
+__device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_t* base, int i0, int i1, int lane) {
+  const AttnDecodeParams& p = w.a;
+  volatile int* fail = &sh.fail;
+  const int ST = w.k_stages, d = p.c.d, part = lane >> 3, blk = lane & 7, in_chunk = blk & 1;
+  const FewStage sg = few_stage(d);
+  const uint32_t codes = kv4_codes(d), scales = kv4_k_scales(d), each = 2 * codes + scales + kKvBlock;
+  const uint32_t to = part == 0   ? in_chunk * sg.kp
+                      : part == 1 ? kFewBlocks * sg.kp + in_chunk * sg.ksp
+                      : part == 2 ? sg.v + in_chunk * sg.vp
+                                  : sg.vs + in_chunk * kKvBlock;
+  const uint32_t size = part == 1 ? scales : part == 3 ? kKvBlock : codes;
+  int loaded = 0, st = 0, ph = 0;
+  bool ok = true;
+  DtItem t{};
+  for (int i = i0; ok && i < i1; ++i) {
+    if (i == i0) t = dt_item<kFewRows>(w, sh.items, i);
+    else dt_next<kFewRows>(w, sh.items, i, t);
+    const int32_t* bt = p.block_table + (int64_t)t.s * p.max_pages;
+    int at = 0, next_at = 0, next = -1;
+    auto look = [&](int j) {   // of the four chunks from j
+      const int pos = t.k0 + j * kFewTok + blk * kKvBlock;
+      next_at = pos / p.c.page_tokens;
+      next = pos < t.k1 && next_at < p.max_pages ? bt[next_at] : -1;
+    };
+    const int chunks = (t.k1 - t.k0 + kFewTok - 1) / kFewTok;
+    if (chunks > 0) look(0);
+    for (int j = 0; ok && j < chunks; j += 4) {
+      const int page = next, pos = t.k0 + j * kFewTok + blk * kKvBlock;
+      at = next_at;
+      if (j + 4 < chunks) look(j + 4);
+      const bool in = pos < t.k1, good = in && page >= 0 && page < p.c.num_pages;
+      if (in && !good && part == 0) set_error(p.err, GDN_ERR_PAGE_RANGE);
+      const unsigned have = __ballot_sync(0xffffffffu, good);
+      const int b = (pos - at * p.c.page_tokens) / kKvBlock;
+      const uint8_t* from = nullptr;
+      if (good)
+        from = part == 0   ? kv4_k_block(p.c, page, t.h, b)
+               : part == 1 ? kv4_k_scale(p.c, page, t.h, b)
+               : part == 2 ? kv4_v_block(p.c, page, t.h, b)
+                           : kv4_v_scale(p.c, page, t.h, b);
+      const int n = min(4, chunks - j);
+      for (int c = 0; c < n; ++c) {
+        if (loaded >= ST) ok = dt_wait(&sh.empty[st], ph ^ 1, fail, w.wait);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (lane == 0) {
+          const unsigned two = have >> (2 * c) & 3u;
+          sh.have[st] = two;
+          tc::mbar_expect_tx(&sh.full[st], __popc(two) * each);
+        }
+        __syncwarp();
+        if (good && blk >> 1 == c) tc::bulk_load(base + (uint32_t)st * sg.bytes + to, from, size, &sh.full[st]);
+        ++loaded;
+        if (++st == ST) st = 0, ph ^= 1;
+      }
+    }
+  }
+  return loaded;
+}
+
+}  // namespace
+
+// GR: groups of 32 channels (d up to 32 GR).
+template <int GR>
+__global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const DtParams w) {
+  extern __shared__ uint8_t dyn[];
+  const AttnDecodeParams& p = w.a;
+  uint8_t* base = dyn + ((128u - (smem_u32(dyn) & 127u)) & 127u);
+  FewShared& sh = *reinterpret_cast<FewShared*>(base + w.misc_off);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d;
+  const int ST = w.k_stages;
+  volatile int* fail = &sh.fail;
+  const long long limit = w.wait;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], 1);
+    sh.fail = limit < 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 0) dt_sums<kFewRows>(w, sh, lane);
+  __syncthreads();
+  // this CTA's run of items
+  const int i0 = dt_first<kFewRows>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
+  const int last_item = dt_first<kFewRows>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int i1 = limit < 0 ? i0 : last_item;
+  int loaded = 0;   // chunks (the loading warp's)
+
+  if (warp == kFewWarps) {
+    loaded = few_load(w, sh, base, i0, i1, lane);
+  } else {
+    const FewStage sg = few_stage(d);
+    const int g = lane >> 2, t = lane & 3, groups = d / kKv4Group;
+    const uint32_t ring = smem_u32(base);
+    // a lane's places in a chunk: the row of K's matrices that it points at, its
+    // tokens' scales (word g / 2 of the four, tokens 4 s + g % 2 and two further), its words of V
+    const int mr = lane & 7, mi = lane >> 3;
+    const uint32_t at_k = (mr >> 2) * sg.kp + ((mr >> 1 & 1) * 8 + (mi >> 1) * 4 + (mi & 1) * 2 + (mr & 1)) * 16;
+    const int tok = (g >> 1 & 1) * 8 + (g & 1);
+    const uint32_t at_ks = kFewBlocks * sg.kp + (g >> 2) * sg.ksp + tok;
+    const uint32_t at_v = sg.v + (t >> 1) * sg.vp + g * 8 + (t & 1) * 4, at_vs = sg.vs + (g >> 2) * kKvBlock + tok;
+    const uint32_t at_nan = kFewBlocks * sg.kp + lane / groups * sg.ksp + lane % groups * 16;   // 16 of K's scales
+    float4* red = reinterpret_cast<float4*>(base + w.p_off);   // [4 warps][4 tiles][32]
+    float cs[2] = {};      // factors of the scores of rows 2 t, 2 t + 1 ...
+    int lim[2] = {};       // ... and the keys that they see
+    bool ok = true;
+    unsigned before = 0;   // chunks of the items before
+    DtItem u{};
+    for (int i = i0; i < i1; ++i) {
+      if (i == i0) u = dt_item<kFewRows>(w, sh.items, i);
+      else dt_next<kFewRows>(w, sh.items, i, u);
+      if (dt_new_rows(u, i == i0)) {
+        uint4 x[GR];
+        float amax = 0.f;
+        const int row = g / p.G, head = g - row * p.G;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(u.q0 + row) * p.q_stride +
+                                   (int64_t)(u.h * p.G + head) * d + t * 8;
+#pragma unroll
+        for (int c = 0; c < GR; ++c)
+          x[c] = g < u.rows && c < groups ? *reinterpret_cast<const uint4*>(src + c * kKv4Group) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < GR; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t v = (&x[c].x)[k];
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xffff0000u))));
+          }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // the largest element to [2^13, 2^14)
+        const int e = max(-100, min(100, (int)(__float_as_uint(amax) >> 23) - 127 - 13));
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < GR; ++c) {
+          float sum = 0.f;
+          uint4 q;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t v = (&x[c].x)[k];
+            const float s = k & 1 ? inv * 0.0625f : inv;   // codes of pairs 1 and 3 stand four bits up
+            const uint32_t b = half2_bits(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
+            sum = fmaf(f.x + f.y, k & 1 ? 16.f : 1.f, sum);
+            (&q.x)[k] = b;
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          sum *= -8.f / kFewUnit;
+          if (c % kFewWarps == warp) {   // (every warp has them all)
+            sh.q[c][lane] = q;
+            if (t == 0) (&sh.start[c][g >> 1].x)[g & 1] = sum;
+          }
+        }
+        // (an infinite element makes its row's scores NaN)
+        const float f = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * kFewUnit : __int_as_float(0x7fffffff);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          cs[k] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * k);
+          lim[k] = u.L - u.n + (2 * t + k) / p.G + 1;
+        }
+        few_any(false);
+      }
+      float o[2 * GR][4], l[2] = {0.f, 0.f}, off[2] = {kFewUnset, kFewUnset};
+#pragma unroll
+      for (int c = 0; c < 2 * GR; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[c][k] = 0.f;
+      const int chunks = (u.k1 - u.k0 + kFewTok - 1) / kFewTok, least = u.L - u.n + 1;   // keys that every row sees
+#pragma unroll 1
+      for (int c0 = warp; ok && c0 < chunks; c0 += kFewWarps) {
+        const unsigned nth = before + c0, st = nth % (unsigned)ST;
+        ok = __all_sync(0xffffffffu, dt_wait(&sh.full[st], nth / (unsigned)ST & 1, fail, limit));
+        if (!ok) break;
+        const uint32_t stage = ring + st * sg.bytes;
+        const int kb = u.k0 + c0 * kFewTok;
+        // ---- scores: 16 tokens at a time, four of each word ----
+        float x[2][4] = {};   // of step s: tokens A (rows 2 t, 2 t + 1), B
+#pragma unroll 2
+        for (int c = 0; c < groups; ++c) {
+          const uint4 q = sh.q[c][lane];
+          const float2 start = sh.start[c][t];
+          uint32_t m[4];
+          ldsm4(stage + at_k + c * 256, m);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const uint32_t a = m[2 * s], b = m[2 * s + 1], a8 = a >> 8, b8 = b >> 8;
+            const uint32_t sa = lds8(stage + at_ks + c * 16 + 4 * s), sb = lds8(stage + at_ks + c * 16 + 4 * s + 2);
+            float y[4];
+            mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start.x, start.y, start.x, start.y);
+            mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w, y[0], y[1], y[2], y[3]);
+            const float fa = __uint_as_float(sa * (1u << 20) + (107u << 23)), fb = __uint_as_float(sb * (1u << 20) + (107u << 23));
+            x[s][0] = fmaf(y[0], fa, x[s][0]), x[s][1] = fmaf(y[1], fa, x[s][1]);
+            x[s][2] = fmaf(y[2], fb, x[s][2]), x[s][3] = fmaf(y[3], fb, x[s][3]);
+          }
+        }
+        // a NaN scale of K (255, above taken for a number) makes its token's scores NaN
+        uint4 some = make_uint4(0, 0, 0, 0);
+        if (lane < kFewBlocks * groups) some = *reinterpret_cast<const uint4*>(base + st * sg.bytes + at_nan);
+        auto full_byte = [](uint32_t v) { return (~v - 0x01010101u) & v & 0x80808080u; };
+        if (__any_sync(0xffffffffu, (full_byte(some.x) | full_byte(some.y) | full_byte(some.z) | full_byte(some.w)) != 0)) {
+          for (int c = 0; c < groups; ++c)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (lds8(stage + at_ks + c * 16 + 4 * s) == kKv4Nan) x[s][0] = x[s][1] = __int_as_float(0x7fffffff);
+              if (lds8(stage + at_ks + c * 16 + 4 * s + 2) == kKv4Nan) x[s][2] = x[s][3] = __int_as_float(0x7fffffff);
+            }
+        }
+        // ---- weights ----
+        const uint32_t have = sh.have[st];
+        const bool edge = have != (1u << kFewBlocks) - 1u || kb + kFewTok > u.k1 || kb + kFewTok > least;
+        const int pos = kb + (g >> 2) * kKvBlock + tok;
+        const bool here = have >> (g >> 2) & 1;
+        float rv[2][2];
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            // of tokens A and B: the exponent of the V scale, and what undoes it in the sums
+            // (a NaN scale makes weights NaN; masked ones stay 0)
+            const float vs = kv4_scale(lds8(stage + at_vs + 4 * s + 2 * k));
+            const float lv = few_log2(vs) - (k ? 4.f : 0.f);
+            rv[s][k] = dt_ex2(fmaxf(-lv, -100.f));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float& v = x[s][2 * k + h];
+              v = fmaf(v, cs[h], lv);
+              const int at = pos + 4 * s + 2 * k;
+              if (edge && (!here || at >= u.k1 || at >= lim[h])) v = -INFINITY;
+              top[h] = fmaxf(top[h], v);
+            }
+          }
+        if (__any_sync(0xffffffffu, top[0] + off[0] > kFewTop || top[1] + off[1] > kFewTop)) {
+          // a row's first keys, or one far above its reference
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mx = column_max(top[h]);
+            float alpha = 1.f;
+            if (off[h] == kFewUnset) {
+              if (mx > -INFINITY) off[h] = kFewBase - mx;
+            } else if (mx + off[h] > kFewTop) {
+              alpha = dt_ex2(kFewBase - mx - off[h]);
+              off[h] = kFewBase - mx;
+            }
+            l[h] *= alpha;
+#pragma unroll
+            for (int c = 0; c < 2 * GR; ++c) o[c][h] *= alpha, o[c][2 + h] *= alpha;
+          }
+        }
+        uint32_t pb[2][2];   // P: row g, tokens of word t
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float a = dt_ex2(x[s][2 * k] + off[0]), b = dt_ex2(x[s][2 * k + 1] + off[1]);
+            l[0] = fmaf(a, rv[s][k], l[0]), l[1] = fmaf(b, rv[s][k], l[1]);
+            pb[s][k] = transposed(half2_bits(a, b));
+          }
+        // ---- outputs: 16 channels at a time ----
+#pragma unroll
+        for (int c = 0; c < 2 * GR; ++c) {
+          if (c < 2 * groups) {
+            uint32_t ya[4], yb[4];
+            kv4_halves(lds32(stage + at_v + c * 128), ya);
+            kv4_halves(lds32(stage + at_v + c * 128 + 64), yb);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              mma_f16(o[c], ya[2 * s], yb[2 * s], ya[2 * s + 1], yb[2 * s + 1], pb[s][0], pb[s][1], o[c][0], o[c][1], o[c][2], o[c][3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) dt_arrive(&sh.empty[st]);
+      }
+      before += chunks;
+      // ---- the four warps' sums, brought to the largest reference and added in order ----
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] = column_sum(l[h]);
+        if (lane < 4) sh.stat[warp][2 * t + h] = make_float2(off[h], l[h]);
+      }
+      if (few_any(!ok)) { ok = false; break; }
+      const int64_t R = p.T * p.Hq;
+      float sum[2], mine[2];
+      int64_t rh[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = 2 * t + h;
+        float2 s[kFewWarps];
+        float least_off = kFewUnset;
+#pragma unroll
+        for (int v = 0; v < kFewWarps; ++v) s[v] = sh.stat[v][col], least_off = fminf(least_off, s[v].x);
+        sum[h] = 0.f;
+#pragma unroll
+        for (int v = 0; v < kFewWarps; ++v) {
+          const float f = dt_ex2(least_off - s[v].x);
+          sum[h] = fmaf(s[v].y, f, sum[h]);
+          if (v == warp) mine[h] = f * kFewUnit;
+        }
+        const int row = col / p.G;
+        rh[h] = (int64_t)(u.q0 + row) * p.Hq + u.h * p.G + col - row * p.G;
+        if (warp == 0 && g == 0 && col < u.rows) {
+          const float m = sum[h] == 0.f ? -INFINITY : -least_off;
+          if (p.part_o) p.part_ml[u.piece * R + rh[h]] = make_float2(m, sum[h]);
+          else if (p.lse) p.lse[rh[h]] = sum[h] == 0.f ? -INFINITY : m * 0.693147180559945309f + logf(sum[h]);
+        }
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < 2 * GR; c0 += kFewWarps) {   // a tile of 16 channels a warp
+#pragma unroll
+        for (int c = 0; c < kFewWarps; ++c) {
+          const float(&v)[4] = o[c0 + c];
+          red[(warp * kFewWarps + c) * 32 + lane] = make_float4(v[0] * mine[0], v[1] * mine[1], v[2] * mine[0], v[3] * mine[1]);
+        }
+        few_any(false);
+        const int ch = (c0 + warp) * 16 + g;
+        if (ch < d) {
+          float4 v = red[warp * 32 + lane];
+#pragma unroll
+          for (int k = 1; k < kFewWarps; ++k) {
+            const float4 x = red[(k * kFewWarps + warp) * 32 + lane];
+            v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (2 * t + h < u.rows) {
+              const float a = h ? v.y : v.x, b = h ? v.w : v.z;
+              if (p.part_o) {
+                float* to = p.part_o + (u.piece * R + rh[h]) * d + ch;
+                to[0] = a, to[8] = b;
+              } else {
+                __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.o) + rh[h] * d + ch;
+                to[0] = __float2bfloat16_rn(sum[h] == 0.f ? 0.f : a / sum[h]);
+                to[8] = __float2bfloat16_rn(sum[h] == 0.f ? 0.f : b / sum[h]);
+              }
+            }
+          }
+        }
+        few_any(false);
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (sh.fail) {
+    // a wait ran out: report, then give the copies in flight one more bounded
+    // wait each before their memory goes
+    dt_report<kFewRows>(w, sh, i0, last_item);
+    if (warp == kFewWarps && lane == 0)
+      for (int n = max(0, loaded - ST); n < loaded; ++n) tc::mbar_wait_bounded(&sh.full[n % ST], (uint32_t)(n / ST) & 1, kDtWait);
+    __syncwarp();
+    __syncthreads();
+  }
+}
+
+namespace {
+
+template <int GR>
+cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
+  DtParams w{};
+  w.a = p;
+  w.wait = dt_limit(p);
+  w.row_lo = 1, w.row_hi = kFewRows;
+  // a third of 227 KB a CTA, of which 1 KB is the system's
+  const uint32_t all = 76800, red = kFewWarps * kFewWarps * 32 * sizeof(float4), misc = (uint32_t)sizeof(FewShared) + 256;
+  const FewStage sg = few_stage(p.c.d);
+  const int stages = (int)((all - red - misc) / sg.bytes);
+  w.k_stages = stages > kFewStages ? kFewStages : stages;
+  w.p_off = w.k_stages * sg.bytes;
+  w.misc_off = w.p_off + red;
+  const uint32_t smem = w.misc_off + misc;
+  cudaError_t e = cudaFuncSetAttribute(attn_decode4_few_kernel<GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  for (int s0 = 0; s0 < p.N; s0 += kDtSeqs) {
+    w.s0 = s0;
+    w.ns = p.N - s0 < kDtSeqs ? p.N - s0 : kDtSeqs;
+    const int64_t most = (int64_t)w.ns * p.max_pieces * p.c.Hkv;
+    attn_decode4_few_kernel<GR><<<(unsigned)(most < 3 * sms ? most : 3 * sms), kFewThreads, smem, st>>>(w);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode4_few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
+  return p.c.d > 128 ? few<8>(p, sms, st) : p.c.d > 64 ? few<4>(p, sms, st) : few<2>(p, sms, st);
+}
+
+}  // namespace gdn

@@ -701,8 +701,7 @@ cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, int hi, cudaStre
   return cudaSuccess;
 }
 
-using Few8 = D4Cfg<__nv_bfloat16, 8, 1, 1, 1, 1, 128, 2>;
-using Few16 = D4Cfg<__nv_bfloat16, 16, 1, 1, 1, 1, 128, 2>;
+using Mid = D4Cfg<__nv_bfloat16, 16, 1, 1, 1, 1, 128, 2>;
 using Many = D4Cfg<__nv_bfloat16, 96, 1, 1, 2, 2, 64, 1>;
 using Full8 = D4Cfg<float, 8, 3, 2, 1, 1, 128, 2>;
 
@@ -715,15 +714,16 @@ cudaError_t launch_attn_decode4_tc(const AttnDecodeParams& p, int dtype, cudaStr
   if (e != cudaSuccess) return e;
   constexpr int kAll = 0x7fffffff;
   if (dtype == GDN_F32) return decode4<Full8>(p, sms, 1, kAll, st);
-  // a sequence's kernel goes by its own rows (a row's bits with it): up to 16
-  // (row, head) pairs of a kv head, or more; a call that may have both launches both
-  if (p.max_q * p.G > kDtNarrow) {
-    // (none has few where all rows together say that each has max_q)
-    const bool few = p.G <= kDtNarrow && (int64_t)p.N * p.max_q != p.T;
-    if (few) e = decode4<Few16>(p, sms, 1, kDtNarrow, st);
-    return e != cudaSuccess ? e : decode4<Many>(p, sms, few ? kDtNarrow + 1 : 1, kAll, st);
-  }
-  return p.max_q * p.G <= 8 ? decode4<Few8>(p, sms, 1, kDtNarrow, st) : decode4<Few16>(p, sms, 1, kDtNarrow, st);
+  // a sequence's kernel goes by its own rows (a row's bits with it): up to 8 (row,
+  // head) pairs of a kv head, or more, of which either form gives the same bits; a
+  // call that may have both launches both
+  const int most = p.max_q * p.G;
+  // (none has few where all rows together say that each has max_q)
+  const bool few = most <= kD4Few || (p.G <= kD4Few && (int64_t)p.N * p.max_q != p.T);
+  if (few) e = launch_attn_decode4_few(p, sms, st);
+  if (e != cudaSuccess || most <= kD4Few) return e;
+  const int lo = few ? kD4Few + 1 : 1;
+  return most <= 16 ? decode4<Mid>(p, sms, lo, kAll, st) : decode4<Many>(p, sms, lo, kAll, st);
 }
 
 }  // namespace gdn
