@@ -123,24 +123,29 @@ inline int64_t prefill_grid(AttnPrefillParams& p, int rows, int times) {
 // tokens 76 pieces a head are one CTA on each of the 152 SMs for two kv heads.
 constexpr int kMaxPieces = 76;
 constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows
-__host__ __device__ inline int decode_piece_target(int tiles, int rows) {   // pieces aimed at
-  const int per = rows > kDtNarrow ? (tiles <= 16 ? 4 : tiles <= 64 ? 8 : 16) : tiles <= 16 ? 2 : 4;
+__host__ __device__ inline int decode_piece_target(int tiles, int rows, int bits) {   // pieces aimed at
+  const int per = rows > kDtNarrow ? (tiles <= 16 ? 4 : tiles <= 64 ? 8 : 16) : tiles <= 16 ? 2 : bits == 8 ? 4 : 8;
   const int n = (tiles + per / 2) / per;
   return n < 1 ? 1 : n > kMaxPieces ? kMaxPieces : n;
 }
-__host__ __device__ inline int decode_piece_tokens(int L, int rows) {
-  const int tiles = L < 1 ? 1 : (int)(((int64_t)L + 127) / 128), n = decode_piece_target(tiles, rows);
+__host__ __device__ inline int decode_piece_tokens(int L, int rows, int bits) {
+  const int tiles = L < 1 ? 1 : (int)(((int64_t)L + 127) / 128), n = decode_piece_target(tiles, rows, bits);
   return (tiles + n - 1) / n * 128;
 }
-__host__ __device__ inline int decode_pieces(int L, int rows) {
-  const int c = decode_piece_tokens(L, rows);
+__host__ __device__ inline int decode_pieces(int L, int rows, int bits) {
+  const int c = decode_piece_tokens(L, rows, bits);
   return L < 1 ? 1 : (int)(((int64_t)L + c - 1) / c);
 }
 // At least the pieces of any length up to L and any number of rows.
-__host__ __device__ inline int decode_max_pieces(int L) {
+__host__ __device__ inline int decode_max_pieces(int L, int bits) {
   const int tiles = (int)(((int64_t)(L < 1 ? 1 : L) + 127) / 128);
-  const int s = decode_piece_target(tiles < 16 ? tiles : 16, 1), m = decode_piece_target(tiles, 1);
-  return m > s ? m : s;
+  int most = 1;
+  for (int rows = 1; rows <= kDtNarrow + 1; rows += kDtNarrow)
+    for (int at = 16; at <= 128; at *= 2) {   // (up to 16 or 64 tiles, from where pieces are longer)
+      const int n = decode_piece_target(tiles < at || at == 128 ? tiles : at, rows, bits);
+      most = n > most ? n : most;
+    }
+  return most;
 }
 
 // In place of a row's sum (never negative) in a piece that was not finished.

@@ -133,7 +133,7 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool, const 
 size_t gdn_attn_decode_workspace_size(const gdn_attn_desc* desc, int32_t num_seqs, int64_t total_tokens,
                                       int32_t max_kv_len) {
   if (check_desc(desc) != GDN_OK || num_seqs < 0 || total_tokens < 0 || max_kv_len < 0) return 0;
-  const int pieces = decode_max_pieces(max_kv_len);
+  const int pieces = decode_max_pieces(max_kv_len, desc->kv_bits == 4 ? 4 : 8);
   if (pieces == 1) return 256;
   return part_o_bytes(desc, total_tokens, pieces) +
          ((size_t)total_tokens * desc->num_q_heads * pieces * sizeof(float2) + 255) / 256 * 256;
@@ -153,7 +153,7 @@ gdn_status gdn_attn_decode(const gdn_attn_desc* desc, const gdn_pool* pool, cons
     return GDN_ERR_INVALID_ARG;
   st = check_rows(desc, a->q, a->q_stride, desc->num_q_heads);
   if (st != GDN_OK) return st;
-  const int pieces = decode_max_pieces(a->max_kv_len);
+  const int pieces = decode_max_pieces(a->max_kv_len, desc->kv_bits == 4 ? 4 : 8);
   const size_t need = gdn_attn_decode_workspace_size(desc, a->num_seqs, a->total_tokens, a->max_kv_len);
   if (pieces > 1 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return GDN_ERR_WORKSPACE;
   AttnDecodeParams p{};

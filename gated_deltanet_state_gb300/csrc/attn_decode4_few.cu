@@ -83,16 +83,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(r) : "r"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(r) : "r"(a));
-  return r;
-}
 __device__ __forceinline__ float few_log2(float x) {   // (normal numbers and NaN)
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -299,7 +289,9 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
         const unsigned nth = before + c0, st = nth % (unsigned)ST;
         ok = __all_sync(0xffffffffu, dt_wait(&sh.full[st], nth / (unsigned)ST & 1, fail, limit));
         if (!ok) break;
-        const uint32_t stage = ring + st * sg.bytes;
+        const uint8_t* stage = base + st * sg.bytes;
+        const uint32_t stage_k = ring + st * sg.bytes + at_k;
+        const uint8_t *k_scale = stage + at_ks, *v_scale = stage + at_vs, *v_word = stage + at_v;
         const int kb = u.k0 + c0 * kFewTok;
         // ---- scores: 16 tokens at a time, four of each word ----
         float x[2][4] = {};   // of step s: tokens A (rows 2 t, 2 t + 1), B
@@ -308,11 +300,11 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
           const uint4 q = sh.q[c][lane];
           const float2 start = sh.start[c][t];
           uint32_t m[4];
-          ldsm4(stage + at_k + c * 256, m);
+          ldsm4(stage_k + c * 256, m);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const uint32_t a = m[2 * s], b = m[2 * s + 1], a8 = a >> 8, b8 = b >> 8;
-            const uint32_t sa = lds8(stage + at_ks + c * 16 + 4 * s), sb = lds8(stage + at_ks + c * 16 + 4 * s + 2);
+            const uint32_t sa = k_scale[c * 16 + 4 * s], sb = k_scale[c * 16 + 4 * s + 2];
             float y[4];
             mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start.x, start.y, start.x, start.y);
             mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w, y[0], y[1], y[2], y[3]);
@@ -323,41 +315,43 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
         }
         // a NaN scale of K (255, above taken for a number) makes its token's scores NaN
         uint4 some = make_uint4(0, 0, 0, 0);
-        if (lane < kFewBlocks * groups) some = *reinterpret_cast<const uint4*>(base + st * sg.bytes + at_nan);
+        if (lane < kFewBlocks * groups) some = *reinterpret_cast<const uint4*>(stage + at_nan);
         auto full_byte = [](uint32_t v) { return (~v - 0x01010101u) & v & 0x80808080u; };
         if (__any_sync(0xffffffffu, (full_byte(some.x) | full_byte(some.y) | full_byte(some.z) | full_byte(some.w)) != 0)) {
           for (int c = 0; c < groups; ++c)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              if (lds8(stage + at_ks + c * 16 + 4 * s) == kKv4Nan) x[s][0] = x[s][1] = __int_as_float(0x7fffffff);
-              if (lds8(stage + at_ks + c * 16 + 4 * s + 2) == kKv4Nan) x[s][2] = x[s][3] = __int_as_float(0x7fffffff);
+              if (k_scale[c * 16 + 4 * s] == kKv4Nan) x[s][0] = x[s][1] = __int_as_float(0x7fffffff);
+              if (k_scale[c * 16 + 4 * s + 2] == kKv4Nan) x[s][2] = x[s][3] = __int_as_float(0x7fffffff);
             }
         }
         // ---- weights ----
         const uint32_t have = sh.have[st];
         const bool edge = have != (1u << kFewBlocks) - 1u || kb + kFewTok > u.k1 || kb + kFewTok > least;
-        const int pos = kb + (g >> 2) * kKvBlock + tok;
-        const bool here = have >> (g >> 2) & 1;
         float rv[2][2];
-        float top[2] = {-INFINITY, -INFINITY};
+        float top[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             // of tokens A and B: the exponent of the V scale, and what undoes it in the sums
             // (a NaN scale makes weights NaN; masked ones stay 0)
-            const float vs = kv4_scale(lds8(stage + at_vs + 4 * s + 2 * k));
-            const float lv = few_log2(vs) - (k ? 4.f : 0.f);
+            const float lv = few_log2(kv4_scale(v_scale[4 * s + 2 * k])) - (k ? 4.f : 0.f);
             rv[s][k] = dt_ex2(fmaxf(-lv, -100.f));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float& v = x[s][2 * k + h];
-              v = fmaf(v, cs[h], lv);
-              const int at = pos + 4 * s + 2 * k;
-              if (edge && (!here || at >= u.k1 || at >= lim[h])) v = -INFINITY;
-              top[h] = fmaxf(top[h], v);
-            }
+            for (int h = 0; h < 2; ++h) x[s][2 * k + h] = fmaf(x[s][2 * k + h], cs[h], lv);
           }
+        if (edge) {
+          const int pos = kb + (g >> 2) * kKvBlock + tok;
+          const int end = have >> (g >> 2) & 1 ? u.k1 : 0;
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (pos + 4 * s + (k & 2) >= min(end, lim[k & 1])) x[s][k] = -INFINITY;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(x[0][h], x[0][2 + h]), fmaxf(x[1][h], x[1][2 + h]));
         if (__any_sync(0xffffffffu, top[0] + off[0] > kFewTop || top[1] + off[1] > kFewTop)) {
           // a row's first keys, or one far above its reference
 #pragma unroll
@@ -389,8 +383,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
         for (int c = 0; c < 2 * GR; ++c) {
           if (c < 2 * groups) {
             uint32_t ya[4], yb[4];
-            kv4_halves(lds32(stage + at_v + c * 128), ya);
-            kv4_halves(lds32(stage + at_v + c * 128 + 64), yb);
+            kv4_halves(*reinterpret_cast<const uint32_t*>(v_word + c * 128), ya);
+            kv4_halves(*reinterpret_cast<const uint32_t*>(v_word + c * 128 + 64), yb);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
               mma_f16(o[c], ya[2 * s], yb[2 * s], ya[2 * s + 1], yb[2 * s + 1], pb[s][0], pb[s][1], o[c][0], o[c][1], o[c][2], o[c][3]);

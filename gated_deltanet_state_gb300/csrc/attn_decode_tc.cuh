@@ -130,7 +130,7 @@ __device__ __forceinline__ int dt_groups(const DtParams& w, int s) {
 }
 // A tile of keys counts 1, an item's fixed cost as much again.
 __device__ __forceinline__ int dt_piece_work(const AttnDecodeParams& p, int s) {
-  return decode_piece_tokens(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G) / kDtTok + 1;
+  return decode_piece_tokens(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G, p.c.bits) / kDtTok + 1;
 }
 
 // The last s with sums[s] <= i.
@@ -167,14 +167,14 @@ __device__ __forceinline__ DtItem dt_item(const DtParams& w, const int* items, i
   t.L = p.kv_len[t.s];
   // of one head: piece after piece, of a piece its row tiles (with one tile a
   // CTA's run of items loads its rows once a head)
-  t.pieces = decode_pieces(t.L, t.n * p.G);
+  t.pieces = decode_pieces(t.L, t.n * p.G, p.c.bits);
   t.rt = (t.n * p.G + NT - 1) / NT;
   t.h = k / (t.pieces * t.rt);
   const int in = k - t.h * t.pieces * t.rt;
   t.piece = in / t.rt;
   t.r0 = (in - t.piece * t.rt) * NT;
   t.rows = min(NT, t.n * p.G - t.r0);
-  t.pt = decode_piece_tokens(t.L, t.n * p.G);
+  t.pt = decode_piece_tokens(t.L, t.n * p.G, p.c.bits);
   t.k0 = t.piece * t.pt;
   t.k1 = min(t.L, t.k0 + t.pt);
   t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
@@ -284,7 +284,7 @@ __device__ __forceinline__ void dt_sums(const DtParams& w, DtItems& sh, int lane
         g = 0;
       }
       if (g > 0) {
-        const int pieces = decode_pieces(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G);
+        const int pieces = decode_pieces(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G, p.c.bits);
         v = g * pieces;
         x = (long long)v * dt_piece_work(p, s);
       }
