@@ -15,9 +15,9 @@
 // n 2^-24 (pairs 0 and 2) or n 2^-20 (pairs 1 and 3, whose partners in Q and P
 // carry 2^-4).  K's offset of 8 is in the products' start value, -8 sum(q) of a
 // group of 32 channels; a group's product is its own and is added under its
-// tokens' scales in fp32.  V's is taken off in f16 (exact).  Which token or channel
-// stands in which row or step of a product is chosen so that a lane's word is its
-// operand: a lane holds eight channels of K, or eight tokens of V.
+// tokens' scales in fp32.  V's is taken off in f16 (exact).  Which channel or token
+// stands in which step of a product is chosen so that a lane's word is its operand:
+// a lane holds eight channels of K, or eight tokens of V.
 //
 // Q is scaled by a power of two for each row: 8 bits of elements down to 2^-27 of
 // the largest, off by 2^-35 of it at most below.  A weight times its V scale is an
@@ -25,9 +25,9 @@
 // only when a weight would pass f16's range: 11 bits down to 2^-20 of it, off by
 // 2^-31 at most below.
 //
-// A warp takes every fourth chunk of 32 tokens of a piece, with statistics and
-// sums of its own, which the four bring together in a fixed order at its end; it
-// waits for nothing but its chunk.
+// A warp takes 32 tokens of every tile of 128, with statistics and sums of its own,
+// which the four bring together in a fixed order at the end of a piece; it waits for
+// nothing but the tile.
 #include "attn_decode_tc.cuh"
 #include "kv4.cuh"
 
@@ -38,29 +38,32 @@ using namespace dt;
 namespace {
 
 constexpr int kFewRows = 8, kFewWarps = 4, kFewThreads = 32 * (kFewWarps + 1);   // and the loads' warp
-constexpr int kFewTok = 32, kFewBlocks = kFewTok / kKvBlock;                     // of a chunk
+constexpr int kFewTok = kDtTok / kFewWarps, kFewBlocks = kFewTok / kKvBlock;     // of a warp, in a tile
 constexpr int kFewStages = 8;
 constexpr float kFewBase = 10.f, kFewTop = 15.75f;   // a weight at its reference is 2^10, none passes 2^15.75
 constexpr float kFewUnset = 3e38f;                   // the offset of a row that has seen no key
 constexpr float kFewUnit = 16777216.f;               // the products count in 2^-24
 
-// A chunk in shared memory: blocks further apart than they are long, so that the
-// lanes of two blocks do not meet in a bank.
+// A stage holds the tokens of CPS warps: K's codes, K's scales, V's codes, V's scales,
+// as they lie in pages.  All four warps' up to d = 128, where a copy is short and its
+// issue what counts; one's above, so that three CTAs an SM hold some ahead.
+template <int GR>
+constexpr int kFewPer = GR <= 4 ? kFewWarps : 1;
 struct FewStage {
-  uint32_t kp, ksp, v, vp, vs, bytes;   // pitch of K's codes and scales, V's codes from here, their pitch, V's scales
+  uint32_t ks, v, vs, bytes;
 };
+template <int GR>
 __host__ __device__ inline FewStage few_stage(int d) {
+  constexpr int kBlocks = kFewPer<GR> * kFewBlocks;
   FewStage s;
-  s.kp = kv4_codes(d) + 64, s.ksp = kv4_k_scales(d) + 16;
-  s.v = kFewBlocks * (s.kp + s.ksp), s.vp = kv4_codes(d) + 64;
-  s.vs = s.v + kFewBlocks * s.vp;
-  s.bytes = (s.vs + kFewBlocks * kKvBlock + 127) / 128 * 128;
+  s.ks = kBlocks * kv4_codes(d), s.v = s.ks + kBlocks * kv4_k_scales(d), s.vs = s.v + kBlocks * kv4_codes(d);
+  s.bytes = (s.vs + kBlocks * kKvBlock + 127) / 128 * 128;
   return s;
 }
 
 struct FewShared : DtItems {
   uint64_t full[kFewStages], empty[kFewStages];
-  uint32_t have[kFewStages];            // blocks of a chunk that were loaded
+  uint32_t have[kFewStages];            // blocks of a stage that were loaded
   float2 stat[kFewWarps][kFewRows];     // a warp's offset and sum of each row
   uint4 q[8][32];                       // Q of row g, eight channels of a group, by lane
   float2 start[8][4];                   // a group's start value for rows 2 t, 2 t + 1
@@ -116,19 +119,20 @@ __device__ __forceinline__ bool few_any(bool x) {
   return r != 0;
 }
 
-// The loads of the CTA's items [i0, i1), four chunks at a time: lane 8 x + b has
-// part x (K's codes and scales, V's) of their block b.  Returns the chunks loaded.
+// The loads of the CTA's items [i0, i1): lane 8 x + b has part x (K's codes and
+// scales, V's) of a tile's block b; blocks of a stage that lie one after another in a
+// page (all of them, in pages of whole tiles) come in one copy.  Returns the stages
+// loaded.
+template <int GR>
 __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_t* base, int i0, int i1, int lane) {
   const AttnDecodeParams& p = w.a;
   volatile int* fail = &sh.fail;
-  const int ST = w.k_stages, d = p.c.d, part = lane >> 3, blk = lane & 7, in_chunk = blk & 1;
-  const FewStage sg = few_stage(d);
+  constexpr int kBlocks = kFewPer<GR> * kFewBlocks;   // of a stage
+  const int ST = w.k_stages, d = p.c.d, part = lane >> 3, blk = lane & 7;
+  const FewStage sg = few_stage<GR>(d);
   const uint32_t codes = kv4_codes(d), scales = kv4_k_scales(d), each = 2 * codes + scales + kKvBlock;
-  const uint32_t to = part == 0   ? in_chunk * sg.kp
-                      : part == 1 ? kFewBlocks * sg.kp + in_chunk * sg.ksp
-                      : part == 2 ? sg.v + in_chunk * sg.vp
-                                  : sg.vs + in_chunk * kKvBlock;
   const uint32_t size = part == 1 ? scales : part == 3 ? kKvBlock : codes;
+  const uint32_t to = (part == 0 ? 0u : part == 1 ? sg.ks : part == 2 ? sg.v : sg.vs) + blk % kBlocks * size;
   int loaded = 0, st = 0, ph = 0;
   bool ok = true;
   DtItem t{};
@@ -136,39 +140,42 @@ __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_
     if (i == i0) t = dt_item<kFewRows>(w, sh.items, i);
     else dt_next<kFewRows>(w, sh.items, i, t);
     const int32_t* bt = p.block_table + (int64_t)t.s * p.max_pages;
-    int at = 0, next_at = 0, next = -1;
-    auto look = [&](int j) {   // of the four chunks from j
-      const int pos = t.k0 + j * kFewTok + blk * kKvBlock;
+    int next_at = 0, next = -1;
+    auto look = [&](int j) {
+      const int pos = t.k0 + j * kDtTok + blk * kKvBlock;
       next_at = pos / p.c.page_tokens;
       next = pos < t.k1 && next_at < p.max_pages ? bt[next_at] : -1;
     };
-    const int chunks = (t.k1 - t.k0 + kFewTok - 1) / kFewTok;
-    if (chunks > 0) look(0);
-    for (int j = 0; ok && j < chunks; j += 4) {
-      const int page = next, pos = t.k0 + j * kFewTok + blk * kKvBlock;
-      at = next_at;
-      if (j + 4 < chunks) look(j + 4);
+    if (t.tiles > 0) look(0);
+    for (int j = 0; ok && j < t.tiles; ++j) {
+      const int page = next, at = next_at, pos = t.k0 + j * kDtTok + blk * kKvBlock;
+      if (j + 1 < t.tiles) look(j + 1);
       const bool in = pos < t.k1, good = in && page >= 0 && page < p.c.num_pages;
       if (in && !good && part == 0) set_error(p.err, GDN_ERR_PAGE_RANGE);
-      const unsigned have = __ballot_sync(0xffffffffu, good);
-      const int b = (pos - at * p.c.page_tokens) / kKvBlock;
+      const unsigned have = __ballot_sync(0xffffffffu, good) & 0xffu;
+      const int b = (pos - at * p.c.page_tokens) / kKvBlock, before = __shfl_up_sync(0xffffffffu, page, 1);
+      // (the same in every part)
+      const unsigned first = __ballot_sync(0xffffffffu, good && !(blk % kBlocks > 0 && b > 0 && (have >> (blk - 1) & 1) && before == page)) & 0xffu;
+      // up to the next copy's first block, or the first one that is not there
+      const unsigned stop = (first | ~have) >> (blk + 1);
+      const int n = min((int)kDtBlocks - blk, __ffs(stop));
       const uint8_t* from = nullptr;
-      if (good)
+      if (first >> blk & 1)
         from = part == 0   ? kv4_k_block(p.c, page, t.h, b)
                : part == 1 ? kv4_k_scale(p.c, page, t.h, b)
                : part == 2 ? kv4_v_block(p.c, page, t.h, b)
                            : kv4_v_scale(p.c, page, t.h, b);
-      const int n = min(4, chunks - j);
-      for (int c = 0; c < n; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < kDtBlocks / kBlocks; ++c) {
         if (loaded >= ST) ok = dt_wait(&sh.empty[st], ph ^ 1, fail, w.wait);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         if (lane == 0) {
-          const unsigned two = have >> (2 * c) & 3u;
-          sh.have[st] = two;
-          tc::mbar_expect_tx(&sh.full[st], __popc(two) * each);
+          const unsigned mine = have >> (c * kBlocks) & ((1u << kBlocks) - 1u);
+          sh.have[st] = mine;
+          tc::mbar_expect_tx(&sh.full[st], __popc(mine) * each);
         }
         __syncwarp();
-        if (good && blk >> 1 == c) tc::bulk_load(base + (uint32_t)st * sg.bytes + to, from, size, &sh.full[st]);
+        if (from && blk / kBlocks == c) tc::bulk_load(base + (uint32_t)st * sg.bytes + to, from, n * size, &sh.full[st]);
         ++loaded;
         if (++st == ST) st = 0, ph ^= 1;
       }
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
   const long long limit = w.wait;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < ST; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], kFewPer<GR>);
     sh.fail = limit < 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -202,27 +209,29 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
   const int i0 = dt_first<kFewRows>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
   const int last_item = dt_first<kFewRows>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
   const int i1 = limit < 0 ? i0 : last_item;
-  int loaded = 0;   // chunks (the loading warp's)
+  int loaded = 0;   // stages (the loading warp's)
 
   if (warp == kFewWarps) {
-    loaded = few_load(w, sh, base, i0, i1, lane);
+    loaded = few_load<GR>(w, sh, base, i0, i1, lane);
   } else {
-    const FewStage sg = few_stage(d);
+    const FewStage sg = few_stage<GR>(d);
     const int g = lane >> 2, t = lane & 3, groups = d / kKv4Group;
     const uint32_t ring = smem_u32(base);
-    // a lane's places in a chunk: the row of K's matrices that it points at, its
-    // tokens' scales (word g / 2 of the four, tokens 4 s + g % 2 and two further), its words of V
-    const int mr = lane & 7, mi = lane >> 3;
-    const uint32_t at_k = (mr >> 2) * sg.kp + ((mr >> 1 & 1) * 8 + (mi >> 1) * 4 + (mi & 1) * 2 + (mr & 1)) * 16;
-    const int tok = (g >> 1 & 1) * 8 + (g & 1);
-    const uint32_t at_ks = kFewBlocks * sg.kp + (g >> 2) * sg.ksp + tok;
-    const uint32_t at_v = sg.v + (t >> 1) * sg.vp + g * 8 + (t & 1) * 4, at_vs = sg.vs + (g >> 2) * kKvBlock + tok;
-    const uint32_t at_nan = kFewBlocks * sg.kp + lane / groups * sg.ksp + lane % groups * 16;   // 16 of K's scales
+    // a lane's places in a stage: the row of K's matrices that it points at (token
+    // lane % 16 of the warp's first or second block), its tokens' scales (g and g + 8 of
+    // either block), its words of V (the warp's t-th)
+    constexpr int PER = kFewPer<GR>, kAhead = kFewWarps / PER;   // warps of a stage, stages of a tile
+    const uint32_t block = kFewBlocks * (warp % PER), next_ks = kv4_k_scales(d);
+    const uint32_t at_k = (block + (lane >> 4)) * kv4_codes(d) + (lane & 15) * 16;
+    const uint32_t at_ks = sg.ks + block * next_ks + g;
+    const uint32_t at_v = sg.v + (block + (t >> 1)) * kv4_codes(d) + g * 8 + (t & 1) * 4;
+    const uint32_t at_vs = sg.vs + block * kKvBlock + g;
+    const uint32_t at_nan = sg.ks + block * next_ks + lane * 16;   // 16 of the warp's scales of K
     float4* red = reinterpret_cast<float4*>(base + w.p_off);   // [4 warps][4 tiles][32]
     float cs[2] = {};      // factors of the scores of rows 2 t, 2 t + 1 ...
     int lim[2] = {};       // ... and the keys that they see
     bool ok = true;
-    unsigned before = 0;   // chunks of the items before
+    int st = warp / PER, ph = 0;   // (fewer than the stages there are)
     DtItem u{};
     for (int i = i0; i < i1; ++i) {
       if (i == i0) u = dt_item<kFewRows>(w, sh.items, i);
@@ -283,18 +292,19 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
       for (int c = 0; c < 2 * GR; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[c][k] = 0.f;
-      const int chunks = (u.k1 - u.k0 + kFewTok - 1) / kFewTok, least = u.L - u.n + 1;   // keys that every row sees
+      const int least = u.L - u.n + 1;   // keys that every row sees
 #pragma unroll 1
-      for (int c0 = warp; ok && c0 < chunks; c0 += kFewWarps) {
-        const unsigned nth = before + c0, st = nth % (unsigned)ST;
-        ok = __all_sync(0xffffffffu, dt_wait(&sh.full[st], nth / (unsigned)ST & 1, fail, limit));
+      for (int j = 0; j < u.tiles; ++j) {
+        ok = __all_sync(0xffffffffu, dt_wait(&sh.full[st], ph, fail, limit));
         if (!ok) break;
         const uint8_t* stage = base + st * sg.bytes;
         const uint32_t stage_k = ring + st * sg.bytes + at_k;
         const uint8_t *k_scale = stage + at_ks, *v_scale = stage + at_vs, *v_word = stage + at_v;
-        const int kb = u.k0 + c0 * kFewTok;
-        // ---- scores: 16 tokens at a time, four of each word ----
-        float x[2][4] = {};   // of step s: tokens A (rows 2 t, 2 t + 1), B
+        const int kb = u.k0 + j * kDtTok + kFewTok * warp;
+        const unsigned have = sh.have[st] >> block & 3u;
+        if (kb < u.k1 && have) {
+        // ---- scores: 16 tokens at a time ----
+        float x[2][4] = {};   // of block s: token g of rows 2 t, 2 t + 1, token g + 8
 #pragma unroll 2
         for (int c = 0; c < groups; ++c) {
           const uint4 q = sh.q[c][lane];
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             const uint32_t a = m[2 * s], b = m[2 * s + 1], a8 = a >> 8, b8 = b >> 8;
-            const uint32_t sa = k_scale[c * 16 + 4 * s], sb = k_scale[c * 16 + 4 * s + 2];
+            const uint32_t sa = k_scale[s * next_ks + c * 16], sb = k_scale[s * next_ks + c * 16 + 8];
             float y[4];
             mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start.x, start.y, start.x, start.y);
             mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w, y[0], y[1], y[2], y[3]);
@@ -321,34 +331,34 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
           for (int c = 0; c < groups; ++c)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              if (k_scale[c * 16 + 4 * s] == kKv4Nan) x[s][0] = x[s][1] = __int_as_float(0x7fffffff);
-              if (k_scale[c * 16 + 4 * s + 2] == kKv4Nan) x[s][2] = x[s][3] = __int_as_float(0x7fffffff);
+              if (k_scale[s * next_ks + c * 16] == kKv4Nan) x[s][0] = x[s][1] = __int_as_float(0x7fffffff);
+              if (k_scale[s * next_ks + c * 16 + 8] == kKv4Nan) x[s][2] = x[s][3] = __int_as_float(0x7fffffff);
             }
         }
         // ---- weights ----
-        const uint32_t have = sh.have[st];
-        const bool edge = have != (1u << kFewBlocks) - 1u || kb + kFewTok > u.k1 || kb + kFewTok > least;
+        const bool edge = have != 3u || kb + kFewTok > u.k1 || kb + kFewTok > least;
         float rv[2][2];
         float top[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            // of tokens A and B: the exponent of the V scale, and what undoes it in the sums
-            // (a NaN scale makes weights NaN; masked ones stay 0)
-            const float lv = few_log2(kv4_scale(v_scale[4 * s + 2 * k])) - (k ? 4.f : 0.f);
+            // of a token: the exponent of its V scale (less 4 where its codes stand four bits
+            // up), and what undoes it in the sums (a NaN scale makes weights NaN; masked ones
+            // stay 0)
+            const float lv = few_log2(kv4_scale(v_scale[s * kKvBlock + 8 * k])) - (g & 2 ? 4.f : 0.f);
             rv[s][k] = dt_ex2(fmaxf(-lv, -100.f));
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[s][2 * k + h] = fmaf(x[s][2 * k + h], cs[h], lv);
           }
         if (edge) {
-          const int pos = kb + (g >> 2) * kKvBlock + tok;
-          const int end = have >> (g >> 2) & 1 ? u.k1 : 0;
 #pragma unroll
-          for (int s = 0; s < 2; ++s)
+          for (int s = 0; s < 2; ++s) {
+            const int end = have >> s & 1 ? u.k1 : 0, pos = kb + s * kKvBlock + g;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (pos + 4 * s + (k & 2) >= min(end, lim[k & 1])) x[s][k] = -INFINITY;
+              if (pos + 4 * (k & 2) >= min(end, lim[k & 1])) x[s][k] = -INFINITY;
+          }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(x[0][h], x[0][2 + h]), fmaxf(x[1][h], x[1][2 + h]));
@@ -369,15 +379,16 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
             for (int c = 0; c < 2 * GR; ++c) o[c][h] *= alpha, o[c][2 + h] *= alpha;
           }
         }
-        uint32_t pb[2][2];   // P: row g, tokens of word t
+        uint32_t pb[4];   // P of row g, first by word (its tokens 2 t, 2 t + 1), then by pair (of word t)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float a = dt_ex2(x[s][2 * k] + off[0]), b = dt_ex2(x[s][2 * k + 1] + off[1]);
             l[0] = fmaf(a, rv[s][k], l[0]), l[1] = fmaf(b, rv[s][k], l[1]);
-            pb[s][k] = transposed(half2_bits(a, b));
+            pb[2 * s + k] = transposed(half2_bits(a, b));
           }
+        kv4_transpose(pb, t);
         // ---- outputs: 16 channels at a time ----
 #pragma unroll
         for (int c = 0; c < 2 * GR; ++c) {
@@ -387,13 +398,15 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
             kv4_halves(*reinterpret_cast<const uint32_t*>(v_word + c * 128 + 64), yb);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-              mma_f16(o[c], ya[2 * s], yb[2 * s], ya[2 * s + 1], yb[2 * s + 1], pb[s][0], pb[s][1], o[c][0], o[c][1], o[c][2], o[c][3]);
+              mma_f16(o[c], ya[2 * s], yb[2 * s], ya[2 * s + 1], yb[2 * s + 1], pb[2 * s], pb[2 * s + 1], o[c][0], o[c][1], o[c][2], o[c][3]);
           }
+        }
         }
         __syncwarp();
         if (lane == 0) dt_arrive(&sh.empty[st]);
+        st += kAhead;
+        if (st >= ST) st -= ST, ph ^= 1;
       }
-      before += chunks;
       // ---- the four warps' sums, brought to the largest reference and added in order ----
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -484,9 +497,10 @@ cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
   w.row_lo = 1, w.row_hi = kFewRows;
   // a third of 227 KB a CTA, of which 1 KB is the system's
   const uint32_t all = 76800, red = kFewWarps * kFewWarps * 32 * sizeof(float4), misc = (uint32_t)sizeof(FewShared) + 256;
-  const FewStage sg = few_stage(p.c.d);
+  const FewStage sg = few_stage<GR>(p.c.d);
   const int stages = (int)((all - red - misc) / sg.bytes);
   w.k_stages = stages > kFewStages ? kFewStages : stages;
+  if (w.k_stages < kFewWarps / kFewPer<GR>) return cudaErrorInvalidValue;
   w.p_off = w.k_stages * sg.bytes;
   w.misc_off = w.p_off + red;
   const uint32_t smem = w.misc_off + misc;

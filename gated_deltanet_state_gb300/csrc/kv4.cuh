@@ -55,6 +55,18 @@ __device__ __forceinline__ uint32_t kv4_byte(uint32_t amax_bits) {
   return b;
 }
 
+// Four words of each of four lanes (lane % 4 = q), transposed: word i of lane q
+// goes to word q of lane i.
+__device__ __forceinline__ void kv4_transpose(uint32_t (&w)[4], int q) {
+  const bool odd = q & 1, up = q & 2;
+  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), b = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+  if (odd) w[0] = a, w[2] = b;
+  else w[1] = a, w[3] = b;
+  a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[2], 2), b = __shfl_xor_sync(0xffffffffu, up ? w[1] : w[3], 2);
+  if (up) w[0] = a, w[1] = b;
+  else w[2] = a, w[3] = b;
+}
+
 // Two neighbouring elements of a word of eight, already shifted to bits 0 .. 3 and
 // 16 .. 19, as bf16 of 128 + n: the codes become the mantissas' last bits.  (One
 // instruction, where the compiler makes two of (w & a) | b with constants.)

@@ -22,18 +22,6 @@ __device__ __forceinline__ uint32_t lanes_umax(uint32_t m) {
   return m;
 }
 
-// Four words of each of four lanes (lane % 4 = q), transposed: word i of lane q
-// goes to word q of lane i.
-__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int q) {
-  const bool odd = q & 1, up = q & 2;
-  uint32_t a = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1), b = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
-  if (odd) w[0] = a, w[2] = b;
-  else w[1] = a, w[3] = b;
-  a = __shfl_xor_sync(0xffffffffu, up ? w[0] : w[2], 2), b = __shfl_xor_sync(0xffffffffu, up ? w[1] : w[3], 2);
-  if (up) w[0] = a, w[1] = b;
-  else w[2] = a, w[3] = b;
-}
-
 // Eight consecutive elements of a row.
 template <typename T> struct Row8;
 template <> struct Row8<__nv_bfloat16> {
@@ -163,7 +151,7 @@ struct AppendRun {
       w[i] = x;
       if (i == q) mine = b;
     }
-    transpose4(w, q);
+    kv4_transpose(w, q);
     if (on && has(t0 + q)) {
       const int at = lane / 4 * kKvBlock + t0 + q;
       *reinterpret_cast<uint4*>(codes + at * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -366,7 +354,7 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv4_gather_kernel(const KvGath
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
-        transpose4(w, q);   // this lane's 8 channels of tokens 4 k .. 4 k + 3
+        kv4_transpose(w, q);   // this lane's 8 channels of tokens 4 k .. 4 k + 3
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t s1 = kv4_scale_bf16((&s4.x)[k] >> (8 * u) & 255u), s = s1 << 16 | s1, off = kv4_offset(s);
