@@ -66,7 +66,7 @@ struct FewShared : DtItems {
   uint32_t have[kFewStages];            // blocks of a stage that were loaded
   float2 stat[kFewWarps][kFewRows];     // a warp's offset and sum of each row
   uint4 q[8][32];                       // Q of row g, eight channels of a group, by lane
-  float2 start[8][4];                   // a group's start value for rows 2 t, 2 t + 1
+  float4 start[8][4];                   // a group's start values for rows 2 t, 2 t + 1 (twice, as a product's)
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -79,12 +79,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
 }
-// D = A B + C: 16 x 16 by 16 x 8 in f16, fp32 sums.
+// D = A B + C, or D += A B: 16 x 16 by 16 x 8 in f16, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                        float c0, float c1, float c2, float c3) {
+                                        const float4& c) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z), "f"(c.w));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float few_log2(float x) {   // (normal numbers and NaN)
   float y;
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
           sum *= -8.f / kFewUnit;
           if (c % kFewWarps == warp) {   // (every warp has them all)
             sh.q[c][lane] = q;
-            if (t == 0) (&sh.start[c][g >> 1].x)[g & 1] = sum;
+            if (t == 0) (&sh.start[c][g >> 1].x)[g & 1] = (&sh.start[c][g >> 1].x)[2 + (g & 1)] = sum;
           }
         }
         // (an infinite element makes its row's scores NaN)
@@ -308,7 +313,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
 #pragma unroll 2
         for (int c = 0; c < groups; ++c) {
           const uint4 q = sh.q[c][lane];
-          const float2 start = sh.start[c][t];
+          const float4 start = sh.start[c][t];
           uint32_t m[4];
           ldsm4(stage_k + c * 256, m);
 #pragma unroll
@@ -316,8 +321,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
             const uint32_t a = m[2 * s], b = m[2 * s + 1], a8 = a >> 8, b8 = b >> 8;
             const uint32_t sa = k_scale[s * next_ks + c * 16], sb = k_scale[s * next_ks + c * 16 + 8];
             float y[4];
-            mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start.x, start.y, start.x, start.y);
-            mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w, y[0], y[1], y[2], y[3]);
+            mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start);
+            mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w);
             const float fa = __uint_as_float(sa * (1u << 20) + (107u << 23)), fb = __uint_as_float(sb * (1u << 20) + (107u << 23));
             x[s][0] = fmaf(y[0], fa, x[s][0]), x[s][1] = fmaf(y[1], fa, x[s][1]);
             x[s][2] = fmaf(y[2], fb, x[s][2]), x[s][3] = fmaf(y[3], fb, x[s][3]);
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
             kv4_halves(*reinterpret_cast<const uint32_t*>(v_word + c * 128 + 64), yb);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-              mma_f16(o[c], ya[2 * s], yb[2 * s], ya[2 * s + 1], yb[2 * s + 1], pb[2 * s], pb[2 * s + 1], o[c][0], o[c][1], o[c][2], o[c][3]);
+              mma_f16(o[c], ya[2 * s], yb[2 * s], ya[2 * s + 1], yb[2 * s + 1], pb[2 * s], pb[2 * s + 1]);
           }
         }
         }
