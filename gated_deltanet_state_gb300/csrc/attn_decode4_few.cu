@@ -64,6 +64,7 @@ __host__ __device__ inline FewStage few_stage(int d) {
 struct FewShared : DtItems {
   uint64_t full[kFewStages], empty[kFewStages];
   uint32_t have[kFewStages];            // blocks of a stage that were loaded
+  uint32_t issued;                      // stages whose loads have begun (one warp's stages)
   float2 stat[kFewWarps][kFewRows];     // a warp's offset and sum of each row
   uint4 q[8][32];                       // Q of row g, eight channels of a group, by lane
   float4 start[8][4];                   // a group's start values for rows 2 t, 2 t + 1 (twice, as a product's)
@@ -110,6 +111,27 @@ __device__ __forceinline__ float column_sum(float x) {
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+// Waits until the loads' warp has begun more than n stages.  A stage of one warp's
+// tokens serves warp after warp, and copies end in any order: only when its n-th
+// round has begun, which needs the round before to be consumed, does the parity of
+// its barrier tell the n-th from the one before.
+__device__ __forceinline__ bool few_issued(const uint32_t* issued, uint32_t n, volatile int* fail, long long limit) {
+  auto begun = [&]() {
+    uint32_t x;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];\n" : "=r"(x) : "r"(smem_u32(issued)) : "memory");
+    return x > n;
+  };
+  if (begun()) return true;
+  const long long t0 = clock64();
+  while (!begun()) {
+    if (*fail) return false;
+    if (clock64() - t0 > limit) {
+      *fail = 1;
+      return false;
+    }
+  }
+  return true;
 }
 // Barrier of the four warps, with a vote.
 __device__ __forceinline__ bool few_any(bool x) {
@@ -178,6 +200,7 @@ __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_
           const unsigned mine = have >> (c * kBlocks) & ((1u << kBlocks) - 1u);
           sh.have[st] = mine;
           tc::mbar_expect_tx(&sh.full[st], __popc(mine) * each);
+          if (kFewPer<GR> < kFewWarps) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;\n" ::"r"(smem_u32(&sh.issued)), "r"(loaded + 1) : "memory");
         }
         __syncwarp();
         if (from && blk / kBlocks == c) tc::bulk_load(base + (uint32_t)st * sg.bytes + to, from, n * size, &sh.full[st]);
@@ -206,6 +229,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], kFewPer<GR>);
     sh.fail = limit < 0;
+    sh.issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 0) dt_sums<kFewRows>(w, sh, lane);
@@ -237,6 +261,7 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
     int lim[2] = {};       // ... and the keys that they see
     bool ok = true;
     int st = warp / PER, ph = 0;   // (fewer than the stages there are)
+    uint32_t nth = warp;           // stages before this one
     DtItem u{};
     for (int i = i0; i < i1; ++i) {
       if (i == i0) u = dt_item<kFewRows>(w, sh.items, i);
@@ -300,7 +325,8 @@ __global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const 
       const int least = u.L - u.n + 1;   // keys that every row sees
 #pragma unroll 1
       for (int j = 0; j < u.tiles; ++j) {
-        ok = __all_sync(0xffffffffu, dt_wait(&sh.full[st], ph, fail, limit));
+        if constexpr (PER < kFewWarps) ok = few_issued(&sh.issued, nth, fail, limit), nth += kFewWarps;
+        ok = __all_sync(0xffffffffu, ok && dt_wait(&sh.full[st], ph, fail, limit));
         if (!ok) break;
         const uint8_t* stage = base + st * sg.bytes;
         const uint32_t stage_k = ring + st * sg.bytes + at_k;
