@@ -49,6 +49,8 @@ constexpr float kFewUnit = 16777216.f;               // the products count in 2^
 // issue what counts; one's above, so that three CTAs an SM hold some ahead.
 template <int GR>
 constexpr int kFewPer = GR <= 4 ? kFewWarps : 1;
+template <int GR>
+constexpr int kFewCtas = GR <= 2 ? 4 : 3;   // on an SM
 struct FewStage {
   uint32_t ks, v, vs, bytes;
 };
@@ -216,7 +218,7 @@ __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_
 
 // GR: groups of 32 channels (d up to 32 GR).
 template <int GR>
-__global__ void __launch_bounds__(kFewThreads, 3) attn_decode4_few_kernel(const DtParams w) {
+__global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_kernel(const DtParams w) {
   extern __shared__ uint8_t dyn[];
   const AttnDecodeParams& p = w.a;
   uint8_t* base = dyn + ((128u - (smem_u32(dyn) & 127u)) & 127u);
@@ -526,8 +528,8 @@ cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
   w.a = p;
   w.wait = dt_limit(p);
   w.row_lo = 1, w.row_hi = kFewRows;
-  // a third of 227 KB a CTA, of which 1 KB is the system's
-  const uint32_t all = 76800, red = kFewWarps * kFewWarps * 32 * sizeof(float4), misc = (uint32_t)sizeof(FewShared) + 256;
+  // a CTA's share of 228 KB, of which 1 KB is the system's
+  const uint32_t all = 233472 / kFewCtas<GR> - 1024, red = kFewWarps * kFewWarps * 32 * sizeof(float4), misc = (uint32_t)sizeof(FewShared) + 256;
   const FewStage sg = few_stage<GR>(p.c.d);
   const int stages = (int)((all - red - misc) / sg.bytes);
   w.k_stages = stages > kFewStages ? kFewStages : stages;
@@ -541,7 +543,7 @@ cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
     w.s0 = s0;
     w.ns = p.N - s0 < kDtSeqs ? p.N - s0 : kDtSeqs;
     const int64_t most = (int64_t)w.ns * p.max_pieces * p.c.Hkv;
-    attn_decode4_few_kernel<GR><<<(unsigned)(most < 3 * sms ? most : 3 * sms), kFewThreads, smem, st>>>(w);
+    attn_decode4_few_kernel<GR><<<(unsigned)(most < kFewCtas<GR> * sms ? most : kFewCtas<GR> * sms), kFewThreads, smem, st>>>(w);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
