@@ -46,8 +46,8 @@ struct D4Cfg {
   static constexpr int THREADS = SOFT + UNPACK + (CTAS == 1 ? 128 : 96);   // and K loads, V loads, products
   static constexpr uint32_t COLS = CTAS == 1 ? 512 : 256;
   static constexpr uint32_t O0 = 2 * NQ, R0 = O0 + 2 * NP; // tensor memory: scores of two tiles, O of 128 elements each, operands
-  static constexpr int SLOT = CH / 2, RING = (COLS - R0) / SLOT;   // columns of an operand, operands
-  static_assert(RING >= 2 && RING <= 8 && NT % SWG == 0 && CW % 8 == 0, "tensor memory");
+  static constexpr int SLOT = CH / 2, FIT = (COLS - R0) / SLOT, RING = FIT < 8 ? FIT : 8;   // columns of an operand, operands
+  static_assert(RING >= 2 && RING % UWG == 0 && NT % SWG == 0 && CW % 8 == 0, "tensor memory");
 };
 
 template <typename C>
@@ -702,6 +702,7 @@ cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, int hi, cudaStre
 }
 
 using Mid = D4Cfg<__nv_bfloat16, 16, 1, 1, 1, 1, 128, 2>;
+using Some = D4Cfg<__nv_bfloat16, 32, 1, 1, 2, 2, 64, 1>;
 using Many = D4Cfg<__nv_bfloat16, 96, 1, 1, 2, 2, 64, 1>;
 using Full8 = D4Cfg<float, 8, 3, 2, 1, 1, 128, 2>;
 
@@ -723,7 +724,7 @@ cudaError_t launch_attn_decode4_tc(const AttnDecodeParams& p, int dtype, cudaStr
   if (few) e = launch_attn_decode4_few(p, sms, st);
   if (e != cudaSuccess || most <= kD4Few) return e;
   const int lo = few ? kD4Few + 1 : 1;
-  return most <= 16 ? decode4<Mid>(p, sms, lo, kAll, st) : decode4<Many>(p, sms, lo, kAll, st);
+  return most <= 16 ? decode4<Mid>(p, sms, lo, kAll, st) : most <= 32 ? decode4<Some>(p, sms, lo, kAll, st) : decode4<Many>(p, sms, lo, kAll, st);
 }
 
 }  // namespace gdn
