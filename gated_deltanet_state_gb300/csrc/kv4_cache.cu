@@ -14,12 +14,25 @@ namespace {
 
 constexpr int kKv4Warps = 4;   // of a CTA
 
-// Lanes of a head at 8 elements each.
-template <int LPT>
-__device__ __forceinline__ uint32_t lanes_umax(uint32_t m) {
+// Largest of each of N values over the LPT lanes of a head, by halves: lane l ends
+// up with value l N / LPT's (LPT >= N).
+template <int LPT, int N>
+__device__ __forceinline__ uint32_t lanes_umax(const uint32_t (&in)[N], int l) {
+  uint32_t v[N];
 #pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+  for (int i = 0; i < N; ++i) v[i] = in[i];
+  int bit = LPT / 2;
+#pragma unroll
+  for (int half = N / 2; half >= 1; half >>= 1, bit >>= 1) {
+    const bool up = l & bit;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const uint32_t send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = max(keep, __shfl_xor_sync(0xffffffffu, send, bit));
+    }
+  }
+  for (; bit >= 1; bit >>= 1) v[0] = max(v[0], __shfl_xor_sync(0xffffffffu, v[0], bit));
+  return v[0];
 }
 
 // Eight consecutive elements of a row.
@@ -72,6 +85,10 @@ __device__ __forceinline__ uint32_t max8_finite(const Row8<T>& r) {
 // A scale, as quantising takes it.
 struct Scale {
   float inv, s;   // 0, 0: of NaN
+  // lane i's, of each `width` lanes
+  __device__ __forceinline__ Scale of(int i, int width) const {
+    return {__shfl_sync(0xffffffffu, inv, i, width), __shfl_sync(0xffffffffu, s, i, width)};
+  }
 };
 __device__ __forceinline__ Scale make_scale(uint32_t byte) {
   if (byte == kKv4Nan) return {0.f, 0.f};
@@ -116,7 +133,7 @@ struct AppendRun {
   const T* src;      // this lane's elements of the run's first row
   int64_t stride;
   int off, run, lane;   // lane within its head
-  bool on;              // whether the lane has elements
+  bool on, head;        // whether the lane has elements, and whether its head is one
 
   __device__ __forceinline__ bool has(int t) const { return t >= off && t < off + run; }
   __device__ __forceinline__ void load(Row8<T>& r, int t) const {
@@ -133,23 +150,19 @@ struct AppendRun {
     for (int i = 0; i < 4; ++i) load(r[i], t0 + i);
 #pragma unroll
     for (int i = 0; i < 4; ++i) m[i] = SAFE ? max8_finite(r[i]) : max8_bits(r[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = lanes_umax<4>(m[i]);
     const int q = lane & 3;
-    if (!SAFE) {
-      const uint32_t top = max(max(m[0], m[1]), max(m[2], m[3]));
-      if (__any_sync(0xffffffffu, top > __float_as_uint(kKv4Most))) return false;
-    }
-    uint32_t w[4], mine = 0;
+    const uint32_t top = lanes_umax<4>(m, q);   // of token t0 + q
+    if (!SAFE && __any_sync(0xffffffffu, top > __float_as_uint(kKv4Most))) return false;
+    const uint32_t mine = top == ~0u ? kKv4Nan : kv4_byte(top);
+    const Scale own = make_scale(mine);
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t b = m[i] == ~0u ? kKv4Nan : kv4_byte(m[i]);
-      const Scale s = make_scale(b);
+      const Scale s = own.of(i, 4);
       uint32_t x = 0u - word_bias();
 #pragma unroll
       for (int e = 0; e < 8; ++e) x += code_bits<SAFE>(r[i].get(e), s, T()) << word_shift(e);
       w[i] = x;
-      if (i == q) mine = b;
     }
     kv4_transpose(w, q);
     if (on && has(t0 + q)) {
@@ -167,51 +180,80 @@ struct AppendRun {
     }
   }
 
-  // V: codes [d][8 B], scales [16].  Eight tokens at a time, a word of each
-  // channel; a word with other tokens in it is merged with what it holds.
+  // V: codes [d][8 B], scales [16].  Eight tokens at a time, a word of each channel.
   template <bool SAFE>
-  __device__ __forceinline__ bool v_tokens(uint8_t* codes, uint8_t* scales, int t0) const {
+  __device__ __forceinline__ bool v_tokens(uint8_t* scales, int t0, uint32_t (&w)[8]) const {
     Row8<T> r[8];
     uint32_t m[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) load(r[i], t0 + i);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m[i] = SAFE ? max8_finite(r[i]) : max8_bits(r[i]);
+    // lane l of a head: token t0 + l / STEP (of four lanes each has two)
+    constexpr int N = LPT < 8 ? LPT : 8, STEP = LPT / N;
+    Scale own[8 / N];
+    uint32_t mine[8 / N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = lanes_umax<LPT>(m[i]);
-    if (!SAFE) {
-      uint32_t top = 0;
+    for (int k = 0; k < 8 / N; ++k) {
+      uint32_t part[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, m[i]);
-      if (__any_sync(0xffffffffu, top > __float_as_uint(kKv4Most))) return false;
+      for (int i = 0; i < N; ++i) part[i] = m[k * N + i];
+      const uint32_t top = lanes_umax<LPT>(part, lane);
+      if (!SAFE && __any_sync(0xffffffffu, top > __float_as_uint(kKv4Most))) return false;
+      mine[k] = top == ~0u ? kKv4Nan : kv4_byte(top);
+      own[k] = make_scale(mine[k]);
     }
-    uint32_t w[8], keep = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = 0u - word_bias();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t b = m[i] == ~0u ? kKv4Nan : kv4_byte(m[i]);
-      const Scale s = make_scale(b);
+      const Scale s = own[i / N].of(i % N * STEP, LPT);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] += code_bits<SAFE>(r[i].get(e), s, T()) << word_shift(i);
-      if (!has(t0 + i)) keep |= 15u << word_shift(i);
-      else if (lane == 0 && on) scales[t0 + i] = (uint8_t)b;
     }
-    if (on) {
+#pragma unroll
+    for (int k = 0; k < 8 / N; ++k) {
+      const int at = t0 + k * N + lane / STEP;
+      if (head && lane % STEP == 0 && has(at)) scales[at] = (uint8_t)mine[k];
+    }
+    return true;
+  }
+  __device__ __forceinline__ void v(uint8_t* codes, uint8_t* scales) const {
+    if (run == kKvBlock) {
+      uint32_t w[2][8];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (!v_tokens<false>(scales, 8 * k, w[k])) v_tokens<true>(scales, 8 * k, w[k]);
+      // a lane's 64 bytes, 16 at a time to four lanes, so that four write 64 in a row
+      const int q = lane & 3;
+      uint32_t to[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // word k of each 16 bytes: channels 2 i, 2 i + 1, tokens 0 .. 7, 8 .. 15
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[k][i] = w[k & 1][2 * i + (k >> 1)];
+        kv4_transpose(to[k], q);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (on) *reinterpret_cast<uint4*>(codes + ((lane & ~3) + i) * 64 + q * 16) = make_uint4(to[0][i], to[1][i], to[2][i], to[3][i]);
+      return;
+    }
+    // a word with other tokens in it is merged with what it holds
+#pragma unroll 1
+    for (int t0 = 0; t0 < kKvBlock; t0 += 8) {
+      if (off >= t0 + 8 || off + run <= t0) continue;
+      uint32_t w[8], keep = 0;
+      if (!v_tokens<false>(scales, t0, w)) v_tokens<true>(scales, t0, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (!has(t0 + i)) keep |= 15u << word_shift(i);
+      if (!on) continue;
       uint32_t* to = reinterpret_cast<uint32_t*>(codes + lane * 64 + t0 / 2);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (keep) w[e] = (w[e] & ~keep) | (to[2 * e] & keep);
         to[2 * e] = w[e];
       }
-    }
-    return true;
-  }
-  __device__ __forceinline__ void v(uint8_t* codes, uint8_t* scales) const {
-#pragma unroll 1
-    for (int t0 = 0; t0 < kKvBlock; t0 += 8) {
-      if (off >= t0 + 8 || off + run <= t0) continue;
-      if (!v_tokens<false>(codes, scales, t0)) v_tokens<true>(codes, scales, t0);
     }
   }
 };
@@ -235,7 +277,8 @@ __global__ void __launch_bounds__(32 * kKv4Warps) kv4_append_kernel(const KvAppe
   unsigned starts = __ballot_sync(0xffffffffu, lane < W && slot >= 0) & ~cont;
   AppendRun<T, LPT> a;
   a.lane = lane % LPT;
-  a.on = a.lane * 8 < d && h < p.c.Hkv;
+  a.head = h < p.c.Hkv;
+  a.on = a.lane * 8 < d && a.head;
   a.stride = is_v ? p.v_stride : p.k_stride;
   const T* rows = static_cast<const T*>(is_v ? p.v : p.k) + t0 * a.stride + (int64_t)h * d + a.lane * 8;
   for (; starts; starts &= starts - 1) {
