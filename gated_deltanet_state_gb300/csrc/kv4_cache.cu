@@ -141,13 +141,10 @@ struct AppendRun {
     if (on && has(t)) r.load(src + (int64_t)(t - off) * stride);
   }
 
-  // K: codes [d/32][16][16 B], scales [d/32][16].  Four tokens at a time.
+  // K: codes [d/32][16][16 B], scales [d/32][16].  Four tokens at a time, eight loaded.
   template <bool SAFE>
-  __device__ __forceinline__ bool k_tokens(uint8_t* codes, uint8_t* scales, int t0) const {
-    Row8<T> r[4];
+  __device__ __forceinline__ bool k_tokens(uint8_t* codes, uint8_t* scales, int t0, const Row8<T>* r) const {
     uint32_t m[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load(r[i], t0 + i);
 #pragma unroll
     for (int i = 0; i < 4; ++i) m[i] = SAFE ? max8_finite(r[i]) : max8_bits(r[i]);
     const int q = lane & 3;
@@ -174,9 +171,15 @@ struct AppendRun {
   }
   __device__ __forceinline__ void k(uint8_t* codes, uint8_t* scales) const {
 #pragma unroll 1
-    for (int t0 = 0; t0 < kKvBlock; t0 += 4) {
-      if (off >= t0 + 4 || off + run <= t0) continue;
-      if (!k_tokens<false>(codes, scales, t0)) k_tokens<true>(codes, scales, t0);
+    for (int t0 = 0; t0 < kKvBlock; t0 += 8) {
+      if (off >= t0 + 8 || off + run <= t0) continue;
+      Row8<T> r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load(r[i], t0 + i);
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        if (off < t0 + i + 4 && off + run > t0 + i)
+          if (!k_tokens<false>(codes, scales, t0 + i, r + i)) k_tokens<true>(codes, scales, t0 + i, r + i);
     }
   }
 
@@ -262,7 +265,7 @@ struct AppendRun {
 
 // New rows into the cache.  Window w of W rows; grid y: K or V of 32 / LPT heads.
 template <typename T, int LPT, int W>
-__global__ void __launch_bounds__(32 * kKv4Warps) kv4_append_kernel(const KvAppendParams p) {
+__global__ void __launch_bounds__(32 * kKv4Warps, sizeof(T) == 2 ? 5 : 4) kv4_append_kernel(const KvAppendParams p) {
   constexpr int HPW = 32 / LPT;
   const int lane = threadIdx.x & 31, sub = lane / LPT;
   const int64_t t0 = ((int64_t)blockIdx.x * kKv4Warps + (threadIdx.x >> 5)) * W;
