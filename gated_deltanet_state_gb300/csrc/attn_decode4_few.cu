@@ -50,6 +50,8 @@ constexpr float kFewUnit = 16777216.f;               // the products count in 2^
 template <int GR>
 constexpr int kFewPer = GR <= 4 ? kFewWarps : 1;
 template <int GR>
+constexpr bool kFewBulk = kFewPer<GR> < kFewWarps;   // scales in bulk copies
+template <int GR>
 constexpr int kFewCtas = GR <= 2 ? 4 : 3;   // on an SM
 struct FewStage {
   uint32_t ks, v, vs, bytes;
@@ -148,20 +150,28 @@ __device__ __forceinline__ bool few_any(bool x) {
   return r != 0;
 }
 
-// The loads of the CTA's items [i0, i1): lane 8 x + b has part x (K's codes and
-// scales, V's) of a tile's block b; blocks of a stage that lie one after another in a
-// page (all of them, in pages of whole tiles) come in one copy.  Returns the stages
-// loaded.
+// The loads of the CTA's items [i0, i1).  Bulk copies, which the lanes with one issue in
+// turn: lane 8 x + b has part x (K's codes, V's, K's scales, V's) of a tile's block b and
+// of the blocks of the stage that follow it in its page (all, in pages of whole tiles).
+// In stages of a whole tile the scales come 16 bytes a lane instead, all at once: bulk
+// copies of them keep the issue busy where pages are small (64 sequences, 8 kv heads, d =
+// 64, pages of 16: 104 us with, 92 without; at d = 256, where a stage is a warp's, 373
+// with, 385 without).  Returns the stages loaded.
 template <int GR>
 __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_t* base, int i0, int i1, int lane) {
   const AttnDecodeParams& p = w.a;
   volatile int* fail = &sh.fail;
   constexpr int kBlocks = kFewPer<GR> * kFewBlocks;   // of a stage
-  const int ST = w.k_stages, d = p.c.d, part = lane >> 3, blk = lane & 7;
+  const int ST = w.k_stages, d = p.c.d, part = lane >> 3, blk = lane & 7, groups = d / kKv4Group;
   const FewStage sg = few_stage<GR>(d);
-  const uint32_t codes = kv4_codes(d), scales = kv4_k_scales(d), each = 2 * codes + scales + kKvBlock;
-  const uint32_t size = part == 1 ? scales : part == 3 ? kKvBlock : codes;
-  const uint32_t to = (part == 0 ? 0u : part == 1 ? sg.ks : part == 2 ? sg.v : sg.vs) + blk % kBlocks * size;
+  const uint32_t codes = kv4_codes(d), scales = kv4_k_scales(d);
+  const uint32_t size = part < 2 ? codes : part == 2 ? scales : kKvBlock;
+  const uint32_t to = (part == 0 ? 0u : part == 1 ? sg.v : part == 2 ? sg.ks : sg.vs) + blk % kBlocks * size;
+  // this lane's 16 bytes of scales: the i-th group of K's of a block, or V's after those
+  constexpr int kScales = (kBlocks * (GR + 1) + 31) / 32;
+  int sblk[kScales], sgrp[kScales];
+#pragma unroll
+  for (int k = 0; k < kScales; ++k) sblk[k] = (lane + 32 * k) / (groups + 1), sgrp[k] = (lane + 32 * k) % (groups + 1);
   int loaded = 0, st = 0, ph = 0;
   bool ok = true;
   DtItem t{};
@@ -189,10 +199,10 @@ __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_
       const unsigned stop = (first | ~have) >> (blk + 1);
       const int n = min((int)kDtBlocks - blk, __ffs(stop));
       const uint8_t* from = nullptr;
-      if (first >> blk & 1)
+      if ((first >> blk & 1) && (kFewBulk<GR> || part < 2))
         from = part == 0   ? kv4_k_block(p.c, page, t.h, b)
-               : part == 1 ? kv4_k_scale(p.c, page, t.h, b)
-               : part == 2 ? kv4_v_block(p.c, page, t.h, b)
+               : part == 1 ? kv4_v_block(p.c, page, t.h, b)
+               : part == 2 ? kv4_k_scale(p.c, page, t.h, b)
                            : kv4_v_scale(p.c, page, t.h, b);
 #pragma unroll 1
       for (int c = 0; c < kDtBlocks / kBlocks; ++c) {
@@ -201,16 +211,30 @@ __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_
         if (lane == 0) {
           const unsigned mine = have >> (c * kBlocks) & ((1u << kBlocks) - 1u);
           sh.have[st] = mine;
-          tc::mbar_expect_tx(&sh.full[st], __popc(mine) * each);
-          if (kFewPer<GR> < kFewWarps) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;\n" ::"r"(smem_u32(&sh.issued)), "r"(loaded + 1) : "memory");
+          tc::mbar_expect_tx(&sh.full[st], __popc(mine) * (2 * codes + (kFewBulk<GR> ? scales + kKvBlock : 0)));
+          if (kFewBulk<GR>) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;\n" ::"r"(smem_u32(&sh.issued)), "r"(loaded + 1) : "memory");
         }
         __syncwarp();
-        if (from && blk / kBlocks == c) tc::bulk_load(base + (uint32_t)st * sg.bytes + to, from, n * size, &sh.full[st]);
+        uint8_t* stage = base + (uint32_t)st * sg.bytes;
+        if (from && blk / kBlocks == c) tc::bulk_load(stage + to, from, n * size, &sh.full[st]);
+        if constexpr (!kFewBulk<GR>) {
+#pragma unroll
+          for (int k = 0; k < kScales; ++k) {
+            const int of = c * kBlocks + sblk[k], pg = __shfl_sync(0xffffffffu, page, of & 7), pb = __shfl_sync(0xffffffffu, b, of & 7);
+            if (sblk[k] < kBlocks && (have >> of & 1)) {
+              if (sgrp[k] < groups) cp_async16(stage + sg.ks + sblk[k] * scales + sgrp[k] * 16, kv4_k_scale(p.c, pg, t.h, pb) + sgrp[k] * 16, 16);
+              else cp_async16(stage + sg.vs + sblk[k] * kKvBlock, kv4_v_scale(p.c, pg, t.h, pb), 16);
+            }
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(&sh.full[st])) : "memory");
+        }
         ++loaded;
         if (++st == ST) st = 0, ph ^= 1;
       }
     }
   }
+  cp_async_commit();
+  cp_async_wait<0>();
   return loaded;
 }
 
@@ -229,7 +253,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
   const long long limit = w.wait;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < ST; ++i) tc::mbar_init(&sh.full[i], 1), tc::mbar_init(&sh.empty[i], kFewPer<GR>);
+    for (int i = 0; i < ST; ++i) tc::mbar_init(&sh.full[i], kFewBulk<GR> ? 1 : 33), tc::mbar_init(&sh.empty[i], kFewPer<GR>);   // (33: a lane's own copies each)
     sh.fail = limit < 0;
     sh.issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
