@@ -30,15 +30,18 @@ namespace {
 constexpr float kTop = 15.75f;
 constexpr float kCodes = 16777216.f;   // the outputs' products count in 2^-24
 constexpr float kUnset = 3e38f;        // the offset of a row that has seen no key
+// Channels of K, or tokens of V, of an operand: 64 columns of tensor memory.  (64 of
+// them, so twice the operands in twice the places: 16 drafts of 16 rows 236 us, 214.)
+constexpr int kChunk = 128;
 
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
 
 // NT rows a tile, QP parts of Q and PP of P side by side as columns, SWG softmax
-// and UWG unpacking warpgroups, operands of CH tokens or channels, CTAS on an SM.
-template <typename T_, int NT_, int QP_, int PP_, int SWG_, int UWG_, int CH_, int CTAS_>
+// and UWG unpacking warpgroups, CTAS on an SM.
+template <typename T_, int NT_, int QP_, int PP_, int SWG_, int UWG_, int CTAS_>
 struct D4Cfg {
   using T = T_;
-  static constexpr int NT = NT_, QP = QP_, PP = PP_, SWG = SWG_, UWG = UWG_, CH = CH_, CTAS = CTAS_;
+  static constexpr int NT = NT_, QP = QP_, PP = PP_, SWG = SWG_, UWG = UWG_, CTAS = CTAS_;
   static constexpr float BASE = sizeof(T) == 2 ? 10.f : 12.f;
   static constexpr int CW = NT / SWG;                      // columns (rows) of a softmax warpgroup
   static constexpr int NQ = round16(NT * QP), NP = round16(NT * PP);
@@ -46,7 +49,7 @@ struct D4Cfg {
   static constexpr int THREADS = SOFT + UNPACK + (CTAS == 1 ? 128 : 96);   // and K loads, V loads, products
   static constexpr uint32_t COLS = CTAS == 1 ? 512 : 256;
   static constexpr uint32_t O0 = 2 * NQ, R0 = O0 + 2 * NP; // tensor memory: scores of two tiles, O of 128 elements each, operands
-  static constexpr int SLOT = CH / 2, FIT = (COLS - R0) / SLOT, RING = FIT < 8 ? FIT : 8;   // columns of an operand, operands
+  static constexpr int SLOT = kChunk / 2, FIT = (COLS - R0) / SLOT, RING = FIT < 8 ? FIT : 8;   // columns of an operand, operands
   static_assert(RING >= 2 && RING % UWG == 0 && NT % SWG == 0 && CW % 8 == 0, "tensor memory");
 };
 
@@ -217,8 +220,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
   D4Shared<C>& sh = *reinterpret_cast<D4Shared<C>*>(base + w.misc_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d, quad = warp & 3;
   const int KS = w.k_stages, VS = w.v_stages;
-  constexpr int CH = C::CH, VC = 128 / CH;
-  const int nk = (d + CH - 1) / CH, halves = (d + 127) / 128;   // operands of K, and of V (VC for each half), a tile
+  const int halves = (d + kChunk - 1) / kChunk;   // operands of K, and of V, a tile
   volatile int* fail = &sh.fail;
   const long long limit = w.wait;
 
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
   int loaded = 0;                               // tiles loaded (a loading warp's)
 
   if (warp >= SW + UW) {
-    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
     if (warp < SW + UW + 2) {
       // ---- loads, a warp for K and one for V ----
       loaded = d4_load<NT>(w, sh, base, i0, i1, warp == SW + UW + 1, lane);
@@ -269,9 +271,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         if (!all(dt_wait(&sh.a_full[r], rp, fail, limit))) return false;
         tc::fence_after_sync();
         const uint32_t a = tb + C::R0 + r * C::SLOT;
-        if (steps == CH / 16) {
+        if (steps == kChunk / 16) {
 #pragma unroll
-          for (int k = 0; k < CH / 16; ++k) tc::mma_bf16_ts_if(lead, dst, a + 8 * k, b + 16 * k, id, acc || k != 0);
+          for (int k = 0; k < kChunk / 16; ++k) tc::mma_bf16_ts_if(lead, dst, a + 8 * k, b + 16 * k, id, acc || k != 0);
         } else {
           for (int k = 0; k < steps; ++k) tc::mma_bf16_ts_if(lead, dst, a + 8 * k, b + 16 * k, id, acc || k != 0);
         }
@@ -280,8 +282,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         return true;
       };
       auto qk = [&](unsigned tt) {
-        for (int c = 0; c < nk; ++c)
-          if (!operand(tb + (tt & 1) * C::NQ, qd + c * CH, id_qk, min(CH, d - c * CH) / 16, c != 0)) return false;
+        for (int c = 0; c < halves; ++c)
+          if (!operand(tb + (tt & 1) * C::NQ, qd + c * kChunk, id_qk, min(kChunk, d - c * kChunk) / 16, c != 0)) return false;
         tc::mma_commit_if(lead, &sh.s_full[tt & 1]);
         return true;
       };
@@ -297,9 +299,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           ok = ok && all(dt_wait(&sh.p_full[T & 1], (T >> 1) & 1, fail, limit));
           if (!ok) break;
           tc::fence_after_sync();
-          for (int c = 0; ok && c < VC; ++c)
-            for (int hf = 0; ok && hf < halves; ++hf)
-              ok = operand(tb + C::O0 + hf * C::NP, pd + (T & 1) * (C::NP * kDtTok * 2 / 16) + c * CH, id_pv, CH / 16, j != 0 || c != 0);
+          for (int hf = 0; ok && hf < halves; ++hf)
+            ok = operand(tb + C::O0 + hf * C::NP, pd + (T & 1) * (C::NP * kDtTok * 2 / 16), id_pv, kDtTok / 16, j != 0);
           tc::mma_commit_if(lead, &sh.o_done[T & 1]);
         }
       }
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
     }
   } else if (warp >= SW) {
     // ---- codes to operands: a thread a row of them, K's tokens or V's channels ----
-    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
     const int wg = (warp - SW) >> 2, row = quad * 32 + lane;
     const uint32_t lanes = tb + C::R0 + ((uint32_t)quad << 21);
     const uint8_t *kr = base + w.k_off, *vr = base + w.v_off;
@@ -343,18 +344,18 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           ok = __all_sync(0xffffffffu, dt_wait(&sh.k_full[ks], kp, fail, limit));
           const uint8_t* blk = kr + (uint32_t)ks * k_unit + (row >> 4) * codes + (row & 15) * 16;
           const uint8_t* sc = kr + (uint32_t)ks * k_unit + kDtBlocks * codes + (row >> 4) * kv4_k_scales(d) + (row & 15);
-          for (int c = 0; ok && c < nk; ++c, next()) {
+          for (int c = 0; ok && c < halves; ++c, next()) {
             if (!mine()) continue;
-            const int groups = min(CH, d - c * CH) / kKv4Group;
-            uint4 x[CH / 32];
-            uint32_t s[CH / 32];
+            const int groups = min(kChunk, d - c * kChunk) / kKv4Group;
+            uint4 x[kChunk / 32];
+            uint32_t s[kChunk / 32];
 #pragma unroll
-            for (int g = 0; g < CH / 32; ++g)
-              if (g < groups) x[g] = *reinterpret_cast<const uint4*>(blk + (c * (CH / 32) + g) * 256), s[g] = sc[(c * (CH / 32) + g) * 16];
+            for (int g = 0; g < kChunk / 32; ++g)
+              if (g < groups) x[g] = *reinterpret_cast<const uint4*>(blk + (c * (kChunk / 32) + g) * 256), s[g] = sc[(c * (kChunk / 32) + g) * 16];
             ok = free_wait();
             if (!ok) break;
 #pragma unroll
-            for (int g = 0; g < CH / 32; ++g)
+            for (int g = 0; g < kChunk / 32; ++g)
               if (g < groups) {
                 const uint32_t s1 = kv4_scale_bf16(s[g]), s2 = s1 << 16 | s1, off = kv4_offset(s2);
                 uint32_t y[16];
@@ -371,29 +372,28 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         if (ok && j > 0) {
           ok = __all_sync(0xffffffffu, dt_wait(&sh.v_full[vs], vp, fail, limit));
           const uint8_t* blk = vr + (uint32_t)vs * v_unit + row * 8;
-          for (int c = 0; ok && c < VC; ++c)
-            for (int hf = 0; ok && hf < halves; ++hf, next()) {
-              if (!mine()) continue;
-              const bool live = hf * 128 + quad * 32 < d;   // (channels past the head's: rows of O that no one reads)
-              uint2 x[CH / 16];
+          for (int hf = 0; ok && hf < halves; ++hf, next()) {
+            if (!mine()) continue;
+            const bool live = hf * 128 + quad * 32 < d;   // (channels past the head's: rows of O that no one reads)
+            uint2 x[kDtBlocks];
 #pragma unroll
-              for (int b = 0; b < CH / 16; ++b)
-                if (live) x[b] = *reinterpret_cast<const uint2*>(blk + (c * (CH / 16) + b) * codes + hf * 1024);
-              ok = free_wait();
-              if (!ok) break;
-              if (live) {
+            for (int b = 0; b < kDtBlocks; ++b)
+              if (live) x[b] = *reinterpret_cast<const uint2*>(blk + b * codes + hf * 1024);
+            ok = free_wait();
+            if (!ok) break;
+            if (live) {
 #pragma unroll
-                for (int g = 0; g < CH / 32; ++g) {
-                  uint32_t y[4][4], z[16];
+              for (int g = 0; g < kChunk / 32; ++g) {
+                uint32_t y[4][4], z[16];
 #pragma unroll
-                  for (int u = 0; u < 4; ++u) kv4_halves(u & 1 ? x[2 * g + (u >> 1)].y : x[2 * g + (u >> 1)].x, y[u]);
+                for (int u = 0; u < 4; ++u) kv4_halves(u & 1 ? x[2 * g + (u >> 1)].y : x[2 * g + (u >> 1)].x, y[u]);
 #pragma unroll
-                  for (int u = 0; u < 16; ++u) z[u] = y[u >> 2][u & 3];
-                  tc::tmem_st16u(lanes + r * C::SLOT + g * 16, z);
-                }
+                for (int u = 0; u < 16; ++u) z[u] = y[u >> 2][u & 3];
+                tc::tmem_st16u(lanes + r * C::SLOT + g * 16, z);
               }
-              done();
             }
+            done();
+          }
           __syncwarp();
           if (lane == 0) dt_arrive(&sh.v_empty[vs]);
           if (++vs == VS) vs = 0, vp ^= 1;
@@ -701,10 +701,10 @@ cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, int hi, cudaStre
   return cudaSuccess;
 }
 
-using Mid = D4Cfg<__nv_bfloat16, 16, 1, 1, 1, 1, 128, 2>;
-using Some = D4Cfg<__nv_bfloat16, 32, 1, 1, 2, 2, 64, 1>;
-using Many = D4Cfg<__nv_bfloat16, 96, 1, 1, 2, 2, 64, 1>;
-using Full8 = D4Cfg<float, 8, 3, 2, 1, 1, 128, 2>;
+using Mid = D4Cfg<__nv_bfloat16, 16, 1, 1, 1, 1, 2>;
+using Some = D4Cfg<__nv_bfloat16, 32, 1, 1, 2, 2, 1>;
+using Many = D4Cfg<__nv_bfloat16, 96, 1, 1, 2, 2, 1>;
+using Full8 = D4Cfg<float, 8, 3, 2, 1, 1, 2>;
 
 }  // namespace
 
