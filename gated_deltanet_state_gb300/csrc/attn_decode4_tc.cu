@@ -103,12 +103,15 @@ __device__ __forceinline__ void split_pairs(float a, float b, uint32_t (&w)[PART
 template <int CW, int NT, int PARTS>
 __device__ __forceinline__ void read_columns(uint32_t col, float (&x)[CW]) {
   if constexpr (PARTS == 1 && CW % 16 == 0) {
+    uint32_t v[CW / 16][16];   // all loads, then one wait
 #pragma unroll
-    for (int k = 0; k < CW; k += 16) {
-      float v[16];
-      tc::tmem_ld16(col + k, v);
+    for (int k = 0; k < CW / 16; ++k) tc::tmem_ld16_nowait(col + 16 * k, v[k]);
+    tc::tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[k + i] = v[i];
+    for (int k = 0; k < CW / 16; ++k) {
+      tc::tmem_ld_fence(v[k]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[16 * k + i] = __uint_as_float(v[k][i]);
     }
   } else if constexpr (CW == 8) {
     float v[16];
