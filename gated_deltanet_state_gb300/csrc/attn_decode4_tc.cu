@@ -476,18 +476,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       for (int j = 0; j < t.tiles; ++j, ++T) {
         const int kb = t.k0 + j * kDtTok, pos = kb + tid;
         const uint32_t scol = lanes + (T & 1) * C::NQ + c0;
-        ok = dt_wait(&sh.v_full[st], vp, fail, limit) && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail, limit);
-        __syncwarp();
-        tc::fence_after_sync();
+        // V's part first: it is there before the scores
+        ok = dt_wait(&sh.v_full[st], vp, fail, limit);
         const float vscale = kv4_scale((base + w.v_off + (uint32_t)st * v_unit + kDtBlocks * codes)[tid]);
         const bool valid = pos < t.k1 && (sh.have[st] >> (tid >> 4) & 1);
+        __syncwarp();
+        if (lane == 0) dt_arrive(&sh.v_empty[st]);
         // of this token: the exponent of its V scale, and what undoes it in the sums of
         // weights (a NaN scale makes weights NaN; masked ones stay 0)
         const float lv = __log2f(vscale) - (tid & 2 ? 4.f : 0.f);
         const float rv = vscale == vscale ? __fdividef(tid & 2 ? 16.f : 1.f, vscale) : 1.f;
-        __syncwarp();
-        if (lane == 0) dt_arrive(&sh.v_empty[st]);
         const bool part = !__all_sync(0xffffffffu, valid), edge = kb + kDtTok > least;   // some row does not see some token
+        ok = ok && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail, limit);
+        __syncwarp();
+        tc::fence_after_sync();
         float x[CW];
         // s + log2(vs) + off, where off is the rows' offsets or nothing; masked -inf
         auto scores = [&](bool against) {
@@ -509,10 +511,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           }
         };
         scores(true);
-        float top = x[0];
+        float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int k = 1; k < CW; ++k) top = fmaxf(top, x[k]);
-        if (soft_any<C::SOFT>(top > kTop || !ok)) {
+        for (int k = 4; k < CW; ++k) top[k & 3] = fmaxf(top[k & 3], x[k]);
+        if (soft_any<C::SOFT>(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kTop || !ok)) {
           // a row's first keys, or one far above its reference (or a wait that ran
           // out): a row's reference moves by that row's scores alone
           scores(false);
