@@ -11,11 +11,12 @@
 //
 //   S^T [16 tokens x 8 rows] = K Q^T,    O^T [16 channels x 8 rows] += V^T P^T
 //
-// Codes are f16 subnormals as they stand: four of a word's eight after one mask,
-// n 2^-24 (pairs 0 and 2) or n 2^-20 (pairs 1 and 3, whose partners in Q and P
-// carry 2^-4).  K's offset of 8 is in the products' start value, -8 sum(q) of a
-// group of 32 channels; a group's product is its own and is added under its
-// tokens' scales in fp32.  V's is taken off in f16 (exact).  Which channel or token
+// K's codes are f16 subnormals as they stand: four of a word's eight after one mask,
+// n 2^-24 (pairs 0 and 2) or n 2^-20 (pairs 1 and 3, whose partners in Q carry
+// 2^-4).  Their offset of 8 is in the products' start value, -8 sum(q) of a group of
+// 32 channels; a group's product is its own and is added under its tokens' scales in
+// fp32.  V's are whole numbers in f16, less 8 (pairs 1 and 3 sixteenfold, whose
+// weights carry 2^-4).  Which channel or token
 // stands in which step of a product is chosen so that a lane's word is its operand:
 // a lane holds eight channels of K, or eight tokens of V.
 //
@@ -42,7 +43,7 @@ constexpr int kFewTok = kDtTok / kFewWarps, kFewBlocks = kFewTok / kKvBlock;    
 constexpr int kFewStages = 8;
 constexpr float kFewBase = 10.f, kFewTop = 15.75f;   // a weight at its reference is 2^10, none passes 2^15.75
 constexpr float kFewUnset = 3e38f;                   // the offset of a row that has seen no key
-constexpr float kFewUnit = 16777216.f;               // the products count in 2^-24
+constexpr float kFewUnit = 16777216.f;               // the scores' products count in 2^-24
 
 // A stage holds the tokens of CPS warps: K's codes, K's scales, V's codes, V's scales,
 // as they lie in pages.  All four warps' up to d = 128, where a copy is short and its
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
         for (int v = 0; v < kFewWarps; ++v) {
           const float f = dt_ex2(least_off - s[v].x);
           sum[h] = fmaf(s[v].y, f, sum[h]);
-          if (v == warp) mine[h] = f * kFewUnit;
+          if (v == warp) mine[h] = f;
         }
         const int row = col / p.G;
         rh[h] = (int64_t)(u.q0 + row) * p.Hq + u.h * p.G + col - row * p.G;

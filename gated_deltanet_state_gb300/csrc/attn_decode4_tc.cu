@@ -7,8 +7,8 @@
 // codes and the products, one that unpacks codes of shared memory into operands
 // there, one that makes the weights.  A code under its scale is exact in bf16, so
 // K enters as it is cached, in bf16, and Q as it is given (fp32 rows in three bf16
-// parts, which hold their 24 bits).  V's codes enter as whole numbers, subnormals
-// of f16; V's scale, one for a token and head, goes into the token's weight, an
+// parts, which hold their 24 bits).  V's codes enter as whole numbers in
+// f16; V's scale, one for a token and head, goes into the token's weight, an
 // f16 (two parts for fp32 rows).
 //
 // A weight times its V scale is 2^(s + log2(vs) - M) for a reference M of its row:
@@ -28,7 +28,6 @@ namespace {
 // A weight at its row's reference is 2^BASE, and none passes 2^kTop (f16 ends at
 // 2^16); a token whose codes stand four bits up (kv4_halves) has 2^-4 of that.
 constexpr float kTop = 15.75f;
-constexpr float kCodes = 16777216.f;   // the outputs' products count in 2^-24
 constexpr float kUnset = 3e38f;        // the offset of a row that has seen no key
 // Channels of K, or tokens of V, of an operand: 64 columns of tensor memory.  (64 of
 // them, so twice the operands in twice the places: 16 drafts of 16 rows 236 us, 214.)
@@ -635,10 +634,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
               if (k0 + k < rows) {
                 const uint32_t at = sh.out[was][c0 + k0 + k] * (uint32_t)d;   // at most 32 rows of 1,024 heads of 256 elements
                 if (p.part_o) {
-                  po[at] = o[k] * kCodes;
+                  po[at] = o[k];
                 } else {
                   const float sum = u.tiles > 0 ? total(c0 + k0 + k) : 0.f;
-                  oo[at] = from_f32<E>(sum == 0.f ? 0.f : o[k] * kCodes / sum);
+                  oo[at] = from_f32<E>(sum == 0.f ? 0.f : o[k] / sum);
                 }
               }
             }
