@@ -121,6 +121,8 @@ inline int64_t prefill_grid(AttnPrefillParams& p, int rows, int times) {
 // draft's take 1,024, and 2,048 from 8,192 keys on (16 drafts of 16 rows over
 // 2,048 to 32,768 keys: 262 us with 1,024, 226 with 2,048); beyond 38,912
 // tokens 76 pieces a head are one CTA on each of the 152 SMs for two kv heads.
+// Over 4 bits, half the keys' bytes, a few rows' pieces are of 1,024 keys from 2,048
+// on, so that the outputs' share is the same.
 constexpr int kMaxPieces = 76;
 constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows
 __host__ __device__ inline int decode_piece_target(int tiles, int rows, int bits) {   // pieces aimed at

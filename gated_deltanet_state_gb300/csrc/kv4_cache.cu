@@ -264,6 +264,12 @@ struct AppendRun {
 }  // namespace
 
 // New rows into the cache.  Window w of W rows; grid y: K or V of 32 / LPT heads.
+// A head's rows are read once; a group's or row's largest value is a maximum over
+// lanes, and codes leave as whole words: K's word of eight channels is a lane's own,
+// V's of eight tokens are formed in the lane that has their channel.  29,500 rows of
+// 4 heads, d = 256, bf16 (139.5 MB, 20.5 us of memory): 34.8 us, five CTAs an SM; a
+// warp's time goes to waits for its loads (36 %), and the 3,384 CTAs
+// take 4.5 rounds of what is resident.  CTAs of 1 or 2 warps: the same.
 template <typename T, int LPT, int W>
 __global__ void __launch_bounds__(32 * kKv4Warps, sizeof(T) == 2 ? 5 : 4) kv4_append_kernel(const KvAppendParams p) {
   constexpr int HPW = 32 / LPT;
@@ -306,6 +312,9 @@ namespace {
 template <typename T, int LPT>
 cudaError_t append4_rows(const KvAppendParams& p, cudaStream_t st) {
   const unsigned gy = 2u * ((p.c.Hkv + 32 / LPT - 1) / (32 / LPT));
+  // Few rows are often each of a sequence of their own, and a window's runs go one
+  // after another: 256 such rows 6.2 us in windows of 1, 35.9 of 16 (2 and 4: 8.3, 11.8);
+  // 2,048 rows in one run 8.1 and 4.5 us, 8,192 rows 22.7 and 8.7 (4 heads, d = 256, bf16).
   if (p.T <= 2048) kv4_append_kernel<T, LPT, 1><<<dim3((unsigned)((p.T + kKv4Warps - 1) / kKv4Warps), gy), 32 * kKv4Warps, 0, st>>>(p);
   else kv4_append_kernel<T, LPT, 16><<<dim3((unsigned)((p.T + 16 * kKv4Warps - 1) / (16 * kKv4Warps)), gy), 32 * kKv4Warps, 0, st>>>(p);
   return cudaGetLastError();
@@ -342,7 +351,9 @@ __device__ __forceinline__ void put8(float* p, const uint32_t (&w)[4]) {
 }  // namespace
 
 // The cached rows of a prefix back as plain rows: a warp takes 16 output rows,
-// K or V of 32 / LPT heads.
+// K or V of 32 / LPT heads.  (n - 8) scale is exact in bf16, one operation for a
+// pair.  The rows that go out are four fifths of the bytes: 961 MB in 148 to 150 us
+// (6.4 to 6.5 TB/s, 95 % of a copy's rate), 202 MB of 19 ragged prefixes in 36 us.
 template <typename T, int LPT>
 __global__ void __launch_bounds__(32 * kKv4Warps) kv4_gather_kernel(const KvGatherParams p) {
   constexpr int HPW = 32 / LPT;

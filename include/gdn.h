@@ -728,7 +728,7 @@ typedef struct gdn_kv_gather_args {
 gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
                          const gdn_kv_gather_args* args, void* stream);
 
-/* Attention of 1 to 32 new rows a sequence over the 8-bit cache: a decode
+/* Attention of 1 to 32 new rows a sequence over the cache, of either width: a decode
  * step, or the rows of a draft being verified.  The new rows' own K and V are
  * in the cache already (kv_len[s] counts them).  A sequence with more rows
  * than max_q_len or more keys than max_kv_len, or whose table holds a page
@@ -739,6 +739,11 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
  * down to 2^-13 of its row's largest (smaller ones to 2^-21 of that), and 9 of
  * a weight (times its block's V scale) down to 2^-19 of the largest of its
  * piece (smaller ones to 2^-28 of that).
+ * Over 4 bits K and V enter exactly.  In bf16 q enters exactly too (with up to 8
+ * (row, head) pairs a kv head: all 8 bits down to 2^-27 of its row's largest, smaller
+ * ones to 2^-35 of that), and 11 bits of a weight times its token's V scale down to
+ * 2^-20 of the largest of its piece (smaller ones to 2^-31 of that); in fp32 q's 24
+ * bits count, and 23 of such a weight down to 2^-10 (smaller ones to 2^-33).
  *
  * The keys of a sequence are cut into pieces by its own kv_len and number of
  * rows alone, the pieces run in parallel and are joined in order: a row's bits
