@@ -266,7 +266,7 @@ struct AppendRun {
 // New rows into the cache.  Window w of W rows; grid y: K or V of 32 / LPT heads.
 // A head's rows are read once; a group's or row's largest value is a maximum over
 // lanes, and codes leave as whole words: K's word of eight channels is a lane's own,
-// V's of eight tokens are formed in the lane that has their channel.  29,500 rows of
+// V's of eight tokens are formed in the lane that has their channel.  27,057 rows of
 // 4 heads, d = 256, bf16 (139.5 MB, 20.5 us of memory): 34.8 us, five CTAs an SM; a
 // warp's time goes to waits for its loads (36 %), and the 3,384 CTAs
 // take 4.5 rounds of what is resident.  CTAs of 1 or 2 warps: the same.
