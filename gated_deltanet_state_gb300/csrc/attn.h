@@ -122,20 +122,25 @@ inline int64_t prefill_grid(AttnPrefillParams& p, int rows, int times) {
 // 2,048 to 32,768 keys: 262 us with 1,024, 226 with 2,048); beyond 38,912
 // tokens 76 pieces a head are one CTA on each of the 152 SMs for two kv heads.
 // Over 4 bits, half the keys' bytes, a few rows' pieces are of 1,024 keys from 2,048
-// on, so that the outputs' share is the same.
-constexpr int kMaxPieces = 76;
+// on, so that the outputs' share is the same.  There the kernel of a few rows has three
+// CTAs on an SM at d = 256, and 114 pieces a head are theirs for four kv heads (one
+// sequence of 229,376 tokens: 75 us with 76, 66 with 112, before the join).
+constexpr int kMaxPieces = 76, kMaxPieces4 = 114;
 constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows
+template <int MOST = kMaxPieces>
 __host__ __device__ inline int decode_piece_target(int tiles, int rows, int bits) {   // pieces aimed at
   const int per = rows > kDtNarrow ? (tiles <= 16 ? 4 : tiles <= 64 ? 8 : 16) : tiles <= 16 ? 2 : bits == 8 ? 4 : 8;
   const int n = (tiles + per / 2) / per;
-  return n < 1 ? 1 : n > kMaxPieces ? kMaxPieces : n;
+  return n < 1 ? 1 : n > MOST ? MOST : n;
 }
+template <int MOST = kMaxPieces>
 __host__ __device__ inline int decode_piece_tokens(int L, int rows, int bits) {
-  const int tiles = L < 1 ? 1 : (int)(((int64_t)L + 127) / 128), n = decode_piece_target(tiles, rows, bits);
+  const int tiles = L < 1 ? 1 : (int)(((int64_t)L + 127) / 128), n = decode_piece_target<MOST>(tiles, rows, bits);
   return (tiles + n - 1) / n * 128;
 }
+template <int MOST = kMaxPieces>
 __host__ __device__ inline int decode_pieces(int L, int rows, int bits) {
-  const int c = decode_piece_tokens(L, rows, bits);
+  const int c = decode_piece_tokens<MOST>(L, rows, bits);
   return L < 1 ? 1 : (int)(((int64_t)L + c - 1) / c);
 }
 // At least the pieces of any length up to L and any number of rows.
@@ -144,7 +149,8 @@ __host__ __device__ inline int decode_max_pieces(int L, int bits) {
   int most = 1;
   for (int rows = 1; rows <= kDtNarrow + 1; rows += kDtNarrow)
     for (int at = 16; at <= 128; at *= 2) {   // (up to 16 or 64 tiles, from where pieces are longer)
-      const int n = decode_piece_target(tiles < at || at == 128 ? tiles : at, rows, bits);
+      const int t = tiles < at || at == 128 ? tiles : at;
+      const int n = bits == 8 ? decode_piece_target<kMaxPieces>(t, rows, bits) : decode_piece_target<kMaxPieces4>(t, rows, bits);
       most = n > most ? n : most;
     }
   return most;

@@ -31,7 +31,7 @@
 // nothing but the tile.
 //
 // 256 sequences of 1,024 to 8,192 tokens, 24 heads, 4 kv heads, d = 256 (1.24 GB):
-// 368 us, 3.4 TB/s; one of 229,376 tokens 82 us.  What bounds it is the warps' own
+// 368 us, 3.4 TB/s; one of 229,376 tokens 72 us.  What bounds it is the warps' own
 // chains: 5,700 instructions a tile at 1.9 a cycle (issue slots 48 % used, 28 % of a
 // warp's time waiting for an instruction's fixed latency), which take 3,000 cycles
 // where the memory takes 1,500.  Registers hold the warps at 12 an SM and one for
@@ -186,8 +186,8 @@ __device__ __forceinline__ int few_load(const DtParams& w, FewShared& sh, uint8_
   bool ok = true;
   DtItem t{};
   for (int i = i0; ok && i < i1; ++i) {
-    if (i == i0) t = dt_item<kFewRows>(w, sh.items, i);
-    else dt_next<kFewRows>(w, sh.items, i, t);
+    if (i == i0) t = dt_item<kFewRows, kMaxPieces4>(w, sh.items, i);
+    else dt_next<kFewRows, kMaxPieces4>(w, sh.items, i, t);
     const int32_t* bt = p.block_table + (int64_t)t.s * p.max_pages;
     int next_at = 0, next = -1;
     auto look = [&](int j) {
@@ -268,11 +268,11 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
     sh.issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 0) dt_sums<kFewRows>(w, sh, lane);
+  if (warp == 0) dt_sums<kFewRows, kMaxPieces4>(w, sh, lane);
   __syncthreads();
   // this CTA's run of items
-  const int i0 = dt_first<kFewRows>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
-  const int last_item = dt_first<kFewRows>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
+  const int i0 = dt_first<kFewRows, kMaxPieces4>(w, sh.items, sh.work, blockIdx.x, gridDim.x);
+  const int last_item = dt_first<kFewRows, kMaxPieces4>(w, sh.items, sh.work, blockIdx.x + 1, gridDim.x);
   const int i1 = limit < 0 ? i0 : last_item;
   int loaded = 0;   // stages (the loading warp's)
 
@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
     uint32_t nth = warp;           // stages before this one
     DtItem u{};
     for (int i = i0; i < i1; ++i) {
-      if (i == i0) u = dt_item<kFewRows>(w, sh.items, i);
-      else dt_next<kFewRows>(w, sh.items, i, u);
+      if (i == i0) u = dt_item<kFewRows, kMaxPieces4>(w, sh.items, i);
+      else dt_next<kFewRows, kMaxPieces4>(w, sh.items, i, u);
       if (dt_new_rows(u, i == i0)) {
         uint4 x[GR];
         float amax = 0.f;
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
   if (sh.fail) {
     // a wait ran out: report, then give the copies in flight one more bounded
     // wait each before their memory goes
-    dt_report<kFewRows>(w, sh, i0, last_item);
+    dt_report<kFewRows, kMaxPieces4>(w, sh, i0, last_item);
     if (warp == kFewWarps && lane == 0)
       for (int n = max(0, loaded - ST); n < loaded; ++n) tc::mbar_wait_bounded(&sh.full[n % ST], (uint32_t)(n / ST) & 1, kDtWait);
     __syncwarp();

@@ -129,8 +129,9 @@ __device__ __forceinline__ int dt_groups(const DtParams& w, int s) {
   return p.c.Hkv * ((n * p.G + NT - 1) / NT);
 }
 // A tile of keys counts 1, an item's fixed cost as much again.
+template <int MOST>
 __device__ __forceinline__ int dt_piece_work(const AttnDecodeParams& p, int s) {
-  return decode_piece_tokens(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G, p.c.bits) / kDtTok + 1;
+  return decode_piece_tokens<MOST>(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G, p.c.bits) / kDtTok + 1;
 }
 
 // The last s with sums[s] <= i.
@@ -146,16 +147,16 @@ __device__ __forceinline__ int dt_find(const I* sums, int n, I i) {
 }
 
 // First item of CTA b: the work before it is b / CTAs of all.
-template <int NT>
+template <int NT, int MOST = kMaxPieces>
 __device__ __forceinline__ int dt_first(const DtParams& w, const int* items, const long long* work, int b, int ctas) {
   const long long at = work[w.ns] * b / ctas;
   if (at >= work[w.ns]) return items[w.ns];
   const int s = dt_find(work, w.ns, at);
-  const int per = dt_piece_work(w.a, w.s0 + s);   // of each of its items
+  const int per = dt_piece_work<MOST>(w.a, w.s0 + s);   // of each of its items
   return min(items[s + 1], items[s] + (int)((at - work[s] + per - 1) / per));
 }
 
-template <int NT>
+template <int NT, int MOST = kMaxPieces>
 __device__ __forceinline__ DtItem dt_item(const DtParams& w, const int* items, int i) {
   const AttnDecodeParams& p = w.a;
   const int lo = dt_find(items, w.ns, i);
@@ -167,21 +168,21 @@ __device__ __forceinline__ DtItem dt_item(const DtParams& w, const int* items, i
   t.L = p.kv_len[t.s];
   // of one head: piece after piece, of a piece its row tiles (with one tile a
   // CTA's run of items loads its rows once a head)
-  t.pieces = decode_pieces(t.L, t.n * p.G, p.c.bits);
+  t.pieces = decode_pieces<MOST>(t.L, t.n * p.G, p.c.bits);
   t.rt = (t.n * p.G + NT - 1) / NT;
   t.h = k / (t.pieces * t.rt);
   const int in = k - t.h * t.pieces * t.rt;
   t.piece = in / t.rt;
   t.r0 = (in - t.piece * t.rt) * NT;
   t.rows = min(NT, t.n * p.G - t.r0);
-  t.pt = decode_piece_tokens(t.L, t.n * p.G, p.c.bits);
+  t.pt = decode_piece_tokens<MOST>(t.L, t.n * p.G, p.c.bits);
   t.k0 = t.piece * t.pt;
   t.k1 = min(t.L, t.k0 + t.pt);
   t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
   return t;
 }
 // The item after it.
-template <int NT>
+template <int NT, int MOST = kMaxPieces>
 __device__ __forceinline__ void dt_next(const DtParams& w, const int* items, int i, DtItem& t) {
   if (t.rt == 1 && t.piece + 1 < t.pieces) {
     ++t.piece;
@@ -189,7 +190,7 @@ __device__ __forceinline__ void dt_next(const DtParams& w, const int* items, int
     t.k1 = min(t.L, t.k0 + t.pt);
     t.tiles = (t.k1 - t.k0 + kDtTok - 1) / kDtTok;
   } else {
-    t = dt_item<NT>(w, items, i);
+    t = dt_item<NT, MOST>(w, items, i);
   }
 }
 
@@ -267,7 +268,7 @@ __device__ __forceinline__ float split_row(const uint4& x, uint2& hi, uint2& lo)
 
 // Running sums of the items (one warp); lengths out of bounds are reported and
 // have none.
-template <int NT>
+template <int NT, int MOST = kMaxPieces>
 __device__ __forceinline__ void dt_sums(const DtParams& w, DtItems& sh, int lane) {
   const AttnDecodeParams& p = w.a;
   int sum = 0;
@@ -284,9 +285,9 @@ __device__ __forceinline__ void dt_sums(const DtParams& w, DtItems& sh, int lane
         g = 0;
       }
       if (g > 0) {
-        const int pieces = decode_pieces(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G, p.c.bits);
+        const int pieces = decode_pieces<MOST>(p.kv_len[s], (p.cu[s + 1] - p.cu[s]) * p.G, p.c.bits);
         v = g * pieces;
-        x = (long long)v * dt_piece_work(p, s);
+        x = (long long)v * dt_piece_work<MOST>(p, s);
       }
     }
 #pragma unroll
@@ -381,13 +382,13 @@ __device__ __forceinline__ void dt_drain(const DtParams& w, SH& sh, int loaded, 
 
 // Reports a run-out and marks the rows of the pieces that this CTA had, items
 // [i0, i1): what it has not written of them must not be joined.
-template <int NT>
+template <int NT, int MOST = kMaxPieces>
 __device__ __forceinline__ void dt_report(const DtParams& w, const DtItems& sh, int i0, int i1) {
   const AttnDecodeParams& p = w.a;
   if (threadIdx.x == 0) atomicExch(p.err, GDN_ERR_TIMEOUT);   // over an earlier code
   if (!p.part_o) return;
   for (int i = i0; i < i1; ++i) {
-    const DtItem t = dt_item<NT>(w, sh.items, i);
+    const DtItem t = dt_item<NT, MOST>(w, sh.items, i);
     for (int n = threadIdx.x; n < t.rows; n += blockDim.x) {
       const int row = (t.r0 + n) / p.G, g = t.r0 + n - row * p.G;
       p.part_ml[t.piece * (p.T * p.Hq) + (int64_t)(t.q0 + row) * p.Hq + t.h * p.G + g] = make_float2(0.f, kLostPiece);

@@ -178,41 +178,51 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_simt_kernel(const 
   }
 }
 
+// The pieces of a sequence of n rows, as the kernel that served it cut them.
+template <typename T, int K>
+__device__ __forceinline__ int join_pieces(const AttnDecodeParams& p, int L, int n) {
+  if (sizeof(T) == 2 && 32 * K >= kMaxPieces4 && n * p.G <= kD4Few) return decode_pieces<kMaxPieces4>(L, n * p.G, p.c.bits);
+  return decode_pieces(L, n * p.G, p.c.bits);
+}
+
 // Joins the pieces of every row in their order: o = sum_i w_i O_i / sum_i w_i l_i,
 // w_i = 2^(m_i - max m).  A warp a (row, head): the lanes hold the pieces'
-// weights (76 at most), then an element of the head each.  Bound by the pieces'
+// weights (32 K at most), then an element of the head each.  Bound by the pieces'
 // bytes: 15.6 us after 256 single rows (24 heads, d = 256), 22 us after 16 drafts of 16.
 // (Four CTAs an SM leave 128 registers, which hold eight pieces' loads; with the
 // bound open the compiler loads one by one: 417 us for the 256 rows' call, 405.)
-template <typename T>
+template <typename T, int K>
 __global__ void __launch_bounds__(128, 4) attn_decode_join_kernel(const AttnDecodeParams p) {
   const int s = blockIdx.y, lane = threadIdx.x & 31, d = p.c.d;
   const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the pieces' kernel before this one
   if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
-  const int pieces = decode_pieces(L, n * p.G, p.c.bits);
+  const int pieces = join_pieces<T, K>(p, L, n);
   const int64_t R = p.T * p.Hq;
   for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n * p.Hq; i += gridDim.x * 4) {
     const int64_t rh = (int64_t)q0 * p.Hq + i;
-    float2 ml[3];
+    float2 ml[K];
     float mx = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < K; ++k) {
       ml[k] = lane + 32 * k < pieces ? p.part_ml[(lane + 32 * k) * R + rh] : make_float2(-INFINITY, 0.f);
       mx = fmaxf(mx, ml[k].x);
     }
     // a wait ran out in a piece of this row: the row is not written
-    const bool lost = __any_sync(0xffffffffu, ml[0].y == kLostPiece || ml[1].y == kLostPiece || ml[2].y == kLostPiece);
+    bool lost = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) lost = lost || ml[k].y == kLostPiece;
+    lost = __any_sync(0xffffffffu, lost);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float ref = mx == -INFINITY ? 0.f : mx;
-    float w[3];
+    float w[K];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) w[k] = fast_exp2(ml[k].x - ref);
+    for (int k = 0; k < K; ++k) w[k] = fast_exp2(ml[k].x - ref);
     float sum = 0.f;
     float4 acc[2] = {};
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < K; ++k) {
       const int most = min(32, pieces - 32 * k);
       const float4* o = reinterpret_cast<const float4*>(p.part_o + (32 * k * R + rh) * d) + lane;
       // eight pieces' loads at once; those past the last have weight 0
@@ -245,6 +255,56 @@ __global__ void __launch_bounds__(128, 4) attn_decode_join_kernel(const AttnDeco
   }
 }
 
+// The same for a few rows, where rounds of loads are what the time goes to: a warp
+// takes 32 elements of a (row, head), 32 pieces at once.  (One row of 24 heads over 112
+// pieces, d = 256: the call takes 72 us, with the kernel above 75; over 4 pieces 17.3
+// and 16.9.)
+template <typename T, int K>
+__global__ void __launch_bounds__(128, 4) attn_decode_join_few_kernel(const AttnDecodeParams p) {
+  const int s = blockIdx.y, lane = threadIdx.x & 31, d = p.c.d, parts = (d + 31) / 32;
+  const int q0 = p.cu[s], n = p.cu[s + 1] - q0, L = p.kv_len[s];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");   // the pieces' kernel before this one
+  if (n <= 0 || n > p.max_q || L > p.max_kv || L < 0 || q0 < 0 || (int64_t)q0 + n > p.T) return;
+  const int pieces = join_pieces<T, K>(p, L, n);
+  const int64_t R = p.T * p.Hq;
+  for (int i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n * p.Hq * parts; i += gridDim.x * 4) {
+    const int64_t rh = (int64_t)q0 * p.Hq + i / parts;
+    const int e = i % parts * 32 + lane;
+    float2 ml[K];
+    float mx = -INFINITY;
+    bool lost = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      ml[k] = lane + 32 * k < pieces ? p.part_ml[(lane + 32 * k) * R + rh] : make_float2(-INFINITY, 0.f);
+      mx = fmaxf(mx, ml[k].x);
+      lost = lost || ml[k].y == kLostPiece;
+    }
+    lost = __any_sync(0xffffffffu, lost);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (32 * k >= pieces) break;
+      const float w = fast_exp2(ml[k].x - ref);
+      const float* o = p.part_o + (32 * k * R + rh) * d + e;
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 32 * k + j < pieces && e < d ? o[j * (R * d)] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        sum = fmaf(wj, __shfl_sync(0xffffffffu, ml[k].y, j), sum);
+        acc = fmaf(wj, v[j], acc);
+      }
+    }
+    if (lost) continue;
+    if (e < d) put1<T>(p.o, rh * d + e, sum == 0.f ? 0.f : acc / sum);
+    if (p.lse && e == 0) p.lse[rh] = sum == 0.f ? -INFINITY : mx * 0.693147180559945309f + logf(sum);
+  }
+}
+
 namespace {
 
 template <typename T>
@@ -257,16 +317,15 @@ cudaError_t decode_simt(const AttnDecodeParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
-  const cudaError_t e = p.c.bits == 4                      ? launch_attn_decode4_tc(p, dtype, st)
-                        : attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st)
-                                                             : decode_simt<T>(p, st);
-  if (e != cudaSuccess || !p.part_o) return e;
-  // launched as the last CTAs of the pieces' kernel leave, waiting on the device for
-  // its end
+// The join of a few rows is taken up to the warps that the SMs hold at once, over more
+// pieces than its lanes load in one round.
+constexpr int64_t kJoinFew = 2400;
+
+// A join with so many warps a (row, head), launched as the last CTAs of the pieces'
+// kernel leave, waiting on the device for its end.
+cudaError_t join(const AttnDecodeParams& p, void (*kernel)(AttnDecodeParams), int parts, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p.max_q * p.Hq + 3) / 4), p.N);
+  cfg.gridDim = dim3((unsigned)((p.max_q * p.Hq * parts + 3) / 4), p.N);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute at{};
@@ -274,7 +333,20 @@ cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) 
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <typename T>
+cudaError_t decode_dtype(const AttnDecodeParams& p, int dtype, cudaStream_t st) {
+  const cudaError_t e = p.c.bits == 4                      ? launch_attn_decode4_tc(p, dtype, st)
+                        : attn_decode_tc_supported(p, dtype) ? launch_attn_decode_tc(p, st)
+                                                             : decode_simt<T>(p, st);
+  if (e != cudaSuccess || !p.part_o) return e;
+  constexpr int K8 = (kMaxPieces + 31) / 32, K4 = (kMaxPieces4 + 31) / 32;
+  if (p.c.bits == 8) return join(p, attn_decode_join_kernel<T, K8>, 1, st);
+  const int parts = (p.c.d + 31) / 32;
+  return p.max_pieces > 32 && (int64_t)p.N * p.max_q * p.Hq * parts <= kJoinFew ? join(p, attn_decode_join_few_kernel<T, K4>, parts, st)
+                                                           : join(p, attn_decode_join_kernel<T, K4>, 1, st);
 }
 
 }  // namespace

@@ -83,6 +83,15 @@ def test_one_row_each(d):
     Batch(AttnShape(16, 2, d, 16, kv_bits=4), [1] * 70, lens, seed=5).check(every=9)
 
 
+@pytest.mark.parametrize("n,others", [(1, 0), (2, 3), (1, 170), (9, 2), (16, 90)])
+def test_as_many_pieces_as_there_can_be(n, others):
+    """A context of 1,016 tiles (113 pieces for a few rows, 64 for more), joined by itself and in a batch."""
+    b = Batch(AttnShape(8, 1, 64, 512, kv_bits=4), [n] + [1] * others, [130000] + [40] * others, seed=n)
+    b.check(every=64)
+    o, lse, err = b.run([0], wait=-1)
+    assert err == TIMEOUT and bool((o == 7).all()) and bool((lse == 7).all())
+
+
 @pytest.mark.parametrize("G", [1, 2, 3, 5, 7, 8, 9, 16, 17, 33])
 def test_group_sizes(G):
     """Pairs at and around the widths of the row tiles; rows of one sequence of every number."""
