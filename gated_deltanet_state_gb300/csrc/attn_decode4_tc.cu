@@ -18,7 +18,7 @@
 // 2^-10, 2^-33 of it below).
 //
 // 16 drafts of 16 rows over 2,048 to 32,768 tokens, 24 heads, 4 kv heads, d = 256 (117
-// GF, 321 MB): 213 us, 205 of them here.  A tile takes 5,100 cycles with its share of
+// GF, 321 MB): 210 to 214 us, all but 10 here.  A tile takes 5,000 cycles with its share of
 // the items' ends, 11,000 instructions of all kinds of warps at once (issue slots 54 %
 // used, the ALU pipe 45 %, most of it unpacking; the tensor pipe 33 %); what waits is
 // the softmax's chain of scores, vote and weights.  Pieces of other sizes, two
@@ -41,6 +41,11 @@ constexpr float kUnset = 3e38f;        // the offset of a row that has seen no k
 // them, so twice the operands in twice the places: 16 drafts of 16 rows 236 us, 214.)
 constexpr int kChunk = 128;
 
+// Registers of a thread by kind of warp, with one CTA on an SM: together what the
+// block is launched with (16 drafts of 16 rows 210 us; 136, 80, 48: 215; 128, 80, 64:
+// 217; 144, 64, 64: 225).
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kUnpackRegs = 72, kRestRegs = 64;
+
 constexpr int round16(int x) { return (x + 15) / 16 * 16; }
 
 // NT rows a tile, QP parts of Q and PP of P side by side as columns, SWG softmax
@@ -57,6 +62,7 @@ struct D4Cfg {
   static constexpr uint32_t COLS = CTAS == 1 ? 512 : 256;
   static constexpr uint32_t O0 = 2 * NQ, R0 = O0 + 2 * NP; // tensor memory: scores of two tiles, O of 128 elements each, operands
   static constexpr int SLOT = kChunk / 2, FIT = (COLS - R0) / SLOT, RING = FIT < 8 ? FIT : 8;   // columns of an operand, operands
+  static_assert(CTAS > 1 || kSoftRegs * SOFT + kUnpackRegs * UNPACK + kRestRegs * (THREADS - SOFT - UNPACK) <= kLaunchRegs * THREADS, "registers");
   static_assert(RING >= 2 && RING % UWG == 0 && NT % SWG == 0 && CW % 8 == 0, "tensor memory");
 };
 
@@ -262,7 +268,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
   int loaded = 0;                               // tiles loaded (a loading warp's)
 
   if (warp >= SW + UW) {
-    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRestRegs));
     if (warp < SW + UW + 2) {
       // ---- loads, a warp for K and one for V ----
       loaded = d4_load<NT>(w, sh, base, i0, i1, warp == SW + UW + 1, lane);
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
     }
   } else if (warp >= SW) {
     // ---- codes to operands: a thread a row of them, K's tokens or V's channels ----
-    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kUnpackRegs));
     const int wg = (warp - SW) >> 2, row = quad * 32 + lane;
     const uint32_t lanes = tb + C::R0 + ((uint32_t)quad << 21);
     const uint8_t *kr = base + w.k_off, *vr = base + w.v_off;
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
     }
   } else {
     // ---- softmax: a thread a token of the tile, CW rows ----
-    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n");
+    if constexpr (C::CTAS == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftRegs));
     const int wg = warp >> 2, tid = threadIdx.x & 127, c0 = wg * CW;   // this warpgroup's first column
     const uint32_t lanes = tb + ((uint32_t)quad << 21);
     uint8_t *qs = base + w.q_off, *ps = base + w.p_off;
