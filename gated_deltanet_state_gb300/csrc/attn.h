@@ -172,7 +172,7 @@ cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st);
 // The decode over the 4-bit cache: the pieces, without the join.
 constexpr int kD4Few = 8;   // (row, head of the group) pairs up to which bf16 sequences take the kernel of a few rows
 cudaError_t launch_attn_decode4_tc(const AttnDecodeParams& p, int dtype, cudaStream_t st);
-cudaError_t launch_attn_decode4_few(const AttnDecodeParams& p, int sms, cudaStream_t st);
+cudaError_t launch_attn_decode4_few(const AttnDecodeParams& p, int sms, bool follows, cudaStream_t st);
 cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overlap, cudaStream_t st);
 // The tensor-core prefill: bf16, d = 64, 128 or 256, at least one key row.
 bool attn_prefill_tc_supported(const AttnPrefillParams& p, int dtype);

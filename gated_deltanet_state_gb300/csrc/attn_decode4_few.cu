@@ -552,12 +552,13 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
     __syncwarp();
     __syncthreads();
   }
+  dt_end_after_first();
 }
 
 namespace {
 
 template <int GR>
-cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
+cudaError_t few(const AttnDecodeParams& p, int sms, bool follows, cudaStream_t st) {
   DtParams w{};
   w.a = p;
   w.wait = dt_limit(p);
@@ -577,8 +578,7 @@ cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
     w.s0 = s0;
     w.ns = p.N - s0 < kDtSeqs ? p.N - s0 : kDtSeqs;
     const int64_t most = (int64_t)w.ns * p.max_pieces * p.c.Hkv;
-    attn_decode4_few_kernel<GR><<<(unsigned)(most < kFewCtas<GR> * sms ? most : kFewCtas<GR> * sms), kFewThreads, smem, st>>>(w);
-    e = cudaGetLastError();
+    e = dt_launch(attn_decode4_few_kernel<GR>, w, most < kFewCtas<GR> * sms ? most : kFewCtas<GR> * sms, kFewThreads, smem, follows, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -586,8 +586,8 @@ cudaError_t few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attn_decode4_few(const AttnDecodeParams& p, int sms, cudaStream_t st) {
-  return p.c.d > 128 ? few<8>(p, sms, st) : p.c.d > 64 ? few<4>(p, sms, st) : few<2>(p, sms, st);
+cudaError_t launch_attn_decode4_few(const AttnDecodeParams& p, int sms, bool follows, cudaStream_t st) {
+  return p.c.d > 128 ? few<8>(p, sms, follows, st) : p.c.d > 64 ? few<4>(p, sms, follows, st) : few<2>(p, sms, follows, st);
 }
 
 }  // namespace gdn

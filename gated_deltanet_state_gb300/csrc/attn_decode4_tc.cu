@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
   volatile int* fail = &sh.fail;
   const long long limit = w.wait;
 
+  dt_let_next(w);
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) tc::mbar_init(&sh.k_full[i], 1), tc::mbar_init(&sh.k_empty[i], UW);
     for (int i = 0; i < VS; ++i) tc::mbar_init(&sh.v_full[i], 1), tc::mbar_init(&sh.v_empty[i], UW + SW);
@@ -683,11 +684,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
 namespace {
 
 template <typename C>
-cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, int hi, cudaStream_t st) {
+cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, bool first, cudaStream_t st) {
   DtParams w{};
   w.a = p;
   w.wait = dt_limit(p);
-  w.row_lo = lo, w.row_hi = hi;
+  w.row_lo = lo, w.row_hi = 0x7fffffff;
+  w.first = first;
   const uint32_t d = (uint32_t)p.c.d, q = C::NQ * d * 2, pp = 2 * C::NP * kDtTok * 2, misc = (uint32_t)sizeof(D4Shared<C>);
   // 227 KB, or half of them a CTA, of which 1 KB is the system's
   const uint32_t all = C::CTAS == 1 ? 232448 : 115712;
@@ -731,18 +733,19 @@ cudaError_t launch_attn_decode4_tc(const AttnDecodeParams& p, int dtype, cudaStr
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  constexpr int kAll = 0x7fffffff;
-  if (dtype == GDN_F32) return decode4<Full8>(p, sms, 1, kAll, st);
+  if (dtype == GDN_F32) return decode4<Full8>(p, sms, 1, false, st);
   // a sequence's kernel goes by its own rows (a row's bits with it): up to 8 (row,
   // head) pairs of a kv head, or more, of which either form gives the same bits; a
-  // call that may have both launches both
+  // call that may have both launches both.  (What rows there are in all does not
+  // tell: one sequence may have too many and be left out, or rows may stand behind
+  // the last sequence.)
   const int most = p.max_q * p.G;
-  // (none has few where all rows together say that each has max_q)
-  const bool few = most <= kD4Few || (p.G <= kD4Few && (int64_t)p.N * p.max_q != p.T);
-  if (few) e = launch_attn_decode4_few(p, sms, st);
-  if (e != cudaSuccess || most <= kD4Few) return e;
+  const bool few = p.G <= kD4Few, many = most > kD4Few;
   const int lo = few ? kD4Few + 1 : 1;
-  return most <= 16 ? decode4<Mid>(p, sms, lo, kAll, st) : most <= 32 ? decode4<Some>(p, sms, lo, kAll, st) : decode4<Many>(p, sms, lo, kAll, st);
+  if (many) e = most <= 16   ? decode4<Mid>(p, sms, lo, few, st)
+                : most <= 32 ? decode4<Some>(p, sms, lo, few, st)
+                             : decode4<Many>(p, sms, lo, few, st);
+  return e == cudaSuccess && few ? launch_attn_decode4_few(p, sms, many, st) : e;
 }
 
 }  // namespace gdn

@@ -42,6 +42,7 @@ struct DtParams {
   int32_t s0, ns;       // this launch's sequences ...
   int32_t row_lo, row_hi;   // ... those with (row, head of the group) pairs in [row_lo, row_hi]
   int32_t k_stages, v_stages;
+  int32_t first;        // whether the call's other kernel follows (dt_let_next)
   long long wait;       // SM clocks that a wait may take; < 0: every one has run out
   uint32_t k_off, v_off, q_off, p_off, misc_off;   // dynamic shared memory
 };
@@ -82,6 +83,17 @@ __device__ __forceinline__ float dt_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// A call's two kernels over 4 bits, of sequences with many rows and with few, share
+// nothing, and the host does not know whether there is work for both.  So the first
+// lets the second start wherever its own CTAs have left, and the second ends only
+// after it.  (Where the second has no work, it costs 16 drafts of 16 rows 5 us of 200,
+// launched in the other order without overlap 9; four drafts of 4 rows over 2,000
+// keys 2 of 25, and 5.  The join started early as well: 7, and 3.)
+__device__ __forceinline__ void dt_let_next(const DtParams& w) {
+  if (w.first) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+__device__ __forceinline__ void dt_end_after_first() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // e4m3 x e4m3 -> fp32: D[tmem] (+)= A[smem] B[smem]^T, 32 deep; a whole warp
 // runs it, the lane with `lead` issues (tc::elect_one).
@@ -418,6 +430,22 @@ __device__ __forceinline__ void dt_clean(uint8_t* v, int* bad, const DtItem& t, 
 
 inline long long dt_limit(const AttnDecodeParams& p) {
   return p.wait_cycles > 0 ? p.wait_cycles : p.wait_cycles < 0 ? -1 : kDtWait;
+}
+
+// A launch; `follows`: behind the call's first kernel, which it may overlap.
+template <typename F>
+inline cudaError_t dt_launch(F* kernel, const DtParams& w, int64_t ctas, int threads, uint32_t smem, bool follows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = follows ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, w);
 }
 
 // The cache's share of dynamic shared memory: K and V stages in what `fixed`

@@ -754,7 +754,9 @@ typedef struct gdn_attn_decode_args {
   int32_t max_q_len;             /* host bound on new rows a sequence, 1..32  */
   int32_t max_kv_len;            /* host bound on kv_len (one above 2^31 -
                                     1,024 counts as that)                     */
-  int64_t total_tokens;          /* T = cu_seqlens[N]                         */
+  int64_t total_tokens;          /* T >= cu_seqlens[N]; rows behind the last
+                                    sequence (a captured step's padding) stay
+                                    as they were                              */
   int64_t q_stride;              /* elements between rows of q, >= Hq*d       */
   const int32_t* cu_seqlens;     /* [N+1] rows of q                           */
   const int32_t* kv_len;         /* [N]                                       */
