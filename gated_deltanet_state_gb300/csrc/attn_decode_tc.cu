@@ -515,10 +515,12 @@ cudaError_t launch_attn_decode_tc(const AttnDecodeParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // a sequence's kernel goes by its own rows (a row's bits with it): up to 16
   // (row, head) pairs of a kv head here, more with the rows as the products'
-  // 128 (attn_draft_tc.cu); a call that may have both launches both
+  // 128 (attn_draft_tc.cu); a call that may have both launches both.  (What rows
+  // there are in all does not tell: one sequence may have too many and be left
+  // out, or rows may stand behind the last sequence.  The launch costs 16 drafts of
+  // 16 rows 6 us of 221 where it has no work.)
   if (p.max_q * p.G > kDtNarrow) {
-    // (none has few where all rows together say that each has max_q: a launch, 6 us, less)
-    const bool few = p.G <= kDtNarrow && (int64_t)p.N * p.max_q != p.T;
+    const bool few = p.G <= kDtNarrow;
     if (few) e = decode_tc<16>(p, sms, st);
     return e != cudaSuccess ? e : launch_attn_draft_tc(p, sms, few, st);
   }

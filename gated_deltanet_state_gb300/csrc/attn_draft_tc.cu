@@ -468,17 +468,7 @@ cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overla
     w.ns = p.N - s0 < kDtSeqs ? p.N - s0 : kDtSeqs;
     const int64_t most = (int64_t)w.ns * p.max_pieces * p.c.Hkv * rt;
     // behind the kernel of the sequences with few rows, which share nothing with these
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
-    cfg.blockDim = dim3(kDrThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = overlap ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, attn_draft_tc_kernel, w);
+    e = dt_launch(attn_draft_tc_kernel, w, most < sms ? most : sms, kDrThreads, smem, overlap, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -52,7 +52,7 @@ class Step:
         assert_attention(o[r], lse[r], attention64(self.q[r], k, v, self.sh.softmax_scale), self.sh.dtype)
 
 
-@pytest.mark.parametrize("bits", [4])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("G,news,max_q", [(8, [1, 3], 2), (8, [1, 5], 3), (4, [1, 8, 3], 4), (1, [2, 18], 10)])
 def test_a_neighbour_with_too_many_rows(bits, G, news, max_q):
     """As many rows in all as if each sequence had the most."""
@@ -67,7 +67,7 @@ def test_a_neighbour_with_too_many_rows(bits, G, news, max_q):
             st.check(s, o, lse)
 
 
-@pytest.mark.parametrize("bits", [4])
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("G,news,max_q,padded", [(8, [3, 1, 2], 3, 9), (8, [1, 1], 2, 4), (8, [0, 1, 0, 2], 4, 16), (4, [1, 1, 1], 5, 15),
                                                  (8, [1, 1], 1, 5), (24, [1, 2], 2, 4)])
 def test_rows_behind_the_last_sequence(bits, G, news, max_q, padded):
