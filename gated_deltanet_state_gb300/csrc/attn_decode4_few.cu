@@ -106,7 +106,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float few_log2(float x) {   // (normal numbers and NaN)
+__device__ __forceinline__ float few_log2(float x) {   // (normal numbers)
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
@@ -291,7 +291,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
     const uint32_t at_ks = sg.ks + block * next_ks + g;
     const uint32_t at_v = sg.v + (block + (t >> 1)) * kv4_codes(d) + g * 8 + (t & 1) * 4;
     const uint32_t at_vs = sg.vs + block * kKvBlock + g;
-    const uint32_t at_nan = sg.ks + block * next_ks + lane * 16;   // 16 of the warp's scales of K
+    // 16 of the warp's scales, of K's or behind those of V's
+    const uint32_t k_parts = kFewBlocks * groups;
+    const uint32_t at_nan = lane < k_parts ? sg.ks + block * next_ks + lane * 16 : sg.vs + (block + lane - k_parts) * kKvBlock;
     float4* red = reinterpret_cast<float4*>(base + w.p_off);   // [4 warps][4 tiles][32]
     float cs[2] = {};      // factors of the scores of rows 2 t, 2 t + 1 ...
     int lim[2] = {};       // ... and the keys that they see
@@ -385,16 +387,18 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
             float y[4];
             mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start);
             mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w);
-            const float fa = __uint_as_float(sa * (1u << 20) + (107u << 23)), fb = __uint_as_float(sb * (1u << 20) + (107u << 23));
+            const float fa = kv4_number(sa), fb = kv4_number(sb);
             x[s][0] = fmaf(y[0], fa, x[s][0]), x[s][1] = fmaf(y[1], fa, x[s][1]);
             x[s][2] = fmaf(y[2], fb, x[s][2]), x[s][3] = fmaf(y[3], fb, x[s][3]);
           }
         }
-        // a NaN scale of K (255, above taken for a number) makes its token's scores NaN
+        // a NaN scale (255, taken for a number) of K makes its token's scores NaN, one of V
+        // its token's weights, but not their sum
         uint4 some = make_uint4(0, 0, 0, 0);
-        if (lane < kFewBlocks * groups) some = *reinterpret_cast<const uint4*>(stage + at_nan);
+        if (lane < k_parts + kFewBlocks) some = *reinterpret_cast<const uint4*>(stage + at_nan);
         auto full_byte = [](uint32_t v) { return (~v - 0x01010101u) & v & 0x80808080u; };
-        if (__any_sync(0xffffffffu, (full_byte(some.x) | full_byte(some.y) | full_byte(some.z) | full_byte(some.w)) != 0)) {
+        const bool nan = __any_sync(0xffffffffu, (full_byte(some.x) | full_byte(some.y) | full_byte(some.z) | full_byte(some.w)) != 0);
+        if (nan) {
           for (int c = 0; c < groups; ++c)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -411,10 +415,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             // of a token: the exponent of its V scale (less 4 where its codes stand four bits
-            // up), and what undoes it in the sums (a NaN scale makes weights NaN; masked ones
-            // stay 0)
-            const float lv = few_log2(kv4_scale(v_scale[s * kKvBlock + 8 * k])) - (g & 2 ? 4.f : 0.f);
-            rv[s][k] = dt_ex2(fmaxf(-lv, -100.f));
+            // up), and what undoes it in the sums
+            const float lv = few_log2(kv4_number(v_scale[s * kKvBlock + 8 * k])) - (g & 2 ? 4.f : 0.f);
+            rv[s][k] = dt_ex2(-lv);
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[s][2 * k + h] = fmaf(x[s][2 * k + h], cs[h], lv);
           }
@@ -455,6 +458,15 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
             l[0] = fmaf(a, rv[s][k], l[0]), l[1] = fmaf(b, rv[s][k], l[1]);
             pb[2 * s + k] = transposed(half2_bits(a, b));
           }
+        if (nan) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {   // token 2 t + j of word i, where row g sees it
+              const int at = i % 2 * 8 + 2 * t + j, end = min(have >> (i / 2) & 1 ? u.k1 : 0, least + g / p.G);
+              if (stage[sg.vs + (block + i / 2) * kKvBlock + at] == kKv4Nan && kb + i / 2 * kKvBlock + at < end) pb[i] |= 0x7fffu << (16 * j);
+            }
+        }
         kv4_transpose(pb, t);
         // ---- outputs: 16 channels at a time ----
 #pragma unroll

@@ -492,14 +492,15 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         const uint32_t scol = lanes + (T & 1) * C::NQ + c0;
         // V's part first: it is there before the scores
         ok = dt_wait(&sh.v_full[st], vp, fail, limit);
-        const float vscale = kv4_scale((base + w.v_off + (uint32_t)st * v_unit + kDtBlocks * codes)[tid]);
+        const uint32_t vbyte = (base + w.v_off + (uint32_t)st * v_unit + kDtBlocks * codes)[tid];
         const bool valid = pos < t.k1 && (sh.have[st] >> (tid >> 4) & 1);
+        const unsigned nan = __ballot_sync(0xffffffffu, valid && vbyte == kKv4Nan);   // tokens with a NaN scale of V
         __syncwarp();
         if (lane == 0) dt_arrive(&sh.v_empty[st]);
         // of this token: the exponent of its V scale, and what undoes it in the sums of
-        // weights (a NaN scale makes weights NaN; masked ones stay 0)
-        const float lv = __log2f(vscale) - (tid & 2 ? 4.f : 0.f);
-        const float rv = vscale == vscale ? __fdividef(tid & 2 ? 16.f : 1.f, vscale) : 1.f;
+        // weights (a NaN scale counts as a number until the weights are made)
+        const float vscale = kv4_number(vbyte), lv = __log2f(vscale) - (tid & 2 ? 4.f : 0.f);
+        const float rv = __fdividef(tid & 2 ? 16.f : 1.f, vscale);
         const bool part = !__all_sync(0xffffffffu, valid), edge = kb + kDtTok > least;   // some row does not see some token
         ok = ok && dt_wait(&sh.s_full[T & 1], (T >> 1) & 1, fail, limit);
         __syncwarp();
@@ -595,6 +596,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           for (int v = 0; v < C::PP; ++v)
             *reinterpret_cast<uint4*>(pw + ((v * NT + c0 + k) >> 3) * (16 * kDtTok)) =
                 make_uint4(word[0][v], word[1][v], word[2][v], word[3][v]);
+        }
+        // a NaN scale of V makes the weights of the rows that see its token NaN, not their sums
+        if (nan >> lane & 1) {
+#pragma unroll 1
+          for (int n = c0; n < c0 + CW; ++n)
+            if (pos < sh.lim[par][n]) reinterpret_cast<uint16_t*>(pw + (n >> 3) * (16 * kDtTok))[n & 7] = 0x7fff;
         }
         __syncwarp();
         tc::fence_async_smem();

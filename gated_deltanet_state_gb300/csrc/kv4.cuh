@@ -38,10 +38,9 @@ __device__ __forceinline__ uint8_t* kv4_v_scale(const KvCache& c, int page, int 
 
 // Value of a scale byte: (8 + b % 8) 2^(b / 8 - 23), whose fp32 bits are the byte
 // next to an exponent of 107; its bf16 bits the upper half of those (4
-// significant bits: exact).
-__device__ __forceinline__ float kv4_scale(uint32_t b) {
-  return b == kKv4Nan ? __int_as_float(0x7fffffff) : __uint_as_float((b << 20) + (107u << 23));
-}
+// significant bits: exact).  As a number, also where the byte stands for NaN.
+__device__ __forceinline__ float kv4_number(uint32_t b) { return __uint_as_float((b << 20) + (107u << 23)); }
+__device__ __forceinline__ float kv4_scale(uint32_t b) { return b == kKv4Nan ? __int_as_float(0x7fffffff) : kv4_number(b); }
 __device__ __forceinline__ uint32_t kv4_scale_bf16(uint32_t b) { return b == kKv4Nan ? 0x7fffu : (b << 4) + (107u << 7); }
 
 // The least byte whose scale times 7 (exact: 7 bits) reaches a magnitude, given by its bits.
