@@ -11,20 +11,21 @@
 //
 //   S^T [16 tokens x 8 rows] = K Q^T,    O^T [16 channels x 8 rows] += V^T P^T
 //
-// K's codes are f16 subnormals as they stand: four of a word's eight after one mask,
-// n 2^-24 (pairs 0 and 2) or n 2^-20 (pairs 1 and 3, whose partners in Q carry
-// 2^-4).  Their offset of 8 is in the products' start value, -8 sum(q) of a group of
-// 32 channels; a group's product is its own and is added under its tokens' scales in
-// fp32.  V's are whole numbers in f16, less 8 (pairs 1 and 3 sixteenfold, whose
-// weights carry 2^-4).  Which channel or token
+// K's and V's codes are whole numbers in f16, less 8 (pairs 1 and 3 of a word's four
+// sixteenfold, whose partners in Q and whose weights carry 2^-4).  A group of 32
+// channels of K is a product of its own, added under its tokens' scales in fp32.  (K's
+// codes as they stand, as subnormals, with the offset of 8 taken out by the products'
+// start value, took no less: the 256 sequences below 381 us, 373 so.  And what is then
+// summed and taken away again is 8 times a group's largest q, also where its code is
+// 0, so elements of 2^-10 of that lost bits.)  Which channel or token
 // stands in which step of a product is chosen so that a lane's word is its operand:
 // a lane holds eight channels of K, or eight tokens of V.
 //
-// Q is scaled by a power of two for each row: 8 bits of elements down to 2^-27 of
-// the largest, off by 2^-35 of it at most below.  A weight times its V scale is an
-// f16 against a reference of its row that is the first chunk's maximum and moves
-// only when a weight would pass f16's range: 11 bits down to 2^-20 of it, off by
-// 2^-31 at most below.
+// Q is scaled by a power of two for each row, its largest element to [2^15, 2^16):
+// all 8 bits of elements down to 2^-29 of the largest, off by 2^-36 of it at most
+// below.  A weight times its V scale is an f16 against a reference of its row that is
+// the first chunk's maximum and moves only when a weight would pass f16's range: 11
+// bits down to 2^-20 of it, off by 2^-31 at most below.
 //
 // A warp takes 32 tokens of every tile of 128, with statistics and sums of its own,
 // which the four bring together in a fixed order at the end of a piece; it waits for
@@ -50,7 +51,6 @@ constexpr int kFewTok = kDtTok / kFewWarps, kFewBlocks = kFewTok / kKvBlock;    
 constexpr int kFewStages = 8;
 constexpr float kFewBase = 10.f, kFewTop = 15.75f;   // a weight at its reference is 2^10, none passes 2^15.75
 constexpr float kFewUnset = 3e38f;                   // the offset of a row that has seen no key
-constexpr float kFewUnit = 16777216.f;               // the scores' products count in 2^-24
 
 // A stage holds the tokens of CPS warps: K's codes, K's scales, V's codes, V's scales,
 // as they lie in pages.  All four warps' up to d = 128, where a copy is short and its
@@ -81,7 +81,6 @@ struct FewShared : DtItems {
   uint32_t issued;                      // stages whose loads have begun (one warp's stages)
   float2 stat[kFewWarps][kFewRows];     // a warp's offset and sum of each row
   uint4 q[8][32];                       // Q of row g, eight channels of a group, by lane
-  float4 start[8][4];                   // a group's start values for rows 2 t, 2 t + 1 (twice, as a product's)
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -94,13 +93,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
 }
-// D = A B + C, or D += A B: 16 x 16 by 16 x 8 in f16, fp32 sums.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                        const float4& c) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};\n"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c.x), "f"(c.y), "f"(c.z), "f"(c.w));
-}
+// D += A B: 16 x 16 by 16 x 8 in f16, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -322,32 +315,23 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
           }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // the largest element to [2^13, 2^14)
-        const int e = max(-100, min(100, (int)(__float_as_uint(amax) >> 23) - 127 - 13));
+        // the largest element to [2^15, 2^16)
+        const int e = max(-100, min(100, (int)(__float_as_uint(amax) >> 23) - 127 - 15));
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int c = 0; c < GR; ++c) {
-          float sum = 0.f;
+          if (c % kFewWarps != warp) continue;   // (every warp has them all)
           uint4 q;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t v = (&x[c].x)[k];
             const float s = k & 1 ? inv * 0.0625f : inv;   // codes of pairs 1 and 3 stand four bits up
-            const uint32_t b = half2_bits(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
-            sum = fmaf(f.x + f.y, k & 1 ? 16.f : 1.f, sum);
-            (&q.x)[k] = b;
+            (&q.x)[k] = half2_bits(__uint_as_float(v << 16) * s, __uint_as_float(v & 0xffff0000u) * s);
           }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum *= -8.f / kFewUnit;
-          if (c % kFewWarps == warp) {   // (every warp has them all)
-            sh.q[c][lane] = q;
-            if (t == 0) (&sh.start[c][g >> 1].x)[g & 1] = (&sh.start[c][g >> 1].x)[2 + (g & 1)] = sum;
-          }
+          sh.q[c][lane] = q;
         }
         // (an infinite element makes its row's scores NaN)
-        const float f = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) * kFewUnit : __int_as_float(0x7fffffff);
+        const float f = amax < INFINITY ? p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23) : __int_as_float(0x7fffffff);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           cs[k] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * k);
@@ -377,16 +361,17 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
 #pragma unroll 2
         for (int c = 0; c < groups; ++c) {
           const uint4 q = sh.q[c][lane];
-          const float4 start = sh.start[c][t];
           uint32_t m[4];
           ldsm4(stage_k + c * 256, m);
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            const uint32_t a = m[2 * s], b = m[2 * s + 1], a8 = a >> 8, b8 = b >> 8;
             const uint32_t sa = k_scale[s * next_ks + c * 16], sb = k_scale[s * next_ks + c * 16 + 8];
-            float y[4];
-            mma_f16(y, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, q.x, q.y, start);
-            mma_f16(y, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, q.z, q.w);
+            uint32_t ya[4], yb[4];
+            kv4_halves(m[2 * s], ya);
+            kv4_halves(m[2 * s + 1], yb);
+            float y[4] = {};
+            mma_f16(y, ya[0], yb[0], ya[1], yb[1], q.x, q.y);
+            mma_f16(y, ya[2], yb[2], ya[3], yb[3], q.z, q.w);
             const float fa = kv4_number(sa), fb = kv4_number(sb);
             x[s][0] = fmaf(y[0], fa, x[s][0]), x[s][1] = fmaf(y[1], fa, x[s][1]);
             x[s][2] = fmaf(y[2], fb, x[s][2]), x[s][3] = fmaf(y[3], fb, x[s][3]);

@@ -740,8 +740,8 @@ gdn_status gdn_kv_gather(const gdn_attn_desc* desc, const gdn_pool* pool,
  * a weight (times its block's V scale) down to 2^-19 of the largest of its
  * piece (smaller ones to 2^-28 of that).
  * Over 4 bits K and V enter exactly.  In bf16 q enters exactly too (with up to 8
- * (row, head) pairs a kv head: all 8 bits down to 2^-27 of its row's largest, smaller
- * ones to 2^-35 of that), and 11 bits of a weight times its token's V scale down to
+ * (row, head) pairs a kv head: all 8 bits down to 2^-29 of its row's largest, smaller
+ * ones to 2^-36 of that), and 11 bits of a weight times its token's V scale down to
  * 2^-20 of the largest of its piece (smaller ones to 2^-31 of that); in fp32 q's 24
  * bits count, and 23 of such a weight down to 2^-10 (smaller ones to 2^-33).
  *

@@ -1,0 +1,48 @@
+"""Query rows over the 4-bit cache whose elements are far apart (bounds: attn_harness.py;
+the cases' q and K enter exactly)."""
+import pytest
+import torch
+
+import gated_deltanet_state_gb300 as gdn
+from gated_deltanet_state_gb300.inputs import AttnShape
+
+from attn4_harness import sequence_rows
+from attn_harness import assert_attention, attention64, err_word, slots_for, table_for
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(sh, q, k, v):
+    """One sequence of q's rows over k, v, cached in 4 bits; against 64 bits."""
+    L, n = k.shape[0], q.shape[0]
+    pages = -(-L // sh.page_tokens) + 1
+    pool, table, err = gdn.KVPool(sh, pages, fill=0xFF), table_for([L], sh.page_tokens, pages, 2), err_word()
+    dt = sh.torch_dtype()
+    gdn.gdn_kv_append(sh, pool, k=k.to(dt).cuda(), v=v.to(dt).cuda(), slot_map=slots_for(table, [L], [L], sh.page_tokens).cuda(), dev_error=err)
+    q = q.to(dt).cuda()
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    gdn.gdn_attn_decode(sh, pool, q=q, cu_seqlens=torch.tensor([0, n], dtype=torch.int32).cuda(),
+                        kv_len=torch.tensor([L], dtype=torch.int32).cuda(), block_table=table.cuda(), o=o, lse=lse, max_q_len=n,
+                        max_kv_len=L, dev_error=err)
+    assert err.item() == 0
+    kk, vv = sequence_rows(pool, table[0], L)
+    ref = attention64(q, kk, vv, sh.softmax_scale)
+    assert bool(torch.isfinite(ref[1]).all())
+    assert_attention(o, lse, ref, sh.dtype)
+    return kk
+
+
+@pytest.mark.parametrize("n", [1, 16])
+@pytest.mark.parametrize("gap", [10, 14, 17, 22])
+@pytest.mark.parametrize("residue", [0, 2, 5, 7])
+def test_large_elements_beside_codes_of_zero(n, gap, residue):
+    """Every eighth element of a row 2^gap of the others in the same groups of 32, where K is 0: a large
+    element times 0 adds nothing, so scores are the small elements', and no error goes with the large ones."""
+    L, d = 600, 128
+    sh = AttnShape(6, 1, d, 64, kv_bits=4)
+    g = torch.Generator().manual_seed(gap + residue)
+    q, k, v = torch.randn(n, 6, d, generator=g), torch.randn(L, 1, d, generator=g), torch.randn(L, 1, d, generator=g)
+    q[..., residue::8] = 2.0 ** gap * (1 + torch.rand(n, 6, d // 8, generator=g))
+    k[..., residue::8] = 0
+    kk = attend(sh, q, k, v)
+    assert not kk[..., residue::8].any()
