@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
           }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // the largest element to [2^15, 2^16)
-        const int e = max(-100, min(100, (int)(__float_as_uint(amax) >> 23) - 127 - 15));
+        // the largest element to [2^15, 2^16), whatever finite size it has (from below 2^-111
+        // as near as 2^e and its inverse are normal)
+        const int e = max(-126, min(112, (int)(__float_as_uint(amax) >> 23) - 127 - 15));
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
         for (int c = 0; c < GR; ++c) {

@@ -1,10 +1,10 @@
-"""Query rows over the 4-bit cache whose elements are far apart (bounds: attn_harness.py;
-the cases' q and K enter exactly)."""
+"""Query rows over the 4-bit cache whose elements are far apart, or far from 1
+(bounds: attn_harness.py; the cases' q and K enter exactly)."""
 import pytest
 import torch
 
 import gated_deltanet_state_gb300 as gdn
-from gated_deltanet_state_gb300.inputs import AttnShape
+from gated_deltanet_state_gb300.inputs import BF16, F32, AttnShape
 
 from attn4_harness import sequence_rows
 from attn_harness import assert_attention, attention64, err_word, slots_for, table_for
@@ -46,3 +46,17 @@ def test_large_elements_beside_codes_of_zero(n, gap, residue):
     k[..., residue::8] = 0
     kk = attend(sh, q, k, v)
     assert not kk[..., residue::8].any()
+
+
+@pytest.mark.parametrize("n,dt", [(1, BF16), (16, BF16), (2, F32)])
+@pytest.mark.parametrize("power", [-112, -60, 60, 96, 110, 117, 123])
+def test_rows_far_from_one(n, dt, power):
+    """q of about 2^power under a scale that brings the scores back to a few units: from the
+    smallest to within 2^5 of the largest finite values, products and scores are fp32 numbers."""
+    L, d = 300, 64
+    g = torch.Generator().manual_seed(abs(power))
+    q, k, v = torch.randn(n, 4, d, generator=g), torch.randn(L, 1, d, generator=g), torch.randn(L, 1, d, generator=g)
+    # K small where q is large, so that the products are far from overflow; 2^-10 of 1 has scales of its own all the same
+    size = 2.0 ** -10 if power > 0 else 1.0
+    q.clamp_(-8, 8)
+    attend(AttnShape(4, 1, d, 64, dtype=dt, kv_bits=4, scale=d ** -0.5 * 2.0 ** -power / size), q * 2.0 ** power, k * size, v)
