@@ -258,9 +258,10 @@ __device__ __forceinline__ float split_row(const uint4& x, uint2& hi, uint2& lo)
     amax = fmaxf(amax, fabsf(f[k]));
   }
   amax = warp_max(amax);
-  // largest element to (224, 448]; exponents kept where both factors are normal
+  // largest element to (224, 448], whatever finite size it has (from below 2^-118 as near
+  // as 2^e and its inverse are normal)
   int e = (int)(__float_as_uint(amax) >> 23) - 127 - 8 + ((__float_as_uint(amax) & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = max(-100, min(100, e));
+  e = max(-126, min(120, e));
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {

@@ -1,19 +1,20 @@
-"""Query rows over the 4-bit cache whose elements are far apart, or far from 1
-(bounds: attn_harness.py; the cases' q and K enter exactly)."""
+"""Query rows over the cache whose elements are far apart, or far from 1
+(bounds: attn_harness.py; over 4 bits the cases' q and K enter exactly)."""
 import pytest
 import torch
 
 import gated_deltanet_state_gb300 as gdn
 from gated_deltanet_state_gb300.inputs import BF16, F32, AttnShape
 
-from attn4_harness import sequence_rows
+import attn4_harness
+import attn_harness
 from attn_harness import assert_attention, attention64, err_word, slots_for, table_for
 
 pytestmark = pytest.mark.gpu
 
 
 def attend(sh, q, k, v):
-    """One sequence of q's rows over k, v, cached in 4 bits; against 64 bits."""
+    """One sequence of q's rows over k, v, cached; against 64 bits."""
     L, n = k.shape[0], q.shape[0]
     pages = -(-L // sh.page_tokens) + 1
     pool, table, err = gdn.KVPool(sh, pages, fill=0xFF), table_for([L], sh.page_tokens, pages, 2), err_word()
@@ -25,7 +26,7 @@ def attend(sh, q, k, v):
                         kv_len=torch.tensor([L], dtype=torch.int32).cuda(), block_table=table.cuda(), o=o, lse=lse, max_q_len=n,
                         max_kv_len=L, dev_error=err)
     assert err.item() == 0
-    kk, vv = sequence_rows(pool, table[0], L)
+    kk, vv = (attn4_harness if sh.kv_bits == 4 else attn_harness).sequence_rows(pool, table[0], L)
     ref = attention64(q, kk, vv, sh.softmax_scale)
     assert bool(torch.isfinite(ref[1]).all())
     assert_attention(o, lse, ref, sh.dtype)
@@ -48,9 +49,10 @@ def test_large_elements_beside_codes_of_zero(n, gap, residue):
     assert not kk[..., residue::8].any()
 
 
-@pytest.mark.parametrize("n,dt", [(1, BF16), (16, BF16), (2, F32)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("n,dt", [(1, BF16), (4, BF16), (16, BF16), (2, F32)])
 @pytest.mark.parametrize("power", [-112, -60, 60, 96, 110, 117, 123])
-def test_rows_far_from_one(n, dt, power):
+def test_rows_far_from_one(bits, n, dt, power):
     """q of about 2^power under a scale that brings the scores back to a few units: from the
     smallest to within 2^5 of the largest finite values, products and scores are fp32 numbers."""
     L, d = 300, 64
@@ -59,4 +61,4 @@ def test_rows_far_from_one(n, dt, power):
     # K small where q is large, so that the products are far from overflow; 2^-10 of 1 has scales of its own all the same
     size = 2.0 ** -10 if power > 0 else 1.0
     q.clamp_(-8, 8)
-    attend(AttnShape(4, 1, d, 64, dtype=dt, kv_bits=4, scale=d ** -0.5 * 2.0 ** -power / size), q * 2.0 ** power, k * size, v)
+    attend(AttnShape(4, 1, d, 64, dtype=dt, kv_bits=bits, scale=d ** -0.5 * 2.0 ** -power / size), q * 2.0 ** power, k * size, v)
