@@ -570,7 +570,7 @@ cudaError_t few(const AttnDecodeParams& p, int sms, bool follows, cudaStream_t s
   w.p_off = w.k_stages * sg.bytes;
   w.misc_off = w.p_off + red;
   const uint32_t smem = w.misc_off + misc;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode4_few_kernel<GR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(attn_decode4_few_kernel<GR>);
   if (e != cudaSuccess) return e;
   for (int s0 = 0; s0 < p.N; s0 += kDtSeqs) {
     w.s0 = s0;

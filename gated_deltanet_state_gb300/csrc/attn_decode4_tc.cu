@@ -714,7 +714,7 @@ cudaError_t decode4(const AttnDecodeParams& p, int sms, int lo, bool first, cuda
   // no more than CTAS on an SM, which share its tensor memory
   const uint32_t least = C::CTAS == 1 ? 120 * 1024 : 80 * 1024;
   if (smem < least) smem = least;
-  cudaError_t e = cudaFuncSetAttribute(attn_decode4_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(attn_decode4_tc_kernel<C>);
   if (e != cudaSuccess) return e;
   const int tiles = (p.max_q * p.G + C::NT - 1) / C::NT;
   for (int s0 = 0; s0 < p.N; s0 += kDtSeqs) {

@@ -489,7 +489,7 @@ cudaError_t decode_tc(const AttnDecodeParams& p, int sms, cudaStream_t st) {
   w.misc_off = (w.p_off + pp + 127) / 128 * 128;
   uint32_t smem = w.misc_off + (uint32_t)sizeof(DtShared<NT>) + 128;
   if (smem < 80 * 1024) smem = 80 * 1024;   // no more than two CTAs an SM share its tensor memory
-  cudaError_t e = cudaFuncSetAttribute(attn_decode_tc_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(attn_decode_tc_kernel<NT>);
   if (e != cudaSuccess) return e;
   for (int s0 = 0; s0 < p.N; s0 += kDtSeqs) {
     w.s0 = s0;

@@ -460,7 +460,7 @@ cudaError_t launch_attn_draft_tc(const AttnDecodeParams& p, int sms, bool overla
   w.misc_off = (w.q_off + q + 127) / 128 * 128;
   uint32_t smem = w.misc_off + (uint32_t)sizeof(DrShared) + 128;
   if (smem < 120 * 1024) smem = 120 * 1024;   // one CTA an SM: it takes the tensor memory whole
-  cudaError_t e = cudaFuncSetAttribute(attn_draft_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_shared(attn_draft_tc_kernel);
   if (e != cudaSuccess) return e;
   const int rt = (p.max_q * p.G + kDrRows - 1) / kDrRows;
   for (int s0 = 0; s0 < p.N; s0 += kDtSeqs) {

@@ -611,7 +611,7 @@ cudaError_t prefill_simt(AttnPrefillParams p, cudaStream_t st) {
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   const size_t sm =   // 217,088 B at d = 256
       (size_t)(kPreRows<D> * (p.d + 4) + kPreGroups<D> * (2 * kPreKeys * (p.d + 4) + kPreRows<D> * kPreLdP)) * 4;
-  cudaError_t e = cudaFuncSetAttribute(attn_prefill_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  cudaError_t e = allow_shared(attn_prefill_simt_kernel<T, D>);
   if (e != cudaSuccess) return e;
   attn_prefill_simt_kernel<T, D><<<(unsigned)grid, 4 * kPreRows<D> * kPreGroups<D>, sm, st>>>(p);
   return cudaGetLastError();

@@ -65,6 +65,19 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 namespace gdn {
 
+// Lets a kernel have as much dynamic shared memory as a CTA can.  Its launches may need
+// less, by their shapes, but the attribute is the kernel's: set to each call's own need,
+// another host thread's call would lower it between a call's setting and its launch,
+// which is then refused.
+template <typename F>
+inline cudaError_t allow_shared(F* kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+}
+
+}  // namespace gdn
+
+namespace gdn {
+
 // ---- Ampere-style asynchronous copies global -> shared (LDGSTS).  A
 // src_bytes of 0 zero-fills the destination without reading the source.
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

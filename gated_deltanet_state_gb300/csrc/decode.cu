@@ -205,7 +205,7 @@ static cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
   const size_t smem = sizeof(float) * (NC + 2 * G) + sizeof(TIN) * 3 * NC + sizeof(float) * G * DV + 16;
   auto kern = decode_kernel<DK, DV, TIN, TOUT>;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
   }
   dim3 grid(p.Hqk, p.num_seqs);
