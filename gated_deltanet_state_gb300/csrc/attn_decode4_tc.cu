@@ -94,14 +94,15 @@ __device__ __forceinline__ bool soft_any(bool x) {
 }
 
 // 32-bit words of pairs (f16, or bf16): a rounding, and what it leaves, PARTS times.
+// (In bf16 towards zero: three parts hold the 24 bits so too, and no finite number
+// becomes infinite.)
 template <int PARTS, bool BF16>
 __device__ __forceinline__ void split_pairs(float a, float b, uint32_t (&w)[PARTS]) {
 #pragma unroll
   for (int i = 0; i < PARTS; ++i) {
     float2 back;
     if constexpr (BF16) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
       back = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     } else {
       const __half2 h = __floats2half2_rn(a, b);

@@ -62,3 +62,14 @@ def test_rows_far_from_one(bits, n, dt, power):
     size = 2.0 ** -10 if power > 0 else 1.0
     q.clamp_(-8, 8)
     attend(AttnShape(4, 1, d, 64, dtype=dt, kv_bits=bits, scale=d ** -0.5 * 2.0 ** -power / size), q * 2.0 ** power, k * size, v)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("n,dt", [(1, BF16), (16, BF16), (1, F32), (9, F32)])
+def test_the_largest_finite_elements(bits, n, dt):
+    """Half of a row's elements at or next to the largest number of the type."""
+    L, d, most = 200, 64, torch.finfo(torch.bfloat16 if dt == BF16 else torch.float32).max
+    g = torch.Generator().manual_seed(n)
+    q, k, v = torch.randn(n, 4, d, generator=g), torch.randn(L, 1, d, generator=g), torch.randn(L, 1, d, generator=g)
+    q = (q.double() * 2.0 ** 127.5).clamp(-most, most)
+    attend(AttnShape(4, 1, d, 64, dtype=dt, kv_bits=bits, scale=2.0 ** -114), q, k * 2.0 ** -16, v)
