@@ -124,7 +124,9 @@ inline int64_t prefill_grid(AttnPrefillParams& p, int rows, int times) {
 // Over 4 bits, half the keys' bytes, a few rows' pieces are of 1,024 keys from 2,048
 // on, so that the outputs' share is the same.  There the kernel of a few rows has three
 // CTAs on an SM at d = 256, and 114 pieces a head are theirs for four kv heads (one
-// sequence of 229,376 tokens: 75 us with 76, 66 with 112, before the join).
+// sequence of 229,376 tokens: 75 us with 76, 66 with 112, before the join).  One or
+// two kv heads leave three quarters or half of those places empty: the cut does not
+// go by the number of heads.
 constexpr int kMaxPieces = 76, kMaxPieces4 = 114;
 constexpr int kDtNarrow = 16;   // (row, head of the group) pairs up to which a sequence counts as a few rows
 template <int MOST = kMaxPieces>
@@ -184,6 +186,27 @@ cudaError_t launch_attn_prefill_tc(const AttnPrefillParams& p, cudaStream_t st);
 #include <cuda_fp16.h>
 
 namespace gdn {
+
+// Eight consecutive elements of a row, as loaded.
+template <typename T> struct Row8;
+template <> struct Row8<__nv_bfloat16> {
+  uint4 w;
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void load(const void* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ float get(int i) const {
+    const uint32_t x = (&w.x)[i >> 1];
+    return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+  }
+};
+template <> struct Row8<float> {
+  float4 a, b;
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ void load(const void* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ float get(int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
+};
 
 // ---- e4m3 ----------------------------------------------------------------------
 // Two fp32 values to e4m3, nearest even, saturating (lo in the low byte); NaN stays NaN.

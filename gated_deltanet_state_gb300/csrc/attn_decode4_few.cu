@@ -140,19 +140,6 @@ __device__ __forceinline__ bool few_issued(const uint32_t* issued, uint32_t n, v
   }
   return true;
 }
-// Barrier of the four warps, with a vote.
-__device__ __forceinline__ bool few_any(bool x) {
-  int r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
-      " selp.s32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((int)x)
-      : "memory");
-  __syncwarp();
-  return r != 0;
-}
-
 // The loads of the CTA's items [i0, i1).  Bulk copies, which the lanes with one issue in
 // turn: lane 8 x + b has part x (K's codes, V's, K's scales, V's) of a tile's block b and
 // of the blocks of the stage that follow it in its page (all, in pages of whole tiles).
@@ -338,7 +325,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
           cs[k] = __shfl_sync(0xffffffffu, f, 8 * t + 4 * k);
           lim[k] = u.L - u.n + (2 * t + k) / p.G + 1;
         }
-        few_any(false);
+        dt_any<32 * kFewWarps>(false);
       }
       float o[2 * GR][4], l[2] = {0.f, 0.f}, off[2] = {kFewUnset, kFewUnset};
 #pragma unroll
@@ -478,7 +465,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
         l[h] = column_sum(l[h]);
         if (lane < 4) sh.stat[warp][2 * t + h] = make_float2(off[h], l[h]);
       }
-      if (few_any(!ok)) { ok = false; break; }
+      if (dt_any<32 * kFewWarps>(!ok)) { ok = false; break; }
       const int64_t R = p.T * p.Hq;
       float sum[2], mine[2];
       int64_t rh[2];
@@ -511,7 +498,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
           const float(&v)[4] = o[c0 + c];
           red[(warp * kFewWarps + c) * 32 + lane] = make_float4(v[0] * mine[0], v[1] * mine[1], v[2] * mine[0], v[3] * mine[1]);
         }
-        few_any(false);
+        dt_any<32 * kFewWarps>(false);
         const int ch = (c0 + warp) * 16 + g;
         if (ch < d) {
           float4 v = red[warp * 32 + lane];
@@ -535,7 +522,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtas<GR>) attn_decode4_few_ke
             }
           }
         }
-        few_any(false);
+        dt_any<32 * kFewWarps>(false);
       }
     }
   }

@@ -79,20 +79,6 @@ struct D4Shared : DtItems {
   uint32_t out[2][C::NT];         // (row, head) counted from the item's first row's head 0
 };
 
-// Barrier of the softmax threads, with a vote.
-template <int N>
-__device__ __forceinline__ bool soft_any(bool x) {
-  int r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
-      " selp.s32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((int)x), "n"(N)
-      : "memory");
-  __syncwarp();
-  return r != 0;
-}
-
 // 32-bit words of pairs (f16, or bf16): a rounding, and what it leaves, PARTS times.
 // (In bf16 towards zero: three parts hold the 24 bits so too, and no finite number
 // becomes infinite.)
@@ -127,22 +113,17 @@ __device__ __forceinline__ void read_columns(uint32_t col, float (&x)[CW]) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[16 * k + i] = __uint_as_float(v[k][i]);
     }
-  } else if constexpr (CW == 8) {
+  } else {
+    static_assert(CW == 8 && NT == 8 && PARTS > 1, "");
     float v[16];
     tc::tmem_ld16(col, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = PARTS == 1 ? v[i] : v[i] + v[8 + i];
+    for (int i = 0; i < 8; ++i) x[i] = v[i] + v[8 + i];
     if constexpr (PARTS == 3) {
       tc::tmem_ld16(col + 16, v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] += v[i];
     }
-  } else {
-    static_assert(PARTS == 2 && CW == 16 && NT == 16, "");
-    float v[16];
-    tc::tmem_ld16x2(col, col + 16, x, v);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] += v[i];
   }
 }
 
@@ -482,7 +463,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
       t = dt_item<NT>(w, sh.items, i0);
       load_q(t, 0);
     }
-    soft_any<C::SOFT>(false);
+    dt_any<C::SOFT>(false);
     for (int i = i0; i < i1; ++i) {
       float l[CW];
 #pragma unroll
@@ -530,7 +511,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int k = 4; k < CW; ++k) top[k & 3] = fmaxf(top[k & 3], x[k]);
-        if (soft_any<C::SOFT>(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kTop || !ok)) {
+        if (dt_any<C::SOFT>(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kTop || !ok)) {
           // a row's first keys, or one far above its reference (or a wait that ran
           // out): a row's reference moves by that row's scores alone
           scores(false);
@@ -541,7 +522,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
           }
           // the products before this tile's are done with O
           if (j > 0) ok = ok && dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit);
-          if (soft_any<C::SOFT>(!ok)) { ok = false; break; }
+          if (dt_any<C::SOFT>(!ok)) { ok = false; break; }
           if (tid < CW) {
             const int n = c0 + tid;
             const float mx = fmaxf(fmaxf(sh.cmax[0][n], sh.cmax[1][n]), fmaxf(sh.cmax[2][n], sh.cmax[3][n]));
@@ -555,7 +536,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
             }
             sh.alpha[n] = alpha;
           }
-          soft_any<C::SOFT>(false);
+          dt_any<C::SOFT>(false);
           if (j > 0) {
             tc::fence_after_sync();
 #pragma unroll
@@ -621,7 +602,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
 #pragma unroll
       for (int k = 0; k < CW; k += 16) sums16(l + k, sh.lsum + c0 + k, CW - k < 16 ? CW - k : 16, lane, quad);
       if (u.tiles > 0) ok = dt_wait(&sh.o_done[(T - 1) & 1], ((T - 1) >> 1) & 1, fail, limit);
-      if (soft_any<C::SOFT>(!ok)) { ok = false; break; }
+      if (dt_any<C::SOFT>(!ok)) { ok = false; break; }
       tc::fence_after_sync();
       const int64_t R = p.T * p.Hq, rh0 = (int64_t)(u.q0 + u.r0 / p.G) * p.Hq;
       const int rows = min(CW, u.rows - c0);   // columns of this warpgroup that are rows
@@ -669,9 +650,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         }
       }
       tc::fence_before_sync();
-      soft_any<C::SOFT>(false);   // lsum, references and O are free
+      dt_any<C::SOFT>(false);   // lsum, references and O are free
       if (threadIdx.x < NT) sh.off[threadIdx.x] = kUnset;
-      soft_any<C::SOFT>(false);
+      dt_any<C::SOFT>(false);
     }
   }
   __syncwarp();

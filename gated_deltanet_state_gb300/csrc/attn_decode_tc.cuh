@@ -84,6 +84,20 @@ __device__ __forceinline__ float dt_ex2(float x) {
   return y;
 }
 
+// Barrier 1, of N threads, with a vote.
+template <int N>
+__device__ __forceinline__ bool dt_any(bool x) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
+      " selp.s32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((int)x), "n"(N)
+      : "memory");
+  __syncwarp();
+  return r != 0;
+}
+
 // A call's two kernels over 4 bits, of sequences with many rows and with few, share
 // nothing, and the host does not know whether there is work for both.  So the first
 // lets the second start wherever its own CTAs have left, and the second ends only

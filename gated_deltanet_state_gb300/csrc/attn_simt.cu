@@ -317,8 +317,8 @@ cudaError_t decode_simt(const AttnDecodeParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// The join of a few rows is taken up to the warps that the SMs hold at once, over more
-// pieces than its lanes load in one round.
+// The join of a few rows is taken up to about the warps that 152 SMs hold at once (16
+// each: 2,432), over more pieces than its lanes load in one round.
 constexpr int64_t kJoinFew = 2400;
 
 // A join with so many warps a (row, head), launched as the last CTAs of the pieces'

@@ -35,27 +35,6 @@ __device__ __forceinline__ uint32_t lanes_umax(const uint32_t (&in)[N], int l) {
   return v[0];
 }
 
-// Eight consecutive elements of a row.
-template <typename T> struct Row8;
-template <> struct Row8<__nv_bfloat16> {
-  uint4 w;
-  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
-  __device__ void load(const void* p) { w = *reinterpret_cast<const uint4*>(p); }
-  __device__ float get(int i) const {
-    const uint32_t x = (&w.x)[i >> 1];
-    return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
-  }
-};
-template <> struct Row8<float> {
-  float4 a, b;
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void load(const void* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ float get(int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
-};
-
 // Largest magnitude of eight elements as fp32 bits: an infinity or a NaN gives
 // bits above every finite value's.
 __device__ __forceinline__ uint32_t max8_bits(const Row8<__nv_bfloat16>& r) {
@@ -299,7 +278,7 @@ __global__ void __launch_bounds__(32 * kKv4Warps, sizeof(T) == 2 ? 5 : 4) kv4_ap
     }
     const int in_page = (int)(first - page * p.c.page_tokens), b = in_page / kKvBlock;
     a.off = in_page % kKvBlock;
-    a.run = i == 31 ? 1 : 1 + __ffs(~(cont >> (i + 1))) - 1;   // (W <= 16: rows up to t0 + 31 reach a run's end)
+    a.run = __ffs(~(cont >> (i + 1)));   // (i < W <= 16: rows up to t0 + 31 reach a run's end)
     a.src = rows + i * a.stride;
     const int hh = h < p.c.Hkv ? h : 0;
     if (is_v) a.v(kv4_v_block(p.c, (int)page, hh, b), kv4_v_scale(p.c, (int)page, hh, b));
@@ -313,8 +292,10 @@ template <typename T, int LPT>
 cudaError_t append4_rows(const KvAppendParams& p, cudaStream_t st) {
   const unsigned gy = 2u * ((p.c.Hkv + 32 / LPT - 1) / (32 / LPT));
   // Few rows are often each of a sequence of their own, and a window's runs go one
-  // after another: 256 such rows 6.2 us in windows of 1, 35.9 of 16 (2 and 4: 8.3, 11.8);
-  // 2,048 rows in one run 8.1 and 4.5 us, 8,192 rows 22.7 and 8.7 (4 heads, d = 256, bf16).
+  // after another: 256 such rows 6.2 us in windows of 1, 35.9 of 16 (2 and 4: 8.3, 11.8).
+  // A run's rows are better off in windows of 16 from few rows on, but the host does
+  // not know the runs: up to 2,048 rows it takes them for single ones, where one run
+  // loses least (2,048 rows 8.1 and 4.5 us, 8,192 rows 22.7 and 8.7; 4 heads, d = 256, bf16).
   if (p.T <= 2048) kv4_append_kernel<T, LPT, 1><<<dim3((unsigned)((p.T + kKv4Warps - 1) / kKv4Warps), gy), 32 * kKv4Warps, 0, st>>>(p);
   else kv4_append_kernel<T, LPT, 16><<<dim3((unsigned)((p.T + 16 * kKv4Warps - 1) / (16 * kKv4Warps)), gy), 32 * kKv4Warps, 0, st>>>(p);
   return cudaGetLastError();

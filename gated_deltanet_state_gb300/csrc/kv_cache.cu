@@ -131,27 +131,6 @@ cudaError_t launch_kv_tables(const KvTablesParams& q, cudaStream_t st) {
 // ---- append -------------------------------------------------------------------------
 namespace {
 
-// Eight consecutive elements of a row, as loaded.
-template <typename T> struct Row8;
-template <> struct Row8<__nv_bfloat16> {
-  uint4 w;
-  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
-  __device__ void load(const void* p) { w = *reinterpret_cast<const uint4*>(p); }
-  __device__ float get(int i) const {
-    const uint32_t x = (&w.x)[i >> 1];
-    return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
-  }
-};
-template <> struct Row8<float> {
-  float4 a, b;
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void load(const void* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ float get(int i) const { return i < 4 ? (&a.x)[i] : (&b.x)[i - 4]; }
-};
-
 // The smallest power of two, at least 2^-64, with amax / scale <= 448 (finite amax >= 0).
 __device__ __forceinline__ float pow2_scale(float amax) {
   const uint32_t b = __float_as_uint(amax);
