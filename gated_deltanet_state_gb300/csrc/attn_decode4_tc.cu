@@ -71,6 +71,7 @@ struct D4Shared : DtItems {
   uint64_t k_full[kDtMaxStages], k_empty[kDtMaxStages], v_full[kDtMaxStages], v_empty[kDtMaxStages];
   uint64_t a_full[8], a_empty[8], s_full[2], p_full[2], o_done[2], q_full, drain;
   uint32_t have[kDtMaxStages];    // blocks of a tile that were loaded, by V stage
+  uint32_t nan[4 * C::SWG];       // of a softmax warp's tokens, those with a NaN scale of V
   float4 lsum[C::NT];
   float cmax[4][C::NT];           // largest score of each column, by warp
   float off[C::NT], alpha[C::NT];   // what a row's exponents are moved by: BASE less its reference
@@ -476,7 +477,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
         ok = dt_wait(&sh.v_full[st], vp, fail, limit);
         const uint32_t vbyte = (base + w.v_off + (uint32_t)st * v_unit + kDtBlocks * codes)[tid];
         const bool valid = pos < t.k1 && (sh.have[st] >> (tid >> 4) & 1);
-        const unsigned nan = __ballot_sync(0xffffffffu, valid && vbyte == kKv4Nan);   // tokens with a NaN scale of V
+        // (kept in shared memory until the weights: in a register, 16 drafts of 16 rows 202 us, 199)
+        const unsigned nan = __ballot_sync(0xffffffffu, valid && vbyte == kKv4Nan);
+        if (lane == 0) sh.nan[warp] = nan;
         __syncwarp();
         if (lane == 0) dt_arrive(&sh.v_empty[st]);
         // of this token: the exponent of its V scale, and what undoes it in the sums of
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS) attn_decode4_tc_kernel(co
                 make_uint4(word[0][v], word[1][v], word[2][v], word[3][v]);
         }
         // a NaN scale of V makes the weights of the rows that see its token NaN, not their sums
-        if (nan >> lane & 1) {
+        if (sh.nan[warp] >> lane & 1) {
 #pragma unroll 1
           for (int n = c0; n < c0 + CW; ++n)
             if (pos < sh.lim[par][n]) reinterpret_cast<uint16_t*>(pw + (n >> 3) * (16 * kDtTok))[n & 7] = 0x7fff;
