@@ -15,7 +15,7 @@
 // sixteenfold, whose partners in Q and whose weights carry 2^-4).  A group of 32
 // channels of K is a product of its own, added under its tokens' scales in fp32.  (K's
 // codes as they stand, as subnormals, with the offset of 8 taken out by the products'
-// start value, took no less: the 256 sequences below 381 us, 373 so.  And what is then
+// start value, took 2 % longer with half the instructions for it.  And what is then
 // summed and taken away again is 8 times a group's largest q, also where its code is
 // 0, so elements of 2^-10 of that lost bits.)  Which channel or token
 // stands in which step of a product is chosen so that a lane's word is its operand:
@@ -32,8 +32,8 @@
 // nothing but the tile.
 //
 // 256 sequences of 1,024 to 8,192 tokens, 24 heads, 4 kv heads, d = 256 (1.24 GB):
-// 368 us, 3.4 TB/s; one of 229,376 tokens 72 us.  What bounds it is the warps' own
-// chains: 5,700 instructions a tile at 1.9 a cycle (issue slots 48 % used, 28 % of a
+// 367 us, 3.4 TB/s; one of 229,376 tokens 72 us.  What bounds it is the warps' own
+// chains: 6,000 instructions a tile at 2.0 a cycle (issue slots 51 % used, 27 % of a
 // warp's time waiting for an instruction's fixed latency), which take 3,000 cycles
 // where the memory takes 1,500.  Registers hold the warps at 12 an SM and one for
 // loads a CTA: with four CTAs 96 registers a thread spill (495 us), with two 410 us.

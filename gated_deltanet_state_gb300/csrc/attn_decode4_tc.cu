@@ -18,9 +18,9 @@
 // 2^-10, 2^-33 of it below).
 //
 // 16 drafts of 16 rows over 2,048 to 32,768 tokens, 24 heads, 4 kv heads, d = 256 (117
-// GF, 321 MB): 210 to 214 us, all but 10 here.  A tile takes 5,000 cycles with its share of
-// the items' ends, 11,000 instructions of all kinds of warps at once (issue slots 54 %
-// used, the ALU pipe 45 %, most of it unpacking; the tensor pipe 33 %); what waits is
+// GF, 321 MB): 220 us, 200 of them here.  A tile takes 5,000 cycles with its share of
+// the items' ends, 11,000 instructions of all kinds of warps at once (issue slots 55 %
+// used, the ALU pipe 47 %, most of it unpacking; the tensor pipe 32 %); what waits is
 // the softmax's chain of scores, vote and weights.  Pieces of other sizes, two
 // softmax warpgroups on their own, and half the registers for twice the unpacking
 // warps took as long or longer.

@@ -101,9 +101,9 @@ __device__ __forceinline__ bool dt_any(bool x) {
 // A call's two kernels over 4 bits, of sequences with many rows and with few, share
 // nothing, and the host does not know whether there is work for both.  So the first
 // lets the second start wherever its own CTAs have left, and the second ends only
-// after it.  (Where the second has no work, it costs 16 drafts of 16 rows 5 us of 200,
+// after it.  (Where the second has no work, it costs 16 drafts of 16 rows 6 us of 220,
 // launched in the other order without overlap 9; four drafts of 4 rows over 2,000
-// keys 2 of 25, and 5.  The join started early as well: 7, and 3.)
+// keys 2 of 25, and 5.  The join started early as well: 8, and 3.)
 __device__ __forceinline__ void dt_let_next(const DtParams& w) {
   if (w.first) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
