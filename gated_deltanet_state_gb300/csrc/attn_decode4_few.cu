@@ -52,7 +52,7 @@ constexpr int kFewStages = 8;
 constexpr float kFewBase = 10.f, kFewTop = 15.75f;   // a weight at its reference is 2^10, none passes 2^15.75
 constexpr float kFewUnset = 3e38f;                   // the offset of a row that has seen no key
 
-// A stage holds the tokens of CPS warps: K's codes, K's scales, V's codes, V's scales,
+// A stage holds the tokens of kFewPer warps: K's codes, K's scales, V's codes, V's scales,
 // as they lie in pages.  All four warps' up to d = 128, where a copy is short and its
 // issue what counts; one's above, so that three CTAs an SM hold some ahead.
 template <int GR>
