@@ -37,9 +37,7 @@ def check_lse(got, q, k, v, sh):
 @pytest.mark.parametrize("n,L", [(1, 300), (2, 90), (9, 700), (20, 40), (1, 5000), (16, 5000), (32, 20)])
 @pytest.mark.parametrize("back", [0, 1, 130])
 def test_lse_beside_a_nan_in_v(Hq, Hkv, d, dt, n, L, back):
-    token = L - 1 - back
-    if token < 0:
-        pytest.skip("no such token")
+    token = max(L - 1 - back, 0)
     sh = AttnShape(Hq, Hkv, d, 64, dtype=dt, kv_bits=4)
     pool, table, q, o, lse = decode_case(sh, [L, 60], [n, 1], seed=n + L)
     nan_value(sh, pool, table, token, 1)
